@@ -30,6 +30,16 @@ __all__ = [
     "sgemm", "linear_fwd", "linear_bwd_input", "linear_bwd_weight", "EmuLinearFunction", "EmuLinear",
     "library_path", "load",
 ]
+# the feed-forward operators (feed_forward.py), loaded with torch on first use
+_FEED_FORWARD = (
+    "EMU_ACT_NONE", "EMU_ACT_RELU", "EMU_ACT_GELU", "EMU_ACT_GELU_TANH", "EMU_ACT_SILU", "ACTS",
+    "emu_layer_norm_fwd", "emu_layer_norm_bwd", "emu_linear_act_fwd", "emu_linear_act_bwd", "emu_gated_fwd",
+    "emu_gated_bwd", "emu_gated_ffn_fwd", "emu_gated_ffn_bwd",
+    "layer_norm_fwd", "layer_norm_bwd", "linear_act_fwd", "linear_act_bwd", "gated_fwd", "gated_bwd",
+    "gated_ffn_fwd", "gated_ffn_bwd", "EmuLayerNormFunction", "EmuLinearActFunction", "EmuGatedFFNFunction",
+    "EmuFeedForwardFunction", "EmuLayerNorm", "EmuLinearAct", "EmuGatedFFN", "EmuFeedForward",
+)
+__all__ += _FEED_FORWARD
 
 EMU_MODE_BF16X9 = 0
 EMU_MODE_TF32X3 = 1
@@ -486,5 +496,10 @@ def __getattr__(name):
     if name in ("EmuLinearFunction", "EmuLinear"):
         f, m = _autograd()
         globals()["EmuLinearFunction"], globals()["EmuLinear"] = f, m
+        return globals()[name]
+    if name in _FEED_FORWARD:
+        from . import feed_forward
+        for n in _FEED_FORWARD:
+            globals()[n] = getattr(feed_forward, n)
         return globals()[name]
     raise AttributeError(name)

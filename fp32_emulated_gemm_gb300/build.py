@@ -1,6 +1,7 @@
 """Build libemu_gemm.so in-tree with nvcc for sm_103a (GB300)."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -8,8 +9,9 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, "emu_gemm.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("emu_kernel.cuh", "ptx.cuh")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("emu_gemm.cu", "feed_forward.cu", "layer_norm.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("activation.cuh", "emu_kernel.cuh", "internal.h", "ptx.cuh",
+                                                  "row_ops.cuh")] + [
     os.path.join(os.path.dirname(HERE), "include", "emu_gemm.h")]
 LIB = os.path.join(HERE, "libemu_gemm.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
@@ -33,14 +35,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-Xptxas", "-v" if verbose else "-O3", "-o", tmp] + SOURCES
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    if verbose:
-        sys.stderr.write(r.stdout + r.stderr)
-    os.replace(tmp, LIB)
+    flags = [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v" if verbose else "-O3"]
+    objects = [f"{tmp}.{os.path.basename(src)}.o" for src in SOURCES]
+
+    def run(cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+        if verbose:
+            sys.stderr.write(r.stdout + r.stderr)
+
+    try:
+        # the files are independent: compiled side by side, then linked
+        with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(run, [[nvcc()] + flags + ["-c", "-o", o, src] for src, o in zip(SOURCES, objects)]))
+        run([nvcc(), ARCH, "-shared", "-o", tmp] + objects)
+        os.replace(tmp, LIB)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     return LIB
 
 

@@ -20,6 +20,7 @@
 
 #include "../../include/emu_gemm.h"
 #include "emu_kernel.cuh"
+#include "internal.h"
 
 namespace emu {
 namespace {
@@ -57,6 +58,8 @@ struct Workspace {
     unsigned long long epoch = 0;
     void* packed = nullptr;   // op(B) split ahead of a product (automatic pre-split)
     size_t packed_bytes = 0;
+    float* reduce = nullptr;  // column-sum partials of the row-wise operators
+    size_t reduce_floats = 0;
 };
 constexpr int kMaxWorkspaces = 64;   // (device, stream) pairs with a workspace at once
 Workspace g_ws[kMaxWorkspaces];
@@ -532,6 +535,25 @@ emu_status_t packed_buffer_for(int dev, cudaStream_t stream, size_t bytes, void*
     return EMU_STATUS_SUCCESS;
 }
 
+// The (device, stream)'s buffer for column-sum partials, grown on demand and kept.
+emu_status_t reduce_buffer_for(int dev, cudaStream_t stream, size_t floats, float** out) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    Workspace* w = workspace_slot(dev, stream);
+    if (!w) return EMU_STATUS_ALLOC_FAILED;
+    if (w->reduce_floats < floats) {
+        if (w->reduce && cudaFreeAsync(w->reduce, stream) != cudaSuccess) cudaGetLastError();
+        w->reduce = nullptr;
+        w->reduce_floats = 0;
+        if (lib_malloc_async(reinterpret_cast<void**>(&w->reduce), floats * sizeof(float), stream) != cudaSuccess) {
+            cudaGetLastError();
+            return EMU_STATUS_ALLOC_FAILED;
+        }
+        w->reduce_floats = floats;
+    }
+    *out = w->reduce;
+    return EMU_STATUS_SUCCESS;
+}
+
 // Automatic pre-split of op(B): for the TF32 modes the split is costly enough
 // that splitting op(B) once per product, ahead of it, and loading its
 // components pays as soon as several tile rows share them (measured 1.2-1.6x
@@ -875,6 +897,7 @@ cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters
 
 // Core: C = alpha * op(A) op(B) + beta * C_old + bias, with C_old == C.
 // packed_b != nullptr: op(B) comes packed (emu_pack_b); B and ldb are unused.
+// check_only: the checks and the buffers' reservation, without a launch.
 // One launch of the pack kernel on `stream` (the caller checked the arguments).
 cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, int64_t ldb, bool k_major,
                         void* packed, int sm_count, cudaStream_t stream) {
@@ -893,7 +916,8 @@ cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, i
 
 emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t N, int64_t K, float alpha,
                       const float* A, int64_t lda, const float* B, int64_t ldb, float beta, float* C,
-                      int64_t ldc, const float* bias, cudaStream_t stream, const void* packed_b = nullptr) {
+                      int64_t ldc, const float* bias, cudaStream_t stream, const void* packed_b = nullptr,
+                      bool check_only = false) {
     if (!valid_mode(mode)) return EMU_STATUS_INVALID_VALUE;
     if (M < 0 || N < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
     if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return EMU_STATUS_NOT_SUPPORTED;
@@ -918,6 +942,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     if (st != EMU_STATUS_SUCCESS) return st;
 
     if (!gemm) {
+        if (check_only) return EMU_STATUS_SUCCESS;
         const int64_t total = M * N;
         const int threads = 256;
         const int64_t blocks64 = (total + threads - 1) / threads;
@@ -931,6 +956,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     if (!packed_b) mode = dispatch_mode(mode, M, N, K, pairs, dev->sm_count);
     if (mode == EMU_MODE_FP32) {
         if (N > 64LL * NAT_MAX_GRID_Y) return EMU_STATUS_NOT_SUPPORTED;
+        if (check_only) return EMU_STATUS_SUCCESS;
         if (log_enabled())
             std::fprintf(stderr, "[emu] fp32 M=%lld N=%lld K=%lld a_mn=%d b_mn=%d (native)\n", (long long)M,
                          (long long)N, (long long)K, (int)a_mn, (int)b_mn);
@@ -985,6 +1011,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         p.workspace = w->partials;
         p.counters = w->counters;
     }
+    if (check_only) return EMU_STATUS_SUCCESS;
     if (autopack_buf && launch_pack(mode, N, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
         return EMU_STATUS_LAUNCH_FAILED;
     const int clusters = plan.clusters;
@@ -1071,6 +1098,25 @@ __global__ void split_timeout_selftest_kernel(unsigned long long* counters, int 
 }
 
 }  // namespace
+
+emu_status_t current_device(DeviceCtx* out) {
+    DeviceInfo* d = nullptr;
+    const emu_status_t st = device_info(&d);
+    if (st != EMU_STATUS_SUCCESS) return st;
+    cudaGetDevice(&out->id);
+    out->sm_count = d->sm_count;
+    return EMU_STATUS_SUCCESS;
+}
+
+emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float** out) {
+    return reduce_buffer_for(dev, stream, floats, out);
+}
+
+emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check) {
+    return run_gemm(mode, g.a_mn, g.b_mn, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.bias, stream,
+                    nullptr, check);
+}
+
 }  // namespace emu
 
 using namespace emu;
@@ -1246,6 +1292,7 @@ emu_status_t emu_shutdown(void) {
         if (w.partials && cudaFree(w.partials) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.counters && cudaFree(w.counters) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.packed && cudaFree(w.packed) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        if (w.reduce && cudaFree(w.reduce) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         w = Workspace{};
     }
     if (have_current && cudaSetDevice(current) != cudaSuccess) cudaGetLastError();

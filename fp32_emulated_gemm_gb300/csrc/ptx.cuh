@@ -12,8 +12,9 @@ namespace emu {
 
 // Device-global error word, read and cleared by emu_stream_check().
 // Bit 0: a wait timed out.  Bits 8..15: the role that timed out (for logs).
-// (The library is a single translation unit, so the definition lives here.)
-__device__ unsigned int g_error_flag = 0;
+// One word per source file that launches kernels with waits (each file is
+// compiled by itself); emu_stream_check() reads them all.
+static __device__ unsigned int g_error_flag = 0;
 
 enum : unsigned { ERR_TIMEOUT = 1u };
 

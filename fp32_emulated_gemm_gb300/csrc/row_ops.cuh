@@ -1,0 +1,57 @@
+// row_ops.cuh -- loads, stores and sums shared by the row-wise FP32 kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace emu {
+
+inline bool vec4_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld & 3) == 0; }
+
+// (Plain loads: a kernel may write the matrix it reads, element by element.)
+// Four values of a row: VEC: columns c .. c + 3 (all inside or all outside the
+// row, whose width is a multiple of 4); otherwise columns c, c + S, c + 2S,
+// c + 3S, each checked, so that neighbouring lanes read neighbouring words at
+// any alignment.
+template <bool VEC, int S>
+__device__ __forceinline__ float4 load4(const float* row, int64_t c, int64_t n) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (VEC) {
+        if (c < n) v = *reinterpret_cast<const float4*>(row + c);
+    } else {
+        if (c < n) v.x = row[c];
+        if (c + S < n) v.y = row[c + S];
+        if (c + 2 * S < n) v.z = row[c + 2 * S];
+        if (c + 3 * S < n) v.w = row[c + 3 * S];
+    }
+    return v;
+}
+template <bool VEC, int S>
+__device__ __forceinline__ void store4(float* row, int64_t c, int64_t n, const float4& v) {
+    if constexpr (VEC) {
+        if (c < n) *reinterpret_cast<float4*>(row + c) = v;
+    } else {
+        if (c < n) row[c] = v.x;
+        if (c + S < n) row[c + S] = v.y;
+        if (c + 2 * S < n) row[c + 2 * S] = v.z;
+        if (c + 3 * S < n) row[c + 3 * S] = v.w;
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// out[c] = sum over p of partial[p * C + c], p ascending in 32 interleaved
+// chains that are then added in a fixed order: the sums do not depend on
+// timing.  Block: 32 columns x 32 chains.
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* partial, int P, int64_t C, int64_t split,
+                                                            float* out0, float* out1);
+// Columns [0, split) go to out0, [split, C) to out1; a null output is skipped.
+cudaError_t launch_sum_partials(const float* partial, int P, int64_t C, int64_t split, float* out0, float* out1,
+                                cudaStream_t stream);
+
+}  // namespace emu

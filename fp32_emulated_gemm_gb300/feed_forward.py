@@ -1,0 +1,483 @@
+"""Feed-forward operators around the emulated products: layer norm, a linear
+layer with bias, activation and residual in one call, and the gated
+feed-forward block, each with its backward pass.
+
+Like the rest of the binding, the functions only marshal arguments; the
+computation runs in libemu_gemm.so (see ``include/emu_gemm.h`` for the
+contract).  Matrices are CUDA float32 with rows of unit column stride.  A
+matrix that enters a product and does not start on a 16-byte boundary with a
+row stride that is a multiple of 4 is copied into one that does (as every
+matrix of a width that is not a multiple of 4 is, unless it has padded rows
+already: the results of these functions have).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _check, _mode, _new_c, _ptr, _stream, load
+
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+EMU_ACT_NONE, EMU_ACT_RELU, EMU_ACT_GELU, EMU_ACT_GELU_TANH, EMU_ACT_SILU = range(5)
+
+# Argument kinds of the C entry points, stream left out: e enum, n int64, f float, p pointer.
+_SIGNATURES = {
+    "emu_layer_norm_fwd": "nnpnppfpnpp",
+    "emu_layer_norm_bwd": "nnpnpnppppnpnpp",
+    "emu_linear_act_fwd": "eennnpnpnppnpnpn",
+    "emu_linear_act_bwd": "eennnpnpnpnpnpnpnpnp",
+    "emu_gated_fwd": "eennnpnpnppnpn",
+    "emu_gated_bwd": "eennnpnpnpnpnpnpnpnp",
+    "emu_gated_ffn_fwd": "eennnnpnpnppnppnpnpnpn",
+    "emu_gated_ffn_bwd": "eennnnpnpnpnpnpnpnpnpnpnppnp",
+}
+_CTYPES = {"e": ctypes.c_int, "n": ctypes.c_int64, "f": ctypes.c_float, "p": ctypes.c_void_p}
+_CAST = {"e": int, "n": int, "f": float, "p": _ptr}
+_functions = {}
+
+
+def _fn(name):
+    f = _functions.get(name)
+    if f is None:
+        f = getattr(load(), name)
+        f.argtypes = [_CTYPES[k] for k in _SIGNATURES[name]] + [ctypes.c_void_p]
+        f.restype = ctypes.c_int
+        _functions[name] = f
+    return f
+
+
+def _c_name(name):
+    kinds = _SIGNATURES[name]
+
+    def call(*args, stream=None):
+        if len(args) != len(kinds):
+            raise TypeError(f"{name} takes {len(kinds)} arguments and a stream")
+        _check(_fn(name)(*[_CAST[k](a) for k, a in zip(kinds, args)], _stream(stream)), name)
+
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = f"{name} of include/emu_gemm.h: its arguments in order, then stream=None (the current one)."
+    return call
+
+
+emu_layer_norm_fwd = _c_name("emu_layer_norm_fwd")
+emu_layer_norm_bwd = _c_name("emu_layer_norm_bwd")
+emu_linear_act_fwd = _c_name("emu_linear_act_fwd")
+emu_linear_act_bwd = _c_name("emu_linear_act_bwd")
+emu_gated_fwd = _c_name("emu_gated_fwd")
+emu_gated_bwd = _c_name("emu_gated_bwd")
+emu_gated_ffn_fwd = _c_name("emu_gated_ffn_fwd")
+emu_gated_ffn_bwd = _c_name("emu_gated_ffn_bwd")
+
+
+# ------------------------------------------------------------ arguments ----
+def _act(act):
+    try:
+        return ACTS[act]
+    except KeyError:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}") from None
+
+
+def _rows(t, name, shape=None):
+    """`t` as a matrix of unit column stride whose rows do not overlap."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.float32):
+        raise TypeError(f"{name} must be a CUDA float32 tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {t.shape[0]} x {t.shape[1]}")
+    r, c = t.shape
+    if (c > 1 and t.stride(1) != 1) or (r > 1 and t.stride(0) < c):
+        t = t.contiguous()
+    return t
+
+
+def _ld(t):
+    """The row stride of a matrix from _rows, as the library wants it (a
+    single row's stride means nothing in torch)."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 3) // 4 * 4
+
+
+def _operand(t, name, shape=None):
+    """`t` as a product's operand: rows on 16-byte boundaries."""
+    t = _rows(t, name, shape)
+    if t.data_ptr() & 15 or (t.shape[0] > 1 and t.stride(0) & 3):
+        p = _new_c(t.shape[0], t.shape[1], t.device)
+        p.copy_(t)
+        t = p
+    return t
+
+
+def _vector(t, name, n):
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.float32):
+        raise TypeError(f"{name} must be a CUDA float32 tensor")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be a vector of {n}")
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
+def _result(out, shape, like, name):
+    if out is None:
+        return _new_c(shape[0], shape[1], like.device)
+    if not (isinstance(out, torch.Tensor) and out.is_cuda and out.dtype is torch.float32):
+        raise TypeError(f"{name} must be a CUDA float32 tensor")
+    if tuple(out.shape) != shape or (shape[1] > 1 and out.stride(1) != 1) or (shape[0] > 1 and out.stride(0) < shape[1]):
+        raise ValueError(f"{name} must be {shape[0]} x {shape[1]} with unit column stride")
+    return out
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(name, tensors):
+    """The current stream of the tensors' device, which has to be one and the
+    current one."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: all tensors must be on the current device (cuda:{dev})")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# ----------------------------------------------------------- layer norm ----
+def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, out=None):
+    """(Y, mean, rstd): Y = (X - mean) * rstd * weight + bias over the rows of X."""
+    X = _rows(X, "X")
+    M, N = X.shape
+    weight, bias = _vector(weight, "weight", N), _vector(bias, "bias", N)
+    Y = out if out is None else _result(out, (M, N), X, "out")
+    if Y is None:
+        Y = torch.empty((M, N), device=X.device, dtype=torch.float32)
+    stats = torch.empty((2, M), device=X.device, dtype=torch.float32)
+    mean, rstd = stats[0], stats[1]
+    s = _raw_stream("layer_norm_fwd", (X, weight, bias, Y))
+    _check(_fn("emu_layer_norm_fwd")(M, N, _p(X), _ld(X), _p(weight), _p(bias), float(eps), _p(Y), _ld(Y), _p(mean),
+                                     _p(rstd), s), "emu_layer_norm_fwd")
+    return Y, mean, rstd
+
+
+def layer_norm_bwd(dY, X, weight, mean, rstd, *, add=None, need_input=True, need_params=True):
+    """(dX, dweight, dbias) of layer_norm_fwd; `add` (a gradient that reaches X
+    by another way) is added to dX.  What is not needed comes back as None."""
+    X = _rows(X, "X")
+    M, N = X.shape
+    dY = _rows(dY, "dY", (M, N))
+    add = None if add is None else _rows(add, "add", (M, N))
+    if add is not None and not need_input:
+        raise ValueError("add needs dX")
+    weight = _vector(weight, "weight", N)
+    for v, name in ((mean, "mean"), (rstd, "rstd")):
+        if v.shape != (M,) or v.dtype is not torch.float32 or (M > 1 and v.stride(0) != 1):
+            raise ValueError(f"{name} must be the forward pass's vector of {M}")
+    dX = torch.empty((M, N), device=X.device, dtype=torch.float32) if need_input else None
+    params = torch.empty((2, N), device=X.device, dtype=torch.float32) if need_params else None
+    dw, db = (params[0], params[1]) if need_params else (None, None)
+    s = _raw_stream("layer_norm_bwd", (dY, X, weight, mean, rstd, add))
+    _check(_fn("emu_layer_norm_bwd")(M, N, _p(dY), _ld(dY), _p(X), _ld(X), _p(weight), _p(mean), _p(rstd), _p(add),
+                                     0 if add is None else _ld(add), _p(dX), N, _p(dw), _p(db), s),
+           "emu_layer_norm_bwd")
+    return dX, dw, db
+
+
+# ----------------------------------------------------------- linear_act ----
+def linear_act_fwd(X, W, bias=None, *, act="none", residual=None, mode="bf16x9", save=False, out=None):
+    """Y = act(X W^T + bias) + residual (X [M,K], W [N,K]); with `save`
+    (Y, Z), Z the pre-activation that linear_act_bwd reads."""
+    X, W = _operand(X, "X"), _operand(W, "W")
+    (M, K), N = X.shape, W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    bias = _vector(bias, "bias", N)
+    residual = None if residual is None else _operand(residual, "residual", (M, N))
+    Y = _result(out, (M, N), X, "out")
+    Z = _new_c(M, N, X.device) if save else None
+    s = _raw_stream("linear_act_fwd", (X, W, bias, residual, Y))
+    _check(_fn("emu_linear_act_fwd")(_mode(mode), _act(act), M, N, K, _p(X), _ld(X), _p(W), _ld(W), _p(bias),
+                                     _p(residual), 0 if residual is None else _ld(residual), _p(Z),
+                                     _ld(Z) if save else 0, _p(Y), _ld(Y), s), "emu_linear_act_fwd")
+    return (Y, Z) if save else Y
+
+
+def linear_act_bwd(dY, X, W, Z=None, *, act="none", mode="bf16x9", need=(True, True, True)):
+    """(dX, dW, dbias) of linear_act_fwd (the residual's gradient is dY); Z is
+    not read for act "none".  `need` says which are wanted; the others are None."""
+    a = _act(act)
+    X, W = _operand(X, "X"), _operand(W, "W")
+    (M, K), N = X.shape, W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    dY = _operand(dY, "dY", (M, N))
+    dZ = None
+    if a != EMU_ACT_NONE:
+        if Z is None:
+            raise ValueError(f"act {act!r} needs Z")
+        Z, dZ = _operand(Z, "Z", (M, N)), _new_c(M, N, X.device)
+    else:
+        Z = None
+    dX = _new_c(M, K, X.device) if need[0] else None
+    dW = _new_c(N, K, X.device) if need[1] else None
+    db = torch.empty(N, device=X.device, dtype=torch.float32) if need[2] else None
+    s = _raw_stream("linear_act_bwd", (dY, X, W, Z))
+    _check(_fn("emu_linear_act_bwd")(_mode(mode), a, M, N, K, _p(dY), _ld(dY), _p(X), _ld(X), _p(W), _ld(W), _p(Z),
+                                     0 if Z is None else _ld(Z), _p(dZ), 0 if dZ is None else _ld(dZ), _p(dX),
+                                     (K + 3) // 4 * 4, _p(dW), (K + 3) // 4 * 4, _p(db), s), "emu_linear_act_bwd")
+    return dX, dW, db
+
+
+# ---------------------------------------------------------------- gated ----
+def _gated_shapes(X, W):
+    if W.shape[0] % 2:
+        raise ValueError("W must have the gate's rows, then as many of the up projection")
+    if W.shape[1] != X.shape[1]:
+        raise ValueError("inner dimensions differ")
+    return X.shape[0], X.shape[1], W.shape[0] // 2
+
+
+def gated_fwd(X, W, bias=None, *, act="silu", mode="bf16x9", save=False):
+    """H = act(G) * U with [G | U] = X W^T + bias (X [M,K]; W [2F,K]: the
+    gate's rows, then the up projection's); with `save` (H, Z), Z = [G | U]."""
+    X, W = _operand(X, "X"), _operand(W, "W")
+    M, K, F = _gated_shapes(X, W)
+    bias = _vector(bias, "bias", 2 * F)
+    H, Z = _new_c(M, F, X.device), _new_c(M, 2 * F, X.device)
+    s = _raw_stream("gated_fwd", (X, W, bias))
+    _check(_fn("emu_gated_fwd")(_mode(mode), _act(act), M, F, K, _p(X), _ld(X), _p(W), _ld(W), _p(bias), _p(Z), _ld(Z),
+                                _p(H), _ld(H), s), "emu_gated_fwd")
+    return (H, Z) if save else H
+
+
+def gated_bwd(dH, X, W, Z, *, act="silu", mode="bf16x9", need=(True, True, True)):
+    """(dX, dW, dbias) of gated_fwd from Z; `need` says which are wanted."""
+    X, W = _operand(X, "X"), _operand(W, "W")
+    M, K, F = _gated_shapes(X, W)
+    dH, Z = _operand(dH, "dH", (M, F)), _operand(Z, "Z", (M, 2 * F))
+    dZ = _new_c(M, 2 * F, X.device)
+    dX = _new_c(M, K, X.device) if need[0] else None
+    dW = _new_c(2 * F, K, X.device) if need[1] else None
+    db = torch.empty(2 * F, device=X.device, dtype=torch.float32) if need[2] else None
+    s = _raw_stream("gated_bwd", (dH, X, W, Z))
+    _check(_fn("emu_gated_bwd")(_mode(mode), _act(act), M, F, K, _p(dH), _ld(dH), _p(X), _ld(X), _p(W), _ld(W), _p(Z),
+                                _ld(Z), _p(dZ), _ld(dZ), _p(dX), (K + 3) // 4 * 4, _p(dW), (K + 3) // 4 * 4, _p(db), s),
+           "emu_gated_bwd")
+    return dX, dW, db
+
+
+def _ffn_shapes(X, W_in, W_out):
+    M, K, F = _gated_shapes(X, W_in)
+    if W_out.shape[1] != F:
+        raise ValueError("W_out must have one column per gated feature")
+    return M, K, F, W_out.shape[0]
+
+
+def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mode="bf16x9", save=False, out=None):
+    """Y = H W_out^T + b_out + residual with H = gated_fwd(X, W_in, b_in)
+    (X [M,K], W_in [2F,K], W_out [N,F]; the biases and the residual may be
+    None); with `save` (Y, Z, H) for gated_ffn_bwd."""
+    X, W_in, W_out = _operand(X, "X"), _operand(W_in, "W_in"), _operand(W_out, "W_out")
+    M, K, F, N = _ffn_shapes(X, W_in, W_out)
+    b_in, b_out = _vector(b_in, "b_in", 2 * F), _vector(b_out, "b_out", N)
+    residual = None if residual is None else _operand(residual, "residual", (M, N))
+    Y = _result(out, (M, N), X, "out")
+    H, Z = _new_c(M, F, X.device), _new_c(M, 2 * F, X.device)
+    s = _raw_stream("gated_ffn_fwd", (X, W_in, b_in, W_out, b_out, residual, Y))
+    _check(_fn("emu_gated_ffn_fwd")(_mode(mode), _act(act), M, K, F, N, _p(X), _ld(X), _p(W_in), _ld(W_in), _p(b_in),
+                                    _p(W_out), _ld(W_out), _p(b_out), _p(residual),
+                                    0 if residual is None else _ld(residual), _p(Z), _ld(Z), _p(H), _ld(H), _p(Y),
+                                    _ld(Y), s), "emu_gated_ffn_fwd")
+    return (Y, Z, H) if save else Y
+
+
+def gated_ffn_bwd(dY, X, W_in, W_out, Z, H, *, act="silu", mode="bf16x9", need=(True, True, True, True, True)):
+    """(dX, dW_in, db_in, dW_out, db_out) of gated_ffn_fwd from its Z and H
+    (the residual's gradient is dY); `need` says which are wanted."""
+    X, W_in, W_out = _operand(X, "X"), _operand(W_in, "W_in"), _operand(W_out, "W_out")
+    M, K, F, N = _ffn_shapes(X, W_in, W_out)
+    dY, Z, H = _operand(dY, "dY", (M, N)), _operand(Z, "Z", (M, 2 * F)), _operand(H, "H", (M, F))
+    dZ = _new_c(M, 2 * F, X.device)
+    dX = _new_c(M, K, X.device) if need[0] else None
+    dWi = _new_c(2 * F, K, X.device) if need[1] else None
+    dbi = torch.empty(2 * F, device=X.device, dtype=torch.float32) if need[2] else None
+    dWo = _new_c(N, F, X.device) if need[3] else None
+    dbo = torch.empty(N, device=X.device, dtype=torch.float32) if need[4] else None
+    s = _raw_stream("gated_ffn_bwd", (dY, X, W_in, W_out, Z, H))
+    _check(_fn("emu_gated_ffn_bwd")(_mode(mode), _act(act), M, K, F, N, _p(dY), _ld(dY), _p(X), _ld(X), _p(W_in),
+                                    _ld(W_in), _p(W_out), _ld(W_out), _p(Z), _ld(Z), _p(H), _ld(H), _p(dZ), _ld(dZ),
+                                    _p(dX), (K + 3) // 4 * 4, _p(dWi), (K + 3) // 4 * 4, _p(dbi), _p(dWo),
+                                    (F + 3) // 4 * 4, _p(dbo), s), "emu_gated_ffn_bwd")
+    return dX, dWi, dbi, dWo, dbo
+
+
+# ------------------------------------------------------------- autograd ----
+class EmuLayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, weight, bias, eps):
+        Y, mean, rstd = layer_norm_fwd(X, weight, bias, eps=eps)
+        ctx.save_for_backward(X, weight, mean, rstd)
+        ctx.has_bias = bias is not None
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dX, dw, db = layer_norm_bwd(dY, X, weight, mean, rstd, need_input=need[0], need_params=need[1] or need[2])
+        return dX, dw if need[1] else None, db if need[2] else None, None
+
+
+class EmuLinearActFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, bias, residual, act, mode):
+        save = act != "none" and any(ctx.needs_input_grad[:3])
+        r = linear_act_fwd(X, W, bias, act=act, residual=residual, mode=mode, save=save)
+        Y, Z = r if save else (r, None)
+        ctx.save_for_backward(X, W, Z)
+        ctx.act, ctx.mode = act, mode
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, W, Z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dX = dW = db = None
+        if any(need[:3]):
+            dX, dW, db = linear_act_bwd(dY, X, W, Z, act=ctx.act, mode=ctx.mode, need=need[:3])
+        return dX, dW, db, dY if need[3] else None, None, None
+
+
+class EmuGatedFFNFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W_in, b_in, W_out, b_out, residual, act, mode):
+        save = any(ctx.needs_input_grad[:5])
+        r = gated_ffn_fwd(X, W_in, b_in, W_out, b_out, act=act, residual=residual, mode=mode, save=save)
+        Y, Z, H = r if save else (r, None, None)
+        ctx.save_for_backward(X, W_in, W_out, Z, H)
+        ctx.act, ctx.mode = act, mode
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, W_in, W_out, Z, H = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grads = (None,) * 5
+        if any(need[:5]):
+            grads = gated_ffn_bwd(dY, X, W_in, W_out, Z, H, act=ctx.act, mode=ctx.mode, need=need[:5])
+        return (*grads, dY if need[5] else None, None, None)
+
+
+class EmuFeedForwardFunction(torch.autograd.Function):
+    """x + gated_ffn(layer_norm(x)): the residual's gradient joins in the norm's
+    backward pass."""
+
+    @staticmethod
+    def forward(ctx, X, norm_weight, norm_bias, W_in, b_in, W_out, b_out, eps, act, mode):
+        save = any(ctx.needs_input_grad[:7])
+        Xn, mean, rstd = layer_norm_fwd(X, norm_weight, norm_bias, eps=eps)
+        r = gated_ffn_fwd(Xn, W_in, b_in, W_out, b_out, act=act, residual=X, mode=mode, save=save)
+        Y, Z, H = r if save else (r, None, None)
+        ctx.save_for_backward(X, norm_weight, mean, rstd, Xn, W_in, W_out, Z, H)
+        ctx.act, ctx.mode = act, mode
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, norm_weight, mean, rstd, Xn, W_in, W_out, Z, H = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dX = dnw = dnb = None
+        inner = any(need[:3])
+        dXn, *grads = gated_ffn_bwd(dY, Xn, W_in, W_out, Z, H, act=ctx.act, mode=ctx.mode, need=(inner, *need[3:7]))
+        if inner:
+            dX, dnw, dnb = layer_norm_bwd(dXn, X, norm_weight, mean, rstd, add=dY if need[0] else None,
+                                          need_input=need[0], need_params=need[1] or need[2])
+        return (dX, dnw if need[1] else None, dnb if need[2] else None, *grads, None, None, None)
+
+
+class EmuLayerNorm(torch.nn.LayerNorm):
+    """Drop-in nn.LayerNorm on the library's kernels."""
+
+    def forward(self, x):
+        n = 1
+        for d in self.normalized_shape:
+            n *= d
+        if tuple(x.shape[x.dim() - len(self.normalized_shape):]) != tuple(self.normalized_shape):
+            raise ValueError(f"the input must end in {tuple(self.normalized_shape)}")
+        flat = [None if p is None else p.reshape(n) for p in (self.weight, self.bias)]
+        rows = x.numel() // n if n else 0
+        return EmuLayerNormFunction.apply(x.reshape(rows, n), *flat, self.eps).reshape(x.shape)
+
+
+class EmuLinearAct(torch.nn.Linear):
+    """nn.Linear with an activation and an optional residual:
+    act(x W^T + b) + residual."""
+
+    def __init__(self, in_features, out_features, bias=True, act="gelu", mode="bf16x9", **kw):
+        _act(act), _mode(mode)
+        super().__init__(in_features, out_features, bias=bias, **kw)
+        self.act, self.mode = act, mode
+
+    def forward(self, x, residual=None):
+        shape = (*x.shape[:-1], self.out_features)
+        if residual is not None:
+            residual = residual.reshape(-1, self.out_features)
+        y = EmuLinearActFunction.apply(x.reshape(-1, self.in_features), self.weight, self.bias, residual, self.act,
+                                       self.mode)
+        return y.reshape(shape)
+
+
+class EmuGatedFFN(torch.nn.Module):
+    """The gated feed-forward block act(x Wg^T + bg) * (x Wu^T + bu), projected
+    back by W_out: weight_in holds Wg's rows, then Wu's."""
+
+    def __init__(self, in_features, hidden_features, out_features=None, bias=True, act="silu", mode="bf16x9",
+                 device=None, dtype=torch.float32):
+        super().__init__()
+        _act(act), _mode(mode)
+        out_features = in_features if out_features is None else out_features
+        self.in_features, self.hidden_features, self.out_features = in_features, hidden_features, out_features
+        self.act, self.mode = act, mode
+        new = lambda *s: torch.nn.Parameter(torch.empty(s, device=device, dtype=dtype))
+        self.weight_in, self.weight_out = new(2 * hidden_features, in_features), new(out_features, hidden_features)
+        self.bias_in = new(2 * hidden_features) if bias else None
+        self.bias_out = new(out_features) if bias else None
+        self.reset_parameters()
+
+    def reset_parameters(self):
+        """nn.Linear's initial values, for each of the three projections."""
+        for w, b in ((self.weight_in, self.bias_in), (self.weight_out, self.bias_out)):
+            bound = w.shape[1] ** -0.5 if w.shape[1] else 0.0
+            torch.nn.init.uniform_(w, -bound, bound)
+            if b is not None:
+                torch.nn.init.uniform_(b, -bound, bound)
+
+    def forward(self, x, residual=None):
+        shape = (*x.shape[:-1], self.out_features)
+        if residual is not None:
+            residual = residual.reshape(-1, self.out_features)
+        y = EmuGatedFFNFunction.apply(x.reshape(-1, self.in_features), self.weight_in, self.bias_in, self.weight_out,
+                                      self.bias_out, residual, self.act, self.mode)
+        return y.reshape(shape)
+
+
+class EmuFeedForward(torch.nn.Module):
+    """The pre-norm feed-forward sub-layer of a transformer:
+    x + ffn(norm(x)), with an EmuLayerNorm and an EmuGatedFFN."""
+
+    def __init__(self, features, hidden_features, bias=True, act="silu", mode="bf16x9", eps=1e-5, device=None,
+                 dtype=torch.float32):
+        super().__init__()
+        self.norm = EmuLayerNorm(features, eps=eps, device=device, dtype=dtype)
+        self.ffn = EmuGatedFFN(features, hidden_features, bias=bias, act=act, mode=mode, device=device, dtype=dtype)
+
+    def forward(self, x):
+        f = self.ffn
+        y = EmuFeedForwardFunction.apply(x.reshape(-1, f.in_features), self.norm.weight, self.norm.bias, f.weight_in,
+                                         f.bias_in, f.weight_out, f.bias_out, self.norm.eps, f.act, f.mode)
+        return y.reshape(x.shape)

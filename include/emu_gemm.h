@@ -194,6 +194,122 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
                                          const float *dY, const void *Wt_packed, float *dX,
                                          emu_stream_t stream);
 
+/*
+ * Feed-forward operators: what a transformer layer does next to its products.
+ * FP32 in and out, row-major with a leading dimension for every matrix; the
+ * products run in `mode` with its accuracy, everything else in FP32.
+ *
+ * Activations a(z): none z; relu max(z, 0); gelu z Phi(z); gelu_tanh
+ *   0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); silu z / (1 + exp(-z)).
+ *   Finite z gives a finite value and derivative; relu'(0) = 0.
+ * Alignment: every matrix that enters or leaves a product (X, W, residual, Y,
+ *   Z, dZ, H, dY, dH, dX, dW and the weights' gradients) starts on a 16-byte
+ *   boundary and has a leading dimension that is a multiple of 4, as in
+ *   emu_sgemm, biases start on a 16-byte boundary; else
+ *   EMU_STATUS_NOT_SUPPORTED.  Widths are free.  emu_layer_norm_* takes any
+ *   alignment of whole words.
+ * Outputs must not overlap inputs or one another.
+ * Sizes: M == 0 writes nothing but zero sums (weight and bias gradients);
+ *   K == 0 leaves the bias.
+ * Buffers: the sums over rows take a buffer of partial sums from the
+ *   library, kept per (device, stream) like the split-K workspace.
+ * Repeatability: all sums are added in an order fixed by the sizes and the
+ *   device; no atomics.
+ */
+typedef enum {
+    EMU_ACT_NONE = 0,
+    EMU_ACT_RELU = 1,
+    EMU_ACT_GELU = 2,
+    EMU_ACT_GELU_TANH = 3,
+    EMU_ACT_SILU = 4
+} emu_act_t;
+
+/*
+ * emu_layer_norm_fwd -- Y = (X - mean) * rstd * weight + bias over the rows of
+ *   X[M,N]: mean and rstd = 1 / sqrt(var + eps) per row, var the mean squared
+ *   deviation.  weight and bias (N) may be NULL (1 and 0); mean and rstd (M
+ *   each, for the backward pass) may be NULL.  eps >= 0, else INVALID_VALUE.
+ */
+emu_status_t emu_layer_norm_fwd(int64_t M, int64_t N, const float *X, int64_t ldx, const float *weight,
+                                const float *bias, float eps, float *Y, int64_t ldy, float *mean, float *rstd,
+                                emu_stream_t stream);
+
+/*
+ * emu_layer_norm_bwd -- with g = dY * weight and xh = (X - mean) * rstd:
+ *   dX = rstd * (g - mean(g) - xh * mean(g * xh)) + add, dweight = sum over
+ *   rows of dY * xh, dbias = sum over rows of dY.  `add` (M x N, may be NULL)
+ *   is a gradient that reaches X by another way, such as the residual's; it
+ *   needs dX.  dX, dweight and dbias may each be NULL (not wanted).
+ */
+emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float *dY, int64_t lddy, const float *X, int64_t ldx,
+                                const float *weight, const float *mean, const float *rstd, const float *add,
+                                int64_t ldadd, float *dX, int64_t lddx, float *dweight, float *dbias,
+                                emu_stream_t stream);
+
+/*
+ * emu_linear_act_fwd -- Z = X W^T + bias, Y = a(Z) + residual.
+ *   X: M x K, W: N x K, bias: N (may be NULL), residual: M x N (may be NULL),
+ *   Y: M x N.  Z (M x N) receives the pre-activation for the backward pass;
+ *   NULL when it is not needed.
+ */
+emu_status_t emu_linear_act_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t N, int64_t K, const float *X,
+                                int64_t ldx, const float *W, int64_t ldw, const float *bias, const float *residual,
+                                int64_t ldr, float *Z, int64_t ldz, float *Y, int64_t ldy, emu_stream_t stream);
+
+/*
+ * emu_linear_act_bwd -- dZ = dY * a'(Z); dX = dZ W, dW = dZ^T X, dbias = sum
+ *   over rows of dZ.  (The residual's gradient is dY itself.)  dZ (M x N) is
+ *   written too.  EMU_ACT_NONE needs neither Z nor dZ (NULL).  dX, dW and
+ *   dbias may each be NULL (not wanted).
+ */
+emu_status_t emu_linear_act_bwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t N, int64_t K, const float *dY,
+                                int64_t lddy, const float *X, int64_t ldx, const float *W, int64_t ldw, const float *Z,
+                                int64_t ldz, float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW, int64_t lddw,
+                                float *dbias, emu_stream_t stream);
+
+/*
+ * emu_gated_fwd -- Z = [G | U] = X W^T + bias, H = a(G) * U.
+ *   W: 2F x K (the gate's F rows, then the up projection's), bias: 2F (may be
+ *   NULL), Z: M x 2F, H: M x F.
+ */
+emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F, int64_t K, const float *X, int64_t ldx,
+                           const float *W, int64_t ldw, const float *bias, float *Z, int64_t ldz, float *H, int64_t ldh,
+                           emu_stream_t stream);
+
+/*
+ * emu_gated_bwd -- dZ = [dH * U * a'(G) | dH * a(G)] (M x 2F, written too);
+ *   dX = dZ W, dW = dZ^T X (2F x K), dbias = sum over rows of dZ (2F).  dX, dW
+ *   and dbias may each be NULL (not wanted).
+ */
+emu_status_t emu_gated_bwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F, int64_t K, const float *dH,
+                           int64_t lddh, const float *X, int64_t ldx, const float *W, int64_t ldw, const float *Z,
+                           int64_t ldz, float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW, int64_t lddw,
+                           float *dbias, emu_stream_t stream);
+
+/*
+ * emu_gated_ffn_fwd -- the whole block: emu_gated_fwd, then Y = H W_out^T +
+ *   b_out + residual.  X: M x K, W_in: 2F x K, W_out: N x F, Y and residual
+ *   (may be NULL): M x N; Z and H as in emu_gated_fwd.
+ */
+emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t K, int64_t F, int64_t N,
+                               const float *X, int64_t ldx, const float *W_in, int64_t ldwi, const float *b_in,
+                               const float *W_out, int64_t ldwo, const float *b_out, const float *residual, int64_t ldr,
+                               float *Z, int64_t ldz, float *H, int64_t ldh, float *Y, int64_t ldy,
+                               emu_stream_t stream);
+
+/*
+ * emu_gated_ffn_bwd -- its gradients, from Z and H of the forward pass:
+ *   dW_out = dY^T H, db_out = sum over rows of dY, dH = dY W_out, then
+ *   emu_gated_bwd's dZ, dX, dW_in and db_in.  dX, dW_in, db_in, dW_out and
+ *   db_out may each be NULL (not wanted).
+ */
+emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t K, int64_t F, int64_t N,
+                               const float *dY, int64_t lddy, const float *X, int64_t ldx, const float *W_in,
+                               int64_t ldwi, const float *W_out, int64_t ldwo, const float *Z, int64_t ldz,
+                               const float *H, int64_t ldh, float *dZ, int64_t lddz, float *dX, int64_t lddx,
+                               float *dW_in, int64_t lddwi, float *db_in, float *dW_out, int64_t lddwo, float *db_out,
+                               emu_stream_t stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *emu_status_string(emu_status_t s);
 
