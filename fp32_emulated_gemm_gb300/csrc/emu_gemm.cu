@@ -796,6 +796,32 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int pairs) {
     return plan;
 }
 
+// make_plan for a launch, remembered per host thread: a plan depends on nothing
+// but the sizes, the pairs and the overrides, and planning a chained product
+// costs 8 us on a GB300's host, as much as a small call's launches.
+const Plan& plan_for(int64_t M, int64_t N, int64_t K, int pairs) {
+    struct Entry {
+        int64_t M = -1, N = -1, K = -1;
+        int pairs = 0, env[4] = {};
+        Plan plan;
+    };
+    constexpr int kEntries = 32;
+    static thread_local Entry entries[kEntries];
+    const int env[4] = {env_int("EMU_SPLIT_K", 0), env_int("EMU_SPLIT_TAIL", 0), env_int("EMU_CHAIN", -1),
+                        env_int("EMU_PIPE", -1)};
+    const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15ull ^ (uint64_t)N * 0xC2B2AE3D27D4EB4Full ^
+                        (uint64_t)K * 0x165667B19E3779F9ull);
+    Entry& e = entries[(h >> 40) % kEntries];
+    bool same = e.M == M && e.N == N && e.K == K && e.pairs == pairs;
+    for (int i = 0; i < 4; ++i) same = same && e.env[i] == env[i];
+    if (!same) {
+        e.plan = make_plan(M, N, K, pairs);
+        e.M = M; e.N = N; e.K = K; e.pairs = pairs;
+        for (int i = 0; i < 4; ++i) e.env[i] = env[i];
+    }
+    return e.plan;
+}
+
 // The mode a product runs in: the requested one, except that the performant
 // strategy runs an emulated product in native FP32 when that is predicted
 // faster.  `pairs`: the device's co-resident CTA pairs; `sm_count`: its SMs.
@@ -963,7 +989,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         return launch_native(M, N, K, alpha, A, lda, a_mn, B, ldb, b_mn, beta, C, ldc, bias, dev->sm_count, stream) == cudaSuccess
                    ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
     }
-    Plan plan = make_plan(M, N, K, pairs);
+    Plan plan = plan_for(M, N, K, pairs);
     int devid = 0;
     cudaGetDevice(&devid);
     // Everything that can fail -- the library's buffers, the tensor maps --
@@ -1427,7 +1453,7 @@ emu_status_t run_gemm_noalloc(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, 
         return launch_native(M, N, K, alpha, A, lda, a_mn, B, ldb, b_mn, beta, C, ldc, nullptr, dev->sm_count, stream) == cudaSuccess
                    ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
     }
-    const Plan plan = make_plan(M, N, K, pairs);
+    const Plan& plan = plan_for(M, N, K, pairs);
     Params p{};
     if (!encode_operand(&p.tmA, A, a_mn, M, K, lda, HALF) ||
         !encode_operand(&p.tmB, B, b_mn, N, K, ldb, (uint32_t)plan.tn / 2))

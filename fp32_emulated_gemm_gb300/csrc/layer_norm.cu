@@ -8,12 +8,217 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "row_ops.cuh"
 
 namespace emu {
 namespace {
 
+// ------------------------------------------------- rows held in registers --
+// T threads share a row and hold it in NV float4 each (4 T NV >= N), so X and
+// dY are read once.  T = 32: a warp a row, eight rows a block, sums by
+// shuffles alone; wider rows take a block each, so that a thread never holds
+// more than 4 float4 of a matrix and enough rows are in flight per SM.
+template <int T> constexpr int kBlockThreads = T == 32 ? 256 : T;
+template <int T> constexpr int kBlockRows = T == 32 ? 8 : 1;
+
+// Sums over the T threads of a row of two values, returned to all of them.
+// `flip` alternates between two sets of slots from one call to the next, so
+// one barrier per call is enough.
+template <int T>
+__device__ __forceinline__ float2 row_sum2(float a, float b, int& flip) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if constexpr (T == 32) return make_float2(a, b);
+    __shared__ float2 part[2][T / 32];
+    float2* p = part[flip];
+    flip ^= 1;
+    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    float2 s = p[0];
+#pragma unroll
+    for (int i = 1; i < T / 32; ++i) { s.x += p[i].x; s.y += p[i].y; }
+    return s;
+}
+
+// Column of value j of float4 i of thread t (see load4).
+template <int T, bool VEC> __device__ __forceinline__ int64_t col_of(int t, int i) {
+    return (VEC ? 4 * t : t) + (int64_t)4 * T * i;
+}
+template <int T, bool VEC> __device__ __forceinline__ bool inside(int64_t c, int j, int64_t n) {
+    return VEC ? c < n : c + j * T < n;
+}
+
+template <int T, int NV, bool VEC>
+__global__ void __launch_bounds__(kBlockThreads<T>)
+ln_fwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ X, int64_t ldx, const float* __restrict__ w,
+                   const float* __restrict__ b, float eps, float* __restrict__ Y, int64_t ldy, float* mean, float* rstd) {
+    constexpr int G = kBlockRows<T>;
+    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x, g = T == 32 ? threadIdx.x >> 5 : 0;
+    const float inv_n = 1.0f / (float)N;
+    int flip = 0;
+    for (int64_t r = blockIdx.x * (int64_t)G + g; r < M; r += (int64_t)gridDim.x * G) {
+        float4 x[NV];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = load4<VEC, T>(X + r * ldx, col_of<T, VEC>(t, i), N);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s += (x[i].x + x[i].y) + (x[i].z + x[i].w);
+        const float mu = row_sum2<T>(s, 0.f, flip).x * inv_n;
+        // the squared deviations from the mean just found, not E x^2 - mu^2:
+        // no cancellation when the mean is large
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = col_of<T, VEC>(t, i);
+            x[i] = make_float4(x[i].x - mu, x[i].y - mu, x[i].z - mu, x[i].w - mu);
+            if (inside<T, VEC>(c, 0, N)) q = fmaf(x[i].x, x[i].x, q);
+            if (inside<T, VEC>(c, 1, N)) q = fmaf(x[i].y, x[i].y, q);
+            if (inside<T, VEC>(c, 2, N)) q = fmaf(x[i].z, x[i].z, q);
+            if (inside<T, VEC>(c, 3, N)) q = fmaf(x[i].w, x[i].w, q);
+        }
+        const float rs = 1.0f / sqrtf(fmaf(row_sum2<T>(q, 0.f, flip).x, inv_n, eps));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = col_of<T, VEC>(t, i);
+            float4 v = make_float4(x[i].x * rs, x[i].y * rs, x[i].z * rs, x[i].w * rs);
+            if (w) {
+                const float4 k = load4<VEC, T>(w, c, N);
+                v = make_float4(v.x * k.x, v.y * k.y, v.z * k.z, v.w * k.w);
+            }
+            if (b) {
+                const float4 k = load4<VEC, T>(b, c, N);
+                v = make_float4(v.x + k.x, v.y + k.y, v.z + k.z, v.w + k.w);
+            }
+            store4<VEC, T>(Y + r * ldy, c, N, v);
+        }
+        if (t == 0) {
+            if (mean) mean[r] = mu;
+            if (rstd) rstd[r] = rs;
+        }
+    }
+}
+
+// dX and, over the rows this block takes, the sums of dw and db, which stay in
+// registers until the end and go to partial[blockIdx.x][0 and 1][column].
+template <int T, int NV, bool VEC>
+__global__ void __launch_bounds__(kBlockThreads<T>, T == 32 && NV <= 2 ? 4 : 1)
+ln_bwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ dY, int64_t lddy, const float* __restrict__ X,
+                   int64_t ldx, const float* __restrict__ w, const float* __restrict__ mean,
+                   const float* __restrict__ rstd, const float* __restrict__ add, int64_t ldadd, float* __restrict__ dX,
+                   int64_t lddx, float* __restrict__ partial) {
+    constexpr int G = kBlockRows<T>;
+    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x, g = T == 32 ? threadIdx.x >> 5 : 0;
+    const float inv_n = 1.0f / (float)N;
+    int flip = 0;
+    float4 dw[NV], db[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) dw[i] = db[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t r = blockIdx.x * (int64_t)G + g; r < M; r += (int64_t)gridDim.x * G) {
+        float4 x[NV], y[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = load4<VEC, T>(X + r * ldx, col_of<T, VEC>(t, i), N);
+            y[i] = load4<VEC, T>(dY + r * lddy, col_of<T, VEC>(t, i), N);
+        }
+        const float mu = mean[r], rs = rstd[r];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = make_float4((x[i].x - mu) * rs, (x[i].y - mu) * rs, (x[i].z - mu) * rs, (x[i].w - mu) * rs);
+            dw[i] = make_float4(fmaf(y[i].x, x[i].x, dw[i].x), fmaf(y[i].y, x[i].y, dw[i].y),
+                                fmaf(y[i].z, x[i].z, dw[i].z), fmaf(y[i].w, x[i].w, dw[i].w));
+            db[i] = make_float4(db[i].x + y[i].x, db[i].y + y[i].y, db[i].z + y[i].z, db[i].w + y[i].w);
+            if (w) {
+                const float4 k = load4<VEC, T>(w, col_of<T, VEC>(t, i), N);
+                y[i] = make_float4(y[i].x * k.x, y[i].y * k.y, y[i].z * k.z, y[i].w * k.w);
+            }
+            // (outside the row dY is zero, whatever xh is)
+            s1 += (y[i].x + y[i].y) + (y[i].z + y[i].w);
+            s2 += fmaf(y[i].x, x[i].x, y[i].y * x[i].y) + fmaf(y[i].z, x[i].z, y[i].w * x[i].w);
+        }
+        if (!dX) continue;
+        const float2 m = row_sum2<T>(s1, s2, flip);
+        const float m1 = m.x * inv_n, m2 = m.y * inv_n;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = col_of<T, VEC>(t, i);
+            float4 v = make_float4(rs * (y[i].x - m1 - x[i].x * m2), rs * (y[i].y - m1 - x[i].y * m2),
+                                   rs * (y[i].z - m1 - x[i].z * m2), rs * (y[i].w - m1 - x[i].w * m2));
+            if (add) {
+                const float4 a = load4<VEC, T>(add + r * ldadd, c, N);
+                v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+            }
+            store4<VEC, T>(dX + r * lddx, c, N, v);
+        }
+    }
+    if (!partial) return;
+    float* out = partial + (int64_t)blockIdx.x * 2 * N;
+    if constexpr (T == 32) {
+        // the eight warps' sums, added in order
+        __shared__ float4 part[2][G][32 * NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            part[0][g][32 * i + t] = dw[i];
+            part[1][g][32 * i + t] = db[i];
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 2 * 32 * NV; e += 256) {
+            const int which = e / (32 * NV), q = e % (32 * NV);
+            float4 v = part[which][0][q];
+#pragma unroll
+            for (int i = 1; i < G; ++i) {
+                const float4 k = part[which][i][q];
+                v = make_float4(v.x + k.x, v.y + k.y, v.z + k.z, v.w + k.w);
+            }
+            store4<VEC, T>(out + which * N, col_of<T, VEC>(q % 32, q / 32), N, v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            store4<VEC, T>(out, col_of<T, VEC>(t, i), N, dw[i]);
+            store4<VEC, T>(out + N, col_of<T, VEC>(t, i), N, db[i]);
+        }
+    }
+}
+
+constexpr int64_t kMaxRegsWidth = 16384;
+
+// f(T, NV) for the width: the fewest threads that hold a row in 4 float4 (a
+// warp) or 2 (a block) each.
+template <class F> void for_width(int64_t N, F f) {
+    using std::integral_constant;
+    if (N <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    else if (N <= 256) f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+    else if (N <= 512) f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+    else if (N <= 1024) f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+    else if (N <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (N <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (N <= 8192) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+}
+
+// Blocks of a kernel that are resident on an SM at once (asked for once; the
+// library holds code for one architecture).
+template <class K> int resident_blocks(K kernel, int threads) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = 1;
+    }
+    return n;
+}
+
+// Blocks that take the rows in turns of equal length: at most `resident`.
+unsigned even_grid(int64_t M, int rows, int64_t resident) {
+    const int64_t groups = (M + rows - 1) / rows, turns = (groups + resident - 1) / resident;
+    return (unsigned)((groups + turns - 1) / turns);
+}
+
+// ------------------------------------------------------------- wide rows ---
+// Rows wider than the registers hold: a block a row, several passes over it.
 constexpr int kRowThreads = 256;
 
 // Sum over the block of two values, returned to every thread.
@@ -29,7 +234,6 @@ __device__ __forceinline__ float2 block_sum2(float a, float b) {
     return s;
 }
 
-// One block per row, three passes over it.
 __global__ void __launch_bounds__(kRowThreads)
 ln_fwd_kernel(int64_t M, int64_t N, const float* X, int64_t ldx, const float* w, const float* b, float eps, float* Y,
               int64_t ldy, float* mean, float* rstd) {
@@ -136,10 +340,24 @@ emu_status_t emu_layer_norm_fwd(int64_t M, int64_t N, const float* X, int64_t ld
     DeviceCtx dev;
     const emu_status_t st = current_device(&dev);
     if (st != EMU_STATUS_SUCCESS) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaGetLastError();
-    const int64_t grid = M < dev.sm_count * 8 ? M : dev.sm_count * 8;
-    ln_fwd_kernel<<<(unsigned)grid, kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        M, N, X, ldx, weight, bias, eps, Y, ldy, mean, rstd);
+    if (N <= kMaxRegsWidth) {
+        const bool vec = (N & 3) == 0 && vec4_ok(X, ldx) && vec4_ok(Y, ldy) && vec4_ok(weight, 0) && vec4_ok(bias, 0);
+        for_width(N, [&](auto T, auto NV) {
+            constexpr int t = decltype(T)::value, nv = decltype(NV)::value;
+            auto launch = [&](auto VEC) {
+                constexpr auto kernel = ln_fwd_regs_kernel<t, nv, decltype(VEC)::value>;
+                static const int per_sm = resident_blocks(kernel, kBlockThreads<t>);
+                const unsigned grid = even_grid(M, kBlockRows<t>, (int64_t)dev.sm_count * per_sm);
+                kernel<<<grid, kBlockThreads<t>, 0, s>>>(M, N, X, ldx, weight, bias, eps, Y, ldy, mean, rstd);
+            };
+            if (vec) launch(std::true_type{}); else launch(std::false_type{});
+        });
+    } else {
+        const int64_t grid = M < dev.sm_count * 8 ? M : dev.sm_count * 8;
+        ln_fwd_kernel<<<(unsigned)grid, kRowThreads, 0, s>>>(M, N, X, ldx, weight, bias, eps, Y, ldy, mean, rstd);
+    }
     return cudaGetLastError() == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }
 
@@ -165,6 +383,30 @@ emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float* dY, int64_t l
             return EMU_STATUS_LAUNCH_FAILED;
         }
         return EMU_STATUS_SUCCESS;
+    }
+    if (N <= kMaxRegsWidth) {
+        const bool vec = (N & 3) == 0 && vec4_ok(dY, lddy) && vec4_ok(X, ldx) && vec4_ok(weight, 0) &&
+                         vec4_ok(add, add ? ldadd : 0) && vec4_ok(dX, dX ? lddx : 0);
+        cudaError_t e = cudaSuccess;
+        for_width(N, [&](auto T, auto NV) {
+            constexpr int t = decltype(T)::value, nv = decltype(NV)::value;
+            auto launch = [&](auto VEC) {
+                constexpr auto kernel = ln_bwd_regs_kernel<t, nv, decltype(VEC)::value>;
+                static const int per_sm = resident_blocks(kernel, kBlockThreads<t>);
+                const unsigned grid = even_grid(M, kBlockRows<t>, (int64_t)dev.sm_count * per_sm);
+                float* partial = nullptr;
+                if (params) st = reduce_scratch(dev.id, s, (size_t)grid * 2 * N, &partial);
+                if (st != EMU_STATUS_SUCCESS) return;
+                cudaGetLastError();
+                kernel<<<grid, kBlockThreads<t>, 0, s>>>(M, N, dY, lddy, X, ldx, weight, mean, rstd, add, ldadd, dX, lddx,
+                                                         partial);
+                e = cudaGetLastError();
+                if (e == cudaSuccess && params) e = launch_sum_partials(partial, (int)grid, 2 * N, N, dweight, dbias, s);
+            };
+            if (vec) launch(std::true_type{}); else launch(std::false_type{});
+        });
+        if (st != EMU_STATUS_SUCCESS) return st;
+        return e == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
     }
     const int64_t col_blocks = (N + 255) / 256;
     int64_t chunks = (dev.sm_count * 8 + col_blocks - 1) / col_blocks;

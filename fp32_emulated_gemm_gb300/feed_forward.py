@@ -48,6 +48,7 @@ def _fn(name):
     return f
 
 
+
 def _c_name(name):
     kinds = _SIGNATURES[name]
 
@@ -72,6 +73,13 @@ emu_gated_ffn_bwd = _c_name("emu_gated_ffn_bwd")
 
 
 # ------------------------------------------------------------ arguments ----
+# A small call costs as much on the host as on the GPU, so the helpers look at
+# each tensor once and hand back what the call needs of it: (tensor, address,
+# row stride).  A matrix that is not wanted is (None, None, 0).
+_float32, _empty = torch.float32, torch.empty
+_NONE = (None, None, 0)
+
+
 def _act(act):
     try:
         return ACTS[act]
@@ -81,106 +89,131 @@ def _act(act):
 
 def _rows(t, name, shape=None):
     """`t` as a matrix of unit column stride whose rows do not overlap."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.float32):
+    if not isinstance(t, torch.Tensor) or t.dtype is not _float32 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA float32 tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {t.shape[0]} x {t.shape[1]}")
     r, c = t.shape
+    if shape is not None and (r, c) != shape:
+        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {r} x {c}")
+    if t.is_contiguous():
+        return t, t.data_ptr(), c
     if (c > 1 and t.stride(1) != 1) or (r > 1 and t.stride(0) < c):
         t = t.contiguous()
-    return t
-
-
-def _ld(t):
-    """The row stride of a matrix from _rows, as the library wants it (a
-    single row's stride means nothing in torch)."""
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 3) // 4 * 4
+        return t, t.data_ptr(), c
+    return t, t.data_ptr(), t.stride(0) if r > 1 else c
 
 
 def _operand(t, name, shape=None):
     """`t` as a product's operand: rows on 16-byte boundaries."""
-    t = _rows(t, name, shape)
-    if t.data_ptr() & 15 or (t.shape[0] > 1 and t.stride(0) & 3):
-        p = _new_c(t.shape[0], t.shape[1], t.device)
-        p.copy_(t)
-        t = p
-    return t
+    t, p, ld = m = _rows(t, name, shape)
+    if not (p & 15 or ld & 3):
+        return m
+    if t.shape[0] == 1 and not p & 15:  # a single row's stride means nothing
+        return t, p, _pad4(ld)
+    q = _new(*t.shape, t.device)
+    q[0].copy_(t)
+    return q
+
+
+def _pad4(n):
+    return (n + 3) // 4 * 4
 
 
 def _vector(t, name, n):
+    """(tensor, address) of a vector on a 16-byte boundary."""
     if t is None:
-        return None
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.float32):
+        return None, None
+    if not isinstance(t, torch.Tensor) or t.dtype is not _float32 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA float32 tensor")
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must be a vector of {n}")
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() & 15 else t
+    if not t.is_contiguous():
+        t = t.contiguous()
+    p = t.data_ptr()
+    if p & 15:
+        t = t.clone()
+        p = t.data_ptr()
+    return t, p
 
 
-def _result(out, shape, like, name):
+def _new(M, N, device):
+    """A new matrix with rows on 16-byte boundaries."""
+    t = _empty((M, N), device=device, dtype=_float32) if not N & 3 else _new_c(M, N, device)
+    return t, t.data_ptr(), _pad4(N)
+
+
+def _new_vector(n, device):
+    t = _empty(n, device=device, dtype=_float32)
+    return t, t.data_ptr()
+
+
+def _result(out, shape, device, name):
     if out is None:
-        return _new_c(shape[0], shape[1], like.device)
-    if not (isinstance(out, torch.Tensor) and out.is_cuda and out.dtype is torch.float32):
+        return _new(*shape, device)
+    if not isinstance(out, torch.Tensor) or out.dtype is not _float32 or not out.is_cuda:
         raise TypeError(f"{name} must be a CUDA float32 tensor")
     if tuple(out.shape) != shape or (shape[1] > 1 and out.stride(1) != 1) or (shape[0] > 1 and out.stride(0) < shape[1]):
         raise ValueError(f"{name} must be {shape[0]} x {shape[1]} with unit column stride")
-    return out
+    return out, out.data_ptr(), out.stride(0) if shape[0] > 1 else _pad4(shape[1])
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(name, tensors):
-    """The current stream of the tensors' device, which has to be one and the
-    current one."""
+def _stream_of(name, *tensors):
+    """The current stream, for tensors that have to be on the current device."""
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: all tensors must be on the current device (cuda:{dev})")
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev)
+
+
+# (the Stream object that torch.cuda.current_stream builds costs 3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # ----------------------------------------------------------- layer norm ----
 def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, out=None):
     """(Y, mean, rstd): Y = (X - mean) * rstd * weight + bias over the rows of X."""
-    X = _rows(X, "X")
+    X, px, ldx = _rows(X, "X")
     M, N = X.shape
-    weight, bias = _vector(weight, "weight", N), _vector(bias, "bias", N)
-    Y = out if out is None else _result(out, (M, N), X, "out")
-    if Y is None:
-        Y = torch.empty((M, N), device=X.device, dtype=torch.float32)
-    stats = torch.empty((2, M), device=X.device, dtype=torch.float32)
-    mean, rstd = stats[0], stats[1]
-    s = _raw_stream("layer_norm_fwd", (X, weight, bias, Y))
-    _check(_fn("emu_layer_norm_fwd")(M, N, _p(X), _ld(X), _p(weight), _p(bias), float(eps), _p(Y), _ld(Y), _p(mean),
-                                     _p(rstd), s), "emu_layer_norm_fwd")
+    weight, pw = _vector(weight, "weight", N)
+    bias, pb = _vector(bias, "bias", N)
+    device = X.device
+    if out is None:
+        Y, ldy = _empty((M, N), device=device, dtype=_float32), N
+        py = Y.data_ptr()
+    else:
+        Y, py, ldy = _result(out, (M, N), device, "out")
+    mean, pm = _new_vector(M, device)
+    rstd, pr = _new_vector(M, device)
+    _check(_fn("emu_layer_norm_fwd")(M, N, px, ldx, pw, pb, eps, py, ldy, pm, pr,
+                                     _stream_of("layer_norm_fwd", X, weight, bias, Y)), "emu_layer_norm_fwd")
     return Y, mean, rstd
 
 
 def layer_norm_bwd(dY, X, weight, mean, rstd, *, add=None, need_input=True, need_params=True):
     """(dX, dweight, dbias) of layer_norm_fwd; `add` (a gradient that reaches X
     by another way) is added to dX.  What is not needed comes back as None."""
-    X = _rows(X, "X")
-    M, N = X.shape
-    dY = _rows(dY, "dY", (M, N))
-    add = None if add is None else _rows(add, "add", (M, N))
+    X, px, ldx = _rows(X, "X")
+    M, N = shape = tuple(X.shape)
+    dY, pdy, lddy = _rows(dY, "dY", shape)
+    add, pa, lda = _NONE if add is None else _rows(add, "add", shape)
     if add is not None and not need_input:
         raise ValueError("add needs dX")
-    weight = _vector(weight, "weight", N)
-    for v, name in ((mean, "mean"), (rstd, "rstd")):
-        if v.shape != (M,) or v.dtype is not torch.float32 or (M > 1 and v.stride(0) != 1):
-            raise ValueError(f"{name} must be the forward pass's vector of {M}")
-    dX = torch.empty((M, N), device=X.device, dtype=torch.float32) if need_input else None
-    params = torch.empty((2, N), device=X.device, dtype=torch.float32) if need_params else None
-    dw, db = (params[0], params[1]) if need_params else (None, None)
-    s = _raw_stream("layer_norm_bwd", (dY, X, weight, mean, rstd, add))
-    _check(_fn("emu_layer_norm_bwd")(M, N, _p(dY), _ld(dY), _p(X), _ld(X), _p(weight), _p(mean), _p(rstd), _p(add),
-                                     0 if add is None else _ld(add), _p(dX), N, _p(dw), _p(db), s),
-           "emu_layer_norm_bwd")
+    weight, pw = _vector(weight, "weight", N)
+    mean, pm = _vector(mean, "mean", M)
+    rstd, pr = _vector(rstd, "rstd", M)
+    device = X.device
+    dX = pdx = dw = pdw = db = pdb = None
+    if need_input:
+        dX = _empty(shape, device=device, dtype=_float32)
+        pdx = dX.data_ptr()
+    if need_params:
+        dw, pdw = _new_vector(N, device)
+        db, pdb = _new_vector(N, device)
+    _check(_fn("emu_layer_norm_bwd")(M, N, pdy, lddy, px, ldx, pw, pm, pr, pa, lda, pdx, N, pdw, pdb,
+                                     _stream_of("layer_norm_bwd", X, dY, weight, mean, rstd, add)), "emu_layer_norm_bwd")
     return dX, dw, db
 
 
@@ -188,18 +221,19 @@ def layer_norm_bwd(dY, X, weight, mean, rstd, *, add=None, need_input=True, need
 def linear_act_fwd(X, W, bias=None, *, act="none", residual=None, mode="bf16x9", save=False, out=None):
     """Y = act(X W^T + bias) + residual (X [M,K], W [N,K]); with `save`
     (Y, Z), Z the pre-activation that linear_act_bwd reads."""
-    X, W = _operand(X, "X"), _operand(W, "W")
-    (M, K), N = X.shape, W.shape[0]
-    if W.shape[1] != K:
+    X, px, ldx = _operand(X, "X")
+    W, pw, ldw = _operand(W, "W")
+    M, K = X.shape
+    N, Kw = W.shape
+    if Kw != K:
         raise ValueError("inner dimensions differ")
-    bias = _vector(bias, "bias", N)
-    residual = None if residual is None else _operand(residual, "residual", (M, N))
-    Y = _result(out, (M, N), X, "out")
-    Z = _new_c(M, N, X.device) if save else None
-    s = _raw_stream("linear_act_fwd", (X, W, bias, residual, Y))
-    _check(_fn("emu_linear_act_fwd")(_mode(mode), _act(act), M, N, K, _p(X), _ld(X), _p(W), _ld(W), _p(bias),
-                                     _p(residual), 0 if residual is None else _ld(residual), _p(Z),
-                                     _ld(Z) if save else 0, _p(Y), _ld(Y), s), "emu_linear_act_fwd")
+    bias, pb = _vector(bias, "bias", N)
+    residual, pr, ldr = _NONE if residual is None else _operand(residual, "residual", (M, N))
+    device = X.device
+    Y, py, ldy = _result(out, (M, N), device, "out")
+    Z, pz, ldz = _new(M, N, device) if save else _NONE
+    _check(_fn("emu_linear_act_fwd")(_mode(mode), _act(act), M, N, K, px, ldx, pw, ldw, pb, pr, ldr, pz, ldz, py, ldy,
+                                     _stream_of("linear_act_fwd", X, W, bias, residual, Y)), "emu_linear_act_fwd")
     return (Y, Z) if save else Y
 
 
@@ -207,63 +241,68 @@ def linear_act_bwd(dY, X, W, Z=None, *, act="none", mode="bf16x9", need=(True, T
     """(dX, dW, dbias) of linear_act_fwd (the residual's gradient is dY); Z is
     not read for act "none".  `need` says which are wanted; the others are None."""
     a = _act(act)
-    X, W = _operand(X, "X"), _operand(W, "W")
-    (M, K), N = X.shape, W.shape[0]
-    if W.shape[1] != K:
+    X, px, ldx = _operand(X, "X")
+    W, pw, ldw = _operand(W, "W")
+    M, K = X.shape
+    N, Kw = W.shape
+    if Kw != K:
         raise ValueError("inner dimensions differ")
-    dY = _operand(dY, "dY", (M, N))
-    dZ = None
+    dY, pdy, lddy = _operand(dY, "dY", (M, N))
+    device = X.device
+    pz, ldz, pdz, lddz = None, 0, None, 0
     if a != EMU_ACT_NONE:
         if Z is None:
             raise ValueError(f"act {act!r} needs Z")
-        Z, dZ = _operand(Z, "Z", (M, N)), _new_c(M, N, X.device)
+        Z, pz, ldz = _operand(Z, "Z", (M, N))
+        dZ, pdz, lddz = _new(M, N, device)
     else:
         Z = None
-    dX = _new_c(M, K, X.device) if need[0] else None
-    dW = _new_c(N, K, X.device) if need[1] else None
-    db = torch.empty(N, device=X.device, dtype=torch.float32) if need[2] else None
-    s = _raw_stream("linear_act_bwd", (dY, X, W, Z))
-    _check(_fn("emu_linear_act_bwd")(_mode(mode), a, M, N, K, _p(dY), _ld(dY), _p(X), _ld(X), _p(W), _ld(W), _p(Z),
-                                     0 if Z is None else _ld(Z), _p(dZ), 0 if dZ is None else _ld(dZ), _p(dX),
-                                     (K + 3) // 4 * 4, _p(dW), (K + 3) // 4 * 4, _p(db), s), "emu_linear_act_bwd")
+    dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
+    dW, pdw, lddw = _new(N, K, device) if need[1] else _NONE
+    db, pdb = _new_vector(N, device) if need[2] else (None, None)
+    _check(_fn("emu_linear_act_bwd")(_mode(mode), a, M, N, K, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdz, lddz, pdx, lddx,
+                                     pdw, lddw, pdb, _stream_of("linear_act_bwd", dY, X, W, Z)), "emu_linear_act_bwd")
     return dX, dW, db
 
 
 # ---------------------------------------------------------------- gated ----
 def _gated_shapes(X, W):
-    if W.shape[0] % 2:
+    (M, K), (F2, Kw) = X.shape, W.shape
+    if F2 % 2:
         raise ValueError("W must have the gate's rows, then as many of the up projection")
-    if W.shape[1] != X.shape[1]:
+    if Kw != K:
         raise ValueError("inner dimensions differ")
-    return X.shape[0], X.shape[1], W.shape[0] // 2
+    return M, K, F2 // 2
 
 
 def gated_fwd(X, W, bias=None, *, act="silu", mode="bf16x9", save=False):
     """H = act(G) * U with [G | U] = X W^T + bias (X [M,K]; W [2F,K]: the
     gate's rows, then the up projection's); with `save` (H, Z), Z = [G | U]."""
-    X, W = _operand(X, "X"), _operand(W, "W")
+    X, px, ldx = _operand(X, "X")
+    W, pw, ldw = _operand(W, "W")
     M, K, F = _gated_shapes(X, W)
-    bias = _vector(bias, "bias", 2 * F)
-    H, Z = _new_c(M, F, X.device), _new_c(M, 2 * F, X.device)
-    s = _raw_stream("gated_fwd", (X, W, bias))
-    _check(_fn("emu_gated_fwd")(_mode(mode), _act(act), M, F, K, _p(X), _ld(X), _p(W), _ld(W), _p(bias), _p(Z), _ld(Z),
-                                _p(H), _ld(H), s), "emu_gated_fwd")
+    bias, pb = _vector(bias, "bias", 2 * F)
+    H, ph, ldh = _new(M, F, X.device)
+    Z, pz, ldz = _new(M, 2 * F, X.device)
+    _check(_fn("emu_gated_fwd")(_mode(mode), _act(act), M, F, K, px, ldx, pw, ldw, pb, pz, ldz, ph, ldh,
+                                _stream_of("gated_fwd", X, W, bias)), "emu_gated_fwd")
     return (H, Z) if save else H
 
 
 def gated_bwd(dH, X, W, Z, *, act="silu", mode="bf16x9", need=(True, True, True)):
     """(dX, dW, dbias) of gated_fwd from Z; `need` says which are wanted."""
-    X, W = _operand(X, "X"), _operand(W, "W")
+    X, px, ldx = _operand(X, "X")
+    W, pw, ldw = _operand(W, "W")
     M, K, F = _gated_shapes(X, W)
-    dH, Z = _operand(dH, "dH", (M, F)), _operand(Z, "Z", (M, 2 * F))
-    dZ = _new_c(M, 2 * F, X.device)
-    dX = _new_c(M, K, X.device) if need[0] else None
-    dW = _new_c(2 * F, K, X.device) if need[1] else None
-    db = torch.empty(2 * F, device=X.device, dtype=torch.float32) if need[2] else None
-    s = _raw_stream("gated_bwd", (dH, X, W, Z))
-    _check(_fn("emu_gated_bwd")(_mode(mode), _act(act), M, F, K, _p(dH), _ld(dH), _p(X), _ld(X), _p(W), _ld(W), _p(Z),
-                                _ld(Z), _p(dZ), _ld(dZ), _p(dX), (K + 3) // 4 * 4, _p(dW), (K + 3) // 4 * 4, _p(db), s),
-           "emu_gated_bwd")
+    dH, pdh, lddh = _operand(dH, "dH", (M, F))
+    Z, pz, ldz = _operand(Z, "Z", (M, 2 * F))
+    device = X.device
+    dZ, pdz, lddz = _new(M, 2 * F, device)
+    dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
+    dW, pdw, lddw = _new(2 * F, K, device) if need[1] else _NONE
+    db, pdb = _new_vector(2 * F, device) if need[2] else (None, None)
+    _check(_fn("emu_gated_bwd")(_mode(mode), _act(act), M, F, K, pdh, lddh, px, ldx, pw, ldw, pz, ldz, pdz, lddz, pdx,
+                                lddx, pdw, lddw, pdb, _stream_of("gated_bwd", dH, X, W, Z)), "emu_gated_bwd")
     return dX, dW, db
 
 
@@ -278,37 +317,44 @@ def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mod
     """Y = H W_out^T + b_out + residual with H = gated_fwd(X, W_in, b_in)
     (X [M,K], W_in [2F,K], W_out [N,F]; the biases and the residual may be
     None); with `save` (Y, Z, H) for gated_ffn_bwd."""
-    X, W_in, W_out = _operand(X, "X"), _operand(W_in, "W_in"), _operand(W_out, "W_out")
+    X, px, ldx = _operand(X, "X")
+    W_in, pwi, ldwi = _operand(W_in, "W_in")
+    W_out, pwo, ldwo = _operand(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
-    b_in, b_out = _vector(b_in, "b_in", 2 * F), _vector(b_out, "b_out", N)
-    residual = None if residual is None else _operand(residual, "residual", (M, N))
-    Y = _result(out, (M, N), X, "out")
-    H, Z = _new_c(M, F, X.device), _new_c(M, 2 * F, X.device)
-    s = _raw_stream("gated_ffn_fwd", (X, W_in, b_in, W_out, b_out, residual, Y))
-    _check(_fn("emu_gated_ffn_fwd")(_mode(mode), _act(act), M, K, F, N, _p(X), _ld(X), _p(W_in), _ld(W_in), _p(b_in),
-                                    _p(W_out), _ld(W_out), _p(b_out), _p(residual),
-                                    0 if residual is None else _ld(residual), _p(Z), _ld(Z), _p(H), _ld(H), _p(Y),
-                                    _ld(Y), s), "emu_gated_ffn_fwd")
+    b_in, pbi = _vector(b_in, "b_in", 2 * F)
+    b_out, pbo = _vector(b_out, "b_out", N)
+    residual, pr, ldr = _NONE if residual is None else _operand(residual, "residual", (M, N))
+    device = X.device
+    Y, py, ldy = _result(out, (M, N), device, "out")
+    H, ph, ldh = _new(M, F, device)
+    Z, pz, ldz = _new(M, 2 * F, device)
+    s = _stream_of("gated_ffn_fwd", X, W_in, b_in, W_out, b_out, residual, Y)
+    _check(_fn("emu_gated_ffn_fwd")(_mode(mode), _act(act), M, K, F, N, px, ldx, pwi, ldwi, pbi, pwo, ldwo, pbo, pr, ldr,
+                                    pz, ldz, ph, ldh, py, ldy, s), "emu_gated_ffn_fwd")
     return (Y, Z, H) if save else Y
 
 
 def gated_ffn_bwd(dY, X, W_in, W_out, Z, H, *, act="silu", mode="bf16x9", need=(True, True, True, True, True)):
     """(dX, dW_in, db_in, dW_out, db_out) of gated_ffn_fwd from its Z and H
     (the residual's gradient is dY); `need` says which are wanted."""
-    X, W_in, W_out = _operand(X, "X"), _operand(W_in, "W_in"), _operand(W_out, "W_out")
+    X, px, ldx = _operand(X, "X")
+    W_in, pwi, ldwi = _operand(W_in, "W_in")
+    W_out, pwo, ldwo = _operand(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
-    dY, Z, H = _operand(dY, "dY", (M, N)), _operand(Z, "Z", (M, 2 * F)), _operand(H, "H", (M, F))
-    dZ = _new_c(M, 2 * F, X.device)
-    dX = _new_c(M, K, X.device) if need[0] else None
-    dWi = _new_c(2 * F, K, X.device) if need[1] else None
-    dbi = torch.empty(2 * F, device=X.device, dtype=torch.float32) if need[2] else None
-    dWo = _new_c(N, F, X.device) if need[3] else None
-    dbo = torch.empty(N, device=X.device, dtype=torch.float32) if need[4] else None
-    s = _raw_stream("gated_ffn_bwd", (dY, X, W_in, W_out, Z, H))
-    _check(_fn("emu_gated_ffn_bwd")(_mode(mode), _act(act), M, K, F, N, _p(dY), _ld(dY), _p(X), _ld(X), _p(W_in),
-                                    _ld(W_in), _p(W_out), _ld(W_out), _p(Z), _ld(Z), _p(H), _ld(H), _p(dZ), _ld(dZ),
-                                    _p(dX), (K + 3) // 4 * 4, _p(dWi), (K + 3) // 4 * 4, _p(dbi), _p(dWo),
-                                    (F + 3) // 4 * 4, _p(dbo), s), "emu_gated_ffn_bwd")
+    dY, pdy, lddy = _operand(dY, "dY", (M, N))
+    Z, pz, ldz = _operand(Z, "Z", (M, 2 * F))
+    H, ph, ldh = _operand(H, "H", (M, F))
+    device = X.device
+    dZ, pdz, lddz = _new(M, 2 * F, device)
+    dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
+    dWi, pdwi, lddwi = _new(2 * F, K, device) if need[1] else _NONE
+    dbi, pdbi = _new_vector(2 * F, device) if need[2] else (None, None)
+    dWo, pdwo, lddwo = _new(N, F, device) if need[3] else _NONE
+    dbo, pdbo = _new_vector(N, device) if need[4] else (None, None)
+    s = _stream_of("gated_ffn_bwd", dY, X, W_in, W_out, Z, H)
+    _check(_fn("emu_gated_ffn_bwd")(_mode(mode), _act(act), M, K, F, N, pdy, lddy, px, ldx, pwi, ldwi, pwo, ldwo, pz, ldz,
+                                    ph, ldh, pdz, lddz, pdx, lddx, pdwi, lddwi, pdbi, pdwo, lddwo, pdbo, s),
+           "emu_gated_ffn_bwd")
     return dX, dWi, dbi, dWo, dbo
 
 
