@@ -20,6 +20,7 @@
 
 #include "../../include/emu_gemm.h"
 #include "emu_kernel.cuh"
+#include "gemm_epi.h"
 #include "internal.h"
 
 namespace emu {
@@ -162,7 +163,9 @@ emu_status_t device_info(DeviceInfo** out) {
             set_smem_attr<MODE_BF16X9, PIPE_SHORT_K_PACKED, true>() != cudaSuccess ||
             set_smem_attr<MODE_BF16X9, PIPE_LONG_K_PACKED, true>() != cudaSuccess ||
             set_smem_attr<MODE_TF32X3, PIPE_SHORT_K, true>() != cudaSuccess ||
-            set_smem_attr<MODE_TF32X3, PIPE_SHORT_K_PACKED, true>() != cudaSuccess) {
+            set_smem_attr<MODE_TF32X3, PIPE_SHORT_K_PACKED, true>() != cudaSuccess ||
+            kEpiAct.set_attributes() != cudaSuccess || kEpiGated.set_attributes() != cudaSuccess ||
+            kEpiGatedBwd.set_attributes() != cudaSuccess) {
             cudaGetLastError();
             return EMU_STATUS_LAUNCH_FAILED;
         }
@@ -456,16 +459,16 @@ __global__ void scale_kernel(int64_t M, int64_t N, float beta, float* C, int64_t
 }
 
 emu_status_t check_error_flag(bool clear) {
-    unsigned int flag = 0;
-    if (cudaMemcpyFromSymbol(&flag, g_error_flag, sizeof(flag)) != cudaSuccess) {
-        cudaGetLastError();
-        return EMU_STATUS_LAUNCH_FAILED;
+    unsigned int any = 0;
+    for (auto read : {epi_error_flag, kEpiAct.error_flag, kEpiGated.error_flag, kEpiGatedBwd.error_flag}) {
+        unsigned int flag = 0;
+        if (read(&flag, clear) != cudaSuccess) {
+            cudaGetLastError();
+            return EMU_STATUS_LAUNCH_FAILED;
+        }
+        any |= flag;
     }
-    if (flag && clear) {
-        const unsigned int zero = 0;
-        cudaMemcpyToSymbol(g_error_flag, &zero, sizeof(zero));
-    }
-    return flag ? EMU_STATUS_DEVICE_TIMEOUT : EMU_STATUS_SUCCESS;
+    return any ? EMU_STATUS_DEVICE_TIMEOUT : EMU_STATUS_SUCCESS;
 }
 
 // The slot of (device, stream) in the workspace table, taken on first use;
@@ -869,7 +872,8 @@ bool pdl_enabled() {
     return v;
 }
 
-cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters, cudaStream_t stream) {
+cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters, cudaStream_t stream,
+                        const EpiTable* epi = nullptr) {
     // only uniform plans: in a hybrid plan the split tail is a small part of
     // the work, and the whole tiles run measurably slower in the staged build
     const bool staged = p.split_a >= kStagedMinPieces;
@@ -886,7 +890,8 @@ cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters
     }
     const bool long_k = pipe == PIPE_LONG_K || pipe == PIPE_LONG_K_PACKED, packed = pipe_packed(pipe);
     cudaError_t e;
-    switch (mode) {
+    if (epi) e = epi->launch(mode, pipe, cfg, p);
+    else switch (mode) {
         case EMU_MODE_TF32X3:
             if (staged)
                 e = packed ? launch_one<MODE_TF32X3, PIPE_SHORT_K_PACKED, true>(cfg, p)
@@ -923,6 +928,8 @@ cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters
 
 // Core: C = alpha * op(A) op(B) + beta * C_old + bias, with C_old == C.
 // packed_b != nullptr: op(B) comes packed (emu_pack_b); B and ldb are unused.
+// fused: the epilogue is one of the EPI_* kinds instead (gated: N is F, op(B)
+// has 2F columns; the plan's tiles have 128 columns of each half).
 // check_only: the checks and the buffers' reservation, without a launch.
 // One launch of the pack kernel on `stream` (the caller checked the arguments).
 cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, int64_t ldb, bool k_major,
@@ -943,7 +950,7 @@ cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, i
 emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t N, int64_t K, float alpha,
                       const float* A, int64_t lda, const float* B, int64_t ldb, float beta, float* C,
                       int64_t ldc, const float* bias, cudaStream_t stream, const void* packed_b = nullptr,
-                      bool check_only = false) {
+                      bool check_only = false, const Fused* fused = nullptr) {
     if (!valid_mode(mode)) return EMU_STATUS_INVALID_VALUE;
     if (M < 0 || N < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
     if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return EMU_STATUS_NOT_SUPPORTED;
@@ -979,7 +986,10 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     }
 
     const int pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
-    if (!packed_b) mode = dispatch_mode(mode, M, N, K, pairs, dev->sm_count);
+    const bool gated = fused && fused->kind == FUSED_GATED;
+    const int64_t b_n = gated ? 2 * N : N;                                // columns of op(B)
+    const int64_t plan_n = gated ? (N + 127) / 128 * 256 : N;
+    if (!packed_b && !fused) mode = dispatch_mode(mode, M, N, K, pairs, dev->sm_count);
     if (mode == EMU_MODE_FP32) {
         if (N > 64LL * NAT_MAX_GRID_Y) return EMU_STATUS_NOT_SUPPORTED;
         if (check_only) return EMU_STATUS_SUCCESS;
@@ -989,7 +999,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         return launch_native(M, N, K, alpha, A, lda, a_mn, B, ldb, b_mn, beta, C, ldc, bias, dev->sm_count, stream) == cudaSuccess
                    ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
     }
-    Plan plan = plan_for(M, N, K, pairs);
+    Plan plan = plan_for(M, plan_n, K, pairs);
     int devid = 0;
     cudaGetDevice(&devid);
     // Everything that can fail -- the library's buffers, the tensor maps --
@@ -998,17 +1008,22 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     static const bool autopack = env_int("EMU_AUTOPACK", 1) != 0;
     void* autopack_buf = nullptr;
     if (!packed_b && autopack && (mode == EMU_MODE_TF32X3 || mode == EMU_MODE_TF32X1) &&
-        plan.tiles_m >= kAutoPackMinTileRows && (size_t)packed_bytes(mode, N, K) <= kAutoPackMaxBytes) {
-        st = packed_buffer_for(devid, stream, (size_t)packed_bytes(mode, N, K), &autopack_buf);
+        plan.tiles_m >= kAutoPackMinTileRows && (size_t)packed_bytes(mode, b_n, K) <= kAutoPackMaxBytes) {
+        st = packed_buffer_for(devid, stream, (size_t)packed_bytes(mode, b_n, K), &autopack_buf);
         if (st != EMU_STATUS_SUCCESS) return st;
     }
     const void* b_packed = packed_b ? packed_b : autopack_buf;
     if (b_packed) plan.pipe = plan.pipe == PIPE_LONG_K ? PIPE_LONG_K_PACKED : PIPE_SHORT_K_PACKED;
     Params p{};
     if (!encode_operand(&p.tmA, A, a_mn, M, K, lda, HALF) ||
-        !(b_packed ? encode_packed(&p.tmB, b_packed, mode, N, K)
-                   : encode_operand(&p.tmB, B, b_mn, N, K, ldb, (uint32_t)plan.tn / 2)))
+        !(b_packed ? encode_packed(&p.tmB, b_packed, mode, b_n, K)
+                   : encode_operand(&p.tmB, B, b_mn, b_n, K, ldb, (uint32_t)plan.tn / 2)))
         return EMU_STATUS_LAUNCH_FAILED;
+    const EpiTable* epi = nullptr;
+    if (fused) {
+        epi = gated ? &kEpiGated : fused->kind == FUSED_ACT ? &kEpiAct : &kEpiGatedBwd;
+        p.epi = {act_params(fused->act), (int)N, (N & 3) == 0, fused->res, fused->ldr, fused->d, fused->ldd, fused->sums};
+    }
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     p.a_mn_major = a_mn; p.b_mn_major = b_packed ? 0 : b_mn;
     p.tiles_m = plan.tiles_m;
@@ -1038,7 +1053,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         p.counters = w->counters;
     }
     if (check_only) return EMU_STATUS_SUCCESS;
-    if (autopack_buf && launch_pack(mode, N, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
+    if (autopack_buf && launch_pack(mode, b_n, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
         return EMU_STATUS_LAUNCH_FAILED;
     const int clusters = plan.clusters;
     if (log_enabled())
@@ -1047,8 +1062,8 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
                      mode_name(mode), (long long)M, (long long)N, (long long)K, (int)a_mn, (int)b_mn, plan.pipe,
                      plan.tn, p.tiles_m, p.tiles_n, p.k_stages, p.num_units, p.tiles_a, p.split_a, p.split_b,
                      clusters, pairs);
-    return launch_gemm(mode, plan.pipe, p, clusters, stream) == cudaSuccess ? EMU_STATUS_SUCCESS
-                                                                             : EMU_STATUS_LAUNCH_FAILED;
+    return launch_gemm(mode, plan.pipe, p, clusters, stream, epi) == cudaSuccess ? EMU_STATUS_SUCCESS
+                                                                                  : EMU_STATUS_LAUNCH_FAILED;
 }
 
 // ----------------------------------------------------------- split dump ----
@@ -1140,8 +1155,9 @@ emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float**
 
 emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check) {
     return run_gemm(mode, g.a_mn, g.b_mn, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.bias, stream,
-                    nullptr, check);
+                    nullptr, check, g.fused);
 }
+static_assert(FUSED_ACT == EPI_ACT && FUSED_GATED == EPI_GATED && FUSED_GATED_BWD == EPI_GATED_BWD, "epilogue kinds");
 
 }  // namespace emu
 

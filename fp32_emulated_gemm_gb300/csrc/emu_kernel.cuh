@@ -55,6 +55,7 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "activation.cuh"
 #include "ptx.cuh"
 
 namespace emu {
@@ -202,6 +203,33 @@ template <int MODE, int PIPE> struct KCfg {
 template <int MODE, int PIPE>
 constexpr uint32_t smem_bytes() { return KCfg<MODE, PIPE>::SMEM; }
 
+// What the epilogue makes of a tile's sums S (before the bias):
+// EPI_STORE      C = alpha S + beta C_old + bias
+// EPI_ACT        C = a(S + bias) + R, and D = a'(S + bias) when wanted
+// EPI_GATED      the tile is 128 columns of the gate G and the same 128 of the
+//                up projection U (CTA 0 loads the gate's rows of the weight,
+//                CTA 1 the up projection's), so a thread has both of an
+//                element: C = a(G) U, and D = [U a'(G) | a(G)] when wanted
+// EPI_GATED_BWD  C = [S | S] * D, and its sums over each 32 rows
+// The forward pass stores the factors D that its backward pass multiplies by,
+// not the pre-activations: they take the same bytes, the sums are at hand, and
+// the backward epilogue needs no special functions (with them, on eight warps,
+// it took 84 us with silu and 109 with gelu where the plain product takes 27:
+// M = 6144, K = 256, F = 1024).
+enum Epi : int { EPI_STORE = 0, EPI_ACT = 1, EPI_GATED = 2, EPI_GATED_BWD = 3 };
+
+// The output the epilogues other than EPI_STORE need beyond Params' C and bias.
+struct EpiParams {
+    ActParams act;
+    int F;             // gated: columns from the gate's half to the up projection's in D, C, W and the bias
+    int vec_up;        // gated: F is a multiple of 4, so both halves of a row are 16-byte aligned
+    const float* res;  // EPI_ACT: R, or null
+    long long ldr;
+    float* d;          // EPI_ACT, EPI_GATED: D, or null; EPI_GATED_BWD: D, read
+    long long ldd;
+    float* sums;       // EPI_GATED_BWD: ceil(M / 32) x 2F partial column sums, or null
+};
+
 struct Params {
     CUtensorMap tmA;  // FP32 op(A): K-major box {32, 128} or MN-major box {32, 32}
     CUtensorMap tmB;  // FP32 op(B): K-major box {32, TN / 2} or MN-major box {32, 32};
@@ -235,6 +263,7 @@ struct Params {
     unsigned long long* counters;  // split tiles: 2 per tile (pieces arrived, per CTA half), epoch-tagged
     unsigned long long epoch;      // this launch's epoch on the counters (> 0, new for every launch)
     unsigned long long wait_budget_ns;
+    EpiParams epi;
 };
 
 // ----------------------------------------------------------- the splits ----
@@ -467,10 +496,39 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const Walk& k, int cid,
     return w;
 }
 
+// A row's four columns gcol .. gcol + 3 of an n-column matrix: a float4 where
+// all four exist and `vec` says the row is aligned, else word by word.
+__device__ __forceinline__ float4 load_cols(const float* p, int gcol, int n, bool vec) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (vec && gcol + 3 < n) return __ldg(reinterpret_cast<const float4*>(p));
+    if (gcol + 0 < n) v.x = __ldg(p);
+    if (gcol + 1 < n) v.y = __ldg(p + 1);
+    if (gcol + 2 < n) v.z = __ldg(p + 2);
+    if (gcol + 3 < n) v.w = __ldg(p + 3);
+    return v;
+}
+__device__ __forceinline__ void store_cols(float* p, int gcol, int n, bool vec, const float4& v) {
+    if (vec && gcol + 3 < n) { *reinterpret_cast<float4*>(p) = v; return; }
+    if (gcol + 0 < n) p[0] = v.x;
+    if (gcol + 1 < n) p[1] = v.y;
+    if (gcol + 2 < n) p[2] = v.z;
+    if (gcol + 3 < n) p[3] = v.w;
+}
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 shfl_xor4(const float4& v, int o) {
+    return make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o),
+                       __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o));
+}
+__device__ __forceinline__ float4 mul4(const float4& a, const float4& b) {
+    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+
 // STAGED: split tiles of many pieces read the other pieces' partials through
 // the output staging area (see the epilogue); a separate instantiation, so
 // that plans with few pieces keep the register-only reduction's code.
-template <int MODE, int PIPE, bool STAGED = false>
+template <int MODE, int PIPE, bool STAGED = false, int EPI = EPI_STORE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 emu_gemm_kernel(const __grid_constant__ Params p) {
     using C = Cfg<MODE>;
@@ -519,6 +577,10 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
     // allocates TMEM (the load latency overlaps the set-up).  Like every
     // global access of this kernel they wait for the grids this launch
     // depends on.
+    // this CTA's first row of op(B)^T in tile column tn
+    auto b_row0 = [&](int tn) {
+        return EPI == EPI_GATED ? tn * BH + p.epi.F * static_cast<int>(rank) : tn * TN + BH * static_cast<int>(rank);
+    };
     // (m0, n0): this CTA's first row of op(A) and of op(B)^T in the tile
     auto issue_load_at = [&](int s, int m0, int n0, int ks) {
         uint64_t* full = &fp32_full[s];
@@ -534,7 +596,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         }
     };
     auto issue_load = [&](int s, int tile, int ks) {
-        issue_load_at(s, (tile / p.tiles_n) * TILE_M + HALF * rank, (tile % p.tiles_n) * TN + BH * rank, ks);
+        issue_load_at(s, (tile / p.tiles_n) * TILE_M + HALF * rank, b_row0(tile % p.tiles_n), ks);
     };
     // packed shapes: op(B)'s component tiles of a stage, straight into the
     // component ring (box {32 k, BH rows, 1 component} per component)
@@ -545,7 +607,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         for (int c = 0; c < C::NCOMP; ++c) tma_load_3d(dst + c * KC::COMP_B, &p.tmB, full, ks * BK, n0, c);
     };
     auto issue_bload = [&](int bslot, int tile, int ks) {
-        issue_bload_at(bslot, (tile % p.tiles_n) * TN + BH * rank, ks);
+        issue_bload_at(bslot, b_row0(tile % p.tiles_n), ks);
     };
     int early = 0, early_b = 0;  // stages already issued by thread 0 (warp 0 lane 0, the producer)
     if (threadIdx.x == 0) {
@@ -575,7 +637,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                     const Unit w = unit_at(p, wk, static_cast<int>(cid), u);
                     const int tm = w.tile / p.tiles_n;
                     m0 = tm * TILE_M + HALF * rank;
-                    n0 = (w.tile - tm * p.tiles_n) * TN + BH * rank;
+                    n0 = b_row0(w.tile - tm * p.tiles_n);
                     ks = w.kb; ke = w.ke;
                     u += wk.step;
                 }
@@ -764,6 +826,19 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 return p.workspace + static_cast<size_t>(slot) * (static_cast<size_t>(TILE_M) * TN) +
                        (static_cast<size_t>(rank) * NUM_EPI_WARPS + e) * (32u * ACC) + lane * 4u;
             };
+            if constexpr (EPI == EPI_ACT || EPI == EPI_GATED_BWD) {
+                // What the epilogue reads of this unit's tile (R, or both halves
+                // of D) is brought to L2 while the k-loop runs: thread t asks
+                // for a row of 256 columns
+                const float* base = EPI == EPI_ACT ? p.epi.res : p.epi.d;
+                if (base && w.role != ROLE_HEAD) {
+                    const int t = static_cast<int>(e * 32 + lane), row = (w.tile / p.tiles_n) * TILE_M + static_cast<int>(HALF * rank) + (t & 127);
+                    const int c0 = (w.tile % p.tiles_n) * TN, cols = p.N - c0 < TN ? (p.N - c0) & ~3 : TN;
+                    const bool up = t >= 128;
+                    if (row < p.M && cols > 0 && (!up || (EPI == EPI_GATED_BWD && p.epi.vec_up)))
+                        l2_prefetch(base + row * (EPI == EPI_ACT ? p.epi.ldr : p.epi.ldd) + (up ? p.epi.F : 0) + c0, 4u * cols);
+                }
+            }
             float acc[ACC];
             if (!STAGED && w.role == ROLE_TAIL) {
                 // Start from the running sum of the tile's low k-stages, which
@@ -786,12 +861,14 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             for (int ks = w.kb; ks < w.ke; ++ks) {
                 if (!mbar_wait_warp(&acc_full[b], bph, abort_flag, budget, 4)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t col = tmem_base + lane_base + b * TN + half * ACC;
+                const uint32_t col = tmem_base + lane_base + b * TN + half * (EPI == EPI_GATED ? ACC / 2 : ACC);
 #pragma unroll
                 for (int c = 0; c < ACC / 16; c += 2) {
                     float v0[16], v1[16];
-                    tmem_ld16(col + c * 16, v0);
-                    tmem_ld16(col + (c + 1) * 16, v1);
+                    // (gated: the thread's ACC / 2 gate columns, then the same columns of the up half)
+                    const uint32_t at = col + c * 16 + (EPI == EPI_GATED && c >= ACC / 32 ? TN / 2 - ACC / 2 : 0);
+                    tmem_ld16(at, v0);
+                    tmem_ld16(at + 16, v1);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -831,7 +908,11 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             // order for every chunk -- and stores only those: the result does not
             // depend on timing.
             const int S = w.pieces;
-            auto owns = [&](int c) { return S == 1 || static_cast<int>(4 * e + c) % S == w.piece; };
+            // (gated: chunks c and c + 2 are the gate and the up half of the same
+            // columns, and one piece owns both)
+            auto owns = [&](int c) {
+                return S == 1 || static_cast<int>(EPI == EPI_GATED ? 2 * e + (c & 1) : 4 * e + c) % S == w.piece;
+            };
             if (S > 1) {
                 const size_t per_piece = static_cast<size_t>(TILE_M) * TN;
                 const size_t warp_off = (static_cast<size_t>(rank) * NUM_EPI_WARPS + e) * (32u * ACC) + lane * 4u;
@@ -947,8 +1028,9 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             }
             // (the tile's origin is worked out here, not before the split-tile
             // reduction, so that it holds no registers there)
+            constexpr int TILE_COLS = EPI == EPI_GATED ? TN / 2 : TN, WARP_COLS = EPI == EPI_GATED ? ACC / 2 : ACC;
             const int row0 = (w.tile / p.tiles_n) * TILE_M + static_cast<int>(HALF * rank + quarter * 32u);
-            const int col0 = (w.tile % p.tiles_n) * TN + static_cast<int>(half * ACC);
+            const int col0 = (w.tile % p.tiles_n) * TILE_COLS + static_cast<int>(half * WARP_COLS);
             // ACC / OUT_COLS blocks of 32 rows x OUT_COLS columns: each lane stages
             // its row's sums in shared memory (rows of OUT_COLS * 4 bytes, 16-byte
             // chunks XOR-swizzled by row); the warp then reads them back as whole
@@ -958,11 +1040,12 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             constexpr int CPR = OUT_COLS / 4;   // 16-byte chunks per staged row
             constexpr int RPP = 32 / CPR;       // rows per read-back pass
             uint8_t* stage = out_stage + e * STAGE_OUT_BYTES;
-            const float alpha = p.alpha, beta = p.beta;
-            const uint32_t q = lane % CPR;
             auto chunk_off = [](uint32_t r, uint32_t j) {
                 return OUT_COLS == 32 ? off_f32_chunk(r, j) : off_bf16_chunk(r, j);
             };
+            if constexpr (EPI == EPI_STORE) {
+            const float alpha = p.alpha, beta = p.beta;
+            const uint32_t q = lane % CPR;
 #pragma unroll
             for (int c = 0; c < ACC / OUT_COLS; ++c) {
                 if (!owns(c * OUT_COLS / 32)) continue;  // another piece of a split tile stores it
@@ -1017,6 +1100,229 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                     }
                 }
                 __syncwarp();  // staging buffer free for the next block
+            }
+            } else if constexpr (EPI == EPI_GATED) {
+            // Blocks of OUT_COLS / 2 gate columns and the same columns of the up
+            // half side by side; the rows a lane reads back are chosen so that
+            // the eight lanes of a 128-byte access hit distinct banks.
+            constexpr int GC = OUT_COLS / 2, GPR = CPR / 2;  // columns, 16-byte chunks per row and half
+            constexpr int ROWS = 32 / GPR;                   // rows a pass reads back
+            const EpiParams& ep = p.epi;
+            const uint32_t q = lane % GPR, i = lane / GPR;
+            const uint32_t lane_row = GPR == 4 ? (i >> 1) + ((i & 1u) << 2)
+                                               : (i & 1u) + ((i & 2u) << 1) + ((i & 4u) >> 1) + (i & 8u);
+            const int lrow = row0 + static_cast<int>(lane_row);
+            // One stretch of code per family and per presence of D, chosen once
+            // per tile: with eight warps on the SM it is branches and the order
+            // of a few long latencies that the time goes to (see EPI_ACT).
+            auto phase = [&](auto fam, auto save) {
+#pragma unroll
+            for (int c = 0; c < WARP_COLS / GC; ++c) {
+                if (!owns(c * GC / 32)) continue;
+#pragma unroll
+                for (int j = 0; j < GPR; ++j) {
+                    const int k = GC * c + 4 * j;
+                    *reinterpret_cast<float4*>(stage + chunk_off(lane, j)) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+                    *reinterpret_cast<float4*>(stage + chunk_off(lane, GPR + j)) =
+                        make_float4(acc[ACC / 2 + k], acc[ACC / 2 + k + 1], acc[ACC / 2 + k + 2], acc[ACC / 2 + k + 3]);
+                }
+                const int gcol = col0 + GC * c + static_cast<int>(4 * q);
+                float4 bg = make_float4(0.f, 0.f, 0.f, 0.f), bu = bg;
+                if (p.bias) {
+                    bg = load_cols(p.bias + gcol, gcol, p.N, true);
+                    bu = load_cols(p.bias + ep.F + gcol, gcol, p.N, ep.vec_up);
+                }
+                __syncwarp();
+                auto gate = [&](int pass) {
+                    return add4(*reinterpret_cast<const float4*>(stage + chunk_off(pass * ROWS + lane_row, q)), bg);
+                };
+                auto up = [&](int pass) {
+                    return add4(*reinterpret_cast<const float4*>(stage + chunk_off(pass * ROWS + lane_row, GPR + q)), bu);
+                };
+                float* h = p.c + lrow * p.ldc + gcol;
+                float* d = save.value ? ep.d + lrow * ep.ldd + gcol : nullptr;
+                if (row0 + 32 <= p.M && col0 + GC * (c + 1) <= p.N && ep.vec_up) {
+#pragma unroll
+                    for (int pass = 0; pass < GPR; pass += 2) {
+                        float4 g[2], u[2], f[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) { g[k] = gate(pass + k); u[k] = up(pass + k); }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float4 a;
+                            act_value_grad4<fam.value>(ep.act, g[k], a, f[k]);
+                            g[k] = a;
+                        }
+                        if constexpr (save.value) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                *reinterpret_cast<float4*>(d) = mul4(u[k], f[k]);
+                                *reinterpret_cast<float4*>(d + ep.F) = g[k];
+                                d += ROWS * ep.ldd;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            *reinterpret_cast<float4*>(h) = mul4(g[k], u[k]);
+                            h += ROWS * p.ldc;
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int pass = 0; pass < GPR && lrow + pass * ROWS < p.M; ++pass) {
+                        const float4 g = gate(pass), u = up(pass);
+                        float4 a, f;
+                        act_value_grad4<fam.value>(ep.act, g, a, f);
+                        if constexpr (save.value) {
+                            store_cols(d, gcol, p.N, true, mul4(u, f));
+                            store_cols(d + ep.F, gcol, p.N, ep.vec_up, a);
+                            d += ROWS * ep.ldd;
+                        }
+                        store_cols(h, gcol, p.N, true, mul4(a, u));
+                        h += ROWS * p.ldc;
+                    }
+                }
+                __syncwarp();
+            }
+            };
+            for_family(ep.act.family, [&](auto fam) {
+                if (ep.d) phase(fam, ValueIs<1>{});
+                else phase(fam, ValueIs<0>{});
+            });
+            } else {
+            // the same blocks as EPI_STORE's
+            const EpiParams& ep = p.epi;
+            const uint32_t q = lane % CPR;
+            const int lrow = row0 + static_cast<int>(lane / CPR);
+            constexpr int PASSES = 32 / RPP;
+            auto phase = [&](auto fam, auto save) {
+#pragma unroll
+            for (int c = 0; c < ACC / OUT_COLS; ++c) {
+                if (!owns(c * OUT_COLS / 32)) continue;
+#pragma unroll
+                for (int j = 0; j < CPR; ++j)
+                    *reinterpret_cast<float4*>(stage + chunk_off(lane, j)) =
+                        make_float4(acc[OUT_COLS * c + 4 * j], acc[OUT_COLS * c + 4 * j + 1],
+                                    acc[OUT_COLS * c + 4 * j + 2], acc[OUT_COLS * c + 4 * j + 3]);
+                auto staged = [&](int pass) {
+                    return *reinterpret_cast<const float4*>(stage + chunk_off(pass * RPP + lane / CPR, q));
+                };
+                const int gcol = col0 + OUT_COLS * c + static_cast<int>(4 * q);
+                const bool whole = row0 + 32 <= p.M && col0 + OUT_COLS * (c + 1) <= p.N;
+                float* out = p.c + lrow * p.ldc + gcol;
+                constexpr int BATCH = 4;  // passes whose loads go out together
+                if constexpr (EPI == EPI_ACT) {
+                    float4 bb = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p.bias) bb = load_cols(p.bias + gcol, gcol, p.N, true);
+                    const float* res = ep.res ? ep.res + lrow * ep.ldr + gcol : nullptr;
+                    float* d = save.value ? ep.d + lrow * ep.ldd + gcol : nullptr;
+                    __syncwarp();
+                    if (whole) {
+#pragma unroll
+                        for (int pass = 0; pass < PASSES; pass += BATCH) {
+                            float4 r[BATCH];  // (from L2: the unit's start prefetched it)
+#pragma unroll
+                            for (int k = 0; k < BATCH; ++k) {
+                                r[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (res) r[k] = __ldg(reinterpret_cast<const float4*>(res + k * RPP * ep.ldr));
+                            }
+                            if (res) res += BATCH * RPP * ep.ldr;
+#pragma unroll
+                            for (int k = 0; k < BATCH; k += 2) {
+                                float4 v[2], f[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    act_value_grad4<fam.value>(ep.act, add4(staged(pass + k + j), bb), v[j], f[j]);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    if constexpr (save.value) {
+                                        *reinterpret_cast<float4*>(d) = f[j];
+                                        d += RPP * ep.ldd;
+                                    }
+                                    *reinterpret_cast<float4*>(out) = add4(v[j], r[k + j]);
+                                    out += RPP * p.ldc;
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int pass = 0; pass < PASSES && lrow + pass * RPP < p.M; ++pass) {
+                            float4 v, f;
+                            act_value_grad4<fam.value>(ep.act, add4(staged(pass), bb), v, f);
+                            if constexpr (save.value) {
+                                store_cols(d, gcol, p.N, true, f);
+                                d += RPP * ep.ldd;
+                            }
+                            if (res) {
+                                v = add4(v, load_cols(res, gcol, p.N, true));
+                                res += RPP * ep.ldr;
+                            }
+                            store_cols(out, gcol, p.N, true, v);
+                            out += RPP * p.ldc;
+                        }
+                    }
+                } else {
+                    float4 sg = make_float4(0.f, 0.f, 0.f, 0.f), su = sg;
+                    const float* d = ep.d + lrow * ep.ldd + gcol;
+                    __syncwarp();
+                    if (whole && ep.vec_up) {
+                        // D goes into the registers the staged block left (from
+                        // L2: the unit's start prefetched it)
+#pragma unroll
+                        for (int pass = 0; pass < PASSES; pass += BATCH) {
+                            float4 g[BATCH], u[BATCH];
+#pragma unroll
+                            for (int k = 0; k < BATCH; ++k) {
+                                g[k] = __ldg(reinterpret_cast<const float4*>(d));
+                                u[k] = __ldg(reinterpret_cast<const float4*>(d + ep.F));
+                                d += RPP * ep.ldd;
+                            }
+#pragma unroll
+                            for (int k = 0; k < BATCH; ++k) {
+                                const float4 dh = staged(pass + k), dg = mul4(dh, g[k]), du = mul4(dh, u[k]);
+                                *reinterpret_cast<float4*>(out) = dg;
+                                *reinterpret_cast<float4*>(out + ep.F) = du;
+                                out += RPP * p.ldc;
+                                sg = add4(sg, dg);
+                                su = add4(su, du);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int pass = 0; pass < PASSES && lrow + pass * RPP < p.M; ++pass) {
+                            const float4 dh = staged(pass), dg = mul4(dh, load_cols(d, gcol, p.N, true)),
+                                         du = mul4(dh, load_cols(d + ep.F, gcol, p.N, ep.vec_up));
+                            store_cols(out, gcol, p.N, true, dg);
+                            store_cols(out + ep.F, gcol, p.N, ep.vec_up, du);
+                            d += RPP * ep.ldd;
+                            out += RPP * p.ldc;
+                            sg = add4(sg, dg);
+                            su = add4(su, du);
+                        }
+                    }
+                    if (ep.sums) {  // the lanes of equal q hold the same columns of other rows
+#pragma unroll
+                        for (int o = 16; o >= CPR; o >>= 1) {
+                            sg = add4(sg, shfl_xor4(sg, o));
+                            su = add4(su, shfl_xor4(su, o));
+                        }
+                        if (lane < CPR && row0 < p.M) {
+                            float* dst = ep.sums + static_cast<long long>(row0 / 32) * (2ll * ep.F) + gcol;
+                            store_cols(dst, gcol, p.N, ep.vec_up, sg);
+                            store_cols(dst + ep.F, gcol, p.N, ep.vec_up, su);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            };
+            if constexpr (EPI == EPI_ACT)
+                for_family(ep.act.family, [&](auto fam) {
+                    if (ep.d) phase(fam, ValueIs<1>{});
+                    else phase(fam, ValueIs<0>{});
+                });
+            else
+                phase(ValueIs<FAMILY_LINEAR>{}, ValueIs<0>{});
             }
         }
     }

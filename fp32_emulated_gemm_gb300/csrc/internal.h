@@ -20,6 +20,20 @@ emu_status_t current_device(DeviceCtx* out);
 // workspace, which a product on the same stream may be using in between.
 emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float** out);
 
+// What a product's epilogue does besides the bias (the Epi kinds of
+// emu_kernel.cuh; modes BF16x9 and TF32x3, K > 0).
+struct Fused {
+    int kind;           // a FusedKind
+    int act;
+    const float *res;   // FUSED_ACT: R, or null
+    int64_t ldr;
+    float *d;           // the derivative's factors D: written when not null (FUSED_GATED_BWD: read)
+    int64_t ldd;
+    float *sums;        // FUSED_GATED_BWD: ceil(M / 32) x 2N partial column sums, or null
+};
+enum FusedKind : int { FUSED_ACT = 1, FUSED_GATED = 2, FUSED_GATED_BWD = 3 };
+inline bool fused_mode(emu_mode_t mode) { return mode == EMU_MODE_BF16X9 || mode == EMU_MODE_TF32X3; }
+
 // One product C = op(A) op(B) + beta C + bias as the public entry points run
 // it.  `check` true: argument checks and buffer reservation alone, so that an
 // operator of several launches can make sure of all of them before the first.
@@ -34,6 +48,7 @@ struct Gemm {
     float *C;
     int64_t ldc;
     const float *bias;
+    const Fused *fused = nullptr;  // FUSED_GATED: N is F, B has 2F rows and the bias 2F values
 };
 emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check);
 

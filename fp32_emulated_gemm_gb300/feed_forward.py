@@ -17,7 +17,7 @@ import ctypes
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _check, _mode, _new_c, _ptr, _stream, load
+from . import EMU_MODE_BF16X9, EMU_MODE_TF32X3, _check, _mode, _new_c, _ptr, _stream, load
 
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 EMU_ACT_NONE, EMU_ACT_RELU, EMU_ACT_GELU, EMU_ACT_GELU_TANH, EMU_ACT_SILU = range(5)
@@ -27,11 +27,11 @@ _SIGNATURES = {
     "emu_layer_norm_fwd": "nnpnppfpnpp",
     "emu_layer_norm_bwd": "nnpnpnppppnpnpp",
     "emu_linear_act_fwd": "eennnpnpnppnpnpn",
-    "emu_linear_act_bwd": "eennnpnpnpnpnpnpnpnp",
+    "emu_linear_act_bwd": "ennnpnpnpnpnpnpnpnp",
     "emu_gated_fwd": "eennnpnpnppnpn",
-    "emu_gated_bwd": "eennnpnpnpnpnpnpnpnp",
+    "emu_gated_bwd": "ennnpnpnpnpnpnpnpnp",
     "emu_gated_ffn_fwd": "eennnnpnpnppnppnpnpnpn",
-    "emu_gated_ffn_bwd": "eennnnpnpnpnpnpnpnpnpnpnppnp",
+    "emu_gated_ffn_bwd": "ennnnpnpnpnpnpnpnpnpnpnppnp",
 }
 _CTYPES = {"e": ctypes.c_int, "n": ctypes.c_int64, "f": ctypes.c_float, "p": ctypes.c_void_p}
 _CAST = {"e": int, "n": int, "f": float, "p": _ptr}
@@ -78,6 +78,7 @@ emu_gated_ffn_bwd = _c_name("emu_gated_ffn_bwd")
 # row stride).  A matrix that is not wanted is (None, None, 0).
 _float32, _empty = torch.float32, torch.empty
 _NONE = (None, None, 0)
+_FUSED = (EMU_MODE_BF16X9, EMU_MODE_TF32X3)  # the modes whose products take the activations in their epilogue
 
 
 def _act(act):
@@ -219,28 +220,29 @@ def layer_norm_bwd(dY, X, weight, mean, rstd, *, add=None, need_input=True, need
 
 # ----------------------------------------------------------- linear_act ----
 def linear_act_fwd(X, W, bias=None, *, act="none", residual=None, mode="bf16x9", save=False, out=None):
-    """Y = act(X W^T + bias) + residual (X [M,K], W [N,K]); with `save`
-    (Y, Z), Z the pre-activation that linear_act_bwd reads."""
+    """Y = act(Z) + residual with Z = X W^T + bias (X [M,K], W [N,K]); with
+    `save` (Y, D) for linear_act_bwd, D = act'(Z) (None for act "none")."""
     X, px, ldx = _operand(X, "X")
     W, pw, ldw = _operand(W, "W")
     M, K = X.shape
     N, Kw = W.shape
     if Kw != K:
         raise ValueError("inner dimensions differ")
+    a = _act(act)
     bias, pb = _vector(bias, "bias", N)
     residual, pr, ldr = _NONE if residual is None else _operand(residual, "residual", (M, N))
     device = X.device
     Y, py, ldy = _result(out, (M, N), device, "out")
-    Z, pz, ldz = _new(M, N, device) if save else _NONE
-    _check(_fn("emu_linear_act_fwd")(_mode(mode), _act(act), M, N, K, px, ldx, pw, ldw, pb, pr, ldr, pz, ldz, py, ldy,
+    D, pd, ldd = _new(M, N, device) if save and a != EMU_ACT_NONE else _NONE
+    _check(_fn("emu_linear_act_fwd")(_mode(mode), a, M, N, K, px, ldx, pw, ldw, pb, pr, ldr, pd, ldd, py, ldy,
                                      _stream_of("linear_act_fwd", X, W, bias, residual, Y)), "emu_linear_act_fwd")
-    return (Y, Z) if save else Y
+    return (Y, D) if save else Y
 
 
-def linear_act_bwd(dY, X, W, Z=None, *, act="none", mode="bf16x9", need=(True, True, True)):
-    """(dX, dW, dbias) of linear_act_fwd (the residual's gradient is dY); Z is
-    not read for act "none".  `need` says which are wanted; the others are None."""
-    a = _act(act)
+def linear_act_bwd(dY, X, W, D=None, *, act="none", mode="bf16x9", need=(True, True, True)):
+    """(dX, dW, dbias) of linear_act_fwd from its D, which act "none" does not
+    read (the residual's gradient is dY).  `need` says which are wanted; the
+    others are None."""
     X, px, ldx = _operand(X, "X")
     W, pw, ldw = _operand(W, "W")
     M, K = X.shape
@@ -249,19 +251,19 @@ def linear_act_bwd(dY, X, W, Z=None, *, act="none", mode="bf16x9", need=(True, T
         raise ValueError("inner dimensions differ")
     dY, pdy, lddy = _operand(dY, "dY", (M, N))
     device = X.device
-    pz, ldz, pdz, lddz = None, 0, None, 0
-    if a != EMU_ACT_NONE:
-        if Z is None:
-            raise ValueError(f"act {act!r} needs Z")
-        Z, pz, ldz = _operand(Z, "Z", (M, N))
+    pd, ldd, pdz, lddz = None, 0, None, 0
+    if _act(act) != EMU_ACT_NONE:
+        if D is None:
+            raise ValueError(f"act {act!r} needs D")
+        D, pd, ldd = _operand(D, "D", (M, N))
         dZ, pdz, lddz = _new(M, N, device)
     else:
-        Z = None
+        D = None
     dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
     dW, pdw, lddw = _new(N, K, device) if need[1] else _NONE
     db, pdb = _new_vector(N, device) if need[2] else (None, None)
-    _check(_fn("emu_linear_act_bwd")(_mode(mode), a, M, N, K, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdz, lddz, pdx, lddx,
-                                     pdw, lddw, pdb, _stream_of("linear_act_bwd", dY, X, W, Z)), "emu_linear_act_bwd")
+    _check(_fn("emu_linear_act_bwd")(_mode(mode), M, N, K, pdy, lddy, px, ldx, pw, ldw, pd, ldd, pdz, lddz, pdx, lddx,
+                                     pdw, lddw, pdb, _stream_of("linear_act_bwd", dY, X, W, D)), "emu_linear_act_bwd")
     return dX, dW, db
 
 
@@ -277,32 +279,36 @@ def _gated_shapes(X, W):
 
 def gated_fwd(X, W, bias=None, *, act="silu", mode="bf16x9", save=False):
     """H = act(G) * U with [G | U] = X W^T + bias (X [M,K]; W [2F,K]: the
-    gate's rows, then the up projection's); with `save` (H, Z), Z = [G | U]."""
+    gate's rows, then the up projection's); with `save` (H, D) for
+    gated_bwd, D = [U act'(G) | act(G)]."""
     X, px, ldx = _operand(X, "X")
     W, pw, ldw = _operand(W, "W")
     M, K, F = _gated_shapes(X, W)
     bias, pb = _vector(bias, "bias", 2 * F)
     H, ph, ldh = _new(M, F, X.device)
-    Z, pz, ldz = _new(M, 2 * F, X.device)
-    _check(_fn("emu_gated_fwd")(_mode(mode), _act(act), M, F, K, px, ldx, pw, ldw, pb, pz, ldz, ph, ldh,
+    mode = _mode(mode)
+    D, pd, ldd = _new(M, 2 * F, X.device) if save or mode not in _FUSED else _NONE
+    _check(_fn("emu_gated_fwd")(mode, _act(act), M, F, K, px, ldx, pw, ldw, pb, pd, ldd, ph, ldh,
                                 _stream_of("gated_fwd", X, W, bias)), "emu_gated_fwd")
-    return (H, Z) if save else H
+    return (H, D) if save else H
 
 
-def gated_bwd(dH, X, W, Z, *, act="silu", mode="bf16x9", need=(True, True, True)):
-    """(dX, dW, dbias) of gated_fwd from Z; `need` says which are wanted."""
+def gated_bwd(dH, X, W, D, *, act="silu", mode="bf16x9", need=(True, True, True)):
+    """(dX, dW, dbias) of gated_fwd from its D; `need` says which are wanted.
+    (D holds the activation's part; `act` only has to name one.)"""
+    _act(act)
     X, px, ldx = _operand(X, "X")
     W, pw, ldw = _operand(W, "W")
     M, K, F = _gated_shapes(X, W)
     dH, pdh, lddh = _operand(dH, "dH", (M, F))
-    Z, pz, ldz = _operand(Z, "Z", (M, 2 * F))
+    D, pd, ldd = _operand(D, "D", (M, 2 * F))
     device = X.device
     dZ, pdz, lddz = _new(M, 2 * F, device)
     dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
     dW, pdw, lddw = _new(2 * F, K, device) if need[1] else _NONE
     db, pdb = _new_vector(2 * F, device) if need[2] else (None, None)
-    _check(_fn("emu_gated_bwd")(_mode(mode), _act(act), M, F, K, pdh, lddh, px, ldx, pw, ldw, pz, ldz, pdz, lddz, pdx,
-                                lddx, pdw, lddw, pdb, _stream_of("gated_bwd", dH, X, W, Z)), "emu_gated_bwd")
+    _check(_fn("emu_gated_bwd")(_mode(mode), M, F, K, pdh, lddh, px, ldx, pw, ldw, pd, ldd, pdz, lddz, pdx,
+                                lddx, pdw, lddw, pdb, _stream_of("gated_bwd", dH, X, W, D)), "emu_gated_bwd")
     return dX, dW, db
 
 
@@ -316,7 +322,7 @@ def _ffn_shapes(X, W_in, W_out):
 def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mode="bf16x9", save=False, out=None):
     """Y = H W_out^T + b_out + residual with H = gated_fwd(X, W_in, b_in)
     (X [M,K], W_in [2F,K], W_out [N,F]; the biases and the residual may be
-    None); with `save` (Y, Z, H) for gated_ffn_bwd."""
+    None); with `save` (Y, D, H) for gated_ffn_bwd."""
     X, px, ldx = _operand(X, "X")
     W_in, pwi, ldwi = _operand(W_in, "W_in")
     W_out, pwo, ldwo = _operand(W_out, "W_out")
@@ -327,22 +333,25 @@ def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mod
     device = X.device
     Y, py, ldy = _result(out, (M, N), device, "out")
     H, ph, ldh = _new(M, F, device)
-    Z, pz, ldz = _new(M, 2 * F, device)
+    mode = _mode(mode)
+    D, pd, ldd = _new(M, 2 * F, device) if save or mode not in _FUSED else _NONE
     s = _stream_of("gated_ffn_fwd", X, W_in, b_in, W_out, b_out, residual, Y)
-    _check(_fn("emu_gated_ffn_fwd")(_mode(mode), _act(act), M, K, F, N, px, ldx, pwi, ldwi, pbi, pwo, ldwo, pbo, pr, ldr,
-                                    pz, ldz, ph, ldh, py, ldy, s), "emu_gated_ffn_fwd")
-    return (Y, Z, H) if save else Y
+    _check(_fn("emu_gated_ffn_fwd")(mode, _act(act), M, K, F, N, px, ldx, pwi, ldwi, pbi, pwo, ldwo, pbo, pr, ldr,
+                                    pd, ldd, ph, ldh, py, ldy, s), "emu_gated_ffn_fwd")
+    return (Y, D, H) if save else Y
 
 
-def gated_ffn_bwd(dY, X, W_in, W_out, Z, H, *, act="silu", mode="bf16x9", need=(True, True, True, True, True)):
-    """(dX, dW_in, db_in, dW_out, db_out) of gated_ffn_fwd from its Z and H
-    (the residual's gradient is dY); `need` says which are wanted."""
+def gated_ffn_bwd(dY, X, W_in, W_out, D, H, *, act="silu", mode="bf16x9", need=(True, True, True, True, True)):
+    """(dX, dW_in, db_in, dW_out, db_out) of gated_ffn_fwd from its D and H
+    (the residual's gradient is dY); `need` says which are wanted.  (D holds the
+    activation's part; `act` only has to name one.)"""
+    _act(act)
     X, px, ldx = _operand(X, "X")
     W_in, pwi, ldwi = _operand(W_in, "W_in")
     W_out, pwo, ldwo = _operand(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
     dY, pdy, lddy = _operand(dY, "dY", (M, N))
-    Z, pz, ldz = _operand(Z, "Z", (M, 2 * F))
+    D, pd, ldd = _operand(D, "D", (M, 2 * F))
     H, ph, ldh = _operand(H, "H", (M, F))
     device = X.device
     dZ, pdz, lddz = _new(M, 2 * F, device)
@@ -351,8 +360,8 @@ def gated_ffn_bwd(dY, X, W_in, W_out, Z, H, *, act="silu", mode="bf16x9", need=(
     dbi, pdbi = _new_vector(2 * F, device) if need[2] else (None, None)
     dWo, pdwo, lddwo = _new(N, F, device) if need[3] else _NONE
     dbo, pdbo = _new_vector(N, device) if need[4] else (None, None)
-    s = _stream_of("gated_ffn_bwd", dY, X, W_in, W_out, Z, H)
-    _check(_fn("emu_gated_ffn_bwd")(_mode(mode), _act(act), M, K, F, N, pdy, lddy, px, ldx, pwi, ldwi, pwo, ldwo, pz, ldz,
+    s = _stream_of("gated_ffn_bwd", dY, X, W_in, W_out, D, H)
+    _check(_fn("emu_gated_ffn_bwd")(_mode(mode), M, K, F, N, pdy, lddy, px, ldx, pwi, ldwi, pwo, ldwo, pd, ldd,
                                     ph, ldh, pdz, lddz, pdx, lddx, pdwi, lddwi, pdbi, pdwo, lddwo, pdbo, s),
            "emu_gated_ffn_bwd")
     return dX, dWi, dbi, dWo, dbo
@@ -381,19 +390,19 @@ class EmuLinearActFunction(torch.autograd.Function):
     def forward(ctx, X, W, bias, residual, act, mode):
         save = act != "none" and any(ctx.needs_input_grad[:3])
         r = linear_act_fwd(X, W, bias, act=act, residual=residual, mode=mode, save=save)
-        Y, Z = r if save else (r, None)
-        ctx.save_for_backward(X, W, Z)
+        Y, D = r if save else (r, None)
+        ctx.save_for_backward(X, W, D)
         ctx.act, ctx.mode = act, mode
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W, Z = ctx.saved_tensors
+        X, W, D = ctx.saved_tensors
         need = ctx.needs_input_grad
         dX = dW = db = None
         if any(need[:3]):
-            dX, dW, db = linear_act_bwd(dY, X, W, Z, act=ctx.act, mode=ctx.mode, need=need[:3])
+            dX, dW, db = linear_act_bwd(dY, X, W, D, act=ctx.act, mode=ctx.mode, need=need[:3])
         return dX, dW, db, dY if need[3] else None, None, None
 
 
@@ -402,19 +411,19 @@ class EmuGatedFFNFunction(torch.autograd.Function):
     def forward(ctx, X, W_in, b_in, W_out, b_out, residual, act, mode):
         save = any(ctx.needs_input_grad[:5])
         r = gated_ffn_fwd(X, W_in, b_in, W_out, b_out, act=act, residual=residual, mode=mode, save=save)
-        Y, Z, H = r if save else (r, None, None)
-        ctx.save_for_backward(X, W_in, W_out, Z, H)
+        Y, D, H = r if save else (r, None, None)
+        ctx.save_for_backward(X, W_in, W_out, D, H)
         ctx.act, ctx.mode = act, mode
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W_in, W_out, Z, H = ctx.saved_tensors
+        X, W_in, W_out, D, H = ctx.saved_tensors
         need = ctx.needs_input_grad
         grads = (None,) * 5
         if any(need[:5]):
-            grads = gated_ffn_bwd(dY, X, W_in, W_out, Z, H, act=ctx.act, mode=ctx.mode, need=need[:5])
+            grads = gated_ffn_bwd(dY, X, W_in, W_out, D, H, act=ctx.act, mode=ctx.mode, need=need[:5])
         return (*grads, dY if need[5] else None, None, None)
 
 
@@ -427,19 +436,19 @@ class EmuFeedForwardFunction(torch.autograd.Function):
         save = any(ctx.needs_input_grad[:7])
         Xn, mean, rstd = layer_norm_fwd(X, norm_weight, norm_bias, eps=eps)
         r = gated_ffn_fwd(Xn, W_in, b_in, W_out, b_out, act=act, residual=X, mode=mode, save=save)
-        Y, Z, H = r if save else (r, None, None)
-        ctx.save_for_backward(X, norm_weight, mean, rstd, Xn, W_in, W_out, Z, H)
+        Y, D, H = r if save else (r, None, None)
+        ctx.save_for_backward(X, norm_weight, mean, rstd, Xn, W_in, W_out, D, H)
         ctx.act, ctx.mode = act, mode
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, norm_weight, mean, rstd, Xn, W_in, W_out, Z, H = ctx.saved_tensors
+        X, norm_weight, mean, rstd, Xn, W_in, W_out, D, H = ctx.saved_tensors
         need = ctx.needs_input_grad
         dX = dnw = dnb = None
         inner = any(need[:3])
-        dXn, *grads = gated_ffn_bwd(dY, Xn, W_in, W_out, Z, H, act=ctx.act, mode=ctx.mode, need=(inner, *need[3:7]))
+        dXn, *grads = gated_ffn_bwd(dY, Xn, W_in, W_out, D, H, act=ctx.act, mode=ctx.mode, need=(inner, *need[3:7]))
         if inner:
             dX, dnw, dnb = layer_norm_bwd(dXn, X, norm_weight, mean, rstd, add=dY if need[0] else None,
                                           need_input=need[0], need_params=need[1] or need[2])

@@ -203,7 +203,7 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  *   0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); silu z / (1 + exp(-z)).
  *   Finite z gives a finite value and derivative; relu'(0) = 0.
  * Alignment: every matrix that enters or leaves a product (X, W, residual, Y,
- *   Z, dZ, H, dY, dH, dX, dW and the weights' gradients) starts on a 16-byte
+ *   D, dZ, H, dY, dH, dX, dW and the weights' gradients) starts on a 16-byte
  *   boundary and has a leading dimension that is a multiple of 4, as in
  *   emu_sgemm, biases start on a 16-byte boundary; else
  *   EMU_STATUS_NOT_SUPPORTED.  Widths are free.  emu_layer_norm_* takes any
@@ -247,68 +247,69 @@ emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float *dY, int64_t l
                                 emu_stream_t stream);
 
 /*
- * emu_linear_act_fwd -- Z = X W^T + bias, Y = a(Z) + residual.
+ * emu_linear_act_fwd -- Y = a(Z) + residual with Z = X W^T + bias.
  *   X: M x K, W: N x K, bias: N (may be NULL), residual: M x N (may be NULL),
- *   Y: M x N.  Z (M x N) receives the pre-activation for the backward pass;
- *   NULL when it is not needed.
+ *   Y: M x N.  D (M x N) receives a'(Z), the factor of the backward pass; NULL
+ *   when it is not needed.
  */
 emu_status_t emu_linear_act_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t N, int64_t K, const float *X,
                                 int64_t ldx, const float *W, int64_t ldw, const float *bias, const float *residual,
-                                int64_t ldr, float *Z, int64_t ldz, float *Y, int64_t ldy, emu_stream_t stream);
+                                int64_t ldr, float *D, int64_t ldd, float *Y, int64_t ldy, emu_stream_t stream);
 
 /*
- * emu_linear_act_bwd -- dZ = dY * a'(Z); dX = dZ W, dW = dZ^T X, dbias = sum
- *   over rows of dZ.  (The residual's gradient is dY itself.)  dZ (M x N) is
- *   written too.  EMU_ACT_NONE needs neither Z nor dZ (NULL).  dX, dW and
- *   dbias may each be NULL (not wanted).
+ * emu_linear_act_bwd -- dZ = dY * D (M x N, written too); dX = dZ W, dW = dZ^T X,
+ *   dbias = sum over rows of dZ.  (The residual's gradient is dY itself.)  D
+ *   NULL: no activation, dZ = dY (dZ is not written and may be NULL).  dX, dW
+ *   and dbias may each be NULL (not wanted).
  */
-emu_status_t emu_linear_act_bwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t N, int64_t K, const float *dY,
-                                int64_t lddy, const float *X, int64_t ldx, const float *W, int64_t ldw, const float *Z,
-                                int64_t ldz, float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW, int64_t lddw,
+emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float *dY, int64_t lddy,
+                                const float *X, int64_t ldx, const float *W, int64_t ldw, const float *D, int64_t ldd,
+                                float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW, int64_t lddw,
                                 float *dbias, emu_stream_t stream);
 
 /*
- * emu_gated_fwd -- Z = [G | U] = X W^T + bias, H = a(G) * U.
+ * emu_gated_fwd -- H = a(G) * U with [G | U] = X W^T + bias.
  *   W: 2F x K (the gate's F rows, then the up projection's), bias: 2F (may be
- *   NULL), Z: M x 2F, H: M x F.
+ *   NULL), H: M x F.  D (M x 2F) receives [U a'(G) | a(G)], the factors of the
+ *   backward pass; NULL when they are not needed, which the modes BF16X9 and
+ *   TF32X3 allow (the others compute H by way of it).
  */
 emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F, int64_t K, const float *X, int64_t ldx,
-                           const float *W, int64_t ldw, const float *bias, float *Z, int64_t ldz, float *H, int64_t ldh,
+                           const float *W, int64_t ldw, const float *bias, float *D, int64_t ldd, float *H, int64_t ldh,
                            emu_stream_t stream);
 
 /*
- * emu_gated_bwd -- dZ = [dH * U * a'(G) | dH * a(G)] (M x 2F, written too);
- *   dX = dZ W, dW = dZ^T X (2F x K), dbias = sum over rows of dZ (2F).  dX, dW
- *   and dbias may each be NULL (not wanted).
+ * emu_gated_bwd -- dZ = [dH | dH] * D (M x 2F, written too); dX = dZ W,
+ *   dW = dZ^T X (2F x K), dbias = sum over rows of dZ (2F).  dX, dW and dbias
+ *   may each be NULL (not wanted).
  */
-emu_status_t emu_gated_bwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F, int64_t K, const float *dH,
-                           int64_t lddh, const float *X, int64_t ldx, const float *W, int64_t ldw, const float *Z,
-                           int64_t ldz, float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW, int64_t lddw,
-                           float *dbias, emu_stream_t stream);
+emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, const float *dH, int64_t lddh,
+                           const float *X, int64_t ldx, const float *W, int64_t ldw, const float *D, int64_t ldd,
+                           float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW, int64_t lddw, float *dbias,
+                           emu_stream_t stream);
 
 /*
  * emu_gated_ffn_fwd -- the whole block: emu_gated_fwd, then Y = H W_out^T +
  *   b_out + residual.  X: M x K, W_in: 2F x K, W_out: N x F, Y and residual
- *   (may be NULL): M x N; Z and H as in emu_gated_fwd.
+ *   (may be NULL): M x N; D and H as in emu_gated_fwd.
  */
 emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t K, int64_t F, int64_t N,
                                const float *X, int64_t ldx, const float *W_in, int64_t ldwi, const float *b_in,
                                const float *W_out, int64_t ldwo, const float *b_out, const float *residual, int64_t ldr,
-                               float *Z, int64_t ldz, float *H, int64_t ldh, float *Y, int64_t ldy,
+                               float *D, int64_t ldd, float *H, int64_t ldh, float *Y, int64_t ldy,
                                emu_stream_t stream);
 
 /*
- * emu_gated_ffn_bwd -- its gradients, from Z and H of the forward pass:
+ * emu_gated_ffn_bwd -- its gradients, from D and H of the forward pass:
  *   dW_out = dY^T H, db_out = sum over rows of dY, dH = dY W_out, then
  *   emu_gated_bwd's dZ, dX, dW_in and db_in.  dX, dW_in, db_in, dW_out and
  *   db_out may each be NULL (not wanted).
  */
-emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t K, int64_t F, int64_t N,
-                               const float *dY, int64_t lddy, const float *X, int64_t ldx, const float *W_in,
-                               int64_t ldwi, const float *W_out, int64_t ldwo, const float *Z, int64_t ldz,
-                               const float *H, int64_t ldh, float *dZ, int64_t lddz, float *dX, int64_t lddx,
-                               float *dW_in, int64_t lddwi, float *db_in, float *dW_out, int64_t lddwo, float *db_out,
-                               emu_stream_t stream);
+emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F, int64_t N, const float *dY,
+                               int64_t lddy, const float *X, int64_t ldx, const float *W_in, int64_t ldwi,
+                               const float *W_out, int64_t ldwo, const float *D, int64_t ldd, const float *H, int64_t ldh,
+                               float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW_in, int64_t lddwi,
+                               float *db_in, float *dW_out, int64_t lddwo, float *db_out, emu_stream_t stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *emu_status_string(emu_status_t s);

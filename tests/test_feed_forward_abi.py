@@ -53,10 +53,10 @@ def test_host_checks_answer_without_a_device(ff):
     assert la(mode=9) == INVALID and la(act=5) == INVALID and la(act=-1) == INVALID and la(ldy=3) == INVALID
     assert la(r=p, ldr=2) == INVALID and la(X=None) == INVALID and la(M=0) == 0
     assert la(X=p + 4) == NOT_SUPPORTED and la(ldx=6) == NOT_SUPPORTED and la(Y=p + 4) == NOT_SUPPORTED
-    bw = lambda act=1, Z=p, dZ=p, dX=p, lddx=4: fn("emu_linear_act_bwd", 0, act, 40, 4, 4, p, 4, p, 4, p, 4, Z, 4, dZ, 4, dX,
-                                                   lddx, p, 4, p)
-    assert bw(Z=None) == INVALID and bw(dZ=None) == INVALID and bw(lddx=2) == INVALID and bw(lddx=6) == NOT_SUPPORTED
+    bw = lambda D=p, dZ=p, dX=p, lddx=4: fn("emu_linear_act_bwd", 0, 40, 4, 4, p, 4, p, 4, p, 4, D, 4, dZ, 4, dX, lddx, p, 4, p)
+    assert bw(dZ=None) == INVALID and bw(lddx=2) == INVALID and bw(lddx=6) == NOT_SUPPORTED
     gf = lambda F=4, H=p, ldh=4, ldw=4: fn("emu_gated_fwd", 0, 4, 40, F, 4, p, 4, p, ldw, p, p, 8, H, ldh)
+    assert fn("emu_gated_fwd", 4, 4, 40, 4, 4, p, 4, p, 4, p, None, 0, p, 4) == INVALID    # fp32 works by way of D
     assert gf(H=None) == INVALID and gf(ldh=3) == INVALID and gf(ldw=3) == INVALID and gf(F=2 ** 30) == NOT_SUPPORTED
     assert gf(F=0) == 0
 

@@ -110,22 +110,21 @@ def test_layer_norm_many_rows_and_repeatable():
 
 
 # ------------------------------------------------------------- linear_act --
-def linear_act_reference(x, w, b, act, r, dy, mode, z_gpu=None):
+def linear_act_reference(x, w, b, act, r, dy, mode, d_gpu=None):
     z = R.product(x, w.T, mode, b)
     y = R.act_value(act, z) if act != "none" else z
     if r is not None:
         y = y + r
-    if dy is None:
-        return y, z
     if act == "none":
-        dz = V(dy)
+        d = V(np.ones_like(z.val))
     else:
         d = R.act_grad(act, z)
-        if act == "relu":  # the derivative jumps: where Z is within its error of 0, the GPU's own sign stands
-            close = np.abs(z.val) <= z.err
-            d = V(np.where(close, z_gpu > 0, z.val > 0))
-        dz = V(dy) * d
-    return y, z, R.product(dz, w, mode), R.product(dz.T, x, mode), R.column_sum(dz)
+        if act == "relu" and d_gpu is not None:  # the derivative jumps: where Z is within its error of 0, the GPU's own sign stands
+            d = V(np.where(np.abs(z.val) <= z.err, d_gpu > 0, z.val > 0))
+    if dy is None:
+        return y, d
+    dz = V(dy) * d
+    return y, d, R.product(dz, w, mode), R.product(dz.T, x, mode), R.column_sum(dz)
 
 
 LINEAR_SHAPES = [(1, 1, 1), (1, 300, 64), (1, 64, 1024), (2, 129, 33), (5, 96, 100), (8, 257, 260), (9, 40, 7),
@@ -144,13 +143,15 @@ def test_linear_act(M, N, K, act, mode):
     r = f32(rng, M, N) if (M + K) % 2 else None
     dy = f32(rng, M, N)
     y0 = emu.linear_act_fwd(dev(x), dev(w), dev(b), act=act, residual=dev(r), mode=mode)
-    y, z = emu.linear_act_fwd(dev(x), dev(w), dev(b), act=act, residual=dev(r), mode=mode, save=True)
-    dx, dw, db = emu.linear_act_bwd(dev(dy), dev(x), dev(w), z, act=act, mode=mode)
+    y, d = emu.linear_act_fwd(dev(x), dev(w), dev(b), act=act, residual=dev(r), mode=mode, save=True)
+    dx, dw, db = emu.linear_act_bwd(dev(dy), dev(x), dev(w), d, act=act, mode=mode)
     done()
-    want = linear_act_reference(x, w, b, act, r, dy, mode, host(z))
+    assert (d is None) == (act == "none")
+    want = linear_act_reference(x, w, b, act, r, dy, mode, None if d is None else host(d))
     want[0].check(host(y0), "Y")
-    for got, v, name in zip((y, z, dx, dw, db), want, ("Y, saving Z", "Z", "dX", "dW", "dbias")):
-        v.check(host(got), name)
+    for got, v, name in zip((y, d, dx, dw, db), want, ("Y, saving D", "D", "dX", "dW", "dbias")):
+        if got is not None:
+            v.check(host(got), name)
 
 
 @pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
@@ -162,13 +163,13 @@ def test_linear_act_every_plan(M, N, K, mode):
     import fp32_emulated_gemm_gb300 as emu
     rng = rng_of("plans", M, N, K)
     x, w, b, r = f32(rng, M, K), f32(rng, N, K, std=K ** -0.5), f32(rng, N, std=0.1), f32(rng, M, N)
-    y, z = emu.linear_act_fwd(dev(x), dev(w), dev(b), act="gelu", residual=dev(r), mode=mode, save=True)
+    y, d = emu.linear_act_fwd(dev(x), dev(w), dev(b), act="gelu", residual=dev(r), mode=mode, save=True)
     y0 = emu.linear_act_fwd(dev(x), dev(w), dev(b), act="gelu", residual=dev(r), mode=mode)
     done()
     rows = np.unique(np.concatenate([np.arange(0, M, 37), np.arange(max(0, M - 40), M)]))
-    wy, wz = linear_act_reference(x[rows], w, b, "gelu", r[rows], None, mode)
+    wy, wd = linear_act_reference(x[rows], w, b, "gelu", r[rows], None, mode)
     wy.check(host(y)[rows], "Y")
-    wz.check(host(z)[rows], "Z")
+    wd.check(host(d)[rows], "D")
     assert np.array_equal(host(y), host(y0))
 
 
@@ -178,29 +179,35 @@ def test_linear_act_and_block_in_the_other_modes(mode):
     rng = rng_of("other modes")
     M, N, K, F = 150, 140, 100, 60
     x, w, b, dy = f32(rng, M, K), f32(rng, N, K, std=0.1), f32(rng, N), f32(rng, M, N)
-    y, z = emu.linear_act_fwd(dev(x), dev(w), dev(b), act="silu", mode=mode, save=True)
-    g = emu.linear_act_bwd(dev(dy), dev(x), dev(w), z, act="silu", mode=mode)
+    y, d = emu.linear_act_fwd(dev(x), dev(w), dev(b), act="silu", mode=mode, save=True)
+    g = emu.linear_act_bwd(dev(dy), dev(x), dev(w), d, act="silu", mode=mode)
     done()
-    for got, v, name in zip((y, z, *g), linear_act_reference(x, w, b, "silu", None, dy, mode), ("Y", "Z", "dX", "dW", "db")):
+    for got, v, name in zip((y, d, *g), linear_act_reference(x, w, b, "silu", None, dy, mode), ("Y", "D", "dX", "dW", "db")):
         v.check(host(got), name)
     check_ffn(rng, 70, 44, F, 52, "silu", mode, residual=True)
 
 
 # ----------------------------------------------------------- gated blocks --
-def gated_reference(x, w, b, act, mode):
+def beside(p, q):
+    return V(np.concatenate([p.val, q.val], 1), np.concatenate([p.err, q.err], 1))
+
+
+def gated_reference(x, w, b, act, mode, d_gpu=None):
+    """(H, D)"""
     F = w.shape[0] // 2
     z = R.product(x, w.T, mode, b)
     g, u = z.cols(0, F), z.cols(F, 2 * F)
-    return R.act_value(act, g) * u, z, g, u
+    slope = R.act_grad(act, g)
+    if act == "relu":  # (as in linear_act_reference; U = 0 leaves the sign open, and the product zero)
+        on = g.val > 0 if d_gpu is None else np.where(np.abs(g.val) <= g.err, d_gpu[:, :F] != 0, g.val > 0)
+        slope = V(on.astype(np.float64))
+    a = R.act_value(act, g)
+    return a * u, beside(u * slope, a)
 
 
-def gated_grads(dh, x, w, act, mode, z, g, u, z_gpu):
+def gated_grads(dh, x, w, mode, d):
     F = w.shape[0] // 2
-    d = R.act_grad(act, g)
-    if act == "relu":
-        d = V(np.where(np.abs(g.val) <= g.err, z_gpu[:, :F] > 0, g.val > 0))
-    dg, du = dh * u * d, dh * R.act_value(act, g)
-    dz = V(np.concatenate([dg.val, du.val], 1), np.concatenate([dg.err, du.err], 1))
+    dz = beside(dh * d.cols(0, F), dh * d.cols(F, 2 * F))
     return R.product(dz, w, mode), R.product(dz.T, x, mode), R.column_sum(dz)
 
 
@@ -212,19 +219,19 @@ def check_ffn(rng, M, K, F, N, act, mode, residual, bias=True, lay=None):
     r, dy = f32(rng, M, N) if residual else None, f32(rng, M, N)
     args = (mat(x), mat(wi), dev(bi), mat(wo), dev(bo))
     y0 = emu.gated_ffn_fwd(*args, act=act, residual=None if r is None else mat(r), mode=mode)
-    y, z, h = emu.gated_ffn_fwd(*args, act=act, residual=None if r is None else mat(r), mode=mode, save=True)
-    grads = emu.gated_ffn_bwd(mat(dy), args[0], args[1], args[3], z, h, act=act, mode=mode)
+    y, d, h = emu.gated_ffn_fwd(*args, act=act, residual=None if r is None else mat(r), mode=mode, save=True)
+    grads = emu.gated_ffn_bwd(mat(dy), args[0], args[1], args[3], d, h, act=act, mode=mode)
     done()
-    wh, wz, g, u = gated_reference(x, wi, bi, act, mode)
+    wh, wd = gated_reference(x, wi, bi, act, mode, host(d))
     wy = R.product(wh, wo.T, mode, bo)
     if r is not None:
         wy = wy + r
     dh = R.product(dy, wo, mode)
-    dx, dwi, dbi = gated_grads(dh, x, wi, act, mode, wz, g, u, host(z))
+    dx, dwi, dbi = gated_grads(dh, x, wi, mode, wd)
     wy.check(host(y0), "Y")
-    want = (wy, wz, wh, dx, dwi, dbi, R.product(V(dy).T, wh, mode), R.column_sum(dy))
-    names = ("Y, saving", "Z", "H", "dX", "dW_in", "db_in", "dW_out", "db_out")
-    for got, v, name in zip((y, z, h, *grads), want, names):
+    want = (wy, wd, wh, dx, dwi, dbi, R.product(V(dy).T, wh, mode), R.column_sum(dy))
+    names = ("Y, saving", "D", "H", "dX", "dW_in", "db_in", "dW_out", "db_out")
+    for got, v, name in zip((y, d, h, *grads), want, names):
         v.check(host(got), name)
 
 
@@ -245,16 +252,16 @@ def test_gated_every_plan(M, K, F, mode):
     import fp32_emulated_gemm_gb300 as emu
     rng = rng_of("gated plans", M, K, F)
     x, w, b, dh = f32(rng, M, K), f32(rng, 2 * F, K, std=K ** -0.5), f32(rng, 2 * F, std=0.1), f32(rng, M, F)
-    h, z = emu.gated_fwd(dev(x), dev(w), dev(b), mode=mode, save=True)
+    h, d = emu.gated_fwd(dev(x), dev(w), dev(b), mode=mode, save=True)
     h0 = emu.gated_fwd(dev(x), dev(w), dev(b), mode=mode)
-    dx, dw, db = emu.gated_bwd(dev(dh), dev(x), dev(w), z, mode=mode)
+    dx, dw, db = emu.gated_bwd(dev(dh), dev(x), dev(w), d, mode=mode)
     done()
     assert np.array_equal(host(h), host(h0))
     rows = np.unique(np.concatenate([np.arange(0, M, 29), np.arange(max(0, M - 40), M)]))
-    wh, wz, g, u = gated_reference(x, w, b, "silu", mode)
+    wh, wd = gated_reference(x, w, b, "silu", mode)
     V(wh.val[rows], wh.err[rows]).check(host(h)[rows], "H")
-    V(wz.val[rows], wz.err[rows]).check(host(z)[rows], "Z")
-    for got, v, name in zip((dx, dw, db), gated_grads(V(dh), x, w, "silu", mode, wz, g, u, None), ("dX", "dW", "db")):
+    V(wd.val[rows], wd.err[rows]).check(host(d)[rows], "D")
+    for got, v, name in zip((dx, dw, db), gated_grads(V(dh), x, w, mode, wd), ("dX", "dW", "db")):
         v.check(host(got), name)
 
 
@@ -340,11 +347,11 @@ def test_gated_ffn_gradient_against_differences(act):
     M, K, F, N = 10, 24, 36, 20
     x, wi, bi, wo, bo, c = (f32(rng, M, K), f32(rng, 2 * F, K, std=0.3), f32(rng, 2 * F), f32(rng, N, F, std=0.3),
                             f32(rng, N), f32(rng, M, N))
-    y, z, h = emu.gated_ffn_fwd(*(dev(a) for a in (x, wi, bi, wo, bo)), act=act, save=True)
-    got = [host(t).astype(np.float64) for t in emu.gated_ffn_bwd(dev(c), dev(x), dev(wi), dev(wo), z, h, act=act)]
-    wh, wz, g, u = gated_reference(x, wi, bi, act, "bf16x9")
+    y, d, h = emu.gated_ffn_fwd(*(dev(a) for a in (x, wi, bi, wo, bo)), act=act, save=True)
+    got = [host(t).astype(np.float64) for t in emu.gated_ffn_bwd(dev(c), dev(x), dev(wi), dev(wo), d, h, act=act)]
+    wh, wd = gated_reference(x, wi, bi, act, "bf16x9")
     dh = R.product(c, wo, "bf16x9")
-    want = (*gated_grads(dh, x, wi, act, "bf16x9", wz, g, u, None), R.product(V(c).T, wh, "bf16x9"), R.column_sum(c))
+    want = (*gated_grads(dh, x, wi, "bf16x9", wd), R.product(V(c).T, wh, "bf16x9"), R.column_sum(c))
 
     def f(x, wi, bi, wo, bo):
         z = x @ wi.T + bi
