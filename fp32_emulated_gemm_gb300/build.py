@@ -9,9 +9,9 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("emu_gemm.cu", "feed_forward.cu", "gemm_act.cu", "gemm_gated.cu",
+SOURCES = [os.path.join(CSRC, f) for f in ("emu_gemm.cu", "feed_forward.cu", "few_rows.cu", "gemm_act.cu", "gemm_gated.cu",
                                               "gemm_gated_bwd.cu", "layer_norm.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("activation.cuh", "emu_kernel.cuh", "gemm_epi.h", "internal.h",
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("activation.cuh", "emu_kernel.cuh", "few_rows.h", "gemm_epi.h", "internal.h",
                                                   "ptx.cuh", "row_ops.cuh")] + [
     os.path.join(os.path.dirname(HERE), "include", "emu_gemm.h")]
 LIB = os.path.join(HERE, "libemu_gemm.so")

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "activation.cuh"
+#include "few_rows.h"
 #include "internal.h"
 #include "row_ops.cuh"
 
@@ -171,12 +172,23 @@ Gemm weight_product(int64_t M, int64_t N, int64_t K, const float* dZ, int64_t ld
     return {true, true, N, K, M, dZ, lddz, X, ldx, 0.0f, dW, lddw, nullptr};
 }
 
+// A few rows go to the CUDA cores in the modes whose bound that meets (FP32 mode
+// keeps its one chain per output, the comparators their errors).
+bool few_rows(emu_mode_t mode, int64_t M, int64_t N, int64_t K) { return fused_mode(mode) && few_rows_fit(M, N, K); }
+
 // D and the residual of a product's epilogue: 16-byte rows, like C.
 bool aligned_rows(const float* p, int64_t ld) { return !p || vec4_ok(p, ld); }
 
 emu_status_t linear_act_fwd(emu_mode_t mode, int act, int64_t M, int64_t N, int64_t K, const float* X, int64_t ldx,
                             const float* W, int64_t ldw, const float* bias, const float* R, int64_t ldr, float* D,
-                            int64_t ldd, float* Y, int64_t ldy, const DeviceCtx& dev, cudaStream_t s, bool check) {
+                            int64_t ldd, float* Y, int64_t ldy, const DeviceCtx& dev, cudaStream_t s, bool check,
+                            bool after_own = false) {
+    if (few_rows(mode, M, N, K)) {
+        if (K > 0 && (!X || !W || ldx < K || ldw < K)) return EMU_STATUS_INVALID_VALUE;
+        if (check) return EMU_STATUS_SUCCESS;
+        return launched(launch_few_rows({(int)M, N, K, X, ldx, W, ldw, bias, R, ldr, D, ldd, Y, ldy, act_params(act)}, false,
+                                        after_own, dev.sm_count, s));
+    }
     if (!aligned_rows(D, ldd) || !aligned_rows(R, ldr)) return EMU_STATUS_NOT_SUPPORTED;
     Gemm g = forward_product(M, N, K, X, ldx, W, ldw, bias, Y, ldy);
     const Fused f{FUSED_ACT, act, R, ldr, D, ldd, nullptr};
@@ -192,6 +204,12 @@ bool gated_needs_d(emu_mode_t mode) { return !fused_mode(mode); }
 emu_status_t gated_fwd(emu_mode_t mode, int act, int64_t M, int64_t F, int64_t K, const float* X, int64_t ldx,
                        const float* W, int64_t ldw, const float* bias, float* D, int64_t ldd, float* H, int64_t ldh,
                        const DeviceCtx& dev, cudaStream_t s, bool check) {
+    if (few_rows(mode, M, 2 * F, K)) {
+        if (K > 0 && (!X || !W || ldx < K || ldw < K)) return EMU_STATUS_INVALID_VALUE;
+        if (check) return EMU_STATUS_SUCCESS;
+        return launched(launch_few_rows({(int)M, F, K, X, ldx, W, ldw, bias, nullptr, 0, D, ldd, H, ldh, act_params(act)},
+                                        true, false, dev.sm_count, s));
+    }
     if (!aligned_rows(D, ldd)) return EMU_STATUS_NOT_SUPPORTED;
     if (fused_mode(mode) && K > 0) {
         Gemm g = forward_product(M, F, K, X, ldx, W, ldw, bias, H, ldh);
@@ -215,6 +233,8 @@ emu_status_t gated_fwd(emu_mode_t mode, int act, int64_t M, int64_t F, int64_t K
 using namespace emu;
 
 extern "C" {
+
+int emu_few_rows_query(int64_t M, int64_t N, int64_t K) { return M >= 0 && N >= 0 && K >= 0 && few_rows_fit(M, N, K) ? 1 : 0; }
 
 emu_status_t emu_linear_act_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t N, int64_t K, const float* X,
                                 int64_t ldx, const float* W, int64_t ldw, const float* bias, const float* residual,
@@ -307,7 +327,7 @@ emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_
         if (F > 0) EMU_TRY(gated_fwd(mode, act, M, F, K, X, ldx, W_in, ldwi, b_in, D, ldd, H, ldh, dev, s, check));
         if (N > 0)
             EMU_TRY(linear_act_fwd(mode, ACT_NONE, M, N, F, H, ldh, W_out, ldwo, b_out, residual, ldr, nullptr, 0, Y, ldy,
-                                   dev, s, check));
+                                   dev, s, check, F > 0 && few_rows(mode, M, 2 * F, K)));
         if (check) EMU_TRY(current_device(&dev));
     }
     return EMU_STATUS_SUCCESS;

@@ -117,6 +117,20 @@ def _operand(t, name, shape=None):
     return q
 
 
+def few_rows(M, N, K):
+    """Whether a forward pass of M rows through N columns of weights runs in
+    the library's few-row form (emu_few_rows_query), which takes matrices of
+    any alignment."""
+    return M <= 1024 and M * N * K <= 50_000_000
+
+
+def _forward_matrix(X, W, mode):
+    """How a forward pass X W^T wants its matrices: _rows or _operand."""
+    if mode in _FUSED and X.dim() == 2 and W.dim() == 2 and few_rows(X.shape[0], *W.shape):
+        return _rows
+    return _operand
+
+
 def _pad4(n):
     return (n + 3) // 4 * 4
 
@@ -222,19 +236,21 @@ def layer_norm_bwd(dY, X, weight, mean, rstd, *, add=None, need_input=True, need
 def linear_act_fwd(X, W, bias=None, *, act="none", residual=None, mode="bf16x9", save=False, out=None):
     """Y = act(Z) + residual with Z = X W^T + bias (X [M,K], W [N,K]); with
     `save` (Y, D) for linear_act_bwd, D = act'(Z) (None for act "none")."""
-    X, px, ldx = _operand(X, "X")
-    W, pw, ldw = _operand(W, "W")
+    mode = _mode(mode)
+    matrix = _forward_matrix(X, W, mode)
+    X, px, ldx = matrix(X, "X")
+    W, pw, ldw = matrix(W, "W")
     M, K = X.shape
     N, Kw = W.shape
     if Kw != K:
         raise ValueError("inner dimensions differ")
     a = _act(act)
     bias, pb = _vector(bias, "bias", N)
-    residual, pr, ldr = _NONE if residual is None else _operand(residual, "residual", (M, N))
+    residual, pr, ldr = _NONE if residual is None else matrix(residual, "residual", (M, N))
     device = X.device
     Y, py, ldy = _result(out, (M, N), device, "out")
     D, pd, ldd = _new(M, N, device) if save and a != EMU_ACT_NONE else _NONE
-    _check(_fn("emu_linear_act_fwd")(_mode(mode), a, M, N, K, px, ldx, pw, ldw, pb, pr, ldr, pd, ldd, py, ldy,
+    _check(_fn("emu_linear_act_fwd")(mode, a, M, N, K, px, ldx, pw, ldw, pb, pr, ldr, pd, ldd, py, ldy,
                                      _stream_of("linear_act_fwd", X, W, bias, residual, Y)), "emu_linear_act_fwd")
     return (Y, D) if save else Y
 
@@ -281,12 +297,13 @@ def gated_fwd(X, W, bias=None, *, act="silu", mode="bf16x9", save=False):
     """H = act(G) * U with [G | U] = X W^T + bias (X [M,K]; W [2F,K]: the
     gate's rows, then the up projection's); with `save` (H, D) for
     gated_bwd, D = [U act'(G) | act(G)]."""
-    X, px, ldx = _operand(X, "X")
-    W, pw, ldw = _operand(W, "W")
+    mode = _mode(mode)
+    matrix = _forward_matrix(X, W, mode)
+    X, px, ldx = matrix(X, "X")
+    W, pw, ldw = matrix(W, "W")
     M, K, F = _gated_shapes(X, W)
     bias, pb = _vector(bias, "bias", 2 * F)
     H, ph, ldh = _new(M, F, X.device)
-    mode = _mode(mode)
     D, pd, ldd = _new(M, 2 * F, X.device) if save or mode not in _FUSED else _NONE
     _check(_fn("emu_gated_fwd")(mode, _act(act), M, F, K, px, ldx, pw, ldw, pb, pd, ldd, ph, ldh,
                                 _stream_of("gated_fwd", X, W, bias)), "emu_gated_fwd")
@@ -323,17 +340,19 @@ def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mod
     """Y = H W_out^T + b_out + residual with H = gated_fwd(X, W_in, b_in)
     (X [M,K], W_in [2F,K], W_out [N,F]; the biases and the residual may be
     None); with `save` (Y, D, H) for gated_ffn_bwd."""
-    X, px, ldx = _operand(X, "X")
-    W_in, pwi, ldwi = _operand(W_in, "W_in")
-    W_out, pwo, ldwo = _operand(W_out, "W_out")
+    mode = _mode(mode)
+    matrix = _forward_matrix(X, W_in, mode)
+    X, px, ldx = matrix(X, "X")
+    W_in, pwi, ldwi = matrix(W_in, "W_in")
+    matrix = _forward_matrix(X, W_out, mode)  # (as many rows go through W_out)
+    W_out, pwo, ldwo = matrix(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
     b_in, pbi = _vector(b_in, "b_in", 2 * F)
     b_out, pbo = _vector(b_out, "b_out", N)
-    residual, pr, ldr = _NONE if residual is None else _operand(residual, "residual", (M, N))
+    residual, pr, ldr = _NONE if residual is None else matrix(residual, "residual", (M, N))
     device = X.device
     Y, py, ldy = _result(out, (M, N), device, "out")
     H, ph, ldh = _new(M, F, device)
-    mode = _mode(mode)
     D, pd, ldd = _new(M, 2 * F, device) if save or mode not in _FUSED else _NONE
     s = _stream_of("gated_ffn_fwd", X, W_in, b_in, W_out, b_out, residual, Y)
     _check(_fn("emu_gated_ffn_fwd")(mode, _act(act), M, K, F, N, px, ldx, pwi, ldwi, pbi, pwo, ldwo, pbo, pr, ldr,

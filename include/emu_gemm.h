@@ -209,6 +209,11 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  *   EMU_STATUS_NOT_SUPPORTED.  Widths are free.  emu_layer_norm_* takes any
  *   alignment of whole words.
  * Outputs must not overlap inputs or one another.
+ * Few rows: a forward pass of at most 1,024 rows and 50 million multiplications
+ *   (M N K, both halves of a gated weight counted) in the modes BF16X9 and
+ *   TF32X3 runs on the CUDA cores in FP32, within the modes' bounds, and takes
+ *   matrices and biases of any alignment of whole words
+ *   (emu_few_rows_query, host only, says 1 or 0).
  * Sizes: M == 0 writes nothing but zero sums (weight and bias gradients);
  *   K == 0 leaves the bias.
  * Buffers: the sums over rows take a buffer of partial sums from the
@@ -216,6 +221,8 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  * Repeatability: all sums are added in an order fixed by the sizes and the
  *   device; no atomics.
  */
+int emu_few_rows_query(int64_t M, int64_t N, int64_t K);
+
 typedef enum {
     EMU_ACT_NONE = 0,
     EMU_ACT_RELU = 1,

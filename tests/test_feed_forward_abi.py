@@ -48,17 +48,25 @@ def test_host_checks_answer_without_a_device(ff):
     assert ln(N=2 ** 31) == NOT_SUPPORTED and ln(M=0) == 0 and ln(eps=float("nan")) == INVALID
     lb = lambda N=4, dX=p, lddx=4, add=None: fn("emu_layer_norm_bwd", 4, N, p, 4, p, 4, p, p, p, add, 4, dX, lddx, p, p)
     assert lb(lddx=3) == INVALID and lb(N=-1) == INVALID and lb(dX=None, add=p) == INVALID and lb(N=0) == 0
-    la = lambda mode=0, act=1, M=40, X=p, ldx=4, Y=p, ldy=4, r=None, ldr=0: fn(
+    la = lambda mode=0, act=1, M=1040, X=p, ldx=4, Y=p, ldy=4, r=None, ldr=0: fn(
         "emu_linear_act_fwd", mode, act, M, 4, 4, X, ldx, p, 4, p, r, ldr, None, 0, Y, ldy)
     assert la(mode=9) == INVALID and la(act=5) == INVALID and la(act=-1) == INVALID and la(ldy=3) == INVALID
     assert la(r=p, ldr=2) == INVALID and la(X=None) == INVALID and la(M=0) == 0
     assert la(X=p + 4) == NOT_SUPPORTED and la(ldx=6) == NOT_SUPPORTED and la(Y=p + 4) == NOT_SUPPORTED
-    bw = lambda D=p, dZ=p, dX=p, lddx=4: fn("emu_linear_act_bwd", 0, 40, 4, 4, p, 4, p, 4, p, 4, D, 4, dZ, 4, dX, lddx, p, 4, p)
+    bw = lambda D=p, dZ=p, dX=p, lddx=4: fn("emu_linear_act_bwd", 0, 1040, 4, 4, p, 4, p, 4, p, 4, D, 4, dZ, 4, dX, lddx, p, 4, p)
     assert bw(dZ=None) == INVALID and bw(lddx=2) == INVALID and bw(lddx=6) == NOT_SUPPORTED
-    gf = lambda F=4, H=p, ldh=4, ldw=4: fn("emu_gated_fwd", 0, 4, 40, F, 4, p, 4, p, ldw, p, p, 8, H, ldh)
+    gf = lambda F=4, H=p, ldh=4, ldw=4: fn("emu_gated_fwd", 0, 4, 1040, F, 4, p, 4, p, ldw, p, p, 8, H, ldh)
     assert fn("emu_gated_fwd", 4, 4, 40, 4, 4, p, 4, p, 4, p, None, 0, p, 4) == INVALID    # fp32 works by way of D
     assert gf(H=None) == INVALID and gf(ldh=3) == INVALID and gf(ldw=3) == INVALID and gf(F=2 ** 30) == NOT_SUPPORTED
     assert gf(F=0) == 0
+
+
+def test_few_row_rule_is_the_librarys(ff):
+    q = emu.load().emu_few_rows_query
+    q.argtypes = [ctypes.c_int64] * 3
+    for M, N, K in ((1, 1, 1), (1024, 1, 1), (1025, 1, 1), (0, 4, 4), (1024, 128, 381), (1024, 128, 382), (1, 50_000_000, 1),
+                    (1, 50_000_001, 1), (64, 1024, 762), (64, 1024, 763), (1024, 2 ** 31 - 257, 2 ** 31 - 257)):
+        assert q(M, N, K) == int(ff.few_rows(M, N, K)), (M, N, K)
 
 
 def test_exports_and_lazy_names():

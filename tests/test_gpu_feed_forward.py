@@ -129,7 +129,8 @@ def linear_act_reference(x, w, b, act, r, dy, mode, d_gpu=None):
 
 LINEAR_SHAPES = [(1, 1, 1), (1, 300, 64), (1, 64, 1024), (2, 129, 33), (5, 96, 100), (8, 257, 260), (9, 40, 7),
                  (16, 512, 128), (17, 100, 36), (40, 30, 500), (300, 260, 200), (257, 1, 64), (130, 131, 37),
-                 (1100, 520, 72)]
+                 (1100, 520, 72), (1025, 1, 1), (1030, 129, 33), (1100, 257, 260), (1281, 40, 7), (1025, 131, 37),
+                 (63, 1024, 770), (64, 1024, 770)]
 
 
 @pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
@@ -177,7 +178,7 @@ def test_linear_act_every_plan(M, N, K, mode):
 def test_linear_act_and_block_in_the_other_modes(mode):
     import fp32_emulated_gemm_gb300 as emu
     rng = rng_of("other modes")
-    M, N, K, F = 150, 140, 100, 60
+    M, N, K, F = 150, 140, 100, 60  # (these modes have no few-row form)
     x, w, b, dy = f32(rng, M, K), f32(rng, N, K, std=0.1), f32(rng, N), f32(rng, M, N)
     y, d = emu.linear_act_fwd(dev(x), dev(w), dev(b), act="silu", mode=mode, save=True)
     g = emu.linear_act_bwd(dev(dy), dev(x), dev(w), d, act="silu", mode=mode)
@@ -236,7 +237,8 @@ def check_ffn(rng, M, K, F, N, act, mode, residual, bias=True, lay=None):
 
 
 FFN_SHAPES = [(1, 1, 1, 1), (1, 64, 100, 64), (1, 1024, 300, 256), (3, 33, 65, 31), (8, 128, 256, 128), (9, 20, 20, 20),
-              (20, 100, 130, 60), (70, 40, 129, 36), (300, 72, 260, 72), (1030, 64, 150, 32), (261, 37, 41, 43)]
+              (20, 100, 130, 60), (70, 40, 129, 36), (300, 72, 260, 72), (1030, 64, 150, 32), (261, 37, 41, 43), (1025, 1, 1, 1),
+          (1030, 33, 65, 31), (1100, 100, 130, 60), (1281, 20, 20, 20), (1100, 72, 260, 72), (1025, 37, 41, 43)]
 
 
 @pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
@@ -282,7 +284,7 @@ def test_large_preactivations_stay_finite(act):
     n = z.size
     x, w = np.ones((1, 4), np.float32), np.zeros((n, 4), np.float32)
     dy = np.ones((1, n), np.float32)
-    for rows in (1, 40):                       # the few-row form and the tiles
+    for rows in (1, 1040):                       # the few-row form and the tiles
         xr, dyr = np.repeat(x, rows, 0), np.repeat(dy, rows, 0)
         y, zz = emu.linear_act_fwd(dev(xr), dev(w), dev(z), act=act, save=True)
         dx, dw, db = emu.linear_act_bwd(dev(dyr), dev(xr), dev(w), zz, act=act)
@@ -400,10 +402,10 @@ def test_layouts(how):
     import torch
     import fp32_emulated_gemm_gb300 as emu
     lay = lambda a: strided(a, how)
-    for M, K, F, N in ((1, 32, 24, 40), (5, 32, 24, 40), (4, 35, 23, 41), (70, 36, 24, 44), (70, 37, 23, 45)):
+    for M, K, F, N in ((1, 32, 24, 40), (5, 32, 24, 40), (4, 35, 23, 41), (70, 37, 23, 45), (1070, 36, 24, 44), (1070, 37, 23, 45)):
         check_ffn(rng_of("layouts", M, K), M, K, F, N, "silu", "bf16x9", residual=True, lay=lay)
     rng = rng_of("layouts")
-    M, K, F = 70, 36, 24
+    M, K, F = 1070, 36, 24
     x, wi, dh, b = f32(rng, M, K), f32(rng, 2 * F, K), f32(rng, M, F), f32(rng, 2 * F + 1)
 
     def run(m):
@@ -427,7 +429,7 @@ def test_outputs_stay_inside_their_matrix():
     import torch
     import fp32_emulated_gemm_gb300 as emu
     rng = rng_of("guard")
-    for M, K, F, N in ((3, 20, 20, 33), (150, 40, 70, 131)):
+    for M, K, F, N in ((3, 20, 20, 33), (150, 40, 70, 131), (1150, 40, 70, 131)):
         x, w, wi, wo = f32(rng, M, K), f32(rng, N, K), f32(rng, 2 * F, K), f32(rng, N, F)
         guard = torch.full((M + 2, N + 8 - N % 4), 7.5, device=_gpu.device())
         view = guard[1:M + 1, :N]
@@ -450,7 +452,7 @@ def test_other_stream():
     import torch
     import fp32_emulated_gemm_gb300 as emu
     rng = rng_of("stream")
-    M, K, F = 600, 128, 96
+    M, K, F = 1600, 128, 96
     x, wi, wo, dy = f32(rng, M, K), f32(rng, 2 * F, K, std=0.1), f32(rng, K, F, std=0.1), f32(rng, M, K)
     args = [dev(a) for a in (x, wi, wo, dy)]
 
@@ -488,7 +490,7 @@ def test_degenerate_sizes():
     dx, dw, db = emu.layer_norm_bwd(new(0, 8), new(0, 8), new(8), mean, rstd)
     assert dx.shape == (0, 8) and not dw.any() and not db.any()
     assert emu.layer_norm_fwd(new(3, 0))[0].shape == (3, 0)
-    for M in (0, 3, 40):
+    for M in (0, 3, 1040):
         # no input features: the bias alone
         y = emu.linear_act_fwd(new(M, 0), new(5, 0), new(5) * 2, act="silu", residual=new(M, 5))
         want = 2 / (1 + np.exp(-2.0)) + 1
@@ -569,7 +571,7 @@ def test_refusals():
         emu.layer_norm_fwd(x, eps=-1.0)
     assert e.value.status == 1
     with pytest.raises(emu.EmuError) as e:      # an output off the 16-byte boundary, in a product of many rows
-        emu.linear_act_fwd(new(40, 8), w, out=new(40, 12)[:, 1:11])
+        emu.linear_act_fwd(new(1040, 8), w, out=new(1040, 12)[:, 1:11])
     assert e.value.status == 2
     done()
 
