@@ -61,6 +61,8 @@ struct Workspace {
     size_t packed_bytes = 0;
     float* reduce = nullptr;  // column-sum partials of the row-wise operators
     size_t reduce_floats = 0;
+    cudaStream_t side = nullptr;  // for a product that runs beside one on `stream`
+    cudaEvent_t fork = nullptr, join = nullptr;
 };
 constexpr int kMaxWorkspaces = 64;   // (device, stream) pairs with a workspace at once
 Workspace g_ws[kMaxWorkspaces];
@@ -557,6 +559,23 @@ emu_status_t reduce_buffer_for(int dev, cudaStream_t stream, size_t floats, floa
     return EMU_STATUS_SUCCESS;
 }
 
+// The (device, stream)'s side stream and the events that order it with `stream`.
+emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, cudaEvent_t* fork, cudaEvent_t* join) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    Workspace* w = workspace_slot(dev, stream);
+    if (!w) return EMU_STATUS_ALLOC_FAILED;
+    if (!w->join) {
+        if ((!w->side && cudaStreamCreateWithFlags(&w->side, cudaStreamNonBlocking) != cudaSuccess) ||
+            (!w->fork && cudaEventCreateWithFlags(&w->fork, cudaEventDisableTiming) != cudaSuccess) ||
+            cudaEventCreateWithFlags(&w->join, cudaEventDisableTiming) != cudaSuccess) {
+            cudaGetLastError();
+            return EMU_STATUS_ALLOC_FAILED;
+        }
+    }
+    *side = w->side; *fork = w->fork; *join = w->join;
+    return EMU_STATUS_SUCCESS;
+}
+
 // Automatic pre-split of op(B): for the TF32 modes the split is costly enough
 // that splitting op(B) once per product, ahead of it, and loading its
 // components pays as soon as several tile rows share them (measured 1.2-1.6x
@@ -802,25 +821,33 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int pairs) {
 // make_plan for a launch, remembered per host thread: a plan depends on nothing
 // but the sizes, the pairs and the overrides, and planning a chained product
 // costs 8 us on a GB300's host, as much as a small call's launches.
+struct PlanEnv {
+    int v[4];
+    bool operator==(const PlanEnv& o) const {
+        return v[0] == o.v[0] && v[1] == o.v[1] && v[2] == o.v[2] && v[3] == o.v[3];
+    }
+};
+PlanEnv plan_env() {
+    return {{env_int("EMU_SPLIT_K", 0), env_int("EMU_SPLIT_TAIL", 0), env_int("EMU_CHAIN", -1), env_int("EMU_PIPE", -1)}};
+}
+uint64_t mix(uint64_t h, uint64_t v) {
+    h = (h ^ v) * 0x9E3779B97F4A7C15ull;
+    return h ^ (h >> 29);
+}
 const Plan& plan_for(int64_t M, int64_t N, int64_t K, int pairs) {
     struct Entry {
         int64_t M = -1, N = -1, K = -1;
-        int pairs = 0, env[4] = {};
+        int pairs = 0;
+        PlanEnv env{};
         Plan plan;
     };
-    constexpr int kEntries = 32;
+    constexpr int kEntries = 64;
     static thread_local Entry entries[kEntries];
-    const int env[4] = {env_int("EMU_SPLIT_K", 0), env_int("EMU_SPLIT_TAIL", 0), env_int("EMU_CHAIN", -1),
-                        env_int("EMU_PIPE", -1)};
-    const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15ull ^ (uint64_t)N * 0xC2B2AE3D27D4EB4Full ^
-                        (uint64_t)K * 0x165667B19E3779F9ull);
-    Entry& e = entries[(h >> 40) % kEntries];
-    bool same = e.M == M && e.N == N && e.K == K && e.pairs == pairs;
-    for (int i = 0; i < 4; ++i) same = same && e.env[i] == env[i];
-    if (!same) {
+    const PlanEnv env = plan_env();
+    Entry& e = entries[(mix(mix(mix(mix(1, M), N), K), pairs) >> 40) % kEntries];
+    if (e.M != M || e.N != N || e.K != K || e.pairs != pairs || !(e.env == env)) {
         e.plan = make_plan(M, N, K, pairs);
-        e.M = M; e.N = N; e.K = K; e.pairs = pairs;
-        for (int i = 0; i < 4; ++i) e.env[i] = env[i];
+        e.M = M; e.N = N; e.K = K; e.pairs = pairs; e.env = env;
     }
     return e.plan;
 }
@@ -926,11 +953,6 @@ cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters
     return e;
 }
 
-// Core: C = alpha * op(A) op(B) + beta * C_old + bias, with C_old == C.
-// packed_b != nullptr: op(B) comes packed (emu_pack_b); B and ldb are unused.
-// fused: the epilogue is one of the EPI_* kinds instead (gated: N is F, op(B)
-// has 2F columns; the plan's tiles have 128 columns of each half).
-// check_only: the checks and the buffers' reservation, without a launch.
 // One launch of the pack kernel on `stream` (the caller checked the arguments).
 cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, int64_t ldb, bool k_major,
                         void* packed, int sm_count, cudaStream_t stream) {
@@ -947,10 +969,18 @@ cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, i
     return cudaGetLastError();
 }
 
+enum Until { UNTIL_CHECKED, UNTIL_RESERVED, UNTIL_LAUNCHED };
+
+// Core: C = alpha * op(A) op(B) + beta * C_old + bias, with C_old == C.
+// packed_b != nullptr: op(B) comes packed (emu_pack_b); B and ldb are unused.
+// fused: the epilogue is one of the EPI_* kinds instead (gated: N is F, op(B)
+// has 2F columns; the plan's tiles have 128 columns of each half).
+// max_pairs: the plan takes no more CTA pairs than this.
+// until: stop after the arguments' checks, or after the buffers' reservation.
 emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t N, int64_t K, float alpha,
                       const float* A, int64_t lda, const float* B, int64_t ldb, float beta, float* C,
                       int64_t ldc, const float* bias, cudaStream_t stream, const void* packed_b = nullptr,
-                      bool check_only = false, const Fused* fused = nullptr) {
+                      Until until = UNTIL_LAUNCHED, const Fused* fused = nullptr, int max_pairs = INT32_MAX) {
     if (!valid_mode(mode)) return EMU_STATUS_INVALID_VALUE;
     if (M < 0 || N < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
     if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return EMU_STATUS_NOT_SUPPORTED;
@@ -970,12 +1000,14 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     if (!aligned16(C) || (ldc & 3)) return EMU_STATUS_NOT_SUPPORTED;
     if (bias && !aligned16(bias)) return EMU_STATUS_NOT_SUPPORTED;
 
+    if (until == UNTIL_CHECKED) return EMU_STATUS_SUCCESS;
+
     DeviceInfo* dev = nullptr;
     emu_status_t st = device_info(&dev);
     if (st != EMU_STATUS_SUCCESS) return st;
 
     if (!gemm) {
-        if (check_only) return EMU_STATUS_SUCCESS;
+        if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
         const int64_t total = M * N;
         const int threads = 256;
         const int64_t blocks64 = (total + threads - 1) / threads;
@@ -985,14 +1017,15 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         return cudaGetLastError() == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
     }
 
-    const int pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    const int device_pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    const int pairs = device_pairs < max_pairs ? device_pairs : max_pairs;
     const bool gated = fused && fused->kind == FUSED_GATED;
     const int64_t b_n = gated ? 2 * N : N;                                // columns of op(B)
     const int64_t plan_n = gated ? (N + 127) / 128 * 256 : N;
-    if (!packed_b && !fused) mode = dispatch_mode(mode, M, N, K, pairs, dev->sm_count);
+    if (!packed_b && !fused) mode = dispatch_mode(mode, M, N, K, device_pairs, dev->sm_count);
     if (mode == EMU_MODE_FP32) {
         if (N > 64LL * NAT_MAX_GRID_Y) return EMU_STATUS_NOT_SUPPORTED;
-        if (check_only) return EMU_STATUS_SUCCESS;
+        if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
         if (log_enabled())
             std::fprintf(stderr, "[emu] fp32 M=%lld N=%lld K=%lld a_mn=%d b_mn=%d (native)\n", (long long)M,
                          (long long)N, (long long)K, (int)a_mn, (int)b_mn);
@@ -1052,7 +1085,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         p.workspace = w->partials;
         p.counters = w->counters;
     }
-    if (check_only) return EMU_STATUS_SUCCESS;
+    if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
     if (autopack_buf && launch_pack(mode, b_n, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
         return EMU_STATUS_LAUNCH_FAILED;
     const int clusters = plan.clusters;
@@ -1153,9 +1186,106 @@ emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float**
     return reduce_buffer_for(dev, stream, floats, out);
 }
 
-emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check) {
+namespace {
+emu_status_t gemm_on(emu_mode_t mode, const Gemm& g, cudaStream_t stream, Until until, int max_pairs) {
     return run_gemm(mode, g.a_mn, g.b_mn, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.bias, stream,
-                    nullptr, check, g.fused);
+                    nullptr, until, g.fused, max_pairs);
+}
+
+// How two products share `pairs` CTA pairs: the first's share, or 0 when one
+// after the other is predicted faster.  Costs are the plans' (pipeline
+// stages); a launch of its own adds about kLaunchStages (start-up, and the last
+// wave's idle pairs).  Side by side each product's tiles are split into fewer
+// pieces, which is what small products gain from; products of many waves have
+// nothing to gain and stay in order.
+constexpr double kLaunchStages = 5.0;
+int two_share(const Gemm& a, const Gemm& b, int pairs) {
+    // remembered like the plans
+    struct Entry {
+        int64_t key[6] = {-1, -1, -1, -1, -1, -1};
+        int pairs = 0, share = 0;
+        PlanEnv env{};
+    };
+    constexpr int kEntries = 32;
+    static thread_local Entry entries[kEntries];
+    const int64_t key[6] = {a.M, a.N, a.K, b.M, b.N, b.K};
+    const PlanEnv env = plan_env();
+    uint64_t h = pairs;
+    for (int64_t k : key) h = mix(h, k);
+    Entry& e = entries[(h >> 40) % kEntries];
+    bool same = e.pairs == pairs && e.env == env;
+    for (int i = 0; i < 6; ++i) same = same && e.key[i] == key[i];
+    if (same) return e.share;
+    auto cost = [](const Gemm& g, int p) {
+        const Plan plan = make_plan(g.M, g.N, g.K, p);
+        return plan.cost + (plan.split_a > 1 || plan.split_b > 1
+                                ? 0.4 * (plan.split_a > plan.split_b ? plan.split_a : plan.split_b) : 0.0);
+    };
+    const double apart = cost(a, pairs) + cost(b, pairs) + kLaunchStages;
+    double best = 0.95 * apart;
+    int share = 0;
+    for (int i = 2; i <= 6; ++i) {  // quarters to three quarters of the GPU
+        const int p = pairs * i / 8;
+        const double ca = cost(a, p), cb = cost(b, pairs - p), c = ca > cb ? ca : cb;
+        if (c < best) { best = c; share = p; }
+    }
+    for (int i = 0; i < 6; ++i) e.key[i] = key[i];
+    e.pairs = pairs; e.env = env; e.share = share;
+    return share;
+}
+}  // namespace
+
+emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check) {
+    return gemm_on(mode, g, stream, check ? UNTIL_RESERVED : UNTIL_LAUNCHED, INT32_MAX);
+}
+
+emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, bool check) {
+    if (!a || !b) return a ? gemm(mode, *a, stream, check) : b ? gemm(mode, *b, stream, check) : EMU_STATUS_SUCCESS;
+    int share = 0;
+    DeviceInfo* dev = nullptr;
+    if (check) {  // the arguments before anything that needs the device
+        for (const Gemm* g : {a, b}) {
+            const emu_status_t st = gemm_on(mode, *g, stream, UNTIL_CHECKED, INT32_MAX);
+            if (st != EMU_STATUS_SUCCESS) return st;
+        }
+    }
+    // (no caller passes a gated pair: its tiles are not the plan's of M x N)
+    const bool real = !(a->fused && a->fused->kind == FUSED_GATED) && !(b->fused && b->fused->kind == FUSED_GATED) && a->M > 0 && a->N > 0 && a->K > 0 && b->M > 0 && b->N > 0 && b->K > 0 && emulated_mode(mode) &&
+                      a->M <= INT32_MAX - 256 && b->M <= INT32_MAX - 256 && a->N <= INT32_MAX - 256 &&
+                      b->N <= INT32_MAX - 256 && a->K <= INT32_MAX - 256 && b->K <= INT32_MAX - 256;
+    if (real && g_strategy.load(std::memory_order_relaxed) != EMU_STRATEGY_PERFORMANT) {
+        const emu_status_t st = device_info(&dev);
+        if (st != EMU_STATUS_SUCCESS) return st;
+        static const bool on = env_int("EMU_SIDE", 1) != 0;
+        if (on) share = two_share(*a, *b, dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0]);
+    }
+    if (share == 0) {
+        const emu_status_t st = gemm(mode, *a, stream, check);
+        return st == EMU_STATUS_SUCCESS ? gemm(mode, *b, stream, check) : st;
+    }
+    const int rest = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0] - share;
+    int devid = 0;
+    cudaGetDevice(&devid);
+    cudaStream_t side;
+    cudaEvent_t fork, join;
+    emu_status_t st = side_stream_for(devid, stream, &side, &fork, &join);
+    if (st != EMU_STATUS_SUCCESS) return st;
+    if (check) {
+        st = gemm_on(mode, *a, stream, UNTIL_RESERVED, share);
+        return st == EMU_STATUS_SUCCESS ? gemm_on(mode, *b, side, UNTIL_RESERVED, rest) : st;
+    }
+    if (cudaEventRecord(fork, stream) != cudaSuccess || cudaStreamWaitEvent(side, fork, 0) != cudaSuccess) {
+        cudaGetLastError();
+        return EMU_STATUS_LAUNCH_FAILED;
+    }
+    st = gemm_on(mode, *a, stream, UNTIL_LAUNCHED, share);
+    if (st == EMU_STATUS_SUCCESS) st = gemm_on(mode, *b, side, UNTIL_LAUNCHED, rest);
+    // (joined in any case, so that the side stream is never left forked)
+    if (cudaEventRecord(join, side) != cudaSuccess || cudaStreamWaitEvent(stream, join, 0) != cudaSuccess) {
+        cudaGetLastError();
+        return EMU_STATUS_LAUNCH_FAILED;
+    }
+    return st;
 }
 static_assert(FUSED_ACT == EPI_ACT && FUSED_GATED == EPI_GATED && FUSED_GATED_BWD == EPI_GATED_BWD, "epilogue kinds");
 
@@ -1335,6 +1465,9 @@ emu_status_t emu_shutdown(void) {
         if (w.counters && cudaFree(w.counters) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.packed && cudaFree(w.packed) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.reduce && cudaFree(w.reduce) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        if (w.side && cudaStreamDestroy(w.side) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        if (w.fork && cudaEventDestroy(w.fork) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        if (w.join && cudaEventDestroy(w.join) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         w = Workspace{};
     }
     if (have_current && cudaSetDevice(current) != cudaSuccess) cudaGetLastError();

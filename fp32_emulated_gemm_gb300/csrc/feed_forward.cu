@@ -263,17 +263,14 @@ emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K
     const int64_t ldg = D ? lddz : lddy;
     const Gemm gx = input_product(M, N, K, G, ldg, W, ldw, dX, lddx), gw = weight_product(M, N, K, G, ldg, X, ldx, dW, lddw);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dX) EMU_TRY(gemm(mode, gx, s, true));
-    if (dW) EMU_TRY(gemm(mode, gw, s, true));
+    EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, true));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     float* scratch = nullptr;
     if (dbias) EMU_TRY(reduce_scratch(dev.id, s, column_sum_floats(false, M, N, dev.sm_count), &scratch));
     if (apply || dbias)
         EMU_TRY(launched(launch_act_bwd<false>(M, N, dY, lddy, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
-    if (dX) EMU_TRY(gemm(mode, gx, s, false));
-    if (dW) EMU_TRY(gemm(mode, gw, s, false));
-    return EMU_STATUS_SUCCESS;
+    return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
 }
 
 emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F, int64_t K, const float* X, int64_t ldx,
@@ -300,16 +297,13 @@ emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, con
     const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W, ldw, dX, lddx);
     const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW, lddw);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dX) EMU_TRY(gemm(mode, gx, s, true));
-    if (dW) EMU_TRY(gemm(mode, gw, s, true));
+    EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, true));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     float* scratch = nullptr;
     if (dbias) EMU_TRY(reduce_scratch(dev.id, s, column_sum_floats(true, M, F, dev.sm_count), &scratch));
     EMU_TRY(launched(launch_act_bwd<true>(M, F, dH, lddh, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
-    if (dX) EMU_TRY(gemm(mode, gx, s, false));
-    if (dW) EMU_TRY(gemm(mode, gw, s, false));
-    return EMU_STATUS_SUCCESS;
+    return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
 }
 
 emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t K, int64_t F, int64_t N,
@@ -356,10 +350,8 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi);
     const bool inner = dX || dW_in || db_in;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (inner) EMU_TRY(gemm(mode, gh, s, true));
-    if (dW_out) EMU_TRY(gemm(mode, go, s, true));
-    if (dX) EMU_TRY(gemm(mode, gx, s, true));
-    if (dW_in) EMU_TRY(gemm(mode, gw, s, true));
+    EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, true));
+    EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, true));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     // (the two biases' sums take the scratch one after the other)
@@ -369,20 +361,17 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
                              : column_sum_floats(true, M, F, dev.sm_count);
     float* scratch = nullptr;
     if (db_in || db_out) EMU_TRY(reduce_scratch(dev.id, s, n_out > n_in ? n_out : n_in, &scratch));
-    if (dW_out) EMU_TRY(gemm(mode, go, s, false));
     if (db_out)
         EMU_TRY(launched(launch_act_bwd<false>(M, N, dY, lddy, nullptr, 0, nullptr, 0, db_out, scratch, dev.sm_count, s)));
-    if (!inner) return EMU_STATUS_SUCCESS;
     if (fuse && db_in) f.sums = scratch;
-    EMU_TRY(gemm(mode, gh, s, false));
+    EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, false));
+    if (!inner) return EMU_STATUS_SUCCESS;
     if (!fuse)
         EMU_TRY(launched(launch_act_bwd<true>(M, F, dZ, lddz, D, ldd, dZ, lddz, db_in, scratch, dev.sm_count, s)));
     else if (db_in)
         EMU_TRY(launched(launch_act_bwd<false>(blocks, 2 * F, scratch, 2 * F, nullptr, 0, nullptr, 0, db_in,
                                                scratch + (size_t)blocks * 2 * F, dev.sm_count, s)));
-    if (dX) EMU_TRY(gemm(mode, gx, s, false));
-    if (dW_in) EMU_TRY(gemm(mode, gw, s, false));
-    return EMU_STATUS_SUCCESS;
+    return gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, false);
 }
 
 }  // extern "C"

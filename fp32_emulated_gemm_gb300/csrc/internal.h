@@ -52,4 +52,9 @@ struct Gemm {
 };
 emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check);
 
+// Two independent products, each `after` work queued on `stream` before the call
+// and both before work queued after it: side by side on shares of the GPU when
+// that is predicted faster than one after the other.  Either may be absent (null).
+emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, bool check);
+
 }  // namespace emu

@@ -481,6 +481,65 @@ def test_other_stream():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
+def test_backward_products_side_by_side(mode):
+    """The two products of a backward pass that share the GPU (small ones) and
+    the ones that run in turn (many waves): right either way, and the calls
+    after them wait for both."""
+    import fp32_emulated_gemm_gb300 as emu
+    for M, N, K in ((1100, 300, 500), (64, 1024, 700), (5000, 96, 80), (3000, 1500, 700)):
+        rng = rng_of("side", M, N, K)
+        x, w, dy = f32(rng, M, K), f32(rng, N, K, std=K ** -0.5), f32(rng, M, N)
+        xd, wd, dyd = dev(x), dev(w), dev(dy)
+        outs = []
+        for rep in range(3):
+            dx, dw, db = emu.linear_act_bwd(dyd, xd, wd, mode=mode)
+            outs.append([host(emu.linear_fwd(dx, wd, mode=mode)), host(dx), host(dw), host(db)])  # dX used at once
+        done()
+        for other in outs[1:]:
+            for p, q in zip(outs[0], other):
+                assert np.array_equal(p, q)
+        rows = np.arange(0, M, max(1, M // 200))
+        R.product(V(dy[rows]), w, mode).check(outs[0][1][rows], "dX")
+        cols = np.arange(0, N, max(1, N // 60))
+        R.product(V(dy[:, cols]).T, x, mode).check(outs[0][2][cols], "dW")
+        R.column_sum(V(dy)).check(outs[0][3], "db")
+
+
+def test_captured_in_a_graph():
+    """A training step captured after a warm-up on the capturing stream: each
+    replay gives what the calls give on the inputs then in place."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("graph")
+    M, K, F = 1400, 96, 130
+    x, wi, wo, dy = (dev(f32(rng, *s)) for s in ((M, K), (2 * F, K), (K, F), (M, K)))
+
+    def step():
+        n, mean, rstd = emu.layer_norm_fwd(x)
+        y, d, h = emu.gated_ffn_fwd(n, wi, None, wo, None, residual=x, save=True)
+        g = emu.gated_ffn_bwd(dy, n, wi, wo, d, h)
+        dx, dw, db = emu.layer_norm_bwd(g[0], x, None, mean, rstd, add=dy)
+        return [y, dx, *g[1:], emu.linear_act_fwd(dx, wi, act="gelu")]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    for rep in range(3):
+        x.copy_(dev(f32(rng, M, K)))
+        dy.copy_(dev(f32(rng, M, K)))
+        graph.replay()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    done()
+
+
 def test_degenerate_sizes():
     import torch
     import fp32_emulated_gemm_gb300 as emu
