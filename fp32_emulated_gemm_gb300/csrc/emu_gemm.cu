@@ -1048,6 +1048,15 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     const void* b_packed = packed_b ? packed_b : autopack_buf;
     if (b_packed) plan.pipe = plan.pipe == PIPE_LONG_K ? PIPE_LONG_K_PACKED : PIPE_SHORT_K_PACKED;
     Params p{};
+    if (plan.slots > 0) {
+        Workspace* w = nullptr;
+        const size_t floats = (size_t)plan.slots * TILE_M * plan.tn;
+        st = workspace_for(devid, stream, floats, (size_t)plan.num_tiles * 2, &w, &p.epoch);
+        if (st != EMU_STATUS_SUCCESS) return st;
+        p.workspace = w->partials;
+        p.counters = w->counters;
+    }
+    if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
     if (!encode_operand(&p.tmA, A, a_mn, M, K, lda, HALF) ||
         !(b_packed ? encode_packed(&p.tmB, b_packed, mode, b_n, K)
                    : encode_operand(&p.tmB, B, b_mn, b_n, K, ldb, (uint32_t)plan.tn / 2)))
@@ -1077,15 +1086,6 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     p.c_old = C; p.c = C; p.ldc = ldc;
     p.bias = bias;
     p.wait_budget_ns = wait_budget_ns();
-    if (plan.slots > 0) {
-        Workspace* w = nullptr;
-        const size_t floats = (size_t)plan.slots * TILE_M * plan.tn;
-        st = workspace_for(devid, stream, floats, (size_t)p.num_tiles * 2, &w, &p.epoch);
-        if (st != EMU_STATUS_SUCCESS) return st;
-        p.workspace = w->partials;
-        p.counters = w->counters;
-    }
-    if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
     if (autopack_buf && launch_pack(mode, b_n, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
         return EMU_STATUS_LAUNCH_FAILED;
     const int clusters = plan.clusters;

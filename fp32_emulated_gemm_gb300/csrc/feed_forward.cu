@@ -61,9 +61,24 @@ act_fwd_kernel(ActParams act, int64_t M, int64_t N, int64_t rows_per, const floa
     }
 }
 
+// Four columns' sums of the block's eight warps, added in order, to out[c ..].
+template <bool VEC>
+__device__ __forceinline__ void store_block_sums(float4 (&sums)[kWarps][32], float* out, int64_t c, int64_t n) {
+    float4 t = sums[0][threadIdx.x];
+    for (int i = 1; i < kWarps; ++i) {
+        const float4 v = sums[i][threadIdx.x];
+        t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
+    }
+    // (partial rows of odd width: word stores)
+    constexpr int W = VEC ? 1 : 32;
+    if (c < n) out[c] = t.x;
+    if (c + W < n) out[c + W] = t.y;
+    if (c + 2 * W < n) out[c + 2 * W] = t.z;
+    if (c + 3 * W < n) out[c + 3 * W] = t.w;
+}
+
 // dZ = dY D, or with GATED dZ = [dY | dY] D (2N columns); the sums of this
-// block's rows of dZ go to partial[blockIdx.y].  dZ may take dY's place.  D
-// null: dZ = dY, not written (the sums alone).
+// block's rows of dZ go to partial[blockIdx.y].  dZ may take dY's place.
 template <bool GATED, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps)
 act_bwd_kernel(int64_t M, int64_t N, int64_t rows_per, const float* dY, int64_t lddy, const float* D, int64_t ldd,
@@ -75,39 +90,102 @@ act_bwd_kernel(int64_t M, int64_t N, int64_t rows_per, const float* dY, int64_t 
     float4 sg = make_float4(0.f, 0.f, 0.f, 0.f), su = sg;
     for (int64_t r = blockIdx.y * rows_per + threadIdx.y; r < r1; r += kWarps) {
         float4 g = load4<VEC, S>(dY + r * lddy, c, N);
-        if (D) {
-            const float4 d = load4<VEC, S>(D + r * ldd, c, N);
-            if constexpr (GATED) {
-                const float4 a = load4<VEC, S>(D + r * ldd + N, c, N);
-                const float4 du = make_float4(g.x * a.x, g.y * a.y, g.z * a.z, g.w * a.w);
-                store4<VEC, S>(dZ + r * lddz + N, c, N, du);
-                su = make_float4(su.x + du.x, su.y + du.y, su.z + du.z, su.w + du.w);
-            }
-            g = make_float4(g.x * d.x, g.y * d.y, g.z * d.z, g.w * d.w);
-            store4<VEC, S>(dZ + r * lddz, c, N, g);
+        const float4 d = load4<VEC, S>(D + r * ldd, c, N);
+        if constexpr (GATED) {
+            const float4 a = load4<VEC, S>(D + r * ldd + N, c, N);
+            const float4 du = make_float4(g.x * a.x, g.y * a.y, g.z * a.z, g.w * a.w);
+            store4<VEC, S>(dZ + r * lddz + N, c, N, du);
+            su = make_float4(su.x + du.x, su.y + du.y, su.z + du.z, su.w + du.w);
         }
+        g = make_float4(g.x * d.x, g.y * d.y, g.z * d.z, g.w * d.w);
+        store4<VEC, S>(dZ + r * lddz, c, N, g);
         sg = make_float4(sg.x + g.x, sg.y + g.y, sg.z + g.z, sg.w + g.w);
     }
     if (!partial) return;
+    if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
     sums[0][threadIdx.y][threadIdx.x] = sg;
     if constexpr (GATED) sums[1][threadIdx.y][threadIdx.x] = su;
     __syncthreads();
-    if (threadIdx.y < (GATED ? 2 : 1)) {
-        float4 t = sums[threadIdx.y][0][threadIdx.x];
-        for (int i = 1; i < kWarps; ++i) {
-            const float4 v = sums[threadIdx.y][i][threadIdx.x];
-            t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
-        }
-        const int64_t width = (GATED ? 2 : 1) * N;
-        float* out = partial + blockIdx.y * width + threadIdx.y * N;
-        // (partial rows of odd width: word stores)
-        constexpr int W = VEC ? 1 : S;
-        if (c < N) out[c] = t.x;
-        if (c + W < N) out[c + W] = t.y;
-        if (c + 2 * W < N) out[c + 2 * W] = t.z;
-        if (c + 3 * W < N) out[c + 3 * W] = t.w;
+    if (threadIdx.y < (GATED ? 2 : 1))
+        store_block_sums<VEC>(sums[threadIdx.y], partial + blockIdx.y * ((GATED ? 2 : 1) * N) + threadIdx.y * N, c, N);
+}
+
+// Sums of a matrix's columns over chunks of its rows: partial[chunk][column].
+struct SumJob {
+    const float* A;
+    int64_t lda, M, N, rows_per;
+    int col_blocks;
+    float* partial;
+};
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kWarps) column_sums_kernel(const SumJob a) {
+    constexpr int S = 32;
+    __shared__ float4 sums[kWarps][32];
+    const int64_t chunk = blockIdx.x / a.col_blocks;
+    const int64_t c = (blockIdx.x % a.col_blocks) * (int64_t)kCols + (VEC ? 4 * threadIdx.x : threadIdx.x);
+    const int64_t r1 = min(a.M, (chunk + 1) * a.rows_per);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int64_t r = chunk * a.rows_per + threadIdx.y; r < r1; r += kWarps) {
+        const float4 v = load4<VEC, S>(a.A + r * a.lda, c, a.N);
+        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
+    if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0) store_block_sums<VEC>(sums, a.partial + chunk * a.N, c, a.N);
+}
+
+// p ascending in 32 interleaved chains, which are then added in order: the
+// sums do not depend on timing.  Block: 32 columns x 32 chains.
+struct PartialsPair { Partials set[2]; unsigned first_blocks; };
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const PartialsPair pair) {
+    __shared__ float part[32][33];
+    const bool second = blockIdx.x >= pair.first_blocks;
+    const Partials& a = pair.set[second];
+    const int64_t c = (blockIdx.x - (second ? pair.first_blocks : 0)) * 32ll + threadIdx.x;
+    griddep_wait();
+    float s = 0.f;
+    if (c < a.C) {
+#pragma unroll 4
+        for (int p = threadIdx.y; p < a.P; p += 32) s += a.p[(int64_t)p * a.C + c];
+    }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < a.C) {
+        float t = part[0][threadIdx.x];
+        for (int i = 1; i < 32; ++i) t += part[i][threadIdx.x];
+        if (c < a.split) { if (a.out0) a.out0[c] = t; }
+        else if (a.out1) a.out1[c - a.split] = t;
     }
 }
+
+}  // namespace
+
+cudaError_t launch_sum_partials(const Partials* sets, int n, cudaStream_t stream) {
+    PartialsPair pair{};
+    unsigned blocks = 0;
+    for (int i = 0; i < n; ++i) {
+        pair.set[i] = sets[i];
+        blocks += (unsigned)((sets[i].C + 31) / 32);
+        if (i == 0) pair.first_blocks = blocks;
+    }
+    if (blocks == 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(32, 32, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, sum_partials_kernel, pair);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
+namespace {
 
 template <bool GATED>
 cudaError_t launch_act_fwd(int act, int64_t M, int64_t N, const float* Z, int64_t ldz, const float* R, int64_t ldr,
@@ -126,8 +204,8 @@ cudaError_t launch_act_fwd(int act, int64_t M, int64_t N, const float* Z, int64_
     return cudaGetLastError();
 }
 
-// `scratch`: column_sum_floats() floats when dbias is wanted, else null
-size_t column_sum_floats(bool gated, int64_t M, int64_t N, int sm_count) {
+// `scratch`: act_bwd_floats() floats when dbias is wanted, else null
+size_t act_bwd_floats(bool gated, int64_t M, int64_t N, int sm_count) {
     return M > 0 && N > 0 ? (size_t)row_grid(M, N, sm_count).chunks * (gated ? 2 : 1) * N : 0;
 }
 template <bool GATED>
@@ -137,7 +215,7 @@ cudaError_t launch_act_bwd(int64_t M, int64_t N, const float* dY, int64_t lddy, 
     const int64_t width = (GATED ? 2 : 1) * N;
     if (M == 0) return dbias ? cudaMemsetAsync(dbias, 0, width * sizeof(float), s) : cudaSuccess;
     const RowGrid g = row_grid(M, N, sm_count);
-    const bool vec = (N & 3) == 0 && vec4_ok(dY, lddy) && (!D || (vec4_ok(D, ldd) && vec4_ok(dZ, lddz)));
+    const bool vec = (N & 3) == 0 && vec4_ok(dY, lddy) && vec4_ok(D, ldd) && vec4_ok(dZ, lddz);
     float* partial = dbias ? scratch : nullptr;
     cudaGetLastError();
     const dim3 block(32, kWarps);
@@ -145,7 +223,38 @@ cudaError_t launch_act_bwd(int64_t M, int64_t N, const float* dY, int64_t lddy, 
     else act_bwd_kernel<GATED, false><<<g.grid, block, 0, s>>>(M, N, g.rows_per, dY, lddy, D, ldd, dZ, lddz, partial);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !dbias) return e;
-    return launch_sum_partials(partial, g.chunks, width, width, dbias, nullptr, s);
+    const Partials sums{partial, g.chunks, width, width, dbias, nullptr};
+    return launch_sum_partials(&sums, 1, s);
+}
+
+// The column sums of a matrix and, in the same two launches, of a second one
+// that is narrow in rows already (the partial sums of a product's epilogue:
+// dense, at most kDirectRows rows; its out may be null).  scratch:
+// column_sums_floats(M, N).
+constexpr int64_t kDirectRows = 512;
+size_t column_sums_floats(int64_t M, int64_t N, int sm_count) { return act_bwd_floats(false, M, N, sm_count); }
+cudaError_t launch_column_sums(const float* A, int64_t lda, int64_t M, int64_t N, float* out, const Partials* direct,
+                               float* scratch, int sm_count, cudaStream_t s) {
+    Partials sets[2];
+    int n = 0;
+    if (out && N > 0) {
+        if (M == 0) {
+            const cudaError_t e = cudaMemsetAsync(out, 0, N * sizeof(float), s);
+            if (e != cudaSuccess) return e;
+        } else {
+            const RowGrid g = row_grid(M, N, sm_count);
+            const SumJob job{A, lda, M, N, g.rows_per, (int)g.grid.x, scratch};
+            cudaGetLastError();
+            const unsigned blocks = g.grid.x * g.grid.y;
+            if ((N & 3) == 0 && vec4_ok(A, lda)) column_sums_kernel<true><<<blocks, dim3(32, kWarps), 0, s>>>(job);
+            else column_sums_kernel<false><<<blocks, dim3(32, kWarps), 0, s>>>(job);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+            sets[n++] = {scratch, g.chunks, N, N, out, nullptr};
+        }
+    }
+    if (direct) sets[n++] = *direct;
+    return n ? launch_sum_partials(sets, n, s) : cudaSuccess;
 }
 
 bool valid_act(emu_act_t act) { return act >= EMU_ACT_NONE && act <= EMU_ACT_SILU; }
@@ -267,9 +376,11 @@ emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     float* scratch = nullptr;
-    if (dbias) EMU_TRY(reduce_scratch(dev.id, s, column_sum_floats(false, M, N, dev.sm_count), &scratch));
-    if (apply || dbias)
+    if (dbias) EMU_TRY(reduce_scratch(dev.id, s, act_bwd_floats(false, M, N, dev.sm_count), &scratch));
+    if (apply)
         EMU_TRY(launched(launch_act_bwd<false>(M, N, dY, lddy, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
+    else if (dbias)
+        EMU_TRY(launched(launch_column_sums(dY, lddy, M, N, dbias, nullptr, scratch, dev.sm_count, s)));
     return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
 }
 
@@ -301,7 +412,7 @@ emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, con
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     float* scratch = nullptr;
-    if (dbias) EMU_TRY(reduce_scratch(dev.id, s, column_sum_floats(true, M, F, dev.sm_count), &scratch));
+    if (dbias) EMU_TRY(reduce_scratch(dev.id, s, act_bwd_floats(true, M, F, dev.sm_count), &scratch));
     EMU_TRY(launched(launch_act_bwd<true>(M, F, dH, lddh, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
     return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
 }
@@ -354,23 +465,31 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, true));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
-    // (the two biases' sums take the scratch one after the other)
+    // Scratch: the output bias's partial sums, the epilogue's (a row for each 32
+    // rows) and, where those are many, their own partial sums.
     const int64_t blocks = (M + 31) / 32;
-    const size_t n_out = column_sum_floats(false, M, N, dev.sm_count);
-    const size_t n_in = fuse ? (size_t)blocks * 2 * F + column_sum_floats(false, blocks, 2 * F, dev.sm_count)
-                             : column_sum_floats(true, M, F, dev.sm_count);
-    float* scratch = nullptr;
-    if (db_in || db_out) EMU_TRY(reduce_scratch(dev.id, s, n_out > n_in ? n_out : n_in, &scratch));
-    if (db_out)
-        EMU_TRY(launched(launch_act_bwd<false>(M, N, dY, lddy, nullptr, 0, nullptr, 0, db_out, scratch, dev.sm_count, s)));
-    if (fuse && db_in) f.sums = scratch;
+    const bool direct = blocks <= kDirectRows;
+    const size_t n_out = column_sums_floats(M, N, dev.sm_count);
+    const size_t n_in = !fuse ? act_bwd_floats(true, M, F, dev.sm_count)
+                              : (size_t)blocks * 2 * F + (direct ? 0 : column_sums_floats(blocks, 2 * F, dev.sm_count));
+    float *scratch = nullptr, *sums = nullptr;
+    if (db_in || db_out) {
+        const size_t out_floats = (n_out + 3) & ~size_t(3);
+        EMU_TRY(reduce_scratch(dev.id, s, out_floats + n_in, &scratch));
+        sums = scratch + out_floats;
+    }
+    if (fuse && db_in) f.sums = sums;
     EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, false));
+    const bool join = fuse && db_in && direct;
+    const Partials in_sums{sums, (int)blocks, 2 * F, 2 * F, db_in, nullptr};
+    if (db_out || join)
+        EMU_TRY(launched(launch_column_sums(dY, lddy, M, N, db_out, join ? &in_sums : nullptr, scratch, dev.sm_count, s)));
     if (!inner) return EMU_STATUS_SUCCESS;
     if (!fuse)
-        EMU_TRY(launched(launch_act_bwd<true>(M, F, dZ, lddz, D, ldd, dZ, lddz, db_in, scratch, dev.sm_count, s)));
-    else if (db_in)
-        EMU_TRY(launched(launch_act_bwd<false>(blocks, 2 * F, scratch, 2 * F, nullptr, 0, nullptr, 0, db_in,
-                                               scratch + (size_t)blocks * 2 * F, dev.sm_count, s)));
+        EMU_TRY(launched(launch_act_bwd<true>(M, F, dZ, lddz, D, ldd, dZ, lddz, db_in, sums, dev.sm_count, s)));
+    else if (db_in && !direct)
+        EMU_TRY(launched(launch_column_sums(sums, 2 * F, blocks, 2 * F, db_in, nullptr, sums + (size_t)blocks * 2 * F,
+                                            dev.sm_count, s)));
     return gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, false);
 }
 

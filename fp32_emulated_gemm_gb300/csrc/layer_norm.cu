@@ -18,21 +18,24 @@ namespace {
 
 // ------------------------------------------------- rows held in registers --
 // T threads share a row and hold it in NV float4 each (4 T NV >= N), so X and
-// dY are read once.  T = 32: a warp a row, eight rows a block, sums by
-// shuffles alone; wider rows take a block each, so that a thread never holds
-// more than 4 float4 of a matrix and enough rows are in flight per SM.
-template <int T> constexpr int kBlockThreads = T == 32 ? 256 : T;
-template <int T> constexpr int kBlockRows = T == 32 ? 8 : 1;
+// dY are read once.  T <= 32: part of a warp or a warp a row, sums by shuffles
+// alone.  Wider rows take a block each, whose sums cost barriers: there few
+// threads with many values each keep the most rows in flight per SM.
+template <int T> constexpr int kBlockThreads = T <= 32 ? 256 : T;
+template <int T> constexpr int kBlockRows = T <= 32 ? 256 / T : 1;
 
 // Sums over the T threads of a row of two values, returned to all of them.
 // `flip` alternates between two sets of slots from one call to the next, so
 // one barrier per call is enough.
 template <int T>
 __device__ __forceinline__ float2 row_sum2(float a, float b, int& flip) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if constexpr (T == 32) return make_float2(a, b);
-    __shared__ float2 part[2][T / 32];
+#pragma unroll
+    for (int o = T < 32 ? T / 2 : 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if constexpr (T <= 32) return make_float2(a, b);
+    __shared__ float2 part[2][T / 32 + 1];
     float2* p = part[flip];
     flip ^= 1;
     if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
@@ -56,14 +59,18 @@ __global__ void __launch_bounds__(kBlockThreads<T>)
 ln_fwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ X, int64_t ldx, const float* __restrict__ w,
                    const float* __restrict__ b, float eps, float* __restrict__ Y, int64_t ldy, float* mean, float* rstd) {
     constexpr int G = kBlockRows<T>;
-    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x, g = T == 32 ? threadIdx.x >> 5 : 0;
+    const int t = threadIdx.x % T, g = threadIdx.x / T;
     const float inv_n = 1.0f / (float)N;
+    const int64_t step = (int64_t)gridDim.x * G;
     int flip = 0;
-    for (int64_t r = blockIdx.x * (int64_t)G + g; r < M; r += (int64_t)gridDim.x * G) {
+    // (the loop is the same for all threads of a block: shuffles and barriers)
+    for (int64_t first = blockIdx.x * (int64_t)G; first < M; first += step) {
+        const int64_t r = first + g;
+        const bool real = r < M;
         float4 x[NV];
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x[i] = load4<VEC, T>(X + r * ldx, col_of<T, VEC>(t, i), N);
+        for (int i = 0; i < NV; ++i) x[i] = load4<VEC, T>(X + r * ldx, col_of<T, VEC>(t, i), real ? N : 0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) s += (x[i].x + x[i].y) + (x[i].z + x[i].w);
         const float mu = row_sum2<T>(s, 0.f, flip).x * inv_n;
@@ -80,6 +87,7 @@ ln_fwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ X, int64_t ld
             if (inside<T, VEC>(c, 3, N)) q = fmaf(x[i].w, x[i].w, q);
         }
         const float rs = 1.0f / sqrtf(fmaf(row_sum2<T>(q, 0.f, flip).x, inv_n, eps));
+        if (!real) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = col_of<T, VEC>(t, i);
@@ -104,26 +112,29 @@ ln_fwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ X, int64_t ld
 // dX and, over the rows this block takes, the sums of dw and db, which stay in
 // registers until the end and go to partial[blockIdx.x][0 and 1][column].
 template <int T, int NV, bool VEC>
-__global__ void __launch_bounds__(kBlockThreads<T>, T == 32 && NV <= 2 ? 4 : 1)
+__global__ void __launch_bounds__(kBlockThreads<T>, T <= 32 && NV <= 2 ? 4 : 1)
 ln_bwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ dY, int64_t lddy, const float* __restrict__ X,
                    int64_t ldx, const float* __restrict__ w, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const float* __restrict__ add, int64_t ldadd, float* __restrict__ dX,
                    int64_t lddx, float* __restrict__ partial) {
     constexpr int G = kBlockRows<T>;
-    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x, g = T == 32 ? threadIdx.x >> 5 : 0;
+    const int t = threadIdx.x % T, g = threadIdx.x / T;
     const float inv_n = 1.0f / (float)N;
+    const int64_t step = (int64_t)gridDim.x * G;
     int flip = 0;
     float4 dw[NV], db[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) dw[i] = db[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t r = blockIdx.x * (int64_t)G + g; r < M; r += (int64_t)gridDim.x * G) {
+    for (int64_t first = blockIdx.x * (int64_t)G; first < M; first += step) {
+        const int64_t r = first + g;
+        const bool real = r < M;
         float4 x[NV], y[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            x[i] = load4<VEC, T>(X + r * ldx, col_of<T, VEC>(t, i), N);
-            y[i] = load4<VEC, T>(dY + r * lddy, col_of<T, VEC>(t, i), N);
+            x[i] = load4<VEC, T>(X + r * ldx, col_of<T, VEC>(t, i), real ? N : 0);
+            y[i] = load4<VEC, T>(dY + r * lddy, col_of<T, VEC>(t, i), real ? N : 0);
         }
-        const float mu = mean[r], rs = rstd[r];
+        const float mu = real ? mean[r] : 0.f, rs = real ? rstd[r] : 0.f;
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -139,41 +150,44 @@ ln_bwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ dY, int64_t l
             s1 += (y[i].x + y[i].y) + (y[i].z + y[i].w);
             s2 += fmaf(y[i].x, x[i].x, y[i].y * x[i].y) + fmaf(y[i].z, x[i].z, y[i].w * x[i].w);
         }
-        if (!dX) continue;
-        const float2 m = row_sum2<T>(s1, s2, flip);
-        const float m1 = m.x * inv_n, m2 = m.y * inv_n;
+        if (dX) {
+            const float2 m = row_sum2<T>(s1, s2, flip);
+            const float m1 = m.x * inv_n, m2 = m.y * inv_n;
+            if (real) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = col_of<T, VEC>(t, i);
-            float4 v = make_float4(rs * (y[i].x - m1 - x[i].x * m2), rs * (y[i].y - m1 - x[i].y * m2),
-                                   rs * (y[i].z - m1 - x[i].z * m2), rs * (y[i].w - m1 - x[i].w * m2));
-            if (add) {
-                const float4 a = load4<VEC, T>(add + r * ldadd, c, N);
-                v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+                for (int i = 0; i < NV; ++i) {
+                    const int64_t c = col_of<T, VEC>(t, i);
+                    float4 v = make_float4(rs * (y[i].x - m1 - x[i].x * m2), rs * (y[i].y - m1 - x[i].y * m2),
+                                           rs * (y[i].z - m1 - x[i].z * m2), rs * (y[i].w - m1 - x[i].w * m2));
+                    if (add) {
+                        const float4 a = load4<VEC, T>(add + r * ldadd, c, N);
+                        v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+                    }
+                    store4<VEC, T>(dX + r * lddx, c, N, v);
+                }
             }
-            store4<VEC, T>(dX + r * lddx, c, N, v);
         }
     }
     if (!partial) return;
+    if (threadIdx.x == 0) griddep_launch_dependents();  // the partial sums' kernel: its launch, not its reads
     float* out = partial + (int64_t)blockIdx.x * 2 * N;
-    if constexpr (T == 32) {
-        // the eight warps' sums, added in order
-        __shared__ float4 part[2][G][32 * NV];
+    if constexpr (T <= 32) {
+        // the sums of the block's G groups of threads, added in order
+        __shared__ float4 part[2][G][T * NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            part[0][g][32 * i + t] = dw[i];
-            part[1][g][32 * i + t] = db[i];
+            part[0][g][T * i + t] = dw[i];
+            part[1][g][T * i + t] = db[i];
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < 2 * 32 * NV; e += 256) {
-            const int which = e / (32 * NV), q = e % (32 * NV);
+        for (int e = threadIdx.x; e < 2 * T * NV; e += 256) {
+            const int which = e / (T * NV), q = e % (T * NV);
             float4 v = part[which][0][q];
-#pragma unroll
             for (int i = 1; i < G; ++i) {
                 const float4 k = part[which][i][q];
                 v = make_float4(v.x + k.x, v.y + k.y, v.z + k.z, v.w + k.w);
             }
-            store4<VEC, T>(out + which * N, col_of<T, VEC>(q % 32, q / 32), N, v);
+            store4<VEC, T>(out + which * N, col_of<T, VEC>(q % T, q / T), N, v);
         }
     } else {
 #pragma unroll
@@ -186,18 +200,29 @@ ln_bwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ dY, int64_t l
 
 constexpr int64_t kMaxRegsWidth = 16384;
 
-// f(T, NV) for the width: the fewest threads that hold a row in 4 float4 (a
-// warp) or 2 (a block) each.
-template <class F> void for_width(int64_t N, F f) {
+// f(T, NV) for the width.  Measured fractions of the copy rate, forward and
+// backward, at 0.4 GB a matrix: N = 16 0.86
+// and 0.84, 32 0.87 and 0.84, 61 (unaligned rows) 0.73 and 0.79, 256 0.83 and 0.94, 512 0.88 and 0.94, 1024 0.88 and 0.97, 2048 0.97 and 0.95
+// (backward with 256 threads of 2: 0.87), 4096 0.86 and 0.90 (512 threads of 2:
+// 0.83 and 0.60; 128 of 8: 0.85 and 0.85), 8192 0.94 and 0.80 (256 of 8: 0.85
+// and 0.77), 16384 0.84 and 0.62 (1024 of 4: 0.62 and 0.58).  Copying the rows
+// after next to shared memory meanwhile was slower at every width up to 4096.
+template <bool BWD, class F> void for_width(int64_t N, F f) {
+    auto of = [&](auto T, auto NV) { f(T, NV); };
     using std::integral_constant;
-    if (N <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    else if (N <= 256) f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-    else if (N <= 512) f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-    else if (N <= 1024) f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-    else if (N <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (N <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-    else if (N <= 8192) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-    else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+#define EMU_WIDTH(T, NV) of(integral_constant<int, T>{}, integral_constant<int, NV>{})
+    if (N <= 16) EMU_WIDTH(4, 1);
+    else if (N <= 32) EMU_WIDTH(8, 1);
+    else if (N <= 64) EMU_WIDTH(16, 1);
+    else if (N <= 128) EMU_WIDTH(32, 1);
+    else if (N <= 256) EMU_WIDTH(32, 2);
+    else if (N <= 512) EMU_WIDTH(32, 4);
+    else if (N <= 1024) EMU_WIDTH(128, 2);
+    else if (N <= 2048) EMU_WIDTH(BWD ? 128 : 256, BWD ? 4 : 2);
+    else if (N <= 4096) EMU_WIDTH(256, 4);
+    else if (N <= 8192) EMU_WIDTH(512, 4);
+    else EMU_WIDTH(512, 8);
+#undef EMU_WIDTH
 }
 
 // Blocks of a kernel that are resident on an SM at once (asked for once; the
@@ -301,29 +326,6 @@ ln_bwd_params_kernel(int64_t M, int64_t N, int64_t rows_per, const float* dY, in
 
 }  // namespace
 
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* partial, int P, int64_t C, int64_t split,
-                                                            float* out0, float* out1) {
-    __shared__ float part[32][33];
-    const int64_t c = blockIdx.x * 32ll + threadIdx.x;
-    float s = 0.f;
-    if (c < C)
-        for (int p = threadIdx.y; p < P; p += 32) s += partial[(int64_t)p * C + c];
-    part[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < C) {
-        float t = part[0][threadIdx.x];
-        for (int i = 1; i < 32; ++i) t += part[i][threadIdx.x];
-        if (c < split) { if (out0) out0[c] = t; }
-        else if (out1) out1[c - split] = t;
-    }
-}
-cudaError_t launch_sum_partials(const float* partial, int P, int64_t C, int64_t split, float* out0, float* out1,
-                                cudaStream_t stream) {
-    cudaGetLastError();
-    sum_partials_kernel<<<(unsigned)((C + 31) / 32), dim3(32, 32), 0, stream>>>(partial, P, C, split, out0, out1);
-    return cudaGetLastError();
-}
-
 }  // namespace emu
 
 using namespace emu;
@@ -344,7 +346,7 @@ emu_status_t emu_layer_norm_fwd(int64_t M, int64_t N, const float* X, int64_t ld
     cudaGetLastError();
     if (N <= kMaxRegsWidth) {
         const bool vec = (N & 3) == 0 && vec4_ok(X, ldx) && vec4_ok(Y, ldy) && vec4_ok(weight, 0) && vec4_ok(bias, 0);
-        for_width(N, [&](auto T, auto NV) {
+        for_width<false>(N, [&](auto T, auto NV) {
             constexpr int t = decltype(T)::value, nv = decltype(NV)::value;
             auto launch = [&](auto VEC) {
                 constexpr auto kernel = ln_fwd_regs_kernel<t, nv, decltype(VEC)::value>;
@@ -388,7 +390,7 @@ emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float* dY, int64_t l
         const bool vec = (N & 3) == 0 && vec4_ok(dY, lddy) && vec4_ok(X, ldx) && vec4_ok(weight, 0) &&
                          vec4_ok(add, add ? ldadd : 0) && vec4_ok(dX, dX ? lddx : 0);
         cudaError_t e = cudaSuccess;
-        for_width(N, [&](auto T, auto NV) {
+        for_width<true>(N, [&](auto T, auto NV) {
             constexpr int t = decltype(T)::value, nv = decltype(NV)::value;
             auto launch = [&](auto VEC) {
                 constexpr auto kernel = ln_bwd_regs_kernel<t, nv, decltype(VEC)::value>;
@@ -401,7 +403,8 @@ emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float* dY, int64_t l
                 kernel<<<grid, kBlockThreads<t>, 0, s>>>(M, N, dY, lddy, X, ldx, weight, mean, rstd, add, ldadd, dX, lddx,
                                                          partial);
                 e = cudaGetLastError();
-                if (e == cudaSuccess && params) e = launch_sum_partials(partial, (int)grid, 2 * N, N, dweight, dbias, s);
+                const Partials sums{partial, (int)grid, 2 * N, N, dweight, dbias};
+                if (e == cudaSuccess && params) e = launch_sum_partials(&sums, 1, s);
             };
             if (vec) launch(std::true_type{}); else launch(std::false_type{});
         });
@@ -428,8 +431,8 @@ emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float* dY, int64_t l
         ln_bwd_params_kernel<<<dim3((unsigned)col_blocks, (unsigned)chunks), 256, 0, s>>>(M, N, rows_per, dY, lddy, X,
                                                                                           ldx, mean, rstd, partial);
     if (cudaGetLastError() != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
-    if (params && launch_sum_partials(partial, (int)chunks, 2 * N, N, dweight, dbias, s) != cudaSuccess)
-        return EMU_STATUS_LAUNCH_FAILED;
+    const Partials sums{partial, (int)chunks, 2 * N, N, dweight, dbias};
+    if (params && launch_sum_partials(&sums, 1, s) != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
     return EMU_STATUS_SUCCESS;
 }
 

@@ -5,6 +5,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace emu {
 
 inline bool vec4_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld & 3) == 0; }
@@ -45,13 +47,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// out[c] = sum over p of partial[p * C + c], p ascending in 32 interleaved
-// chains that are then added in a fixed order: the sums do not depend on
-// timing.  Block: 32 columns x 32 chains.
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* partial, int P, int64_t C, int64_t split,
-                                                            float* out0, float* out1);
-// Columns [0, split) go to out0, [split, C) to out1; a null output is skipped.
-cudaError_t launch_sum_partials(const float* partial, int P, int64_t C, int64_t split, float* out0, float* out1,
-                                cudaStream_t stream);
+// Sums over the rows of P x C partial sums: out0[c] for columns below `split`,
+// out1[c - split] for the others (a null output is skipped).
+struct Partials {
+    const float* p;
+    int P;
+    int64_t C, split;
+    float *out0, *out1;
+};
+// Up to two sets in one launch, as the dependent of the kernel launched on
+// `stream` just before, which has to be this library's.
+cudaError_t launch_sum_partials(const Partials* sets, int n, cudaStream_t stream);
 
 }  // namespace emu

@@ -44,8 +44,9 @@ def done():
 
 
 # ------------------------------------------------------------- layer norm --
-LN_SHAPES = [(1, 1), (3, 2), (5, 31), (1, 256), (33, 64), (192, 256), (700, 257), (65, 512), (40, 1000), (37, 1001),
-             (9, 1024), (12, 2050), (5, 4096), (3, 8192), (4, 9001), (2, 20000), (2, 40003)]
+LN_SHAPES = [(1, 1), (3, 2), (65, 4), (50, 16), (77, 13), (33, 17), (130, 32), (5, 31), (129, 61), (33, 64), (40, 128),
+             (1, 256), (192, 256), (700, 257), (65, 512), (40, 1000), (37, 1001), (9, 1024), (20, 2048), (12, 2050),
+             (5, 4096), (3, 8192), (4, 9001), (3, 16384), (2, 16383), (2, 20000), (2, 40003)]
 
 
 @pytest.mark.parametrize("M,N", LN_SHAPES)
