@@ -572,6 +572,7 @@ emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, c
             return EMU_STATUS_ALLOC_FAILED;
         }
     }
+    if (!workspace_slot(dev, w->side)) return EMU_STATUS_ALLOC_FAILED;  // the side stream's own buffers
     *side = w->side; *fork = w->fork; *join = w->join;
     return EMU_STATUS_SUCCESS;
 }
@@ -1224,8 +1225,9 @@ int two_share(const Gemm& a, const Gemm& b, int pairs) {
     const double apart = cost(a, pairs) + cost(b, pairs) + kLaunchStages;
     double best = 0.95 * apart;
     int share = 0;
-    for (int i = 2; i <= 6; ++i) {  // quarters to three quarters of the GPU
-        const int p = pairs * i / 8;
+    for (int i = 0; i <= 14; ++i) {  // a half, and from an eighth to seven eighths in steps
+        const int p = i == 0 ? pairs / 2 : pairs / 8 + (pairs * 3 / 4) * (i - 1) / 13;
+        if (p < 1 || p >= pairs) continue;
         const double ca = cost(a, p), cb = cost(b, pairs - p), c = ca > cb ? ca : cb;
         if (c < best) { best = c; share = p; }
     }
@@ -1259,17 +1261,21 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
         static const bool on = env_int("EMU_SIDE", 1) != 0;
         if (on) share = two_share(*a, *b, dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0]);
     }
+    int devid = 0;
+    cudaStream_t side = nullptr;
+    cudaEvent_t fork = nullptr, join = nullptr;
+    // (in turn, too, when the table of streams has no room for the side stream)
+    if (share > 0 && (cudaGetDevice(&devid) != cudaSuccess ||
+                      side_stream_for(devid, stream, &side, &fork, &join) != EMU_STATUS_SUCCESS)) {
+        cudaGetLastError();
+        share = 0;
+    }
     if (share == 0) {
         const emu_status_t st = gemm(mode, *a, stream, check);
         return st == EMU_STATUS_SUCCESS ? gemm(mode, *b, stream, check) : st;
     }
     const int rest = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0] - share;
-    int devid = 0;
-    cudaGetDevice(&devid);
-    cudaStream_t side;
-    cudaEvent_t fork, join;
-    emu_status_t st = side_stream_for(devid, stream, &side, &fork, &join);
-    if (st != EMU_STATUS_SUCCESS) return st;
+    emu_status_t st = EMU_STATUS_SUCCESS;
     if (check) {
         st = gemm_on(mode, *a, stream, UNTIL_RESERVED, share);
         return st == EMU_STATUS_SUCCESS ? gemm_on(mode, *b, side, UNTIL_RESERVED, rest) : st;
@@ -1516,7 +1522,7 @@ emu_status_t emu_dispatch_query(emu_mode_t mode, int64_t M, int64_t N, int64_t K
     return EMU_STATUS_SUCCESS;
 }
 
-int emu_version(void) { return 200; }
+int emu_version(void) { return 300; }
 
 }  // extern "C"
 

@@ -1141,7 +1141,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 };
                 float* h = p.c + lrow * p.ldc + gcol;
                 float* d = save.value ? ep.d + lrow * ep.ldd + gcol : nullptr;
-                if (row0 + 32 <= p.M && col0 + GC * (c + 1) <= p.N && ep.vec_up) {
+                if (row0 + 32 <= p.M && col0 + GC * (c + 1) <= p.N) {
 #pragma unroll
                     for (int pass = 0; pass < GPR; pass += 2) {
                         float4 g[2], u[2], f[2];
@@ -1156,8 +1156,15 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                         if constexpr (save.value) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                *reinterpret_cast<float4*>(d) = mul4(u[k], f[k]);
-                                *reinterpret_cast<float4*>(d + ep.F) = g[k];
+                                __stcs(reinterpret_cast<float4*>(d), mul4(u[k], f[k]));
+                                if constexpr (save.value == 1) {
+                                    __stcs(reinterpret_cast<float4*>(d + ep.F), g[k]);
+                                } else {
+                                    __stcs(d + ep.F, g[k].x);
+                                    __stcs(d + ep.F + 1, g[k].y);
+                                    __stcs(d + ep.F + 2, g[k].z);
+                                    __stcs(d + ep.F + 3, g[k].w);
+                                }
                                 d += ROWS * ep.ldd;
                             }
                         }
@@ -1186,8 +1193,9 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             }
             };
             for_family(ep.act.family, [&](auto fam) {
-                if (ep.d) phase(fam, ValueIs<1>{});
-                else phase(fam, ValueIs<0>{});
+                if (!ep.d) phase(fam, ValueIs<0>{});
+                else if (ep.vec_up) phase(fam, ValueIs<1>{});
+                else phase(fam, ValueIs<2>{});  // D's up half off the 16-byte boundaries
             });
             } else {
             // the same blocks as EPI_STORE's
@@ -1236,7 +1244,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
                                     if constexpr (save.value) {
-                                        *reinterpret_cast<float4*>(d) = f[j];
+                                        __stcs(reinterpret_cast<float4*>(d), f[j]);
                                         d += RPP * ep.ldd;
                                     }
                                     *reinterpret_cast<float4*>(out) = add4(v[j], r[k + j]);
@@ -1265,7 +1273,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                     float4 sg = make_float4(0.f, 0.f, 0.f, 0.f), su = sg;
                     const float* d = ep.d + lrow * ep.ldd + gcol;
                     __syncwarp();
-                    if (whole && ep.vec_up) {
+                    if (whole) {
                         // D goes into the registers the staged block left (from
                         // L2: the unit's start prefetched it)
 #pragma unroll
@@ -1274,14 +1282,22 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                             for (int k = 0; k < BATCH; ++k) {
                                 g[k] = __ldg(reinterpret_cast<const float4*>(d));
-                                u[k] = __ldg(reinterpret_cast<const float4*>(d + ep.F));
+                                if constexpr (save.value) u[k] = __ldg(reinterpret_cast<const float4*>(d + ep.F));
+                                else u[k] = make_float4(__ldg(d + ep.F), __ldg(d + ep.F + 1), __ldg(d + ep.F + 2), __ldg(d + ep.F + 3));
                                 d += RPP * ep.ldd;
                             }
 #pragma unroll
                             for (int k = 0; k < BATCH; ++k) {
                                 const float4 dh = staged(pass + k), dg = mul4(dh, g[k]), du = mul4(dh, u[k]);
                                 *reinterpret_cast<float4*>(out) = dg;
-                                *reinterpret_cast<float4*>(out + ep.F) = du;
+                                if constexpr (save.value) {
+                                    *reinterpret_cast<float4*>(out + ep.F) = du;
+                                } else {
+                                    out[ep.F] = du.x;
+                                    out[ep.F + 1] = du.y;
+                                    out[ep.F + 2] = du.z;
+                                    out[ep.F + 3] = du.w;
+                                }
                                 out += RPP * p.ldc;
                                 sg = add4(sg, dg);
                                 su = add4(su, du);
@@ -1321,7 +1337,9 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                     if (ep.d) phase(fam, ValueIs<1>{});
                     else phase(fam, ValueIs<0>{});
                 });
-            else
+            else if (ep.vec_up)
+                phase(ValueIs<FAMILY_LINEAR>{}, ValueIs<1>{});
+            else  // the up halves off the 16-byte boundaries
                 phase(ValueIs<FAMILY_LINEAR>{}, ValueIs<0>{});
             }
         }

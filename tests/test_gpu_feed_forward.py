@@ -268,7 +268,7 @@ def test_gated_every_plan(M, K, F, mode):
         v.check(host(got), name)
 
 
-@pytest.mark.parametrize("M,K,F,N", [(6144, 64, 300, 96), (700, 96, 520, 2100), (333, 40, 50, 2500)])
+@pytest.mark.parametrize("M,K,F,N", [(6144, 64, 300, 96), (6144, 16, 1000, 64), (700, 96, 520, 2100), (333, 40, 50, 2500)])
 @pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
 def test_gated_ffn_backward_every_plan(M, K, F, N, mode):
     """The block's backward pass where dY W_out is chained or split."""
@@ -539,6 +539,45 @@ def test_captured_in_a_graph():
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
     done()
+
+
+def test_offsets_beyond_32_bits():
+    """Matrices of more than 2^31 elements: the last rows are right and the
+    first ones too."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("long")
+    M, K, F = 530_000, 12, 2048                    # D and dZ: 2.17e9 elements
+    rows = np.concatenate([np.arange(0, M, 100_003), np.arange(M - 5, M)])
+    x, w, b = f32(rng, M, K), f32(rng, 2 * F, K, std=0.3), f32(rng, 2 * F, std=0.1)
+    dh = torch.zeros((M, F), device=_gpu.device())
+    some = f32(rng, len(rows), F)
+    dh[torch.from_numpy(rows).to(_gpu.device())] = dev(some)
+    xd, wd = dev(x), dev(w)
+    h, d = emu.gated_fwd(xd, wd, dev(b), save=True)
+    at = torch.from_numpy(rows).to(_gpu.device())
+    wh, wd64 = gated_reference(x[rows], w, b, "silu", "bf16x9")
+    wh.check(host(h[at]), "H")
+    wd64.check(host(d[at]), "D")
+    dx, dw, db = emu.gated_bwd(dh, xd, wd, d)
+    done()
+    want = gated_grads(V(some), x[rows], w, "bf16x9", wd64)
+    want[0].check(host(dx[at]), "dX")
+    # the other rows of dH are zero; the products' bound counts all of them
+    dz = beside(V(some) * wd64.cols(0, F), V(some) * wd64.cols(F, 2 * F))
+    V(want[1].val, dz.err.T @ np.abs(x[rows]) + R.TERMS["bf16x9"](M) * R.U * (np.abs(dz.val).T @ np.abs(x[rows]))).check(host(dw), "dW")
+    V(want[2].val, dz.err.sum(0) + (M / 32 + 96) * R.U * np.abs(dz.val).sum(0)).check(host(db), "db")
+    del h, d, dh, dx, dw
+    N = 4112                                       # 2.18e9 elements
+    x = torch.empty((M, N), device=_gpu.device()).normal_()
+    wn, bn = f32(rng, N), f32(rng, N)
+    y, mean, rstd = emu.layer_norm_fwd(x, dev(wn), dev(bn))
+    xs = host(x[at]).astype(np.float64)
+    R.layer_norm(xs, wn, bn, EPS)[0].check(host(y[at]), "Y")
+    dx, dwn, dbn = emu.layer_norm_bwd(y, x, dev(wn), mean, rstd)
+    done()
+    ys = host(y[at])
+    R.layer_norm_grads(ys, xs, wn, EPS)[0].check(host(dx[at]), "dX of the norm")
 
 
 def test_degenerate_sizes():
