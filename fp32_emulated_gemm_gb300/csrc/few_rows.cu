@@ -15,7 +15,8 @@
 // one token K = 1024, N = 4096 5.8 us (22.6; 2.5 at the copy rate from memory),
 // K = 4096, N = 1024 3.7 us (31.4), gated K = 1024, F = 4096 8.4 us (31.4);
 // eight tokens 9.0, 9.0 and 16.0 us; 64 tokens K = 256, N = 1024 8.5 us (14.3),
-// K = 1024, N = 4096 56 us (22.8).  From eight rows on it is bound by L1 and
+// K = 1024, N = 4096 56 us (22.8); one token K = 1024, N = 40000, weights from
+// memory, 26.7 us (97; 24.2 at the copy rate).  From eight rows on it is bound by L1 and
 // the FMAs at 5 TFMA/s; eight weight rows a warp (64 sums a thread) were slower
 // (K = 1024, N = 4096, eight tokens: 12.0 us), for they halve the warps.
 #include "few_rows.h"
@@ -191,7 +192,7 @@ cudaError_t launch(const FewRows& p, bool gated, bool after_own, int sm_count, c
 }  // namespace
 
 bool few_rows_fit(int64_t M, int64_t N, int64_t K) {
-    return M <= kFewRowsMax && (double)M * (double)N * (double)K <= kFewRowsFma;
+    return M <= kFewRowsMax && (double)(M - 8) * (double)N * (double)K <= kFewRowsFma;
 }
 
 cudaError_t launch_few_rows(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream) {

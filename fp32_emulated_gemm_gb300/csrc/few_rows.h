@@ -9,12 +9,14 @@
 
 namespace emu {
 
-// A forward pass of few enough multiplications runs on the CUDA cores instead of
-// in 256-row tiles: N counts every column of the weight (both halves of a gated
-// one).  The tiles take 14 us or more, this form 3 us and 0.2 us for each
-// million multiplications, measured for 1 to 64 rows of layers from 256 x 1024
-// to 2048 x 8192 (see few_rows.cu); the bound on M keeps to that range of
-// shapes.
+// A forward pass of few enough rows runs on the CUDA cores instead of in 256-row
+// tiles; N counts every column of the weight (both halves of a gated one).
+// Measured from 1 to 64 rows and from 256 x 1024 to 1024 x 40000 weights, this
+// form takes 3 us and, for a million weights, 0.65 us at one row to 1.5 us at
+// eight and 0.19 us a row from there; the tiles take 14 us and 2.2 us for a
+// million weights.  So up to eight rows always, and more while (M - 8) N K is
+// within the 11 us between the fixed costs; the bound on M keeps to shapes
+// like the measured ones.
 constexpr double kFewRowsFma = 50e6;
 constexpr int64_t kFewRowsMax = 1024;
 bool few_rows_fit(int64_t M, int64_t N, int64_t K);

@@ -121,7 +121,7 @@ def few_rows(M, N, K):
     """Whether a forward pass of M rows through N columns of weights runs in
     the library's few-row form (emu_few_rows_query), which takes matrices of
     any alignment."""
-    return M <= 1024 and M * N * K <= 50_000_000
+    return M <= 1024 and (M - 8) * N * K <= 50_000_000
 
 
 def _forward_matrix(X, W, mode):

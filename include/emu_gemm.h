@@ -209,15 +209,26 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  *   EMU_STATUS_NOT_SUPPORTED.  Widths are free.  emu_layer_norm_* takes any
  *   alignment of whole words.
  * Outputs must not overlap inputs or one another.
- * Few rows: a forward pass of at most 1,024 rows and 50 million multiplications
- *   (M N K, both halves of a gated weight counted) in the modes BF16X9 and
- *   TF32X3 runs on the CUDA cores in FP32, within the modes' bounds, and takes
- *   matrices and biases of any alignment of whole words
- *   (emu_few_rows_query, host only, says 1 or 0).
+ * Few rows: a forward pass of at most 1,024 rows with (M - 8) N K <= 50 million
+ *   (N with both halves of a gated weight) in the modes BF16X9 and TF32X3 runs
+ *   on the CUDA cores in FP32, within the modes' bounds, and takes matrices and
+ *   biases of any alignment of whole words (emu_few_rows_query, host only, says
+ *   1 or 0).
  * Sizes: M == 0 writes nothing but zero sums (weight and bias gradients);
  *   K == 0 leaves the bias.
- * Buffers: the sums over rows take a buffer of partial sums from the
- *   library, kept per (device, stream) like the split-K workspace.
+ * Buffers: the sums over rows take a buffer of partial sums from the library,
+ *   kept per (device, stream) like the split-K workspace; for the gated block
+ *   it holds 2F floats for every 32 rows.  A call that returns an error has
+ *   enqueued nothing, as elsewhere: every launch's buffers are reserved first.
+ * Streams: two independent products of a backward pass run side by side, one of
+ *   them on a stream of the library's (a second entry of its table of 64; with
+ *   no room there they run in turn), where the launch plans' costs predict a
+ *   gain.  The stream is ordered with `stream` by events on both sides, so for
+ *   the caller the call is work on `stream` like any other.  A capture into a
+ *   graph wants one call of the same sizes on the capturing stream before it
+ *   (the buffers' allocation).
+ * Strategy: a product with an epilogue of this section always emulates; the
+ *   plain products of the backward passes follow emu_set_strategy.
  * Repeatability: all sums are added in an order fixed by the sizes and the
  *   device; no atomics.
  */

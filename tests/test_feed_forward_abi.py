@@ -64,8 +64,9 @@ def test_host_checks_answer_without_a_device(ff):
 def test_few_row_rule_is_the_librarys(ff):
     q = emu.load().emu_few_rows_query
     q.argtypes = [ctypes.c_int64] * 3
-    for M, N, K in ((1, 1, 1), (1024, 1, 1), (1025, 1, 1), (0, 4, 4), (1024, 128, 381), (1024, 128, 382), (1, 50_000_000, 1),
-                    (1, 50_000_001, 1), (64, 1024, 762), (64, 1024, 763), (1024, 2 ** 31 - 257, 2 ** 31 - 257)):
+    for M, N, K in ((1, 1, 1), (1024, 1, 1), (1025, 1, 1), (0, 4, 4), (1024, 128, 384), (1024, 128, 385), (9, 50_000_000, 1),
+                    (9, 50_000_001, 1), (8, 2 ** 30, 2 ** 20), (64, 1024, 871), (64, 1024, 872),
+                    (1024, 2 ** 31 - 257, 2 ** 31 - 257)):
         assert q(M, N, K) == int(ff.few_rows(M, N, K)), (M, N, K)
 
 

@@ -131,7 +131,7 @@ def linear_act_reference(x, w, b, act, r, dy, mode, d_gpu=None):
 LINEAR_SHAPES = [(1, 1, 1), (1, 300, 64), (1, 64, 1024), (2, 129, 33), (5, 96, 100), (8, 257, 260), (9, 40, 7),
                  (16, 512, 128), (17, 100, 36), (40, 30, 500), (300, 260, 200), (257, 1, 64), (130, 131, 37),
                  (1100, 520, 72), (1025, 1, 1), (1030, 129, 33), (1100, 257, 260), (1281, 40, 7), (1025, 131, 37),
-                 (63, 1024, 770), (64, 1024, 770)]
+                 (71, 1024, 770), (72, 1024, 770), (8, 4000, 2000)]
 
 
 @pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
