@@ -61,6 +61,8 @@ struct Workspace {
     size_t packed_bytes = 0;
     float* reduce = nullptr;  // column-sum partials of the row-wise operators
     size_t reduce_floats = 0;
+    float* align = nullptr;   // aligned copies of operands
+    size_t align_floats = 0;
     cudaStream_t side = nullptr;  // for a product that runs beside one on `stream`
     cudaEvent_t fork = nullptr, join = nullptr;
 };
@@ -540,22 +542,24 @@ emu_status_t packed_buffer_for(int dev, cudaStream_t stream, size_t bytes, void*
     return EMU_STATUS_SUCCESS;
 }
 
-// The (device, stream)'s buffer for column-sum partials, grown on demand and kept.
-emu_status_t reduce_buffer_for(int dev, cudaStream_t stream, size_t floats, float** out) {
+// A float buffer of the (device, stream) (column-sum partials, aligned copies),
+// grown on demand and kept.
+emu_status_t float_buffer_for(int dev, cudaStream_t stream, float* Workspace::*buffer, size_t Workspace::*size,
+                              size_t floats, float** out) {
     std::lock_guard<std::mutex> lock(g_mutex);
     Workspace* w = workspace_slot(dev, stream);
     if (!w) return EMU_STATUS_ALLOC_FAILED;
-    if (w->reduce_floats < floats) {
-        if (w->reduce && cudaFreeAsync(w->reduce, stream) != cudaSuccess) cudaGetLastError();
-        w->reduce = nullptr;
-        w->reduce_floats = 0;
-        if (lib_malloc_async(reinterpret_cast<void**>(&w->reduce), floats * sizeof(float), stream) != cudaSuccess) {
+    if (w->*size < floats) {
+        if (w->*buffer && cudaFreeAsync(w->*buffer, stream) != cudaSuccess) cudaGetLastError();
+        w->*buffer = nullptr;
+        w->*size = 0;
+        if (lib_malloc_async(reinterpret_cast<void**>(&(w->*buffer)), floats * sizeof(float), stream) != cudaSuccess) {
             cudaGetLastError();
             return EMU_STATUS_ALLOC_FAILED;
         }
-        w->reduce_floats = floats;
+        w->*size = floats;
     }
-    *out = w->reduce;
+    *out = w->*buffer;
     return EMU_STATUS_SUCCESS;
 }
 
@@ -1184,7 +1188,10 @@ emu_status_t current_device(DeviceCtx* out) {
 }
 
 emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float** out) {
-    return reduce_buffer_for(dev, stream, floats, out);
+    return float_buffer_for(dev, stream, &Workspace::reduce, &Workspace::reduce_floats, floats, out);
+}
+emu_status_t align_scratch(int dev, cudaStream_t stream, size_t floats, float** out) {
+    return float_buffer_for(dev, stream, &Workspace::align, &Workspace::align_floats, floats, out);
 }
 
 namespace {
@@ -1252,9 +1259,11 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
         }
     }
     // (no caller passes a gated pair: its tiles are not the plan's of M x N)
-    const bool real = !(a->fused && a->fused->kind == FUSED_GATED) && !(b->fused && b->fused->kind == FUSED_GATED) && a->M > 0 && a->N > 0 && a->K > 0 && b->M > 0 && b->N > 0 && b->K > 0 && emulated_mode(mode) &&
-                      a->M <= INT32_MAX - 256 && b->M <= INT32_MAX - 256 && a->N <= INT32_MAX - 256 &&
-                      b->N <= INT32_MAX - 256 && a->K <= INT32_MAX - 256 && b->K <= INT32_MAX - 256;
+    auto sized = [](const Gemm& g) {
+        return g.M > 0 && g.N > 0 && g.K > 0 && g.M <= INT32_MAX - 256 && g.N <= INT32_MAX - 256 &&
+               g.K <= INT32_MAX - 256 && !(g.fused && g.fused->kind == FUSED_GATED);
+    };
+    const bool real = emulated_mode(mode) && sized(*a) && sized(*b);
     if (real && g_strategy.load(std::memory_order_relaxed) != EMU_STRATEGY_PERFORMANT) {
         const emu_status_t st = device_info(&dev);
         if (st != EMU_STATUS_SUCCESS) return st;
@@ -1471,6 +1480,7 @@ emu_status_t emu_shutdown(void) {
         if (w.counters && cudaFree(w.counters) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.packed && cudaFree(w.packed) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.reduce && cudaFree(w.reduce) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        if (w.align && cudaFree(w.align) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.side && cudaStreamDestroy(w.side) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.fork && cudaEventDestroy(w.fork) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.join && cudaEventDestroy(w.join) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }

@@ -21,6 +21,8 @@ namespace {
 // The row-wise kernels: a warp covers 128 columns (a float4 per lane, or four
 // words 32 apart where rows are not 16-byte aligned) of one row at a time, the
 // eight warps of a block take rows in turn, and a block has one chunk of rows.
+// They are bound by memory: the gated backward kernel with its sums, 65536 x
+// 1024 (1.34 GB), 215 us, 92% of the copy rate.
 constexpr int kWarps = 8, kCols = 128;
 
 struct RowGrid { dim3 grid; int64_t rows_per; int chunks; };
@@ -60,6 +62,89 @@ act_fwd_kernel(ActParams act, int64_t M, int64_t N, int64_t rows_per, const floa
         store4<VEC, S>(Y + r * ldy, c, N, y);
     }
 }
+
+// Copies of matrices, a warp a row at a time.
+struct CopyJob {
+    const float* src;
+    int64_t lds;
+    float* dst;
+    int64_t ldd, rows, cols;
+};
+constexpr int kMaxCopies = 7;
+struct CopyJobs { int n; CopyJob job[kMaxCopies]; };
+__global__ void __launch_bounds__(32 * kWarps) copy_rows_kernel(const CopyJobs jobs) {
+    int64_t r = blockIdx.x * (int64_t)kWarps + threadIdx.y;
+    for (int i = 0; i < jobs.n; ++i) {
+        const CopyJob& j = jobs.job[i];
+        for (; r < j.rows; r += (int64_t)gridDim.x * kWarps) {
+            const float* src = j.src + r * j.lds;
+            float* dst = j.dst + r * j.ldd;
+#pragma unroll 4
+            for (int64_t c = threadIdx.x; c < j.cols; c += 32) dst[c] = src[c];
+        }
+        r -= j.rows;
+    }
+}
+
+// Operands of the products (TMA) whose rows do not start on 16-byte boundaries
+// are read from copies that do, in a buffer of the library's: all of a call's
+// by one launch ahead of its first product.  A matrix off the boundaries that
+// is read once is a quarter of the copies' cost to handle here rather than by
+// the caller: block forward 3740x169x320 ALIGN_WAS -> ALIGN_IS us.
+class Aligned {
+public:
+    void add(const float*& p, int64_t& ld, int64_t rows, int64_t cols) {
+        if (!p || rows < 1 || cols < 1 || ld < cols || vec4_ok(p, rows > 1 ? ld : 0)) {
+            if (rows == 1 && p && ld >= cols) ld = (ld + 3) & ~int64_t(3);  // one row: any stride
+            return;
+        }
+        CopyJob& j = jobs_.job[jobs_.n];
+        j = {p, ld, nullptr, (cols + 3) & ~int64_t(3), rows, cols};
+        p_[jobs_.n] = &p;
+        ld_[jobs_.n++] = &ld;
+        floats_ += (size_t)rows * j.ldd;
+    }
+    void add_vector(const float*& p, int64_t n) {
+        int64_t& ld = vector_ld_[vectors_++];
+        ld = n;
+        add(p, ld, 1, n);
+    }
+    // the copies' addresses take the place of the operands'
+    emu_status_t reserve(cudaStream_t s) {
+        if (jobs_.n == 0) return EMU_STATUS_SUCCESS;
+        DeviceCtx dev;
+        emu_status_t st = current_device(&dev);
+        float* base = nullptr;
+        if (st == EMU_STATUS_SUCCESS) st = align_scratch(dev.id, s, floats_, &base);
+        if (st != EMU_STATUS_SUCCESS) return st;
+        for (int i = 0; i < jobs_.n; ++i) {
+            CopyJob& j = jobs_.job[i];
+            j.dst = base;
+            *p_[i] = base;
+            *ld_[i] = j.ldd;
+            base += j.rows * j.ldd;
+            rows_ += j.rows;
+        }
+        const int64_t blocks = (rows_ + kWarps - 1) / kWarps;
+        blocks_ = (unsigned)(blocks < dev.sm_count * 8 ? blocks : dev.sm_count * 8);
+        return EMU_STATUS_SUCCESS;
+    }
+    cudaError_t launch(cudaStream_t s) const {
+        if (jobs_.n == 0) return cudaSuccess;
+        cudaGetLastError();
+        copy_rows_kernel<<<blocks_, dim3(32, kWarps), 0, s>>>(jobs_);
+        return cudaGetLastError();
+    }
+
+private:
+    CopyJobs jobs_{};
+    const float** p_[kMaxCopies];
+    int64_t* ld_[kMaxCopies];
+    int64_t vector_ld_[2], rows_ = 0;
+    int vectors_ = 0;
+    size_t floats_ = 0;
+    unsigned blocks_ = 0;
+};
 
 // Four columns' sums of the block's eight warps, added in order, to out[c ..].
 template <bool VEC>
@@ -137,7 +222,9 @@ __global__ void __launch_bounds__(32 * kWarps) column_sums_kernel(const SumJob a
 }
 
 // p ascending in 32 interleaved chains, which are then added in order: the
-// sums do not depend on timing.  Block: 32 columns x 32 chains.
+// sums do not depend on timing.  Block: 32 columns x 32 chains.  A few hundred
+// rows of partial sums take 2 to 3 us, mostly the launch, which overlaps the
+// end of the kernel before it.
 struct PartialsPair { Partials set[2]; unsigned first_blocks; };
 __global__ void __launch_bounds__(1024) sum_partials_kernel(const PartialsPair pair) {
     __shared__ float part[32][33];
@@ -354,8 +441,17 @@ emu_status_t emu_linear_act_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64
     if (!Y || ldy < N || (residual && ldr < N) || (D && ldd < N)) return EMU_STATUS_INVALID_VALUE;
     DeviceCtx dev{};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Aligned al;
+    if (!few_rows(mode, M, N, K)) {
+        al.add(X, ldx, M, K);
+        al.add(W, ldw, N, K);
+        al.add(residual, ldr, M, N);
+        al.add_vector(bias, N);
+    }
+    EMU_TRY(al.reserve(s));
     EMU_TRY(linear_act_fwd(mode, act, M, N, K, X, ldx, W, ldw, bias, residual, ldr, D, ldd, Y, ldy, dev, s, true));
     EMU_TRY(current_device(&dev));
+    EMU_TRY(launched(al.launch(s)));
     return linear_act_fwd(mode, act, M, N, K, X, ldx, W, ldw, bias, residual, ldr, D, ldd, Y, ldy, dev, s, false);
 }
 
@@ -368,15 +464,21 @@ emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K
     const bool rows = M > 0 && N > 0;
     if (rows && (!dY || lddy < N || (D && (!dZ || ldd < N || lddz < N)))) return EMU_STATUS_INVALID_VALUE;
     const bool apply = D && rows;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Aligned al;  // (D and, with it, dY are not a product's)
+    if (!D) al.add(dY, lddy, M, N);
+    if (dW) al.add(X, ldx, M, K);
+    if (dX) al.add(W, ldw, N, K);
+    EMU_TRY(al.reserve(s));
     const float* G = D ? dZ : dY;
     const int64_t ldg = D ? lddz : lddy;
     const Gemm gx = input_product(M, N, K, G, ldg, W, ldw, dX, lddx), gw = weight_product(M, N, K, G, ldg, X, ldx, dW, lddw);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, true));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     float* scratch = nullptr;
     if (dbias) EMU_TRY(reduce_scratch(dev.id, s, act_bwd_floats(false, M, N, dev.sm_count), &scratch));
+    EMU_TRY(launched(al.launch(s)));
     if (apply)
         EMU_TRY(launched(launch_act_bwd<false>(M, N, dY, lddy, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
     else if (dbias)
@@ -393,8 +495,16 @@ emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F,
     if (!H || ldh < F || (D && ldd < 2 * F) || (!D && gated_needs_d(mode))) return EMU_STATUS_INVALID_VALUE;
     DeviceCtx dev{};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Aligned al;
+    if (!few_rows(mode, M, 2 * F, K)) {
+        al.add(X, ldx, M, K);
+        al.add(W, ldw, 2 * F, K);
+        al.add_vector(bias, 2 * F);
+    }
+    EMU_TRY(al.reserve(s));
     EMU_TRY(gated_fwd(mode, act, M, F, K, X, ldx, W, ldw, bias, D, ldd, H, ldh, dev, s, true));
     EMU_TRY(current_device(&dev));
+    EMU_TRY(launched(al.launch(s)));
     return gated_fwd(mode, act, M, F, K, X, ldx, W, ldw, bias, D, ldd, H, ldh, dev, s, false);
 }
 
@@ -405,14 +515,19 @@ emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, con
     if (M < 0 || F < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
     if (!size_ok(M) || !size_ok(2 * F) || !size_ok(K)) return EMU_STATUS_NOT_SUPPORTED;
     if (M > 0 && F > 0 && (!dH || !D || !dZ || lddh < F || ldd < 2 * F || lddz < 2 * F)) return EMU_STATUS_INVALID_VALUE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Aligned al;  // (dH and D are not a product's)
+    if (dW) al.add(X, ldx, M, K);
+    if (dX) al.add(W, ldw, 2 * F, K);
+    EMU_TRY(al.reserve(s));
     const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W, ldw, dX, lddx);
     const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW, lddw);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, true));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
     float* scratch = nullptr;
     if (dbias) EMU_TRY(reduce_scratch(dev.id, s, act_bwd_floats(true, M, F, dev.sm_count), &scratch));
+    EMU_TRY(launched(al.launch(s)));
     EMU_TRY(launched(launch_act_bwd<true>(M, F, dH, lddh, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
     return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
 }
@@ -428,7 +543,20 @@ emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_
     if (N > 0 && (!Y || ldy < N || (residual && ldr < N))) return EMU_STATUS_INVALID_VALUE;
     DeviceCtx dev{};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Aligned al;
+    if (!few_rows(mode, M, 2 * F, K)) {
+        al.add(X, ldx, M, K);
+        al.add(W_in, ldwi, 2 * F, K);
+        al.add_vector(b_in, 2 * F);
+    }
+    if (!few_rows(mode, M, N, F)) {
+        al.add(W_out, ldwo, N, F);
+        al.add(residual, ldr, M, N);
+        al.add_vector(b_out, N);
+    }
+    EMU_TRY(al.reserve(s));
     for (const bool check : {true, false}) {
+        if (!check) EMU_TRY(launched(al.launch(s)));
         if (F > 0) EMU_TRY(gated_fwd(mode, act, M, F, K, X, ldx, W_in, ldwi, b_in, D, ldd, H, ldh, dev, s, check));
         if (N > 0)
             EMU_TRY(linear_act_fwd(mode, ACT_NONE, M, N, F, H, ldh, W_out, ldwo, b_out, residual, ldr, nullptr, 0, Y, ldy,
@@ -448,8 +576,20 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     if (M > 0 && N > 0 && (!dY || lddy < N)) return EMU_STATUS_INVALID_VALUE;
     if (M > 0 && F > 0) {
         if (!D || !H || !dZ || ldd < 2 * F || ldh < F || lddz < 2 * F) return EMU_STATUS_INVALID_VALUE;
-        if (!aligned_rows(D, ldd) || !aligned_rows(dZ, lddz)) return EMU_STATUS_NOT_SUPPORTED;
+        if (!aligned_rows(dZ, lddz)) return EMU_STATUS_NOT_SUPPORTED;
     }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool inner = dX || dW_in || db_in;
+    Aligned al;
+    if (inner || dW_out) al.add(dY, lddy, M, N);
+    if (dW_out) al.add(H, ldh, M, F);
+    if (inner) {
+        al.add(W_out, ldwo, N, F);
+        al.add(D, ldd, M, 2 * F);
+    }
+    if (dX) al.add(W_in, ldwi, 2 * F, K);
+    if (dW_in) al.add(X, ldx, M, K);
+    EMU_TRY(al.reserve(s));
     // dZ comes straight from the product's epilogue; or dH takes the gate half
     // of dZ's storage until dZ replaces it in place
     const bool fuse = fused_mode(mode) && N > 0 && M > 0 && F > 0;
@@ -459,8 +599,6 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     const Gemm go = weight_product(M, N, F, dY, lddy, H, ldh, dW_out, lddwo);
     const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W_in, ldwi, dX, lddx);
     const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi);
-    const bool inner = dX || dW_in || db_in;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, true));
     EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, true));
     DeviceCtx dev;
@@ -479,6 +617,7 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
         sums = scratch + out_floats;
     }
     if (fuse && db_in) f.sums = sums;
+    EMU_TRY(launched(al.launch(s)));
     EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, false));
     const bool join = fuse && db_in && direct;
     const Partials in_sums{sums, (int)blocks, 2 * F, 2 * F, db_in, nullptr};

@@ -20,6 +20,9 @@ emu_status_t current_device(DeviceCtx* out);
 // workspace, which a product on the same stream may be using in between.
 emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float** out);
 
+// Likewise its buffer for aligned copies of operands.
+emu_status_t align_scratch(int dev, cudaStream_t stream, size_t floats, float** out);
+
 // What a product's epilogue does besides the bias (the Epi kinds of
 // emu_kernel.cuh; modes BF16x9 and TF32x3, K > 0).
 struct Fused {

@@ -4,11 +4,10 @@ feed-forward block, each with its backward pass.
 
 Like the rest of the binding, the functions only marshal arguments; the
 computation runs in libemu_gemm.so (see ``include/emu_gemm.h`` for the
-contract).  Matrices are CUDA float32 with rows of unit column stride.  A
-matrix that enters a product and does not start on a 16-byte boundary with a
-row stride that is a multiple of 4 is copied into one that does (as every
-matrix of a width that is not a multiple of 4 is, unless it has padded rows
-already: the results of these functions have).
+contract).  Matrices are CUDA float32 with rows of unit column stride (others
+are made contiguous first).  The library copies a product's operand whose rows
+do not start on 16-byte boundaries; the results of these functions have padded
+rows where their width is not a multiple of 4.
 """
 from __future__ import annotations
 
@@ -105,38 +104,12 @@ def _rows(t, name, shape=None):
     return t, t.data_ptr(), t.stride(0) if r > 1 else c
 
 
-def _operand(t, name, shape=None):
-    """`t` as a product's operand: rows on 16-byte boundaries."""
-    t, p, ld = m = _rows(t, name, shape)
-    if not (p & 15 or ld & 3):
-        return m
-    if t.shape[0] == 1 and not p & 15:  # a single row's stride means nothing
-        return t, p, _pad4(ld)
-    q = _new(*t.shape, t.device)
-    q[0].copy_(t)
-    return q
-
-
-def few_rows(M, N, K):
-    """Whether a forward pass of M rows through N columns of weights runs in
-    the library's few-row form (emu_few_rows_query), which takes matrices of
-    any alignment."""
-    return M <= 1024 and (M - 8) * N * K <= 50_000_000
-
-
-def _forward_matrix(X, W, mode):
-    """How a forward pass X W^T wants its matrices: _rows or _operand."""
-    if mode in _FUSED and X.dim() == 2 and W.dim() == 2 and few_rows(X.shape[0], *W.shape):
-        return _rows
-    return _operand
-
-
 def _pad4(n):
     return (n + 3) // 4 * 4
 
 
 def _vector(t, name, n):
-    """(tensor, address) of a vector on a 16-byte boundary."""
+    """(tensor, address) of a vector."""
     if t is None:
         return None, None
     if not isinstance(t, torch.Tensor) or t.dtype is not _float32 or not t.is_cuda:
@@ -145,11 +118,7 @@ def _vector(t, name, n):
         raise ValueError(f"{name} must be a vector of {n}")
     if not t.is_contiguous():
         t = t.contiguous()
-    p = t.data_ptr()
-    if p & 15:
-        t = t.clone()
-        p = t.data_ptr()
-    return t, p
+    return t, t.data_ptr()
 
 
 def _new(M, N, device):
@@ -237,16 +206,15 @@ def linear_act_fwd(X, W, bias=None, *, act="none", residual=None, mode="bf16x9",
     """Y = act(Z) + residual with Z = X W^T + bias (X [M,K], W [N,K]); with
     `save` (Y, D) for linear_act_bwd, D = act'(Z) (None for act "none")."""
     mode = _mode(mode)
-    matrix = _forward_matrix(X, W, mode)
-    X, px, ldx = matrix(X, "X")
-    W, pw, ldw = matrix(W, "W")
+    X, px, ldx = _rows(X, "X")
+    W, pw, ldw = _rows(W, "W")
     M, K = X.shape
     N, Kw = W.shape
     if Kw != K:
         raise ValueError("inner dimensions differ")
     a = _act(act)
     bias, pb = _vector(bias, "bias", N)
-    residual, pr, ldr = _NONE if residual is None else matrix(residual, "residual", (M, N))
+    residual, pr, ldr = _NONE if residual is None else _rows(residual, "residual", (M, N))
     device = X.device
     Y, py, ldy = _result(out, (M, N), device, "out")
     D, pd, ldd = _new(M, N, device) if save and a != EMU_ACT_NONE else _NONE
@@ -259,19 +227,19 @@ def linear_act_bwd(dY, X, W, D=None, *, act="none", mode="bf16x9", need=(True, T
     """(dX, dW, dbias) of linear_act_fwd from its D, which act "none" does not
     read (the residual's gradient is dY).  `need` says which are wanted; the
     others are None."""
-    X, px, ldx = _operand(X, "X")
-    W, pw, ldw = _operand(W, "W")
+    X, px, ldx = _rows(X, "X")
+    W, pw, ldw = _rows(W, "W")
     M, K = X.shape
     N, Kw = W.shape
     if Kw != K:
         raise ValueError("inner dimensions differ")
-    dY, pdy, lddy = _operand(dY, "dY", (M, N))
+    dY, pdy, lddy = _rows(dY, "dY", (M, N))
     device = X.device
     pd, ldd, pdz, lddz = None, 0, None, 0
     if _act(act) != EMU_ACT_NONE:
         if D is None:
             raise ValueError(f"act {act!r} needs D")
-        D, pd, ldd = _operand(D, "D", (M, N))
+        D, pd, ldd = _rows(D, "D", (M, N))
         dZ, pdz, lddz = _new(M, N, device)
     else:
         D = None
@@ -298,9 +266,8 @@ def gated_fwd(X, W, bias=None, *, act="silu", mode="bf16x9", save=False):
     gate's rows, then the up projection's); with `save` (H, D) for
     gated_bwd, D = [U act'(G) | act(G)]."""
     mode = _mode(mode)
-    matrix = _forward_matrix(X, W, mode)
-    X, px, ldx = matrix(X, "X")
-    W, pw, ldw = matrix(W, "W")
+    X, px, ldx = _rows(X, "X")
+    W, pw, ldw = _rows(W, "W")
     M, K, F = _gated_shapes(X, W)
     bias, pb = _vector(bias, "bias", 2 * F)
     H, ph, ldh = _new(M, F, X.device)
@@ -314,11 +281,11 @@ def gated_bwd(dH, X, W, D, *, act="silu", mode="bf16x9", need=(True, True, True)
     """(dX, dW, dbias) of gated_fwd from its D; `need` says which are wanted.
     (D holds the activation's part; `act` only has to name one.)"""
     _act(act)
-    X, px, ldx = _operand(X, "X")
-    W, pw, ldw = _operand(W, "W")
+    X, px, ldx = _rows(X, "X")
+    W, pw, ldw = _rows(W, "W")
     M, K, F = _gated_shapes(X, W)
-    dH, pdh, lddh = _operand(dH, "dH", (M, F))
-    D, pd, ldd = _operand(D, "D", (M, 2 * F))
+    dH, pdh, lddh = _rows(dH, "dH", (M, F))
+    D, pd, ldd = _rows(D, "D", (M, 2 * F))
     device = X.device
     dZ, pdz, lddz = _new(M, 2 * F, device)
     dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
@@ -341,15 +308,13 @@ def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mod
     (X [M,K], W_in [2F,K], W_out [N,F]; the biases and the residual may be
     None); with `save` (Y, D, H) for gated_ffn_bwd."""
     mode = _mode(mode)
-    matrix = _forward_matrix(X, W_in, mode)
-    X, px, ldx = matrix(X, "X")
-    W_in, pwi, ldwi = matrix(W_in, "W_in")
-    matrix = _forward_matrix(X, W_out, mode)  # (as many rows go through W_out)
-    W_out, pwo, ldwo = matrix(W_out, "W_out")
+    X, px, ldx = _rows(X, "X")
+    W_in, pwi, ldwi = _rows(W_in, "W_in")
+    W_out, pwo, ldwo = _rows(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
     b_in, pbi = _vector(b_in, "b_in", 2 * F)
     b_out, pbo = _vector(b_out, "b_out", N)
-    residual, pr, ldr = _NONE if residual is None else matrix(residual, "residual", (M, N))
+    residual, pr, ldr = _NONE if residual is None else _rows(residual, "residual", (M, N))
     device = X.device
     Y, py, ldy = _result(out, (M, N), device, "out")
     H, ph, ldh = _new(M, F, device)
@@ -365,13 +330,13 @@ def gated_ffn_bwd(dY, X, W_in, W_out, D, H, *, act="silu", mode="bf16x9", need=(
     (the residual's gradient is dY); `need` says which are wanted.  (D holds the
     activation's part; `act` only has to name one.)"""
     _act(act)
-    X, px, ldx = _operand(X, "X")
-    W_in, pwi, ldwi = _operand(W_in, "W_in")
-    W_out, pwo, ldwo = _operand(W_out, "W_out")
+    X, px, ldx = _rows(X, "X")
+    W_in, pwi, ldwi = _rows(W_in, "W_in")
+    W_out, pwo, ldwo = _rows(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
-    dY, pdy, lddy = _operand(dY, "dY", (M, N))
-    D, pd, ldd = _operand(D, "D", (M, 2 * F))
-    H, ph, ldh = _operand(H, "H", (M, F))
+    dY, pdy, lddy = _rows(dY, "dY", (M, N))
+    D, pd, ldd = _rows(D, "D", (M, 2 * F))
+    H, ph, ldh = _rows(H, "H", (M, F))
     device = X.device
     dZ, pdz, lddz = _new(M, 2 * F, device)
     dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE

@@ -202,23 +202,22 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  * Activations a(z): none z; relu max(z, 0); gelu z Phi(z); gelu_tanh
  *   0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); silu z / (1 + exp(-z)).
  *   Finite z gives a finite value and derivative; relu'(0) = 0.
- * Alignment: every matrix that enters or leaves a product (X, W, residual, Y,
- *   D, dZ, H, dY, dH, dX, dW and the weights' gradients) starts on a 16-byte
- *   boundary and has a leading dimension that is a multiple of 4, as in
- *   emu_sgemm, biases start on a 16-byte boundary; else
- *   EMU_STATUS_NOT_SUPPORTED.  Widths are free.  emu_layer_norm_* takes any
- *   alignment of whole words.
+ * Alignment: inputs may have any alignment of whole words; a product's operand
+ *   whose rows do not start on 16-byte boundaries is copied into a buffer of
+ *   the library's first.  Outputs (Y, D, H, dZ, dX and the weights' gradients)
+ *   start on a 16-byte boundary and have a leading dimension that is a multiple
+ *   of 4, as in emu_sgemm, else EMU_STATUS_NOT_SUPPORTED, except in the few-row
+ *   form and in emu_layer_norm_*, which take any.  Widths are free.
  * Outputs must not overlap inputs or one another.
  * Few rows: a forward pass of at most 1,024 rows with (M - 8) N K <= 50 million
  *   (N with both halves of a gated weight) in the modes BF16X9 and TF32X3 runs
- *   on the CUDA cores in FP32, within the modes' bounds, and takes matrices and
- *   biases of any alignment of whole words (emu_few_rows_query, host only, says
- *   1 or 0).
+ *   on the CUDA cores in FP32, within the modes' bounds (emu_few_rows_query,
+ *   host only, says 1 or 0).
  * Sizes: M == 0 writes nothing but zero sums (weight and bias gradients);
  *   K == 0 leaves the bias.
- * Buffers: the sums over rows take a buffer of partial sums from the library,
- *   kept per (device, stream) like the split-K workspace; for the gated block
- *   it holds 2F floats for every 32 rows.  A call that returns an error has
+ * Buffers: the sums over rows and the aligned copies take buffers from the
+ *   library, kept per (device, stream) like the split-K workspace; the gated
+ *   block's partial sums are 2F floats for every 32 rows.  A call that returns an error has
  *   enqueued nothing, as elsewhere: every launch's buffers are reserved first.
  * Streams: two independent products of a backward pass run side by side, one of
  *   them on a stream of the library's (a second entry of its table of 64; with

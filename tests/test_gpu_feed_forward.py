@@ -415,6 +415,18 @@ def test_layouts(how):
 
     for p, q in zip(run(dev), run(lay)):
         assert torch.equal(p, q)
+    # what the forward pass saved, in another layout
+    wo, dy = f32(rng, 45, F), f32(rng, M, 45)
+    y, d, h = emu.gated_ffn_fwd(dev(x), dev(wi), None, dev(wo), dev(b)[1:46], save=True)
+    ya, da = emu.linear_act_fwd(dev(x), dev(wi), act="silu", save=True)
+    want = [*emu.gated_ffn_bwd(dev(dy), dev(x), dev(wi), dev(wo), d, h), *emu.linear_act_bwd(d, dev(x), dev(wi), da, act="silu")]
+    sd, sh, sa = (lay(host(t)) for t in (d, h, da))
+    got = [*emu.gated_ffn_bwd(lay(dy), lay(x), lay(wi), lay(wo), sd, sh), *emu.linear_act_bwd(sd, lay(x), lay(wi), sa, act="silu")]
+    for i, (p, q) in enumerate(zip(want, got)):
+        if i == 7:                             # the layer's bias gradient: row sums of unaligned rows, another order
+            np.testing.assert_allclose(host(p), host(q), rtol=0, atol=2 * (M / 32 + 96) * R.U * float((d * da).abs().sum(0).max()))
+        else:
+            assert torch.equal(p, q), i
     for N in (36, 300, 2000):
         x, dy, w = f32(rng, 9, N), f32(rng, 9, N), f32(rng, N)
         y, mean, rstd = emu.layer_norm_fwd(lay(x), dev(w))
