@@ -88,9 +88,8 @@ __global__ void __launch_bounds__(32 * kWarps) copy_rows_kernel(const CopyJobs j
 
 // Operands of the products (TMA) whose rows do not start on 16-byte boundaries
 // are read from copies that do, in a buffer of the library's: all of a call's
-// by one launch ahead of its first product.  A matrix off the boundaries that
-// is read once is a quarter of the copies' cost to handle here rather than by
-// the caller: block forward 3740x169x320 ALIGN_WAS -> ALIGN_IS us.
+// by one launch ahead of its first product (block forward, three copies, 3740 x
+// 169, F = 320, TF32x3: 53 us; with a copy each by the caller 103 us).
 class Aligned {
 public:
     void add(const float*& p, int64_t& ld, int64_t rows, int64_t cols) {

@@ -201,12 +201,13 @@ ln_bwd_regs_kernel(int64_t M, int64_t N, const float* __restrict__ dY, int64_t l
 constexpr int64_t kMaxRegsWidth = 16384;
 
 // f(T, NV) for the width.  Measured fractions of the copy rate, forward and
-// backward, at 0.4 GB a matrix: N = 16 0.86
-// and 0.84, 32 0.87 and 0.84, 61 (unaligned rows) 0.73 and 0.79, 256 0.83 and 0.94, 512 0.88 and 0.94, 1024 0.88 and 0.97, 2048 0.97 and 0.95
-// (backward with 256 threads of 2: 0.87), 4096 0.86 and 0.90 (512 threads of 2:
-// 0.83 and 0.60; 128 of 8: 0.85 and 0.85), 8192 0.94 and 0.80 (256 of 8: 0.85
-// and 0.77), 16384 0.84 and 0.62 (1024 of 4: 0.62 and 0.58).  Copying the rows
-// after next to shared memory meanwhile was slower at every width up to 4096.
+// backward, at 0.4 GB a matrix: N = 16 0.88 and 0.85, 32 0.88 and 0.86, 61
+// (unaligned rows) 0.73 and 0.79, 128 0.87 and 0.94, 256 0.93 and 0.93, 512 0.94
+// and 0.94, 1024 0.95 and 0.95, 2048 0.96 and 0.93 (backward with 256 threads
+// of 2: 0.87), 4096 0.90 and 0.88 (512 threads of 2: 0.83 and 0.60; 128 of 8:
+// 0.85 and 0.85), 8192 0.94 and 0.77 (256 of 8: 0.85 and 0.77), 16384 0.84 and
+// 0.62 (1024 of 4: 0.62 and 0.58).  Copying the rows after next to shared
+// memory meanwhile was slower at every width up to 4096.
 template <bool BWD, class F> void for_width(int64_t N, F f) {
     auto of = [&](auto T, auto NV) { f(T, NV); };
     using std::integral_constant;
@@ -234,6 +235,20 @@ template <class K> int resident_blocks(K kernel, int threads) {
         n = 1;
     }
     return n;
+}
+
+// How many blocks of the forward kernel an SM takes (at most `resident`) when X
+// is larger than L2: with every block resident the reads and writes in flight
+// get in each other's way.  About 43 KB of rows per SM were fastest up to a
+// width of 1024 (fractions of the copy rate, all resident / 43 KB: 256 0.83 /
+// 0.93, 512 0.88 / 0.94, 1024 0.87 / 0.95; up to 128 columns all are less),
+// 64 KB for 2048 and 4096 (0.86 / 0.90), 96 KB above.  Smaller matrices, and
+// the backward kernel, which holds more registers, want all of them.
+int64_t forward_blocks(int64_t M, int64_t N, int rows, int resident) {
+    if (M * N * (int64_t)sizeof(float) < (int64_t(100) << 20)) return resident;
+    const int64_t target = (N <= 1024 ? 43 : N <= 4096 ? 64 : 96) << 10, block = rows * N * (int64_t)sizeof(float);
+    const int64_t n = (target + block / 2) / block;
+    return n < 1 ? 1 : n < resident ? n : resident;
 }
 
 // Blocks that take the rows in turns of equal length: at most `resident`.
@@ -351,7 +366,8 @@ emu_status_t emu_layer_norm_fwd(int64_t M, int64_t N, const float* X, int64_t ld
             auto launch = [&](auto VEC) {
                 constexpr auto kernel = ln_fwd_regs_kernel<t, nv, decltype(VEC)::value>;
                 static const int per_sm = resident_blocks(kernel, kBlockThreads<t>);
-                const unsigned grid = even_grid(M, kBlockRows<t>, (int64_t)dev.sm_count * per_sm);
+                const unsigned grid =
+                    even_grid(M, kBlockRows<t>, dev.sm_count * forward_blocks(M, N, kBlockRows<t>, per_sm));
                 kernel<<<grid, kBlockThreads<t>, 0, s>>>(M, N, X, ldx, weight, bias, eps, Y, ldy, mean, rstd);
             };
             if (vec) launch(std::true_type{}); else launch(std::false_type{});
