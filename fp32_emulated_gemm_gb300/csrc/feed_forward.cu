@@ -72,15 +72,22 @@ struct CopyJob {
 };
 constexpr int kMaxCopies = 7;
 struct CopyJobs { int n; CopyJob job[kMaxCopies]; };
-__global__ void __launch_bounds__(32 * kWarps) copy_rows_kernel(const CopyJobs jobs) {
+__global__ void __launch_bounds__(32 * kWarps) copy_rows_kernel(const __grid_constant__ CopyJobs jobs) {
     int64_t r = blockIdx.x * (int64_t)kWarps + threadIdx.y;
     for (int i = 0; i < jobs.n; ++i) {
         const CopyJob& j = jobs.job[i];
         for (; r < j.rows; r += (int64_t)gridDim.x * kWarps) {
             const float* src = j.src + r * j.lds;
             float* dst = j.dst + r * j.ldd;
-#pragma unroll 4
-            for (int64_t c = threadIdx.x; c < j.cols; c += 32) dst[c] = src[c];
+            for (int64_t c = threadIdx.x; c < j.cols; c += 32 * 8) {  // eight words of a lane in flight
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + 32 * k < j.cols) v[k] = __ldg(src + c + 32 * k);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + 32 * k < j.cols) dst[c + 32 * k] = v[k];
+            }
         }
         r -= j.rows;
     }
@@ -225,15 +232,14 @@ __global__ void __launch_bounds__(32 * kWarps) column_sums_kernel(const SumJob a
 // rows of partial sums take 2 to 3 us, mostly the launch, which overlaps the
 // end of the kernel before it.
 struct PartialsPair { Partials set[2]; unsigned first_blocks; };
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const PartialsPair pair) {
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const __grid_constant__ PartialsPair pair) {
     __shared__ float part[32][33];
     const bool second = blockIdx.x >= pair.first_blocks;
-    const Partials& a = pair.set[second];
+    const Partials a = second ? pair.set[1] : pair.set[0];
     const int64_t c = (blockIdx.x - (second ? pair.first_blocks : 0)) * 32ll + threadIdx.x;
     griddep_wait();
     float s = 0.f;
     if (c < a.C) {
-#pragma unroll 4
         for (int p = threadIdx.y; p < a.P; p += 32) s += a.p[(int64_t)p * a.C + c];
     }
     part[threadIdx.y][threadIdx.x] = s;
