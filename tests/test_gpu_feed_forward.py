@@ -459,6 +459,50 @@ def test_outputs_stay_inside_their_matrix():
     done()
 
 
+@pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
+@pytest.mark.parametrize("M,K,F,N", [(5, 36, 23, 31), (1061, 36, 71, 33), (1150, 40, 128, 256), (700, 260, 901, 300)])
+def test_every_output_stays_inside_its_matrix(M, K, F, N, mode):
+    """Through the C entry points, every output in the middle of a buffer whose
+    other words hold a pattern: none of them changes, and every output word
+    is written."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("guards", M, K, F, N)
+    pattern = torch.from_numpy(np.array([0x7FC0DEAD], np.uint32).view(np.float32)).to(_gpu.device())
+    made = []
+
+    def out(r, c):
+        ld = (c + 3) // 4 * 4 + 8
+        buf = pattern.expand((r + 2) * ld).contiguous()
+        made.append((buf, r, c, ld))
+        return buf[ld + 4:], ld               # (a view: its address is the matrix's)
+
+    x, wi, wo = dev(f32(rng, M, K)), dev(f32(rng, 2 * F, K, std=0.2)), dev(f32(rng, N, F, std=0.2))
+    bi, bo, dy, w = dev(f32(rng, 2 * F)), dev(f32(rng, N)), dev(f32(rng, M, N)), dev(f32(rng, K))
+    (d, ldd), (h, ldh), (y, ldy), (dz, lddz) = out(M, 2 * F), out(M, F), out(M, N), out(M, 2 * F)
+    (dx, lddx), (dwi, lddwi), (dbi, _), (dwo, lddwo), (dbo, _) = out(M, K), out(2 * F, K), out(1, 2 * F), out(N, F), out(1, N)
+    m = emu.MODES[mode]
+    emu.emu_gated_ffn_fwd(m, emu.EMU_ACT_SILU, M, K, F, N, x, K, wi, K, bi, wo, F, bo, None, 0, d, ldd, h, ldh, y, ldy)
+    emu.emu_gated_ffn_bwd(m, M, K, F, N, dy, N, x, K, wi, K, wo, F, d, ldd, h, ldh, dz, lddz, dx, lddx, dwi, lddwi, dbi,
+                          dwo, lddwo, dbo)
+    (d2, ldd2), (y2, ldy2), (dz2, lddz2), (db2, _) = out(M, N), out(M, N), out(M, N), out(1, N)
+    emu.emu_linear_act_fwd(m, emu.EMU_ACT_GELU, M, N, K, x, K, wi if N <= 2 * F else dev(f32(rng, N, K)), K, None, dy, N, d2,
+                           ldd2, y2, ldy2)
+    emu.emu_linear_act_bwd(m, M, N, K, dy, N, x, K, wi, K, d2, ldd2, dz2, lddz2, None, 0, None, 0, db2)
+    (n, ldn), (dn, lddn), (dw, _), (db, _), (mean, _), (rstd, _) = (out(M, K), out(M, K), out(1, K), out(1, K), out(1, M),
+                                                                    out(1, M))
+    emu.emu_layer_norm_fwd(M, K, x, K, w, None, 1e-5, n, ldn, mean, rstd)
+    emu.emu_layer_norm_bwd(M, K, x, K, x, K, w, mean, rstd, None, 0, dn, lddn, dw, db)
+    done()
+    for i, (buf, r, c, ld) in enumerate(made):
+        words = buf.cpu().numpy().view(np.uint32)
+        inside = np.zeros(words.size, bool)
+        for k in range(r):
+            inside[ld + 4 + k * ld:ld + 4 + k * ld + c] = True
+        assert np.all(words[~inside] == 0x7FC0DEAD), f"output {i}: a store outside the matrix"
+        assert np.all(np.isfinite(words[inside].view(np.float32))), f"output {i}: not all written"
+
+
 def test_other_stream():
     """The calls run on the current stream: work queued there before and
     after them is ordered with them."""
