@@ -29,7 +29,8 @@
  *     for the TF32 modes, a buffer for op(B) split ahead of the product (when
  *     op(A) spans four or more 256-row tiles; EMU_AUTOPACK=0 turns that off),
  *     made with cudaMallocAsync on first need per (device, stream) and kept
- *     until emu_shutdown() or the end of the process; emu_sgemm_noalloc never
+ *     until emu_shutdown() or the end of the process (the feed-forward
+ *     operators have buffers of their own, see there); emu_sgemm_noalloc never
  *     allocates.  The library tracks at most 64 (device, stream) pairs with
  *     such buffers at once: a call that would need a 65th returns
  *     EMU_STATUS_ALLOC_FAILED (emu_shutdown() releases all of them).
@@ -422,7 +423,8 @@ emu_status_t emu_selftest_split_timeout(uint64_t budget_ns, int64_t tiles, emu_s
 
 /*
  * emu_shutdown -- release the library's cached device buffers (split-K
- * workspaces, pre-split op(B) buffers) on every device that has them: each
+ * workspaces, pre-split op(B) buffers, the feed-forward operators' partial sums,
+ * aligned copies and side streams) on every device that has them: each
  * such device is synchronised (cudaDeviceSynchronize) first, then the buffers
  * are freed and the (device, stream) slots cleared.  Later calls allocate
  * again on first need.  The current device is left as it was.  Returns
