@@ -588,6 +588,12 @@ emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, c
 // EMU_AUTOPACK=0 turns it off.
 constexpr int kAutoPackMinTileRows = 4;
 constexpr size_t kAutoPackMaxBytes = size_t(1) << 30;
+// The feed-forward operators' products of fewer k-stages per CTA pair than this
+// are not split ahead: the extra launch costs what the shorter stages save
+// (1100 x 512 x 512, 2 stages a pair: 20.2 us, split ahead 22.8; 1537 x 300 x 500
+// training step 65.7 and 68.4; 6144 x 256 x 1024, 10 stages: 34.2 and 32.9; 1100 x
+// 2048 x 2048, 34 stages: 102 and 93).
+constexpr long long kAutoPackMinStages = 6;
 
 // The launch plan: pipeline shape, tiles, and how tiles become work units.
 struct Plan {
@@ -981,11 +987,13 @@ enum Until { UNTIL_CHECKED, UNTIL_RESERVED, UNTIL_LAUNCHED };
 // fused: the epilogue is one of the EPI_* kinds instead (gated: N is F, op(B)
 // has 2F columns; the plan's tiles have 128 columns of each half).
 // max_pairs: the plan takes no more CTA pairs than this.
+// min_pack_stages: see kAutoPackMinStages (0: no such bound).
 // until: stop after the arguments' checks, or after the buffers' reservation.
 emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t N, int64_t K, float alpha,
                       const float* A, int64_t lda, const float* B, int64_t ldb, float beta, float* C,
                       int64_t ldc, const float* bias, cudaStream_t stream, const void* packed_b = nullptr,
-                      Until until = UNTIL_LAUNCHED, const Fused* fused = nullptr, int max_pairs = INT32_MAX) {
+                      Until until = UNTIL_LAUNCHED, const Fused* fused = nullptr, int max_pairs = INT32_MAX,
+                      long long min_pack_stages = 0) {
     if (!valid_mode(mode)) return EMU_STATUS_INVALID_VALUE;
     if (M < 0 || N < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
     if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return EMU_STATUS_NOT_SUPPORTED;
@@ -1046,7 +1054,8 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     static const bool autopack = env_int("EMU_AUTOPACK", 1) != 0;
     void* autopack_buf = nullptr;
     if (!packed_b && autopack && (mode == EMU_MODE_TF32X3 || mode == EMU_MODE_TF32X1) &&
-        plan.tiles_m >= kAutoPackMinTileRows && (size_t)packed_bytes(mode, b_n, K) <= kAutoPackMaxBytes) {
+        plan.tiles_m >= kAutoPackMinTileRows &&
+        (long long)plan.num_tiles * plan.k_stages >= min_pack_stages * plan.clusters && (size_t)packed_bytes(mode, b_n, K) <= kAutoPackMaxBytes) {
         st = packed_buffer_for(devid, stream, (size_t)packed_bytes(mode, b_n, K), &autopack_buf);
         if (st != EMU_STATUS_SUCCESS) return st;
     }
@@ -1197,7 +1206,7 @@ emu_status_t align_scratch(int dev, cudaStream_t stream, size_t floats, float** 
 namespace {
 emu_status_t gemm_on(emu_mode_t mode, const Gemm& g, cudaStream_t stream, Until until, int max_pairs) {
     return run_gemm(mode, g.a_mn, g.b_mn, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.bias, stream,
-                    nullptr, until, g.fused, max_pairs);
+                    nullptr, until, g.fused, max_pairs, kAutoPackMinStages);
 }
 
 // How two products share `pairs` CTA pairs: the first's share, or 0 when one
