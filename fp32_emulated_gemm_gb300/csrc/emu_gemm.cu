@@ -48,7 +48,8 @@ struct DeviceInfo {
 // Split-K workspace: partial tiles plus per-tile arrival counters, owned by
 // the library, one per (device, stream) so that calls on different streams
 // never share it.  Grown on demand, kept until emu_shutdown() or the end of
-// the process.  `epoch` numbers the launches that use its counters.
+// the process.  `epoch` numbers the launches that use its counters (a captured
+// launch, which runs again with the same number, has them cleared first).
 struct Workspace {
     int device = -1;
     cudaStream_t stream = nullptr;
@@ -473,6 +474,24 @@ emu_status_t check_error_flag(bool clear) {
         any |= flag;
     }
     return any ? EMU_STATUS_DEVICE_TIMEOUT : EMU_STATUS_SUCCESS;
+}
+
+// Whether work on `stream` goes into a graph that is being captured.
+bool capturing(cudaStream_t stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return status != cudaStreamCaptureStatusNone;
+}
+
+// A captured launch's epoch is a constant of its graph: the arrivals that one
+// replay leaves would count toward the next.  So a graph gets a node of its own
+// that clears the launch's counters ahead of it (epoch 0, which no launch uses).
+cudaError_t clear_captured_counters(unsigned long long* counters, size_t n, cudaStream_t stream) {
+    if (!capturing(stream)) return cudaSuccess;
+    return cudaMemsetAsync(counters, 0, n * sizeof(*counters), stream);
 }
 
 // The slot of (device, stream) in the workspace table, taken on first use;
@@ -1102,6 +1121,10 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     p.wait_budget_ns = wait_budget_ns();
     if (autopack_buf && launch_pack(mode, b_n, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
         return EMU_STATUS_LAUNCH_FAILED;
+    if (p.counters && clear_captured_counters(p.counters, (size_t)plan.num_tiles * 2, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EMU_STATUS_LAUNCH_FAILED;
+    }
     const int clusters = plan.clusters;
     if (log_enabled())
         std::fprintf(stderr, "[emu] %s M=%lld N=%lld K=%lld a_mn=%d b_mn=%d pipe=%d tile=256x%d tiles=%dx%d "
@@ -1469,6 +1492,10 @@ emu_status_t emu_selftest_split_timeout(uint64_t budget_ns, int64_t tiles, emu_s
     st = workspace_for(devid, s, 0, (size_t)tiles * 2, &w, &epoch);
     if (st != EMU_STATUS_SUCCESS) return st;
     cudaGetLastError();
+    if (clear_captured_counters(w->counters, (size_t)tiles * 2, s) != cudaSuccess) {
+        cudaGetLastError();
+        return EMU_STATUS_LAUNCH_FAILED;
+    }
     split_timeout_selftest_kernel<<<1, 256, 0, s>>>(w->counters, (int)(tiles * 2), epoch, budget_ns);
     return cudaGetLastError() == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }

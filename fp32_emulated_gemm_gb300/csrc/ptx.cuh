@@ -131,7 +131,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // new epoch from the host, so a count left by an earlier launch (one that
 // gave up on a wait before every piece arrived, say) belongs to another epoch
 // and never counts toward this launch's total; the counters need no reset
-// between launches.
+// between launches.  A launch captured into a graph keeps its epoch from replay
+// to replay, so the host captures a reset of its counters ahead of it.
 __device__ __forceinline__ unsigned long long epoch_word(unsigned long long epoch, unsigned count) {
     return (epoch << 8) | count;
 }

@@ -1,0 +1,151 @@
+"""Calls captured into CUDA graphs: what a replay computes is what the call
+computes, however often it runs and whatever runs beside it."""
+import numpy as np
+import pytest
+
+from tests import _gpu
+
+pytestmark = pytest.mark.gpu
+PAIRS = 76
+
+
+def rand(*shape, seed, std=1.0):
+    rng = np.random.default_rng([seed, *shape])
+    return _gpu.to_dev((rng.standard_normal(shape) * std).astype(np.float32))
+
+
+def empty(*shape):
+    import torch
+    return torch.empty(shape, device=_gpu.device())
+
+
+class Product:
+    """C = A B^T by emu_sgemm alone in a graph."""
+    kernels = 1
+
+    def __init__(self, M, N, K, mode):
+        self.size, self.mode = (M, N, K), mode
+        self.a, self.b, self.c = empty(M, K), empty(N, K), empty(M, N)
+        self.inputs, self.outputs = [self.a, self.b], [self.c]
+
+    def draw(self, seed):
+        M, N, K = self.size
+        return [rand(M, K, seed=seed), rand(N, K, seed=seed + 100)]
+
+    def run(self):
+        import fp32_emulated_gemm_gb300 as emu
+        M, N, K = self.size
+        emu.emu_sgemm(emu.MODES[self.mode], 0, 1, M, N, K, 1.0, self.a, K, self.b, K, 0.0, self.c, N)
+
+
+class GatedForward:
+    """emu_gated_fwd alone: the gated epilogue on a split product."""
+
+    def __init__(self, M, F, K, mode):
+        self.size, self.mode = (M, F, K), mode
+        self.x, self.w, self.d, self.h = empty(M, K), empty(2 * F, K), empty(M, 2 * F), empty(M, F)
+        self.inputs, self.outputs = [self.x, self.w], [self.d, self.h]
+
+    def draw(self, seed):
+        M, F, K = self.size
+        return [rand(M, K, seed=seed), rand(2 * F, K, seed=seed + 100, std=K ** -0.5)]
+
+    def run(self):
+        import fp32_emulated_gemm_gb300 as emu
+        M, F, K = self.size
+        emu.emu_gated_fwd(emu.MODES[self.mode], emu.EMU_ACT_SILU, M, F, K, self.x, K, self.w, K, None, self.d, 2 * F,
+                          self.h, F)
+
+
+class LinearBackward:
+    """emu_linear_act_bwd alone: two split products side by side."""
+
+    def __init__(self, M, N, K, mode):
+        self.size, self.mode = (M, N, K), mode
+        self.dy, self.x, self.w, self.d = empty(M, N), empty(M, K), empty(N, K), empty(M, N)
+        self.dz, self.dx, self.dw, self.db = empty(M, N), empty(M, K), empty(N, K), empty(N)
+        self.inputs, self.outputs = [self.dy, self.x, self.w, self.d], [self.dz, self.dx, self.dw, self.db]
+
+    def draw(self, seed):
+        M, N, K = self.size
+        return [rand(M, N, seed=seed), rand(M, K, seed=seed + 100), rand(N, K, seed=seed + 200), rand(M, N, seed=seed + 300)]
+
+    def run(self):
+        import fp32_emulated_gemm_gb300 as emu
+        M, N, K = self.size
+        emu.emu_linear_act_bwd(emu.MODES[self.mode], M, N, K, self.dy, N, self.x, K, self.w, K, self.d, N, self.dz, N,
+                               self.dx, K, self.dw, K, self.db)
+
+
+CASES = {
+    "chained_bf16x9": lambda: Product(2000, 2500, 200, "bf16x9"),
+    "chained_tf32x3": lambda: Product(2000, 2500, 200, "tf32x3"),
+    "split_19_bf16x9": lambda: Product(300, 260, 3000, "bf16x9"),
+    "split_32_tf32x3": lambda: Product(256, 256, 4096, "tf32x3"),
+    "gated_split": lambda: GatedForward(300, 132, 3000, "bf16x9"),
+    "backward_tf32x3": lambda: LinearBackward(1536, 300, 500, "tf32x3"),
+    "backward_bf16x9": lambda: LinearBackward(1536, 300, 500, "bf16x9"),
+}
+
+
+def test_the_products_are_the_kinds_named():
+    import fp32_emulated_gemm_gb300 as emu
+    assert emu.emu_plan_query(2000, 2500, 200, PAIRS)["chain"] == 1
+    assert emu.emu_plan_query(300, 260, 3000, PAIRS)["split_a"] == 19
+    assert emu.emu_plan_query(256, 256, 4096, PAIRS)["split_a"] == 32
+
+
+def prepared(name):
+    """The case's call, warmed up on the stream that it is then captured on."""
+    import torch
+    case = CASES[name]()
+    for t in case.inputs:
+        t.zero_()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        case.run()
+    stream.synchronize()
+    return case, stream
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_a_graph_clears_the_counters_of_split_products(name):
+    """A captured launch has the same epoch in every replay, so the graph has to
+    clear the counters that its split and chained products arrive on."""
+    from tests import _graphs
+    case, stream = prepared(name)
+    graph = _graphs.Graph(stream, case.run)
+    types = graph.types()
+    graph.close()
+    assert types.count(_graphs.MEMSET) >= 1, types
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_many_replays_with_new_inputs(name):
+    """300 replays (more than an 8-bit count holds), each bit for bit the call
+    on the inputs then in place; nothing else runs on the captured stream."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    from tests import _graphs
+    case, stream = prepared(name)
+    sets = [case.draw(seed) for seed in range(5)]
+    want = []
+    for data in sets:                     # the calls themselves, on another stream's buffers
+        for t, v in zip(case.inputs, data):
+            t.copy_(v)
+        case.run()
+        want.append([t.clone() for t in case.outputs])
+    torch.cuda.synchronize()
+    graph = _graphs.Graph(stream, case.run)
+    with torch.cuda.stream(stream):
+        for i in range(300):
+            for t, v in zip(case.inputs, sets[i % 5]):
+                t.copy_(v)
+            for t in case.outputs:
+                t.fill_(float("nan"))
+            graph.launch()
+            for k, (got, w) in enumerate(zip(case.outputs, want[i % 5])):
+                assert torch.equal(got, w), f"replay {i}, output {k}"
+    assert emu.emu_stream_check(stream) == 0
+    graph.close()
