@@ -17,6 +17,7 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <new>
 
 #include "../../include/emu_gemm.h"
 #include "emu_kernel.cuh"
@@ -45,25 +46,34 @@ struct DeviceInfo {
     int max_clusters[2] = {0, 0};  // co-resident CTA pairs per mode (all pipeline shapes)
 };
 
-// Split-K workspace: partial tiles plus per-tile arrival counters, owned by
-// the library, one per (device, stream) so that calls on different streams
-// never share it.  Grown on demand, kept until emu_shutdown() or the end of
-// the process.  `epoch` numbers the launches that use its counters (a captured
-// launch, which runs again with the same number, has them cleared first).
+// A device buffer of the library's, grown on demand.  Once a captured call has
+// used it, a graph holds its address: it is then kept when a larger one takes
+// its place (Retired) instead of being freed.
+struct Buffer {
+    void* ptr = nullptr;
+    size_t bytes = 0;
+    bool captured = false;
+};
+struct Retired {
+    void* ptr;
+    Retired* next;
+};
+
+// The library's buffers of one (device, stream), so that calls on different
+// streams never share them; kept until emu_shutdown() or the end of the process.
+// `epoch` numbers the launches that use the counters (a captured launch, which
+// runs again with the same number, has them cleared first).
 struct Workspace {
     int device = -1;
     cudaStream_t stream = nullptr;
-    float* partials = nullptr;
-    size_t partial_floats = 0;
-    unsigned long long* counters = nullptr;
-    size_t num_counters = 0;
+    cudaStream_t user = nullptr;  // the caller's stream: `stream`, or the one that it is the side stream of
+    Buffer partials;          // split and chained products: partial tiles and running sums
+    Buffer counters;          // and their arrival counters
     unsigned long long epoch = 0;
-    void* packed = nullptr;   // op(B) split ahead of a product (automatic pre-split)
-    size_t packed_bytes = 0;
-    float* reduce = nullptr;  // column-sum partials of the row-wise operators
-    size_t reduce_floats = 0;
-    float* align = nullptr;   // aligned copies of operands
-    size_t align_floats = 0;
+    Buffer packed;            // op(B) split ahead of a product (automatic pre-split)
+    Buffer reduce;            // column-sum partials of the row-wise operators
+    Buffer align;             // aligned copies of operands
+    Retired* retired = nullptr;
     cudaStream_t side = nullptr;  // for a product that runs beside one on `stream`
     cudaEvent_t fork = nullptr, join = nullptr;
 };
@@ -500,8 +510,38 @@ Workspace* workspace_slot(int dev, cudaStream_t stream) {
     for (auto& c : g_ws)
         if (c.device == dev && c.stream == stream) return &c;
     for (auto& c : g_ws)
-        if (c.device < 0) { c.device = dev; c.stream = stream; return &c; }
+        if (c.device < 0) { c.device = dev; c.stream = c.user = stream; return &c; }
     return nullptr;
+}
+
+// `b`, one of w's buffers, with at least `bytes` bytes (new ones zero if asked).
+// No growth while the caller's stream is being captured: an allocation would be
+// a node of the graph, its memory the graph's.  Caller holds g_mutex.
+emu_status_t reserve(Workspace* w, Buffer& b, size_t bytes, bool zero = false) {
+    const bool in_graph = capturing(w->user);
+    if (b.bytes < bytes) {
+        if (in_graph) return EMU_STATUS_ALLOC_FAILED;
+        if (b.captured && b.ptr) {
+            Retired* r = new (std::nothrow) Retired{b.ptr, w->retired};
+            if (!r) return EMU_STATUS_ALLOC_FAILED;
+            w->retired = r;
+        } else if (b.ptr && cudaFreeAsync(b.ptr, w->stream) != cudaSuccess) {
+            cudaGetLastError();
+        }
+        b = Buffer{};
+        if (lib_malloc_async(&b.ptr, bytes, w->stream) != cudaSuccess) {
+            cudaGetLastError();
+            b.ptr = nullptr;
+            return EMU_STATUS_ALLOC_FAILED;
+        }
+        if (zero && cudaMemsetAsync(b.ptr, 0, bytes, w->stream) != cudaSuccess) {
+            cudaGetLastError();
+            return EMU_STATUS_ALLOC_FAILED;
+        }
+        b.bytes = bytes;
+    }
+    if (in_graph) b.captured = true;
+    return EMU_STATUS_SUCCESS;
 }
 
 // The workspace for (current device, stream) with at least `floats` partial
@@ -514,72 +554,22 @@ emu_status_t workspace_for(int dev, cudaStream_t stream, size_t floats, size_t c
     std::lock_guard<std::mutex> lock(g_mutex);
     Workspace* w = workspace_slot(dev, stream);
     if (!w) return EMU_STATUS_ALLOC_FAILED;
-    if (w->partial_floats < floats) {
-        if (w->partials && cudaFreeAsync(w->partials, stream) != cudaSuccess) cudaGetLastError();
-        w->partials = nullptr;
-        w->partial_floats = 0;
-        if (lib_malloc_async(reinterpret_cast<void**>(&w->partials), floats * sizeof(float), stream) != cudaSuccess) {
-            cudaGetLastError();
-            return EMU_STATUS_ALLOC_FAILED;
-        }
-        w->partial_floats = floats;
-    }
-    if (w->num_counters < counters) {
-        if (w->counters && cudaFreeAsync(w->counters, stream) != cudaSuccess) cudaGetLastError();
-        w->counters = nullptr;
-        w->num_counters = 0;
-        const size_t bytes = counters * sizeof(unsigned long long);
-        if (lib_malloc_async(reinterpret_cast<void**>(&w->counters), bytes, stream) != cudaSuccess ||
-            cudaMemsetAsync(w->counters, 0, bytes, stream) != cudaSuccess) {
-            cudaGetLastError();
-            return EMU_STATUS_ALLOC_FAILED;
-        }
-        w->num_counters = counters;
-    }
+    emu_status_t st = reserve(w, w->partials, floats * sizeof(float));
+    if (st == EMU_STATUS_SUCCESS) st = reserve(w, w->counters, counters * sizeof(unsigned long long), true);
+    if (st != EMU_STATUS_SUCCESS) return st;
     *epoch = ++w->epoch;
     *out = w;
     return EMU_STATUS_SUCCESS;
 }
 
-// A buffer for an automatically pre-split op(B), per (device, stream), grown
-// on demand and kept.
-emu_status_t packed_buffer_for(int dev, cudaStream_t stream, size_t bytes, void** out) {
+// Another buffer of the (device, stream)'s.
+emu_status_t buffer_for(int dev, cudaStream_t stream, Buffer Workspace::*buffer, size_t bytes, void** out) {
     std::lock_guard<std::mutex> lock(g_mutex);
     Workspace* w = workspace_slot(dev, stream);
     if (!w) return EMU_STATUS_ALLOC_FAILED;
-    if (w->packed_bytes < bytes) {
-        if (w->packed && cudaFreeAsync(w->packed, stream) != cudaSuccess) cudaGetLastError();
-        w->packed = nullptr;
-        w->packed_bytes = 0;
-        if (lib_malloc_async(&w->packed, bytes, stream) != cudaSuccess) {
-            cudaGetLastError();
-            return EMU_STATUS_ALLOC_FAILED;
-        }
-        w->packed_bytes = bytes;
-    }
-    *out = w->packed;
-    return EMU_STATUS_SUCCESS;
-}
-
-// A float buffer of the (device, stream) (column-sum partials, aligned copies),
-// grown on demand and kept.
-emu_status_t float_buffer_for(int dev, cudaStream_t stream, float* Workspace::*buffer, size_t Workspace::*size,
-                              size_t floats, float** out) {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    Workspace* w = workspace_slot(dev, stream);
-    if (!w) return EMU_STATUS_ALLOC_FAILED;
-    if (w->*size < floats) {
-        if (w->*buffer && cudaFreeAsync(w->*buffer, stream) != cudaSuccess) cudaGetLastError();
-        w->*buffer = nullptr;
-        w->*size = 0;
-        if (lib_malloc_async(reinterpret_cast<void**>(&(w->*buffer)), floats * sizeof(float), stream) != cudaSuccess) {
-            cudaGetLastError();
-            return EMU_STATUS_ALLOC_FAILED;
-        }
-        w->*size = floats;
-    }
-    *out = w->*buffer;
-    return EMU_STATUS_SUCCESS;
+    const emu_status_t st = reserve(w, w->*buffer, bytes);
+    *out = (w->*buffer).ptr;
+    return st;
 }
 
 // The (device, stream)'s side stream and the events that order it with `stream`.
@@ -588,6 +578,7 @@ emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, c
     Workspace* w = workspace_slot(dev, stream);
     if (!w) return EMU_STATUS_ALLOC_FAILED;
     if (!w->join) {
+        if (capturing(stream)) return EMU_STATUS_ALLOC_FAILED;
         if ((!w->side && cudaStreamCreateWithFlags(&w->side, cudaStreamNonBlocking) != cudaSuccess) ||
             (!w->fork && cudaEventCreateWithFlags(&w->fork, cudaEventDisableTiming) != cudaSuccess) ||
             cudaEventCreateWithFlags(&w->join, cudaEventDisableTiming) != cudaSuccess) {
@@ -595,7 +586,9 @@ emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, c
             return EMU_STATUS_ALLOC_FAILED;
         }
     }
-    if (!workspace_slot(dev, w->side)) return EMU_STATUS_ALLOC_FAILED;  // the side stream's own buffers
+    Workspace* own = workspace_slot(dev, w->side);  // the side stream's own buffers
+    if (!own) return EMU_STATUS_ALLOC_FAILED;
+    own->user = stream;
     *side = w->side; *fork = w->fork; *join = w->join;
     return EMU_STATUS_SUCCESS;
 }
@@ -1075,7 +1068,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     if (!packed_b && autopack && (mode == EMU_MODE_TF32X3 || mode == EMU_MODE_TF32X1) &&
         plan.tiles_m >= kAutoPackMinTileRows &&
         (long long)plan.num_tiles * plan.k_stages >= min_pack_stages * plan.clusters && (size_t)packed_bytes(mode, b_n, K) <= kAutoPackMaxBytes) {
-        st = packed_buffer_for(devid, stream, (size_t)packed_bytes(mode, b_n, K), &autopack_buf);
+        st = buffer_for(devid, stream, &Workspace::packed, (size_t)packed_bytes(mode, b_n, K), &autopack_buf);
         if (st != EMU_STATUS_SUCCESS) return st;
     }
     const void* b_packed = packed_b ? packed_b : autopack_buf;
@@ -1086,8 +1079,8 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
         const size_t floats = (size_t)plan.slots * TILE_M * plan.tn;
         st = workspace_for(devid, stream, floats, (size_t)plan.num_tiles * 2, &w, &p.epoch);
         if (st != EMU_STATUS_SUCCESS) return st;
-        p.workspace = w->partials;
-        p.counters = w->counters;
+        p.workspace = static_cast<float*>(w->partials.ptr);
+        p.counters = static_cast<unsigned long long*>(w->counters.ptr);
     }
     if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
     if (!encode_operand(&p.tmA, A, a_mn, M, K, lda, HALF) ||
@@ -1220,10 +1213,10 @@ emu_status_t current_device(DeviceCtx* out) {
 }
 
 emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float** out) {
-    return float_buffer_for(dev, stream, &Workspace::reduce, &Workspace::reduce_floats, floats, out);
+    return buffer_for(dev, stream, &Workspace::reduce, floats * sizeof(float), reinterpret_cast<void**>(out));
 }
 emu_status_t align_scratch(int dev, cudaStream_t stream, size_t floats, float** out) {
-    return float_buffer_for(dev, stream, &Workspace::align, &Workspace::align_floats, floats, out);
+    return buffer_for(dev, stream, &Workspace::align, floats * sizeof(float), reinterpret_cast<void**>(out));
 }
 
 namespace {
@@ -1492,11 +1485,12 @@ emu_status_t emu_selftest_split_timeout(uint64_t budget_ns, int64_t tiles, emu_s
     st = workspace_for(devid, s, 0, (size_t)tiles * 2, &w, &epoch);
     if (st != EMU_STATUS_SUCCESS) return st;
     cudaGetLastError();
-    if (clear_captured_counters(w->counters, (size_t)tiles * 2, s) != cudaSuccess) {
+    unsigned long long* const counters = static_cast<unsigned long long*>(w->counters.ptr);
+    if (clear_captured_counters(counters, (size_t)tiles * 2, s) != cudaSuccess) {
         cudaGetLastError();
         return EMU_STATUS_LAUNCH_FAILED;
     }
-    split_timeout_selftest_kernel<<<1, 256, 0, s>>>(w->counters, (int)(tiles * 2), epoch, budget_ns);
+    split_timeout_selftest_kernel<<<1, 256, 0, s>>>(counters, (int)(tiles * 2), epoch, budget_ns);
     return cudaGetLastError() == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }
 
@@ -1512,11 +1506,15 @@ emu_status_t emu_shutdown(void) {
             result = EMU_STATUS_LAUNCH_FAILED;
         }
         // after the device synchronisation nothing uses these buffers
-        if (w.partials && cudaFree(w.partials) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
-        if (w.counters && cudaFree(w.counters) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
-        if (w.packed && cudaFree(w.packed) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
-        if (w.reduce && cudaFree(w.reduce) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
-        if (w.align && cudaFree(w.align) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        auto release = [&](void* ptr) {
+            if (ptr && cudaFree(ptr) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
+        };
+        for (Buffer* b : {&w.partials, &w.counters, &w.packed, &w.reduce, &w.align}) release(b->ptr);
+        while (Retired* r = w.retired) {
+            w.retired = r->next;
+            release(r->ptr);
+            delete r;
+        }
         if (w.side && cudaStreamDestroy(w.side) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.fork && cudaEventDestroy(w.fork) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }
         if (w.join && cudaEventDestroy(w.join) != cudaSuccess) { cudaGetLastError(); result = EMU_STATUS_LAUNCH_FAILED; }

@@ -16,8 +16,9 @@ struct DeviceCtx { int id, sm_count; };
 emu_status_t current_device(DeviceCtx* out);
 
 // The (device, stream)'s buffer for column-sum partials, at least `floats`
-// long: grown on demand, kept until emu_shutdown().  Not the split-K
-// workspace, which a product on the same stream may be using in between.
+// long: grown on demand (never under capture), kept until emu_shutdown().  Not
+// the split-K workspace, which a product on the same stream may be using in
+// between.
 emu_status_t reduce_scratch(int dev, cudaStream_t stream, size_t floats, float** out);
 
 // Likewise its buffer for aligned copies of operands.

@@ -34,6 +34,14 @@
  *     allocates.  The library tracks at most 64 (device, stream) pairs with
  *     such buffers at once: a call that would need a 65th returns
  *     EMU_STATUS_ALLOC_FAILED (emu_shutdown() releases all of them).
+ *   - Capture: a call may be captured into a graph once the device has run a
+ *     call.  One that needs more of the library's buffers than its stream has
+ *     returns EMU_STATUS_ALLOC_FAILED instead of allocating: make the same call
+ *     on the capturing stream once before.  Buffers that a graph uses stay where
+ *     they are until emu_shutdown() (after which the graph must not run), also
+ *     when a later call on the stream gets larger ones.  Graphs captured on one
+ *     stream, and calls on it, share its buffers: their work must not overlap on
+ *     the GPU.
  *   - Alignment (TMA): A and B must start on a 16-byte boundary and lda, ldb
  *     must be multiples of 4 elements; C the same (ldc multiple of 4).
  *     Violations return EMU_STATUS_NOT_SUPPORTED.
@@ -95,7 +103,8 @@ typedef enum {
     EMU_STATUS_ARCH_MISMATCH = 3,   /* current device is not compute capability 10.3 (the library holds
                                        sm_103a code only) */
     EMU_STATUS_ALLOC_FAILED = 4,    /* a library buffer (split-K workspace, pre-split op(B)) could not be
-                                       allocated, or the 64 (device, stream) slots are taken */
+                                       allocated, or would have to be under capture, or the 64
+                                       (device, stream) slots are taken */
     EMU_STATUS_LAUNCH_FAILED = 5,   /* a CUDA call failed (no device, launch error, TMA encode error) */
     EMU_STATUS_DEVICE_TIMEOUT = 6   /* a kernel gave up on an internal wait and returned early */
 } emu_status_t;
@@ -224,9 +233,7 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  *   them on a stream of the library's (a second entry of its table of 64; with
  *   no room there they run in turn), where the launch plans' costs predict a
  *   gain.  The stream is ordered with `stream` by events on both sides, so for
- *   the caller the call is work on `stream` like any other.  A capture into a
- *   graph wants one call of the same sizes on the capturing stream before it
- *   (the buffers' allocation).
+ *   the caller the call is work on `stream` like any other.
  * Strategy: a product with an epilogue of this section always emulates; the
  *   plain products of the backward passes follow emu_set_strategy.
  * Repeatability: all sums are added in an order fixed by the sizes and the

@@ -43,6 +43,8 @@ class Graph:
     def nodes(self):
         n = ctypes.c_size_t(0)
         _call("cudaGraphGetNodes", self.graph, None, ctypes.byref(n))
+        if n.value == 0:
+            return []
         nodes = (ctypes.c_void_p * n.value)()
         _call("cudaGraphGetNodes", self.graph, nodes, ctypes.byref(n))
         return [ctypes.c_void_p(v) for v in nodes]

@@ -149,3 +149,127 @@ def test_many_replays_with_new_inputs(name):
                 assert torch.equal(got, w), f"replay {i}, output {k}"
     assert emu.emu_stream_check(stream) == 0
     graph.close()
+
+
+class OddBackward(LinearBackward):
+    """Rows off the 16-byte boundaries (aligned copies), column sums, a product
+    split ahead (tf32x3) and split along k: every kind of buffer."""
+
+    def __init__(self, M, N, K, mode="tf32x3"):
+        super().__init__(M, N, K, mode)
+        self.k4 = (K + 3) // 4 * 4
+        self.dx, self.dw = empty(M, self.k4), empty(N, self.k4)
+        self.outputs = [self.dz, self.dx, self.dw, self.db]
+
+    def run(self):
+        import fp32_emulated_gemm_gb300 as emu
+        M, N, K = self.size
+        emu.emu_linear_act_bwd(emu.MODES[self.mode], M, N, K, self.dy, N, self.x, K, self.w, K, self.d, N, self.dz, N,
+                               self.dx, self.k4, self.dw, self.k4, self.db)
+
+    def results(self):
+        K = self.size[2]
+        return [self.dz, self.dx[:, :K], self.dw[:, :K], self.db]
+
+
+class NormBackward:
+    def __init__(self, M, N):
+        self.size = (M, N)
+        self.dy, self.x, self.mean, self.rstd = empty(M, N), empty(M, N), empty(M), empty(M)
+        self.dx, self.dw, self.db = empty(M, N), empty(N), empty(N)
+        self.inputs, self.outputs = [self.dy, self.x, self.mean, self.rstd], [self.dx, self.dw, self.db]
+
+    def draw(self, seed):
+        M, N = self.size
+        return [rand(M, N, seed=seed), rand(M, N, seed=seed + 100), rand(M, seed=seed), rand(M, seed=seed + 100)]
+
+    def run(self):
+        import fp32_emulated_gemm_gb300 as emu
+        M, N = self.size
+        emu.emu_layer_norm_bwd(M, N, self.dy, N, self.x, N, None, self.mean, self.rstd, None, 0, self.dx, N, self.dw,
+                               self.db)
+
+    def results(self):
+        return self.outputs
+
+
+def filled(case, seed):
+    for t, v in zip(case.inputs, case.draw(seed)):
+        t.copy_(v)
+    return case
+
+
+@pytest.mark.parametrize("small,large", [
+    (lambda: OddBackward(1300, 300, 499), lambda: OddBackward(9000, 1100, 2047)),
+    (lambda: NormBackward(500, 260), lambda: NormBackward(70000, 1500)),
+])
+def test_a_larger_call_leaves_a_graphs_buffers_alone(small, large):
+    """A graph's replays after calls of other sizes on its stream, which need
+    larger buffers: each computes its own."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    from tests import _graphs
+    emu.emu_shutdown()                    # the stream may have larger buffers from before
+    a, b = filled(small(), 1), filled(large(), 2)
+    a.run()
+    b.run()
+    want_a, want_b = [t.clone() for t in a.results()], [t.clone() for t in b.results()]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        a.run()
+    graph = _graphs.Graph(stream, a.run)
+    with torch.cuda.stream(stream):
+        for rep in range(6):
+            for t in a.outputs + b.outputs:
+                t.fill_(float("nan"))
+            if rep % 2:
+                graph.launch()
+                b.run()
+            else:
+                b.run()
+                graph.launch()
+            for got, want in zip(a.results() + b.results(), want_a + want_b):
+                assert torch.equal(got, want), rep
+    assert emu.emu_stream_check(stream) == 0
+    graph.close()
+
+
+@pytest.mark.parametrize("make", [lambda: Product(300, 260, 3000, "bf16x9"), lambda: Product(2000, 2500, 200, "tf32x3"),
+                                  lambda: OddBackward(1300, 300, 499), lambda: NormBackward(500, 260)])
+def test_no_allocation_under_capture(make):
+    """A captured call whose buffers its stream does not have is refused; the
+    capture stays valid and the library as it was."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    from tests import _graphs
+    emu.emu_shutdown()
+    case = filled(make(), 3)
+    case.run()
+    want = [t.clone() for t in case.outputs]
+    stream = torch.cuda.Stream()
+    status = []
+
+    def refused():
+        try:
+            case.run()
+        except emu.EmuError as e:
+            status.append(e.status)
+
+    graph = _graphs.Graph(stream, refused)
+    assert status == [4] and graph.nodes() == []
+    graph.close()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        case.run()                        # now the stream has them
+    graph = _graphs.Graph(stream, case.run)
+    with torch.cuda.stream(stream):
+        for t in case.outputs:
+            t.zero_()
+        graph.launch()
+        if hasattr(case, "results"):
+            case.outputs = case.results()
+        for got, w in zip(case.outputs, want):
+            assert torch.equal(got, w[:, :got.shape[1]] if got.dim() == 2 else w)
+    assert emu.emu_stream_check(stream) == 0
+    graph.close()
