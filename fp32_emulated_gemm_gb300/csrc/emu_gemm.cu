@@ -93,7 +93,11 @@ cudaError_t lib_malloc_async(void** ptr, size_t bytes, cudaStream_t stream) {
 }
 
 constexpr int kMaxDevices = 64;
+// The tables (slots, device information).  Taken after a StreamLock, never before.
 std::mutex g_mutex;
+// StreamLock: streams share these by their handles.
+constexpr int kStreamMutexes = 256;
+std::mutex g_stream_mutex[kStreamMutexes];
 DeviceInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
@@ -1203,6 +1207,9 @@ __global__ void split_timeout_selftest_kernel(unsigned long long* counters, int 
 
 }  // namespace
 
+StreamLock::StreamLock(cudaStream_t stream)
+    : lock_(g_stream_mutex[(reinterpret_cast<uintptr_t>(stream) * 0x9E3779B97F4A7C15ull >> 40) % kStreamMutexes]) {}
+
 emu_status_t current_device(DeviceCtx* out) {
     DeviceInfo* d = nullptr;
     const emu_status_t st = device_info(&d);
@@ -1338,6 +1345,7 @@ extern "C" {
 emu_status_t emu_sgemm(emu_mode_t mode, emu_op_t transA, emu_op_t transB, int64_t M, int64_t N, int64_t K,
                        float alpha, const float* A, int64_t lda, const float* B, int64_t ldb, float beta,
                        float* C, int64_t ldc, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     if ((transA != EMU_OP_N && transA != EMU_OP_T) || (transB != EMU_OP_N && transB != EMU_OP_T))
         return EMU_STATUS_INVALID_VALUE;
     // op(A) is K-major in memory when A is stored M x K; op(B) when B is N x K.
@@ -1347,6 +1355,7 @@ emu_status_t emu_sgemm(emu_mode_t mode, emu_op_t transA, emu_op_t transB, int64_
 
 emu_status_t emu_linear_fwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float* X, const float* W,
                             const float* bias, float* Y, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     // Y = X W^T + b: op(A) = X (K-major), op(B) = W^T (W is N x K, K-major)
     return run_gemm(mode, false, false, M, N, K, 1.0f, X, K, W, K, 0.0f, Y, N, bias,
                     reinterpret_cast<cudaStream_t>(stream));
@@ -1354,6 +1363,7 @@ emu_status_t emu_linear_fwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K, co
 
 emu_status_t emu_linear_bwd_input(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float* dY,
                                   const float* W, float* dX, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     // dX[M,K] = dY[M,N] W[N,K]: GEMM with output width K and contraction N;
     // op(B) = W is MN-major (rows are the contraction index)
     return run_gemm(mode, false, true, M, K, N, 1.0f, dY, N, W, K, 0.0f, dX, K, nullptr,
@@ -1362,6 +1372,7 @@ emu_status_t emu_linear_bwd_input(emu_mode_t mode, int64_t M, int64_t N, int64_t
 
 emu_status_t emu_linear_bwd_weight(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float* dY,
                                    const float* X, float beta, float* dW, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     // dW[N,K] = dY^T X: output rows N, output columns K, contraction M; both
     // operands are MN-major (their rows are the contraction index)
     return run_gemm(mode, true, true, N, K, M, 1.0f, dY, N, X, K, beta, dW, K, nullptr,
@@ -1392,6 +1403,7 @@ emu_status_t emu_pack_b(emu_mode_t mode, emu_op_t transB, int64_t N, int64_t K, 
 emu_status_t emu_sgemm_packed_b(emu_mode_t mode, emu_op_t transA, int64_t M, int64_t N, int64_t K, float alpha,
                                 const float* A, int64_t lda, const void* packed_b, float beta, float* C,
                                 int64_t ldc, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     if (!emulated_mode(mode) || (transA != EMU_OP_N && transA != EMU_OP_T)) return EMU_STATUS_INVALID_VALUE;
     if (!packed_b && K > 0 && alpha != 0.0f) return EMU_STATUS_INVALID_VALUE;
     return run_gemm(mode, transA == EMU_OP_T, false, M, N, K, alpha, A, lda, nullptr, 0, beta, C, ldc, nullptr,
@@ -1400,6 +1412,7 @@ emu_status_t emu_sgemm_packed_b(emu_mode_t mode, emu_op_t transA, int64_t M, int
 
 emu_status_t emu_linear_fwd_packed(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float* X,
                                    const void* W_packed, const float* bias, float* Y, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     if (!emulated_mode(mode) || (!W_packed && K > 0)) return EMU_STATUS_INVALID_VALUE;
     return run_gemm(mode, false, false, M, N, K, 1.0f, X, K, nullptr, 0, 0.0f, Y, N, bias,
                     reinterpret_cast<cudaStream_t>(stream), W_packed);
@@ -1407,6 +1420,7 @@ emu_status_t emu_linear_fwd_packed(emu_mode_t mode, int64_t M, int64_t N, int64_
 
 emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float* dY,
                                          const void* Wt_packed, float* dX, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     if (!emulated_mode(mode) || (!Wt_packed && N > 0)) return EMU_STATUS_INVALID_VALUE;
     return run_gemm(mode, false, false, M, K, N, 1.0f, dY, N, nullptr, 0, 0.0f, dX, K, nullptr,
                     reinterpret_cast<cudaStream_t>(stream), Wt_packed);
@@ -1472,6 +1486,7 @@ emu_status_t emu_selftest_wait_timeout(uint64_t budget_ns, emu_stream_t stream) 
 }
 
 emu_status_t emu_selftest_split_timeout(uint64_t budget_ns, int64_t tiles, emu_stream_t stream) {
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     if (budget_ns == 0 || budget_ns > 10000000000ull || tiles < 1 || tiles > (int64_t(1) << 24))
         return EMU_STATUS_INVALID_VALUE;
     DeviceInfo* dev = nullptr;
@@ -1705,6 +1720,7 @@ extern "C" emu_status_t emu_sgemm_noalloc(emu_mode_t mode, emu_op_t transA, emu_
                                           const float* B, int64_t ldb, float beta, float* C, int64_t ldc,
                                           emu_stream_t stream) {
     using namespace emu;
+    const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
     if ((transA != EMU_OP_N && transA != EMU_OP_T) || (transB != EMU_OP_N && transB != EMU_OP_T))
         return EMU_STATUS_INVALID_VALUE;
     return run_gemm_noalloc(mode, transA == EMU_OP_T, transB == EMU_OP_N, M, N, K, alpha, A, lda, B, ldb, beta, C,

@@ -446,6 +446,7 @@ emu_status_t emu_linear_act_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64
     if (!Y || ldy < N || (residual && ldr < N) || (D && ldd < N)) return EMU_STATUS_INVALID_VALUE;
     DeviceCtx dev{};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     Aligned al;
     if (!few_rows(mode, M, N, K)) {
         al.add(X, ldx, M, K);
@@ -470,6 +471,7 @@ emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K
     if (rows && (!dY || lddy < N || (D && (!dZ || ldd < N || lddz < N)))) return EMU_STATUS_INVALID_VALUE;
     const bool apply = D && rows;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     Aligned al;  // (D and, with it, dY are not a product's)
     if (!D) al.add(dY, lddy, M, N);
     if (dW) al.add(X, ldx, M, K);
@@ -500,6 +502,7 @@ emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F,
     if (!H || ldh < F || (D && ldd < 2 * F) || (!D && gated_needs_d(mode))) return EMU_STATUS_INVALID_VALUE;
     DeviceCtx dev{};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     Aligned al;
     if (!few_rows(mode, M, 2 * F, K)) {
         al.add(X, ldx, M, K);
@@ -521,6 +524,7 @@ emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, con
     if (!size_ok(M) || !size_ok(2 * F) || !size_ok(K)) return EMU_STATUS_NOT_SUPPORTED;
     if (M > 0 && F > 0 && (!dH || !D || !dZ || lddh < F || ldd < 2 * F || lddz < 2 * F)) return EMU_STATUS_INVALID_VALUE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     Aligned al;  // (dH and D are not a product's)
     if (dW) al.add(X, ldx, M, K);
     if (dX) al.add(W, ldw, 2 * F, K);
@@ -548,6 +552,7 @@ emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_
     if (N > 0 && (!Y || ldy < N || (residual && ldr < N))) return EMU_STATUS_INVALID_VALUE;
     DeviceCtx dev{};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     Aligned al;
     if (!few_rows(mode, M, 2 * F, K)) {
         al.add(X, ldx, M, K);
@@ -584,6 +589,7 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
         if (!aligned_rows(dZ, lddz)) return EMU_STATUS_NOT_SUPPORTED;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     const bool inner = dX || dW_in || db_in;
     Aligned al;
     if (inner || dW_out) al.add(dY, lddy, M, N);

@@ -6,6 +6,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/emu_gemm.h"
 
@@ -14,6 +15,18 @@ namespace emu {
 // The current device, bound to this host thread and checked to be sm_103.
 struct DeviceCtx { int id, sm_count; };
 emu_status_t current_device(DeviceCtx* out);
+
+// Held by an entry point from its first use of a stream's library buffers (or
+// its side stream and events) to its last launch: calls of several host threads
+// on one stream share those, and their launches must not come between one
+// another.  Not recursive.  Calls on different streams seldom share a lock.
+class StreamLock {
+public:
+    explicit StreamLock(cudaStream_t stream);
+
+private:
+    std::lock_guard<std::mutex> lock_;
+};
 
 // The (device, stream)'s buffer for column-sum partials, at least `floats`
 // long: grown on demand (never under capture), kept until emu_shutdown().  Not

@@ -393,6 +393,7 @@ emu_status_t emu_layer_norm_bwd(int64_t M, int64_t N, const float* dY, int64_t l
     emu_status_t st = current_device(&dev);
     if (st != EMU_STATUS_SUCCESS) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     const bool params = dweight || dbias;
     if (M == 0) {  // empty sums
         if ((dweight && cudaMemsetAsync(dweight, 0, N * sizeof(float), s) != cudaSuccess) ||

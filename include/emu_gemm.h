@@ -64,8 +64,11 @@
  *     on the device (the GEMM calls themselves do not read it).  A timed-out
  *     launch's output is incomplete; later launches are unaffected (the
  *     split-K arrival counters are tagged per launch).
- *   - Thread safety: all entry points may be called concurrently from
- *     several host threads.
+ *   - Thread safety: all entry points (except emu_shutdown, see there) may be
+ *     called concurrently from several host threads, on one stream too: a
+ *     call's launches then follow one another with no other call's in between.
+ *     (cudaStreamPerThread counts as one stream, whose buffers its threads would
+ *     share: not from several threads.)
  */
 #ifndef EMU_GEMM_H
 #define EMU_GEMM_H
