@@ -576,14 +576,19 @@ emu_status_t buffer_for(int dev, cudaStream_t stream, Buffer Workspace::*buffer,
     return st;
 }
 
-// The (device, stream)'s side stream and the events that order it with `stream`.
+// The (device, stream)'s side stream, of the same priority, and the events that
+// order it with `stream`.  (At a lower priority its kernel could hold some of the
+// SMs that a product on another of the caller's streams needs at once, and wait
+// for SMs itself until that one's waits run out.)
 emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, cudaEvent_t* fork, cudaEvent_t* join) {
     std::lock_guard<std::mutex> lock(g_mutex);
     Workspace* w = workspace_slot(dev, stream);
     if (!w) return EMU_STATUS_ALLOC_FAILED;
     if (!w->join) {
         if (capturing(stream)) return EMU_STATUS_ALLOC_FAILED;
-        if ((!w->side && cudaStreamCreateWithFlags(&w->side, cudaStreamNonBlocking) != cudaSuccess) ||
+        int priority = 0;
+        if (cudaStreamGetPriority(stream, &priority) != cudaSuccess ||
+            (!w->side && cudaStreamCreateWithPriority(&w->side, cudaStreamNonBlocking, priority) != cudaSuccess) ||
             (!w->fork && cudaEventCreateWithFlags(&w->fork, cudaEventDisableTiming) != cudaSuccess) ||
             cudaEventCreateWithFlags(&w->join, cudaEventDisableTiming) != cudaSuccess) {
             cudaGetLastError();

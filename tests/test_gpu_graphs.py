@@ -273,3 +273,22 @@ def test_no_allocation_under_capture(make):
             assert torch.equal(got, w[:, :got.shape[1]] if got.dim() == 2 else w)
     assert emu.emu_stream_check(stream) == 0
     graph.close()
+
+
+@pytest.mark.parametrize("priority", [0, -1])
+def test_side_by_side_products_keep_the_streams_priority(priority):
+    """Both products of a backward pass run at the priority of the caller's
+    stream (which a captured kernel node records)."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    from tests import _graphs
+    emu.emu_shutdown()
+    case = filled(LinearBackward(1536, 300, 500, "bf16x9"), 4)
+    stream = torch.cuda.Stream(priority=priority)
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        case.run()
+    graph = _graphs.Graph(stream, case.run)
+    got = graph.kernel_priorities()
+    graph.close()
+    assert len(got) >= 4 and set(got) == {priority}, got
