@@ -352,7 +352,21 @@ def gated_ffn_bwd(dY, X, W_in, W_out, D, H, *, act="silu", mode="bf16x9", need=(
 
 
 # ------------------------------------------------------------- autograd ----
-class EmuLayerNormFunction(torch.autograd.Function):
+class _Function(torch.autograd.Function):
+    """With gradients off, `apply` is the call itself, which stores nothing for a
+    backward pass.  (needs_input_grad cannot tell: it is set for parameters then
+    too, and inside `forward` gradients are always off.)"""
+
+    @classmethod
+    def apply(cls, *args):
+        return super().apply(*args) if torch.is_grad_enabled() else cls.infer(*args)
+
+
+class EmuLayerNormFunction(_Function):
+    @staticmethod
+    def infer(X, weight, bias, eps):
+        return layer_norm_fwd(X, weight, bias, eps=eps)[0]
+
     @staticmethod
     def forward(ctx, X, weight, bias, eps):
         Y, mean, rstd = layer_norm_fwd(X, weight, bias, eps=eps)
@@ -369,7 +383,11 @@ class EmuLayerNormFunction(torch.autograd.Function):
         return dX, dw if need[1] else None, db if need[2] else None, None
 
 
-class EmuLinearActFunction(torch.autograd.Function):
+class EmuLinearActFunction(_Function):
+    @staticmethod
+    def infer(X, W, bias, residual, act, mode):
+        return linear_act_fwd(X, W, bias, act=act, residual=residual, mode=mode)
+
     @staticmethod
     def forward(ctx, X, W, bias, residual, act, mode):
         save = act != "none" and any(ctx.needs_input_grad[:3])
@@ -390,7 +408,11 @@ class EmuLinearActFunction(torch.autograd.Function):
         return dX, dW, db, dY if need[3] else None, None, None
 
 
-class EmuGatedFFNFunction(torch.autograd.Function):
+class EmuGatedFFNFunction(_Function):
+    @staticmethod
+    def infer(X, W_in, b_in, W_out, b_out, residual, act, mode):
+        return gated_ffn_fwd(X, W_in, b_in, W_out, b_out, act=act, residual=residual, mode=mode)
+
     @staticmethod
     def forward(ctx, X, W_in, b_in, W_out, b_out, residual, act, mode):
         save = any(ctx.needs_input_grad[:5])
@@ -411,9 +433,14 @@ class EmuGatedFFNFunction(torch.autograd.Function):
         return (*grads, dY if need[5] else None, None, None)
 
 
-class EmuFeedForwardFunction(torch.autograd.Function):
+class EmuFeedForwardFunction(_Function):
     """x + gated_ffn(layer_norm(x)): the residual's gradient joins in the norm's
     backward pass."""
+
+    @staticmethod
+    def infer(X, norm_weight, norm_bias, W_in, b_in, W_out, b_out, eps, act, mode):
+        Xn = layer_norm_fwd(X, norm_weight, norm_bias, eps=eps)[0]
+        return gated_ffn_fwd(Xn, W_in, b_in, W_out, b_out, act=act, residual=X, mode=mode)
 
     @staticmethod
     def forward(ctx, X, norm_weight, norm_bias, W_in, b_in, W_out, b_out, eps, act, mode):

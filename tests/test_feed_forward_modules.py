@@ -1,0 +1,72 @@
+"""The feed-forward modules' host side, without a GPU: the functional calls are
+replaced by plain ones that record how they were called."""
+import pytest
+import torch
+import torch.nn.functional as F
+
+import fp32_emulated_gemm_gb300 as emu
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    from fp32_emulated_gemm_gb300 import feed_forward as ff
+    made = []
+
+    def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, save=True, out=None):
+        made.append(("layer_norm", None))
+        y = F.layer_norm(X, X.shape[1:], weight, bias, eps)
+        return (y, X.new_zeros(len(X)), X.new_zeros(len(X))) if save else y
+
+    def linear_act_fwd(X, W, bias=None, *, act="none", residual=None, mode="bf16x9", save=False, out=None):
+        made.append(("linear_act", save))
+        y = F.gelu(F.linear(X, W, bias))
+        y = y if residual is None else y + residual
+        return (y, X.new_zeros(len(X), len(W))) if save else y
+
+    def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mode="bf16x9", save=False, out=None):
+        made.append(("gated_ffn", save))
+        g, u = F.linear(X, W_in, b_in).chunk(2, -1)
+        y = F.linear(F.silu(g) * u, W_out, b_out)
+        y = y if residual is None else y + residual
+        return (y, X.new_zeros(len(X), len(W_in)), g * u) if save else y
+
+    for f in (layer_norm_fwd, linear_act_fwd, gated_ffn_fwd):
+        monkeypatch.setattr(ff, f.__name__, f)
+    return made
+
+
+MODULES = {
+    "linear_act": lambda: emu.EmuLinearAct(6, 10),
+    "gated_ffn": lambda: emu.EmuGatedFFN(6, 8),
+    "feed_forward": lambda: emu.EmuFeedForward(6, 8),
+}
+
+
+@pytest.mark.parametrize("off", [torch.no_grad, torch.inference_mode])
+@pytest.mark.parametrize("name", MODULES)
+def test_nothing_is_saved_with_gradients_off(calls, name, off):
+    """Parameters that require gradients do not make an inference call store
+    what only a backward pass reads."""
+    torch.manual_seed(0)
+    m, x = MODULES[name](), torch.randn(5, 6)
+    trained = m(x)
+    assert trained.requires_grad and [s for _, s in calls if s is not None] == [True]
+    calls.clear()
+    with off():
+        y = m(x)
+    assert not y.requires_grad and torch.equal(y, trained.detach())
+    assert [s for _, s in calls if s is not None] == [False]
+
+
+@pytest.mark.parametrize("name", MODULES)
+def test_nothing_is_saved_when_no_input_needs_a_gradient(calls, name):
+    m = MODULES[name]().requires_grad_(False)
+    assert not m(torch.randn(5, 6)).requires_grad
+    assert [s for _, s in calls if s is not None] == [False]
+
+
+def test_layer_norm_with_gradients_off(calls):
+    m, x = emu.EmuLayerNorm(6), torch.randn(5, 6)
+    with torch.no_grad():
+        y = m(x)
+    assert not y.requires_grad and torch.allclose(y, F.layer_norm(x, (6,)), atol=1e-6)
