@@ -157,8 +157,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 # ----------------------------------------------------------- layer norm ----
-def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, out=None):
-    """(Y, mean, rstd): Y = (X - mean) * rstd * weight + bias over the rows of X."""
+def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, save=True, out=None):
+    """(Y, mean, rstd), or Y alone without `save`: Y = (X - mean) * rstd * weight
+    + bias over the rows of X; layer_norm_bwd wants the other two."""
     X, px, ldx = _rows(X, "X")
     M, N = X.shape
     weight, pw = _vector(weight, "weight", N)
@@ -169,11 +170,13 @@ def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, out=None):
         py = Y.data_ptr()
     else:
         Y, py, ldy = _result(out, (M, N), device, "out")
-    mean, pm = _new_vector(M, device)
-    rstd, pr = _new_vector(M, device)
+    mean = rstd = pm = pr = None
+    if save:
+        mean, pm = _new_vector(M, device)
+        rstd, pr = _new_vector(M, device)
     _check(_fn("emu_layer_norm_fwd")(M, N, px, ldx, pw, pb, eps, py, ldy, pm, pr,
                                      _stream_of("layer_norm_fwd", X, weight, bias, Y)), "emu_layer_norm_fwd")
-    return Y, mean, rstd
+    return (Y, mean, rstd) if save else Y
 
 
 def layer_norm_bwd(dY, X, weight, mean, rstd, *, add=None, need_input=True, need_params=True):
@@ -353,19 +356,22 @@ def gated_ffn_bwd(dY, X, W_in, W_out, D, H, *, act="silu", mode="bf16x9", need=(
 
 # ------------------------------------------------------------- autograd ----
 class _Function(torch.autograd.Function):
-    """With gradients off, `apply` is the call itself, which stores nothing for a
-    backward pass.  (needs_input_grad cannot tell: it is set for parameters then
-    too, and inside `forward` gradients are always off.)"""
+    """With gradients off, or wanted by no argument, `apply` is the call itself,
+    which stores nothing for a backward pass.  (needs_input_grad cannot tell: it
+    is set for parameters with gradients off too, and inside `forward` they are
+    always off.)"""
 
     @classmethod
     def apply(cls, *args):
-        return super().apply(*args) if torch.is_grad_enabled() else cls.infer(*args)
+        if torch.is_grad_enabled() and any(isinstance(a, torch.Tensor) and a.requires_grad for a in args):
+            return super().apply(*args)
+        return cls.infer(*args)
 
 
 class EmuLayerNormFunction(_Function):
     @staticmethod
     def infer(X, weight, bias, eps):
-        return layer_norm_fwd(X, weight, bias, eps=eps)[0]
+        return layer_norm_fwd(X, weight, bias, eps=eps, save=False)
 
     @staticmethod
     def forward(ctx, X, weight, bias, eps):
@@ -439,7 +445,7 @@ class EmuFeedForwardFunction(_Function):
 
     @staticmethod
     def infer(X, norm_weight, norm_bias, W_in, b_in, W_out, b_out, eps, act, mode):
-        Xn = layer_norm_fwd(X, norm_weight, norm_bias, eps=eps)[0]
+        Xn = layer_norm_fwd(X, norm_weight, norm_bias, eps=eps, save=False)
         return gated_ffn_fwd(Xn, W_in, b_in, W_out, b_out, act=act, residual=X, mode=mode)
 
     @staticmethod

@@ -70,3 +70,26 @@ def test_layer_norm_with_gradients_off(calls):
     with torch.no_grad():
         y = m(x)
     assert not y.requires_grad and torch.allclose(y, F.layer_norm(x, (6,)), atol=1e-6)
+
+
+def test_the_norms_statistics_are_kept_for_gradients_alone(monkeypatch):
+    from fp32_emulated_gemm_gb300 import feed_forward as ff
+    saves = []
+
+    def layer_norm_fwd(X, weight=None, bias=None, *, eps=1e-5, save=True, out=None):
+        saves.append(save)
+        y = F.layer_norm(X, X.shape[1:], weight, bias, eps)
+        return (y, X.new_zeros(len(X)), X.new_zeros(len(X))) if save else y
+
+    def gated_ffn_fwd(X, *args, residual=None, save=False, **kw):
+        return (X + residual, X, X) if save else X + residual
+
+    monkeypatch.setattr(ff, "layer_norm_fwd", layer_norm_fwd)
+    monkeypatch.setattr(ff, "gated_ffn_fwd", gated_ffn_fwd)
+    x = torch.randn(5, 6)
+    for m in (emu.EmuLayerNorm(6), emu.EmuFeedForward(6, 8)):
+        m(x)
+        with torch.no_grad():
+            m(x)
+        m.requires_grad_(False)(x)
+    assert saves == [True, False, False] * 2

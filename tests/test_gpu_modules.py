@@ -51,3 +51,15 @@ def test_inference_and_training_of_every_module_agree():
                     z = m(x)
                 assert not z.requires_grad and torch.equal(z, y.detach())
     assert emu.emu_stream_check() == 0
+
+
+def test_layer_norm_without_statistics():
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    for M, N in ((192, 256), (5, 31), (3, 20000), (0, 8)):
+        x, w, b = (torch.randn(*s, device=_gpu.device()) for s in ((M, N), (N,), (N,)))
+        y = emu.layer_norm_fwd(x, w, b, save=False)
+        assert torch.equal(y, emu.layer_norm_fwd(x, w, b)[0])
+        out = torch.empty(M, N, device=_gpu.device())
+        assert emu.layer_norm_fwd(x, w, b, save=False, out=out) is out and torch.equal(out, y)
+    assert emu.emu_stream_check() == 0
