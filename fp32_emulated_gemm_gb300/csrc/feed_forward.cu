@@ -584,13 +584,14 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     if (M < 0 || K < 0 || F < 0 || N < 0) return EMU_STATUS_INVALID_VALUE;
     if (!size_ok(M) || !size_ok(K) || !size_ok(2 * F) || !size_ok(N)) return EMU_STATUS_NOT_SUPPORTED;
     if (M > 0 && N > 0 && (!dY || lddy < N)) return EMU_STATUS_INVALID_VALUE;
+    const bool inner = dX || dW_in || db_in;
     if (M > 0 && F > 0) {
-        if (!D || !H || !dZ || ldd < 2 * F || ldh < F || lddz < 2 * F) return EMU_STATUS_INVALID_VALUE;
-        if (!aligned_rows(dZ, lddz)) return EMU_STATUS_NOT_SUPPORTED;
+        if (dW_out && (!H || ldh < F)) return EMU_STATUS_INVALID_VALUE;
+        if (inner && (!D || !dZ || ldd < 2 * F || lddz < 2 * F)) return EMU_STATUS_INVALID_VALUE;
+        if (inner && !aligned_rows(dZ, lddz)) return EMU_STATUS_NOT_SUPPORTED;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const StreamLock lock(s);
-    const bool inner = dX || dW_in || db_in;
     Aligned al;
     if (inner || dW_out) al.add(dY, lddy, M, N);
     if (dW_out) al.add(H, ldh, M, F);

@@ -331,17 +331,19 @@ def gated_ffn_fwd(X, W_in, b_in, W_out, b_out, *, act="silu", residual=None, mod
 def gated_ffn_bwd(dY, X, W_in, W_out, D, H, *, act="silu", mode="bf16x9", need=(True, True, True, True, True)):
     """(dX, dW_in, db_in, dW_out, db_out) of gated_ffn_fwd from its D and H
     (the residual's gradient is dY); `need` says which are wanted.  (D holds the
-    activation's part; `act` only has to name one.)"""
+    activation's part; `act` only has to name one.)  D may be None where only
+    dW_out and db_out are wanted, H where dW_out is not."""
     _act(act)
     X, px, ldx = _rows(X, "X")
     W_in, pwi, ldwi = _rows(W_in, "W_in")
     W_out, pwo, ldwo = _rows(W_out, "W_out")
     M, K, F, N = _ffn_shapes(X, W_in, W_out)
     dY, pdy, lddy = _rows(dY, "dY", (M, N))
-    D, pd, ldd = _rows(D, "D", (M, 2 * F))
-    H, ph, ldh = _rows(H, "H", (M, F))
+    inner = any(need[:3])
+    D, pd, ldd = _rows(D, "D", (M, 2 * F)) if inner or D is not None else _NONE
+    H, ph, ldh = _rows(H, "H", (M, F)) if need[3] or H is not None else _NONE
     device = X.device
-    dZ, pdz, lddz = _new(M, 2 * F, device)
+    dZ, pdz, lddz = _new(M, 2 * F, device) if inner else _NONE
     dX, pdx, lddx = _new(M, K, device) if need[0] else _NONE
     dWi, pdwi, lddwi = _new(2 * F, K, device) if need[1] else _NONE
     dbi, pdbi = _new_vector(2 * F, device) if need[2] else (None, None)

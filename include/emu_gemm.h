@@ -331,7 +331,8 @@ emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_
  * emu_gated_ffn_bwd -- its gradients, from D and H of the forward pass:
  *   dW_out = dY^T H, db_out = sum over rows of dY, dH = dY W_out, then
  *   emu_gated_bwd's dZ, dX, dW_in and db_in.  dX, dW_in, db_in, dW_out and
- *   db_out may each be NULL (not wanted).
+ *   db_out may each be NULL (not wanted); D and dZ are used for the first three
+ *   alone and H for dW_out, and may be NULL otherwise.
  */
 emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F, int64_t N, const float *dY,
                                int64_t lddy, const float *X, int64_t ldx, const float *W_in, int64_t ldwi,

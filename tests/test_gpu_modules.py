@@ -63,3 +63,23 @@ def test_layer_norm_without_statistics():
         out = torch.empty(M, N, device=_gpu.device())
         assert emu.layer_norm_fwd(x, w, b, save=False, out=out) is out and torch.equal(out, y)
     assert emu.emu_stream_check() == 0
+
+
+def test_output_projection_gradients_alone():
+    """dW_out and db_out without the others: the same values, no M x 2F buffer,
+    and D is not asked for; db_out alone does not ask for H either."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(2)
+    M, K, F, N = 20000, 32, 512, 64
+    x, wi, wo, dy = (torch.randn(*s, device=_gpu.device()) for s in ((M, K), (2 * F, K), (N, F), (M, N)))
+    _, d, h = emu.gated_ffn_fwd(x, wi, None, wo, None, save=True)
+    full = emu.gated_ffn_bwd(dy, x, wi, wo, d, h)
+    only = lambda: emu.gated_ffn_bwd(dy, x, wi, wo, None, h, need=(False, False, False, True, True))
+    some = only()
+    assert some[:3] == (None, None, None) and peak(only) <= 4 * (N * F + N) + (1 << 20)
+    bound = 2 * (2 * M + 8) * 2.0 ** -24 * (dy.abs().T @ h.abs())        # two plans of the same product
+    assert bool(((some[3] - full[3]).abs() <= bound).all()) and torch.equal(some[4], full[4])
+    bias = emu.gated_ffn_bwd(dy, x, wi, wo, None, None, need=(False, False, False, False, True))
+    assert torch.equal(bias[4], full[4])
+    assert emu.emu_stream_check() == 0
