@@ -12,6 +12,7 @@ rows where their width is not a multiple of 4.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -488,6 +489,20 @@ class EmuLayerNorm(torch.nn.LayerNorm):
         return EmuLayerNormFunction.apply(x.reshape(rows, n), *flat, self.eps).reshape(x.shape)
 
 
+def _flat(x, residual, in_features, out_features):
+    """(rows of x, rows of the residual, shape of the result).  The residual has
+    that shape, or is the matrix of its rows."""
+    if x.dim() < 1 or x.shape[-1] != in_features:
+        raise ValueError(f"the input must have {in_features} features, not shape {tuple(x.shape)}")
+    shape = (*x.shape[:-1], out_features)
+    rows = math.prod(shape[:-1])
+    if residual is not None:
+        if tuple(residual.shape) not in (shape, (rows, out_features)):
+            raise ValueError(f"the residual must be {tuple(shape)}, not {tuple(residual.shape)}")
+        residual = residual.reshape(rows, out_features)
+    return x.reshape(rows, in_features), residual, shape
+
+
 class EmuLinearAct(torch.nn.Linear):
     """nn.Linear with an activation and an optional residual:
     act(x W^T + b) + residual."""
@@ -498,12 +513,8 @@ class EmuLinearAct(torch.nn.Linear):
         self.act, self.mode = act, mode
 
     def forward(self, x, residual=None):
-        shape = (*x.shape[:-1], self.out_features)
-        if residual is not None:
-            residual = residual.reshape(-1, self.out_features)
-        y = EmuLinearActFunction.apply(x.reshape(-1, self.in_features), self.weight, self.bias, residual, self.act,
-                                       self.mode)
-        return y.reshape(shape)
+        x, residual, shape = _flat(x, residual, self.in_features, self.out_features)
+        return EmuLinearActFunction.apply(x, self.weight, self.bias, residual, self.act, self.mode).reshape(shape)
 
 
 class EmuGatedFFN(torch.nn.Module):
@@ -532,11 +543,9 @@ class EmuGatedFFN(torch.nn.Module):
                 torch.nn.init.uniform_(b, -bound, bound)
 
     def forward(self, x, residual=None):
-        shape = (*x.shape[:-1], self.out_features)
-        if residual is not None:
-            residual = residual.reshape(-1, self.out_features)
-        y = EmuGatedFFNFunction.apply(x.reshape(-1, self.in_features), self.weight_in, self.bias_in, self.weight_out,
-                                      self.bias_out, residual, self.act, self.mode)
+        x, residual, shape = _flat(x, residual, self.in_features, self.out_features)
+        y = EmuGatedFFNFunction.apply(x, self.weight_in, self.bias_in, self.weight_out, self.bias_out, residual, self.act,
+                                      self.mode)
         return y.reshape(shape)
 
 
@@ -552,6 +561,7 @@ class EmuFeedForward(torch.nn.Module):
 
     def forward(self, x):
         f = self.ffn
-        y = EmuFeedForwardFunction.apply(x.reshape(-1, f.in_features), self.norm.weight, self.norm.bias, f.weight_in,
-                                         f.bias_in, f.weight_out, f.bias_out, self.norm.eps, f.act, f.mode)
-        return y.reshape(x.shape)
+        x, _, shape = _flat(x, None, f.in_features, f.out_features)
+        y = EmuFeedForwardFunction.apply(x, self.norm.weight, self.norm.bias, f.weight_in, f.bias_in, f.weight_out,
+                                         f.bias_out, self.norm.eps, f.act, f.mode)
+        return y.reshape(shape)

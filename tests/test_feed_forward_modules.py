@@ -93,3 +93,32 @@ def test_the_norms_statistics_are_kept_for_gradients_alone(monkeypatch):
             m(x)
         m.requires_grad_(False)(x)
     assert saves == [True, False, False] * 2
+
+
+@pytest.mark.parametrize("name", MODULES)
+def test_inputs_of_another_width_are_refused(calls, name):
+    """An input whose elements make a whole number of rows of the right width
+    is no input of that width."""
+    m = MODULES[name]()
+    for shape in ((5, 12), (2, 3, 3), (12,), (4, 18), ()):
+        with pytest.raises(ValueError):
+            m(torch.randn(shape))
+    assert calls == []
+    out = 10 if name == "linear_act" else 6
+    for shape in ((6,), (0, 6), (2, 3, 6), (2, 0, 6)):
+        assert m(torch.randn(shape)).shape == (*shape[:-1], out)
+
+
+@pytest.mark.parametrize("name", ["linear_act", "gated_ffn"])
+def test_residuals_of_another_shape_are_refused(calls, name):
+    """The residual's rows are the result's: another shape of as many elements
+    is refused, as a sum of the two would be; the flat matrix is taken."""
+    m, out = MODULES[name](), 10 if name == "linear_act" else 6
+    x = torch.randn(2, 3, 6)
+    for shape in ((3, 2, out), (6 * out,), (2, 3 * out), (1, 3, out), (2, out, 3)):
+        with pytest.raises(ValueError):
+            m(x, torch.randn(shape))
+    assert calls == []
+    r = torch.randn(2, 3, out)
+    y = m(x, r)
+    assert torch.allclose(y - r, m(x), atol=1e-6) and torch.equal(y, m(x, r.reshape(6, out)))
