@@ -926,7 +926,7 @@ constexpr int kStagedMinPieces = 12;
 // Programmatic dependent launch (EMU_PDL=0 turns it off): the kernel may be
 // scheduled while the previous kernel in the stream finishes; it runs its
 // set-up and then waits for that kernel before touching global memory.
-bool pdl_enabled() {
+bool pdl_on() {
     static const bool v = env_int("EMU_PDL", 1) != 0;
     return v;
 }
@@ -941,7 +941,7 @@ cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters
     cfg.blockDim = dim3(NUM_THREADS, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    if (pdl_enabled()) {
+    if (pdl_on()) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
@@ -1214,6 +1214,8 @@ __global__ void split_timeout_selftest_kernel(unsigned long long* counters, int 
 
 StreamLock::StreamLock(cudaStream_t stream)
     : lock_(g_stream_mutex[(reinterpret_cast<uintptr_t>(stream) * 0x9E3779B97F4A7C15ull >> 40) % kStreamMutexes]) {}
+
+bool pdl_enabled() { return pdl_on(); }
 
 emu_status_t current_device(DeviceCtx* out) {
     DeviceInfo* d = nullptr;

@@ -271,7 +271,7 @@ cudaError_t launch_sum_partials(const Partials* sets, int n, cudaStream_t stream
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, sum_partials_kernel, pair);
     if (e != cudaSuccess) cudaGetLastError();
     return e;

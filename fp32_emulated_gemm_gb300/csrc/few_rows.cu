@@ -21,6 +21,7 @@
 // (K = 1024, N = 4096, eight tokens: 12.0 us), for they halve the warps.
 #include "few_rows.h"
 
+#include "internal.h"
 #include "ptx.cuh"
 #include "row_ops.cuh"
 
@@ -171,7 +172,7 @@ cudaError_t launch(const FewRows& p, bool gated, bool after_own, int sm_count, c
     cfg.blockDim = dim3(32 * kWarpsPerBlock, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    if (after_own) {
+    if (after_own && pdl_enabled()) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;

@@ -16,6 +16,10 @@ namespace emu {
 struct DeviceCtx { int id, sm_count; };
 emu_status_t current_device(DeviceCtx* out);
 
+// Whether launches may overlap the end of the kernel before them on the stream
+// (programmatic dependent launch; EMU_PDL=0 turns it off).
+bool pdl_enabled();
+
 // Held by an entry point from its first use of a stream's library buffers (or
 // its side stream and events) to its last launch: calls of several host threads
 // on one stream share those, and their launches must not come between one

@@ -66,6 +66,17 @@ class Graph:
                 out.append(value[0])
         return out
 
+    def programmatic_edges(self):
+        """How many kernels may start before the one ahead of them has ended."""
+        n = ctypes.c_size_t(0)
+        _call("cudaGraphGetEdges", self.graph, None, None, None, ctypes.byref(n))
+        if n.value == 0:
+            return 0
+        ends = [(ctypes.c_void_p * n.value)() for _ in range(2)]
+        data = (ctypes.c_ubyte * (8 * n.value))()        # cudaGraphEdgeData: two ports, the type, reserved
+        _call("cudaGraphGetEdges", self.graph, *ends, data, ctypes.byref(n))
+        return sum(data[8 * i + 2] == 1 for i in range(n.value))
+
     def launch(self):
         if self.exec is None:
             self.exec = ctypes.c_void_p()

@@ -292,3 +292,35 @@ def test_side_by_side_products_keep_the_streams_priority(priority):
     got = graph.kernel_priorities()
     graph.close()
     assert len(got) >= 4 and set(got) == {priority}, got
+
+
+OVERLAPS = """
+import torch, fp32_emulated_gemm_gb300 as emu
+from tests import _graphs, test_gpu_graphs as t
+norm = t.filled(t.NormBackward(500, 260), 1)
+x, wi, wo = t.rand(3, 64, seed=1), t.rand(2 * 96, 64, seed=2), t.rand(64, 96, seed=3)
+h, y = t.empty(3, 96), t.empty(3, 64)
+def few():
+    emu.emu_gated_ffn_fwd(0, emu.EMU_ACT_SILU, 3, 64, 96, 64, x, 64, wi, 64, None, wo, 96, None, None, 0, None, 0, h, 96, y, 64)
+for work in (norm.run, few):
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        work()
+    g = _graphs.Graph(stream, work)
+    print(g.types().count(_graphs.KERNEL), g.programmatic_edges())
+"""
+
+
+@pytest.mark.parametrize("pdl", [1, 0])
+def test_pdl_off_means_no_overlap(pdl):
+    """EMU_PDL=0 holds for the sums of partial sums and for the few-row form's
+    second kernel too."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", OVERLAPS], capture_output=True, text=True, timeout=300, cwd=root,
+                       env=dict(os.environ, EMU_PDL=str(pdl), PYTHONPATH=root))
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == ["2", str(pdl), "2", str(pdl)], r.stdout
