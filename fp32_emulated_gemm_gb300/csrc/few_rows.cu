@@ -43,10 +43,10 @@ template <bool VEC> __device__ __forceinline__ float4 load_w(const float* row, i
 }
 
 // Sums of V values over the warp.  Each step hands half of the values to the
-// other half of the lanes: V - 1 shuffles and a few instead of 5 V.  Up to 32
-// values: value i ends up in v[0] of lanes 32 / V i onwards; 64: values 2 l and
-// 2 l + 1 in lane l.
+// other half of the lanes: V - 1 shuffles and a few instead of 5 V.  Value i ends
+// up in v[0] of lanes 32 / V i onwards.
 template <int V> __device__ __forceinline__ void warp_sums(float (&v)[V], int lane) {
+    static_assert(V <= 32, "at most a value a lane");
     int n = V / 2;
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2, n /= 2) {
@@ -69,8 +69,8 @@ template <int V> __device__ __forceinline__ void warp_sums(float (&v)[V], int la
 template <int MR, int NR, bool GATED, bool VEC, int FAMILY>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const FewRows p, int wk) {
     constexpr int V = MR * NR, OUT = GATED ? NR / 2 : NR;  // sums of a warp; output columns
-    constexpr int U = MR <= 2 ? 4 : NR >= 8 ? 1 : 2;                      // steps whose weights are in flight together
-    __shared__ __align__(8) float part[kWarpsPerBlock][V];
+    constexpr int U = MR <= 2 ? 4 : 2;                     // steps whose weights are in flight together
+    __shared__ float part[kWarpsPerBlock][V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int groups = kWarpsPerBlock / wk, share = warp % wk;
     const int64_t n0 = ((int64_t)blockIdx.x * groups + warp / wk) * OUT;  // first output column
@@ -119,11 +119,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
         if (s + U < s1) load(c + 128 * U);
     }
     warp_sums<V>(acc, lane);
-    if constexpr (V <= 32) {
-        if (lane % (32 / V) == 0) part[warp][lane / (32 / V)] = acc[0];
-    } else {
-        *reinterpret_cast<float2*>(&part[warp][2 * lane]) = make_float2(acc[0], acc[1]);
-    }
+    if (lane % (32 / V) == 0) part[warp][lane / (32 / V)] = acc[0];
     __syncthreads();
     // one thread per output: the shares in order, then the epilogue
     for (int t = threadIdx.x; t < groups * MR * OUT; t += 32 * kWarpsPerBlock) {
