@@ -39,8 +39,12 @@ bool log_enabled() {
 }
 
 
+// The error word of every kernel of the library (see WaitBudget).
+__device__ unsigned int g_error_flag = 0;
+
 struct DeviceInfo {
     bool ready = false;
+    unsigned* error_word = nullptr;  // g_error_flag's address on the device
     int cc_major = 0, cc_minor = 0, sm_count = 0;
     bool attrs_set = false;
     int max_clusters[2] = {0, 0};  // co-resident CTA pairs per mode (all pipeline shapes)
@@ -184,7 +188,8 @@ emu_status_t device_info(DeviceInfo** out) {
             set_smem_attr<MODE_TF32X3, PIPE_SHORT_K, true>() != cudaSuccess ||
             set_smem_attr<MODE_TF32X3, PIPE_SHORT_K_PACKED, true>() != cudaSuccess ||
             kEpiAct.set_attributes() != cudaSuccess || kEpiGated.set_attributes() != cudaSuccess ||
-            kEpiGatedBwd.set_attributes() != cudaSuccess) {
+            kEpiGatedBwd.set_attributes() != cudaSuccess ||
+            cudaGetSymbolAddress(reinterpret_cast<void**>(&d.error_word), g_error_flag) != cudaSuccess) {
             cudaGetLastError();
             return EMU_STATUS_LAUNCH_FAILED;
         }
@@ -478,16 +483,16 @@ __global__ void scale_kernel(int64_t M, int64_t N, float beta, float* C, int64_t
 }
 
 emu_status_t check_error_flag(bool clear) {
-    unsigned int any = 0;
-    for (auto read : {epi_error_flag, kEpiAct.error_flag, kEpiGated.error_flag, kEpiGatedBwd.error_flag}) {
-        unsigned int flag = 0;
-        if (read(&flag, clear) != cudaSuccess) {
-            cudaGetLastError();
-            return EMU_STATUS_LAUNCH_FAILED;
-        }
-        any |= flag;
+    unsigned int flag = 0;
+    if (cudaMemcpyFromSymbol(&flag, g_error_flag, sizeof(flag)) != cudaSuccess) {
+        cudaGetLastError();
+        return EMU_STATUS_LAUNCH_FAILED;
     }
-    return any ? EMU_STATUS_DEVICE_TIMEOUT : EMU_STATUS_SUCCESS;
+    if (flag && clear) {
+        const unsigned int zero = 0;
+        if (cudaMemcpyToSymbol(g_error_flag, &zero, sizeof(zero)) != cudaSuccess) cudaGetLastError();
+    }
+    return flag ? EMU_STATUS_DEVICE_TIMEOUT : EMU_STATUS_SUCCESS;
 }
 
 // Whether work on `stream` goes into a graph that is being captured.
@@ -1121,6 +1126,7 @@ emu_status_t run_gemm(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, int64_t 
     p.c_old = C; p.c = C; p.ldc = ldc;
     p.bias = bias;
     p.wait_budget_ns = wait_budget_ns();
+    p.error_word = dev->error_word;
     if (autopack_buf && launch_pack(mode, b_n, K, B, ldb, !b_mn, autopack_buf, dev->sm_count, stream) != cudaSuccess)
         return EMU_STATUS_LAUNCH_FAILED;
     if (p.counters && clear_captured_counters(p.counters, (size_t)plan.num_tiles * 2, stream) != cudaSuccess) {
@@ -1161,7 +1167,7 @@ __global__ void __launch_bounds__(256, 1) split_dump_kernel(const __grid_constan
         else for (int j = 0; j < ROWS / 32; ++j) tma_load_2d(f32 + j * 4096, &tm, bar, 32 * j, 0);
     }
     volatile int no_abort = 0;
-    if (!mbar_wait_warp(bar, 0, &no_abort, 1000000000ull, 5)) return;
+    if (!mbar_wait_warp(bar, 0, &no_abort, {1000000000ull, &g_error_flag}, 5)) return;
     split_operand<MODE, 256, ROWS>(f32, comp, mn_major != 0, threadIdx.x);
     __syncthreads();
     for (int i = threadIdx.x; i < R * Kc; i += blockDim.x) {
@@ -1192,7 +1198,7 @@ __global__ void wait_timeout_selftest_kernel(unsigned long long budget_ns) {
         fence_mbar_init();
     }
     __syncwarp();
-    mbar_wait_warp(&bar, 0, &abort_flag, budget_ns, 7);
+    mbar_wait_warp(&bar, 0, &abort_flag, {budget_ns, &g_error_flag}, 7);
 }
 
 // Self-test of the split-K counters after a timeout: for one launch epoch,
@@ -1207,7 +1213,7 @@ __global__ void split_timeout_selftest_kernel(unsigned long long* counters, int 
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x) epoch_arrive(&counters[i], epoch);
     __syncthreads();
-    if (threadIdx.x == 0) wait_epoch_count(&counters[0], epoch, 2u, &abort_flag, budget_ns, 8);
+    if (threadIdx.x == 0) wait_epoch_count(&counters[0], epoch, 2u, &abort_flag, {budget_ns, &g_error_flag}, 8);
 }
 
 }  // namespace
@@ -1699,6 +1705,7 @@ emu_status_t run_gemm_noalloc(emu_mode_t mode, bool a_mn, bool b_mn, int64_t M, 
     p.c_old = C; p.c = C; p.ldc = ldc;
     p.bias = nullptr;
     p.wait_budget_ns = wait_budget_ns();
+    p.error_word = dev->error_word;
     if (plan.slots > 0) {
         // partial tiles first, then the counters
         const size_t partial_bytes = (size_t)plan.slots * TILE_M * plan.tn * sizeof(float);

@@ -270,6 +270,7 @@ struct Params {
     unsigned long long* counters;  // split tiles: 2 per tile (pieces arrived, per CTA half), epoch-tagged
     unsigned long long epoch;      // this launch's epoch on the counters (> 0, new for every launch)
     unsigned long long wait_budget_ns;
+    unsigned* error_word;  // set by a wait that gives up
     EpiParams epi;
 };
 
@@ -693,7 +694,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
     tc_fence_after();
     griddep_wait();           // inputs, C, workspace and counters are the previous grids' to finish
     const uint32_t tmem_base = *tmem_slot;
-    const uint64_t budget = p.wait_budget_ns;
+    const WaitBudget budget{p.wait_budget_ns, p.error_word};
     Walk walk;  // (thread 0's, from shared memory)
     walk.first = walk_sh[0]; walk.last = walk_sh[1]; walk.step = walk_sh[2]; walk.lo = walk_sh[3]; walk.hi = walk_sh[4];
 
@@ -731,12 +732,12 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 for (int t = 0; t < NF; ++t)
                     if (issued_mask & (1u << t)) {
                         volatile int never = 0;
-                        mbar_wait(&fp32_full[t], (issued_parity >> t) & 1u, &never, 50000000ull, 1);
+                        mbar_wait(&fp32_full[t], (issued_parity >> t) & 1u, &never, {50000000ull, p.error_word}, 1);
                     }
                 for (int t = 0; t < NB; ++t)
                     if (bissued_mask & (1u << t)) {
                         volatile int never = 0;
-                        mbar_wait(&bcomp_full[t], (bissued_parity >> t) & 1u, &never, 50000000ull, 1);
+                        mbar_wait(&bcomp_full[t], (bissued_parity >> t) & 1u, &never, {50000000ull, p.error_word}, 1);
                     }
             }
         }
@@ -773,7 +774,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 // let the products in flight finish before TMEM is released
                 mma_commit_pair(drain);
                 volatile int never = 0;
-                mbar_wait(drain, 0, &never, 50000000ull, 2);
+                mbar_wait(drain, 0, &never, {50000000ull, p.error_word}, 2);
             }
         }
         __syncwarp();

@@ -2,5 +2,5 @@
 #include "gemm_epi.h"
 
 namespace emu {
-const EpiTable kEpiAct = {epi_set_attributes<EPI_ACT>, epi_launch<EPI_ACT>, epi_error_flag};
+const EpiTable kEpiAct = {epi_set_attributes<EPI_ACT>, epi_launch<EPI_ACT>};
 }

@@ -14,7 +14,6 @@ struct EpiTable {
     cudaError_t (*set_attributes)();  // once per device, before the first launch
     // mode BF16X9 or TF32X3, any pipeline shape of make_plan
     cudaError_t (*launch)(int mode, int pipe, cudaLaunchConfig_t cfg, const Params& p);
-    cudaError_t (*error_flag)(unsigned* flag, bool clear);  // this file's device error word
 };
 extern const EpiTable kEpiAct, kEpiGated, kEpiGatedBwd;
 
@@ -43,15 +42,6 @@ template <int EPI> cudaError_t epi_launch(int mode, int pipe, cudaLaunchConfig_t
                                  : epi_launch_one<MODE_TF32X3, PIPE_SHORT_K, EPI>(cfg, p);
     return pipe == PIPE_LONG_K ? epi_launch_one<MODE_BF16X9, PIPE_LONG_K, EPI>(cfg, p)
                                : epi_launch_one<MODE_BF16X9, PIPE_SHORT_K, EPI>(cfg, p);
-}
-// (static: each file reads its own g_error_flag)
-static cudaError_t epi_error_flag(unsigned* flag, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(flag, g_error_flag, sizeof(*flag));
-    if (e == cudaSuccess && *flag && clear) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbol(g_error_flag, &zero, sizeof(zero));
-    }
-    return e;
 }
 
 }  // namespace emu

@@ -2,5 +2,5 @@
 #include "gemm_epi.h"
 
 namespace emu {
-const EpiTable kEpiGated = {epi_set_attributes<EPI_GATED>, epi_launch<EPI_GATED>, epi_error_flag};
+const EpiTable kEpiGated = {epi_set_attributes<EPI_GATED>, epi_launch<EPI_GATED>};
 }

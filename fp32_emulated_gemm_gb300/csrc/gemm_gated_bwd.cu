@@ -2,5 +2,5 @@
 #include "gemm_epi.h"
 
 namespace emu {
-const EpiTable kEpiGatedBwd = {epi_set_attributes<EPI_GATED_BWD>, epi_launch<EPI_GATED_BWD>, epi_error_flag};
+const EpiTable kEpiGatedBwd = {epi_set_attributes<EPI_GATED_BWD>, epi_launch<EPI_GATED_BWD>};
 }

@@ -1,7 +1,7 @@
 // ptx.cuh -- thin inline-PTX wrappers for sm_103a: mbarrier, TMA
 // (cp.async.bulk.tensor), tcgen05 (TMEM allocation, MMA, commit, loads) and
 // proxy fences.  Every wait is bounded: it gives up after a time budget,
-// records the reason in a device-global flag and returns false, so that no
+// records the reason in the device's error word and returns false, so that no
 // kernel of this library can hang a GPU.
 #pragma once
 
@@ -10,11 +10,15 @@
 
 namespace emu {
 
-// Device-global error word, read and cleared by emu_stream_check().
-// Bit 0: a wait timed out.  Bits 8..15: the role that timed out (for logs).
-// One word per source file that launches kernels with waits (each file is
-// compiled by itself); emu_stream_check() reads them all.
-static __device__ unsigned int g_error_flag = 0;
+// What bounds a wait: its time budget, and the device's error word, which a wait
+// that gives up sets and emu_stream_check() reads and clears.  Bit 0: a wait
+// timed out.  Bits 8..15: the role that timed out (for logs).  (The word's
+// address is a kernel argument: the kernels are compiled in several files, and
+// one word for all of them is one read for the check.)
+struct WaitBudget {
+    uint64_t ns;
+    unsigned* error;
+};
 
 enum : unsigned { ERR_TIMEOUT = 1u };
 
@@ -109,15 +113,15 @@ __device__ __forceinline__ void cluster_sync_relaxed() {
 // false, without waiting further, when *abort is set by another warp or when
 // the time budget runs out (then it sets the device error flag and *abort).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          uint64_t budget_ns, unsigned role) {
+                                          const WaitBudget& budget, unsigned role) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15u) == 0) {
             if (*abort) return false;
-            if (globaltimer_ns() - t0 > budget_ns) {
-                atomicOr(&g_error_flag, ERR_TIMEOUT | (role << 8));
+            if (globaltimer_ns() - t0 > budget.ns) {
+                atomicOr(budget.error, ERR_TIMEOUT | (role << 8));
                 *abort = 1;
                 return false;
             }
@@ -153,7 +157,7 @@ __device__ __forceinline__ void epoch_arrive(unsigned long long* ctr, unsigned l
 // (acquire at GPU scope, so that the writes the other CTAs released before
 // arriving are visible), bounded like the barrier waits.
 __device__ __forceinline__ bool wait_epoch_count(const unsigned long long* ctr, unsigned long long epoch,
-                                                 unsigned target, volatile int* abort, uint64_t budget_ns,
+                                                 unsigned target, volatile int* abort, const WaitBudget& budget,
                                                  unsigned role) {
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
@@ -165,8 +169,8 @@ __device__ __forceinline__ bool wait_epoch_count(const unsigned long long* ctr, 
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) {
                 t0 = now;
-            } else if (now - t0 > budget_ns) {
-                atomicOr(&g_error_flag, ERR_TIMEOUT | (role << 8));
+            } else if (now - t0 > budget.ns) {
+                atomicOr(budget.error, ERR_TIMEOUT | (role << 8));
                 *abort = 1;
                 return false;
             }
@@ -189,7 +193,7 @@ __device__ __forceinline__ bool warp_published(const unsigned long long* ctr, un
 // polls with acquire semantics until all see them; lane 0 keeps the time
 // budget like the other waits.  False after a timeout or an abort.
 __device__ __forceinline__ bool warp_wait_epoch(const unsigned long long* ctr, unsigned long long epoch,
-                                                unsigned target, volatile int* abort, uint64_t budget_ns,
+                                                unsigned target, volatile int* abort, const WaitBudget& budget,
                                                 unsigned role) {
     const uint32_t lane = threadIdx.x & 31u;
     uint64_t t0 = 0;
@@ -203,8 +207,8 @@ __device__ __forceinline__ bool warp_wait_epoch(const unsigned long long* ctr, u
                     give_up = 1;
                 } else if (t0 == 0) {
                     t0 = now;
-                } else if (now - t0 > budget_ns) {
-                    atomicOr(&g_error_flag, ERR_TIMEOUT | (role << 8));
+                } else if (now - t0 > budget.ns) {
+                    atomicOr(budget.error, ERR_TIMEOUT | (role << 8));
                     *abort = 1;
                     give_up = 1;
                 }
@@ -218,7 +222,7 @@ __device__ __forceinline__ bool warp_wait_epoch(const unsigned long long* ctr, u
 // Warp-collective form: every lane polls, and the warp stops together, so
 // that the .sync.aligned instructions that follow see a converged warp.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                               uint64_t budget_ns, unsigned role) {
+                                               const WaitBudget& budget, unsigned role) {
     const uint32_t lane = threadIdx.x & 31u;
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
@@ -232,8 +236,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
                     give_up = 1;
                 } else if (t0 == 0) {
                     t0 = now;
-                } else if (now - t0 > budget_ns) {
-                    atomicOr(&g_error_flag, ERR_TIMEOUT | (role << 8));
+                } else if (now - t0 > budget.ns) {
+                    atomicOr(budget.error, ERR_TIMEOUT | (role << 8));
                     *abort = 1;
                     give_up = 1;
                 }
