@@ -1006,8 +1006,6 @@ cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, i
     return cudaGetLastError();
 }
 
-enum Until { UNTIL_CHECKED, UNTIL_RESERVED, UNTIL_LAUNCHED };
-
 // Core: C = alpha * op(A) op(B) + beta * C_old + bias, with C_old == C.
 // packed_b != nullptr: op(B) comes packed (emu_pack_b); B and ldb are unused.
 // fused: the epilogue is one of the EPI_* kinds instead (gated: N is F, op(B)
@@ -1289,20 +1287,17 @@ int two_share(const Gemm& a, const Gemm& b, int pairs) {
 }
 }  // namespace
 
-emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check) {
-    return gemm_on(mode, g, stream, check ? UNTIL_RESERVED : UNTIL_LAUNCHED, INT32_MAX);
+emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, Until until) {
+    return gemm_on(mode, g, stream, until, INT32_MAX);
 }
 
-emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, bool check) {
-    if (!a || !b) return a ? gemm(mode, *a, stream, check) : b ? gemm(mode, *b, stream, check) : EMU_STATUS_SUCCESS;
+emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, Until until) {
+    if (!a || !b || until == UNTIL_CHECKED) {
+        const emu_status_t st = a ? gemm(mode, *a, stream, until) : EMU_STATUS_SUCCESS;
+        return st == EMU_STATUS_SUCCESS && b ? gemm(mode, *b, stream, until) : st;
+    }
     int share = 0;
     DeviceInfo* dev = nullptr;
-    if (check) {  // the arguments before anything that needs the device
-        for (const Gemm* g : {a, b}) {
-            const emu_status_t st = gemm_on(mode, *g, stream, UNTIL_CHECKED, INT32_MAX);
-            if (st != EMU_STATUS_SUCCESS) return st;
-        }
-    }
     // (no caller passes a gated pair: its tiles are not the plan's of M x N)
     auto sized = [](const Gemm& g) {
         return g.M > 0 && g.N > 0 && g.K > 0 && g.M <= INT32_MAX - 256 && g.N <= INT32_MAX - 256 &&
@@ -1325,12 +1320,12 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
         share = 0;
     }
     if (share == 0) {
-        const emu_status_t st = gemm(mode, *a, stream, check);
-        return st == EMU_STATUS_SUCCESS ? gemm(mode, *b, stream, check) : st;
+        const emu_status_t st = gemm(mode, *a, stream, until);
+        return st == EMU_STATUS_SUCCESS ? gemm(mode, *b, stream, until) : st;
     }
     const int rest = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0] - share;
     emu_status_t st = EMU_STATUS_SUCCESS;
-    if (check) {
+    if (until == UNTIL_RESERVED) {
         st = gemm_on(mode, *a, stream, UNTIL_RESERVED, share);
         return st == EMU_STATUS_SUCCESS ? gemm_on(mode, *b, side, UNTIL_RESERVED, rest) : st;
     }

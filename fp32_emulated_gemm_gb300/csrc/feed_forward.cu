@@ -115,7 +115,15 @@ public:
         ld = n;
         add(p, ld, 1, n);
     }
-    // the copies' addresses take the place of the operands'
+    // The operands' addresses for the checks of a call's arguments: any that a
+    // copy could have.
+    void stand_in() {
+        for (int i = 0; i < jobs_.n; ++i) {
+            *p_[i] = reinterpret_cast<const float*>(uintptr_t(256));
+            *ld_[i] = jobs_.job[i].ldd;
+        }
+    }
+    // After the checks: the copies' addresses take the place of the operands'.
     emu_status_t reserve(cudaStream_t s) {
         if (jobs_.n == 0) return EMU_STATUS_SUCCESS;
         DeviceCtx dev;
@@ -127,7 +135,6 @@ public:
             CopyJob& j = jobs_.job[i];
             j.dst = base;
             *p_[i] = base;
-            *ld_[i] = j.ldd;
             base += j.rows * j.ldd;
             rows_ += j.rows;
         }
@@ -382,11 +389,11 @@ bool aligned_rows(const float* p, int64_t ld) { return !p || vec4_ok(p, ld); }
 
 emu_status_t linear_act_fwd(emu_mode_t mode, int act, int64_t M, int64_t N, int64_t K, const float* X, int64_t ldx,
                             const float* W, int64_t ldw, const float* bias, const float* R, int64_t ldr, float* D,
-                            int64_t ldd, float* Y, int64_t ldy, const DeviceCtx& dev, cudaStream_t s, bool check,
+                            int64_t ldd, float* Y, int64_t ldy, const DeviceCtx& dev, cudaStream_t s, Until until,
                             bool after_own = false) {
     if (few_rows(mode, M, N, K)) {
         if (K > 0 && (!X || !W || ldx < K || ldw < K)) return EMU_STATUS_INVALID_VALUE;
-        if (check) return EMU_STATUS_SUCCESS;
+        if (until != UNTIL_LAUNCHED) return EMU_STATUS_SUCCESS;
         return launched(launch_few_rows({(int)M, N, K, X, ldx, W, ldw, bias, R, ldr, D, ldd, Y, ldy, act_params(act)}, false,
                                         after_own, dev.sm_count, s));
     }
@@ -395,8 +402,8 @@ emu_status_t linear_act_fwd(emu_mode_t mode, int act, int64_t M, int64_t N, int6
     const Fused f{FUSED_ACT, act, R, ldr, D, ldd, nullptr};
     const bool plain = act == ACT_NONE && !R && !D, fuse = fused_mode(mode) && K > 0 && !plain;
     if (fuse) g.fused = &f;
-    EMU_TRY(gemm(mode, g, s, check));
-    if (check || plain || fuse) return EMU_STATUS_SUCCESS;
+    EMU_TRY(gemm(mode, g, s, until));
+    if (until != UNTIL_LAUNCHED || plain || fuse) return EMU_STATUS_SUCCESS;
     return launched(launch_act_fwd<false>(act, M, N, Y, ldy, R, ldr, D, ldd, Y, ldy, dev.sm_count, s));
 }
 
@@ -404,10 +411,10 @@ emu_status_t linear_act_fwd(emu_mode_t mode, int act, int64_t M, int64_t N, int6
 bool gated_needs_d(emu_mode_t mode) { return !fused_mode(mode); }
 emu_status_t gated_fwd(emu_mode_t mode, int act, int64_t M, int64_t F, int64_t K, const float* X, int64_t ldx,
                        const float* W, int64_t ldw, const float* bias, float* D, int64_t ldd, float* H, int64_t ldh,
-                       const DeviceCtx& dev, cudaStream_t s, bool check) {
+                       const DeviceCtx& dev, cudaStream_t s, Until until) {
     if (few_rows(mode, M, 2 * F, K)) {
         if (K > 0 && (!X || !W || ldx < K || ldw < K)) return EMU_STATUS_INVALID_VALUE;
-        if (check) return EMU_STATUS_SUCCESS;
+        if (until != UNTIL_LAUNCHED) return EMU_STATUS_SUCCESS;
         return launched(launch_few_rows({(int)M, F, K, X, ldx, W, ldw, bias, nullptr, 0, D, ldd, H, ldh, act_params(act)},
                                         true, false, dev.sm_count, s));
     }
@@ -416,16 +423,28 @@ emu_status_t gated_fwd(emu_mode_t mode, int act, int64_t M, int64_t F, int64_t K
         Gemm g = forward_product(M, F, K, X, ldx, W, ldw, bias, H, ldh);
         const Fused f{FUSED_GATED, act, nullptr, 0, D, ldd, nullptr};
         g.fused = &f;
-        return gemm(mode, g, s, check);
+        return gemm(mode, g, s, until);
     }
     if (!D && K == 0) {  // every row is the bias
-        if (check) return EMU_STATUS_SUCCESS;
+        if (until != UNTIL_LAUNCHED) return EMU_STATUS_SUCCESS;
         if (bias) return launched(launch_act_fwd<true>(act, M, F, bias, 0, nullptr, 0, nullptr, 0, H, ldh, dev.sm_count, s));
         return launched(cudaMemset2DAsync(H, ldh * sizeof(float), 0, F * sizeof(float), M, s));
     }
-    EMU_TRY(gemm(mode, forward_product(M, 2 * F, K, X, ldx, W, ldw, bias, D, ldd), s, check));
-    if (check) return EMU_STATUS_SUCCESS;
+    EMU_TRY(gemm(mode, forward_product(M, 2 * F, K, X, ldx, W, ldw, bias, D, ldd), s, until));
+    if (until != UNTIL_LAUNCHED) return EMU_STATUS_SUCCESS;
     return launched(launch_act_fwd<true>(act, M, F, D, ldd, nullptr, 0, D, ldd, H, ldh, dev.sm_count, s));
+}
+
+// A forward pass in its steps: the arguments' checks, the buffers, then the copies
+// of its operands and its launches.
+template <class F> emu_status_t in_steps(Aligned& al, DeviceCtx& dev, cudaStream_t s, F pass) {
+    al.stand_in();
+    EMU_TRY(pass(UNTIL_CHECKED));
+    EMU_TRY(current_device(&dev));
+    EMU_TRY(al.reserve(s));
+    EMU_TRY(pass(UNTIL_RESERVED));
+    EMU_TRY(launched(al.launch(s)));
+    return pass(UNTIL_LAUNCHED);
 }
 
 }  // namespace
@@ -454,11 +473,9 @@ emu_status_t emu_linear_act_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64
         al.add(residual, ldr, M, N);
         al.add_vector(bias, N);
     }
-    EMU_TRY(al.reserve(s));
-    EMU_TRY(linear_act_fwd(mode, act, M, N, K, X, ldx, W, ldw, bias, residual, ldr, D, ldd, Y, ldy, dev, s, true));
-    EMU_TRY(current_device(&dev));
-    EMU_TRY(launched(al.launch(s)));
-    return linear_act_fwd(mode, act, M, N, K, X, ldx, W, ldw, bias, residual, ldr, D, ldd, Y, ldy, dev, s, false);
+    return in_steps(al, dev, s, [&](Until until) {
+        return linear_act_fwd(mode, act, M, N, K, X, ldx, W, ldw, bias, residual, ldr, D, ldd, Y, ldy, dev, s, until);
+    });
 }
 
 emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K, const float* dY, int64_t lddy,
@@ -476,13 +493,19 @@ emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K
     if (!D) al.add(dY, lddy, M, N);
     if (dW) al.add(X, ldx, M, K);
     if (dX) al.add(W, ldw, N, K);
-    EMU_TRY(al.reserve(s));
-    const float* G = D ? dZ : dY;
-    const int64_t ldg = D ? lddz : lddy;
-    const Gemm gx = input_product(M, N, K, G, ldg, W, ldw, dX, lddx), gw = weight_product(M, N, K, G, ldg, X, ldx, dW, lddw);
-    EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, true));
+    auto products = [&](Until until) {
+        const float* G = D ? dZ : dY;
+        const int64_t ldg = D ? lddz : lddy;
+        const Gemm gx = input_product(M, N, K, G, ldg, W, ldw, dX, lddx);
+        const Gemm gw = weight_product(M, N, K, G, ldg, X, ldx, dW, lddw);
+        return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, until);
+    };
+    al.stand_in();
+    EMU_TRY(products(UNTIL_CHECKED));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
+    EMU_TRY(al.reserve(s));
+    EMU_TRY(products(UNTIL_RESERVED));
     float* scratch = nullptr;
     if (dbias) EMU_TRY(reduce_scratch(dev.id, s, act_bwd_floats(false, M, N, dev.sm_count), &scratch));
     EMU_TRY(launched(al.launch(s)));
@@ -490,7 +513,7 @@ emu_status_t emu_linear_act_bwd(emu_mode_t mode, int64_t M, int64_t N, int64_t K
         EMU_TRY(launched(launch_act_bwd<false>(M, N, dY, lddy, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
     else if (dbias)
         EMU_TRY(launched(launch_column_sums(dY, lddy, M, N, dbias, nullptr, scratch, dev.sm_count, s)));
-    return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
+    return products(UNTIL_LAUNCHED);
 }
 
 emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F, int64_t K, const float* X, int64_t ldx,
@@ -509,11 +532,9 @@ emu_status_t emu_gated_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t F,
         al.add(W, ldw, 2 * F, K);
         al.add_vector(bias, 2 * F);
     }
-    EMU_TRY(al.reserve(s));
-    EMU_TRY(gated_fwd(mode, act, M, F, K, X, ldx, W, ldw, bias, D, ldd, H, ldh, dev, s, true));
-    EMU_TRY(current_device(&dev));
-    EMU_TRY(launched(al.launch(s)));
-    return gated_fwd(mode, act, M, F, K, X, ldx, W, ldw, bias, D, ldd, H, ldh, dev, s, false);
+    return in_steps(al, dev, s, [&](Until until) {
+        return gated_fwd(mode, act, M, F, K, X, ldx, W, ldw, bias, D, ldd, H, ldh, dev, s, until);
+    });
 }
 
 emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, const float* dH, int64_t lddh,
@@ -528,17 +549,22 @@ emu_status_t emu_gated_bwd(emu_mode_t mode, int64_t M, int64_t F, int64_t K, con
     Aligned al;  // (dH and D are not a product's)
     if (dW) al.add(X, ldx, M, K);
     if (dX) al.add(W, ldw, 2 * F, K);
-    EMU_TRY(al.reserve(s));
-    const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W, ldw, dX, lddx);
-    const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW, lddw);
-    EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, true));
+    auto products = [&](Until until) {
+        const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W, ldw, dX, lddx);
+        const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW, lddw);
+        return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, until);
+    };
+    al.stand_in();
+    EMU_TRY(products(UNTIL_CHECKED));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
+    EMU_TRY(al.reserve(s));
+    EMU_TRY(products(UNTIL_RESERVED));
     float* scratch = nullptr;
     if (dbias) EMU_TRY(reduce_scratch(dev.id, s, act_bwd_floats(true, M, F, dev.sm_count), &scratch));
     EMU_TRY(launched(al.launch(s)));
     EMU_TRY(launched(launch_act_bwd<true>(M, F, dH, lddh, D, ldd, dZ, lddz, dbias, scratch, dev.sm_count, s)));
-    return gemm_two(mode, dX ? &gx : nullptr, dW ? &gw : nullptr, s, false);
+    return products(UNTIL_LAUNCHED);
 }
 
 emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_t K, int64_t F, int64_t N,
@@ -564,16 +590,13 @@ emu_status_t emu_gated_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t M, int64_
         al.add(residual, ldr, M, N);
         al.add_vector(b_out, N);
     }
-    EMU_TRY(al.reserve(s));
-    for (const bool check : {true, false}) {
-        if (!check) EMU_TRY(launched(al.launch(s)));
-        if (F > 0) EMU_TRY(gated_fwd(mode, act, M, F, K, X, ldx, W_in, ldwi, b_in, D, ldd, H, ldh, dev, s, check));
+    return in_steps(al, dev, s, [&](Until until) {
+        if (F > 0) EMU_TRY(gated_fwd(mode, act, M, F, K, X, ldx, W_in, ldwi, b_in, D, ldd, H, ldh, dev, s, until));
         if (N > 0)
             EMU_TRY(linear_act_fwd(mode, ACT_NONE, M, N, F, H, ldh, W_out, ldwo, b_out, residual, ldr, nullptr, 0, Y, ldy,
-                                   dev, s, check, F > 0 && few_rows(mode, M, 2 * F, K)));
-        if (check) EMU_TRY(current_device(&dev));
-    }
-    return EMU_STATUS_SUCCESS;
+                                   dev, s, until, F > 0 && few_rows(mode, M, 2 * F, K)));
+        return EMU_STATUS_SUCCESS;
+    });
 }
 
 emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F, int64_t N, const float* dY,
@@ -601,20 +624,30 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     }
     if (dX) al.add(W_in, ldwi, 2 * F, K);
     if (dW_in) al.add(X, ldx, M, K);
-    EMU_TRY(al.reserve(s));
     // dZ comes straight from the product's epilogue; or dH takes the gate half
     // of dZ's storage until dZ replaces it in place
     const bool fuse = fused_mode(mode) && N > 0 && M > 0 && F > 0;
-    Fused f{FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, nullptr};
-    Gemm gh = input_product(M, N, F, dY, lddy, W_out, ldwo, dZ, lddz);
-    if (fuse) gh.fused = &f;
-    const Gemm go = weight_product(M, N, F, dY, lddy, H, ldh, dW_out, lddwo);
-    const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W_in, ldwi, dX, lddx);
-    const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi);
-    EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, true));
-    EMU_TRY(gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, true));
+    float *scratch = nullptr, *sums = nullptr;
+    auto outer_products = [&](Until until) {
+        const Fused f{FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, fuse && db_in ? sums : nullptr};
+        Gemm gh = input_product(M, N, F, dY, lddy, W_out, ldwo, dZ, lddz);
+        if (fuse) gh.fused = &f;
+        const Gemm go = weight_product(M, N, F, dY, lddy, H, ldh, dW_out, lddwo);
+        return gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, until);
+    };
+    auto inner_products = [&](Until until) {
+        const Gemm gx = input_product(M, 2 * F, K, dZ, lddz, W_in, ldwi, dX, lddx);
+        const Gemm gw = weight_product(M, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi);
+        return gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, until);
+    };
+    al.stand_in();
+    EMU_TRY(outer_products(UNTIL_CHECKED));
+    EMU_TRY(inner_products(UNTIL_CHECKED));
     DeviceCtx dev;
     EMU_TRY(current_device(&dev));
+    EMU_TRY(al.reserve(s));
+    EMU_TRY(outer_products(UNTIL_RESERVED));
+    EMU_TRY(inner_products(UNTIL_RESERVED));
     // Scratch: the output bias's partial sums, the epilogue's (a row for each 32
     // rows) and, where those are many, their own partial sums.
     const int64_t blocks = (M + 31) / 32;
@@ -622,15 +655,13 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     const size_t n_out = column_sums_floats(M, N, dev.sm_count);
     const size_t n_in = !fuse ? act_bwd_floats(true, M, F, dev.sm_count)
                               : (size_t)blocks * 2 * F + (direct ? 0 : column_sums_floats(blocks, 2 * F, dev.sm_count));
-    float *scratch = nullptr, *sums = nullptr;
     if (db_in || db_out) {
         const size_t out_floats = (n_out + 3) & ~size_t(3);
         EMU_TRY(reduce_scratch(dev.id, s, out_floats + n_in, &scratch));
         sums = scratch + out_floats;
     }
-    if (fuse && db_in) f.sums = sums;
     EMU_TRY(launched(al.launch(s)));
-    EMU_TRY(gemm_two(mode, inner ? &gh : nullptr, dW_out ? &go : nullptr, s, false));
+    EMU_TRY(outer_products(UNTIL_LAUNCHED));
     const bool join = fuse && db_in && direct;
     const Partials in_sums{sums, (int)blocks, 2 * F, 2 * F, db_in, nullptr};
     if (db_out || join)
@@ -641,7 +672,7 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
     else if (db_in && !direct)
         EMU_TRY(launched(launch_column_sums(sums, 2 * F, blocks, 2 * F, db_in, nullptr, sums + (size_t)blocks * 2 * F,
                                             dev.sm_count, s)));
-    return gemm_two(mode, dX ? &gx : nullptr, dW_in ? &gw : nullptr, s, false);
+    return inner_products(UNTIL_LAUNCHED);
 }
 
 }  // extern "C"

@@ -55,9 +55,12 @@ struct Fused {
 enum FusedKind : int { FUSED_ACT = 1, FUSED_GATED = 2, FUSED_GATED_BWD = 3 };
 inline bool fused_mode(emu_mode_t mode) { return mode == EMU_MODE_BF16X9 || mode == EMU_MODE_TF32X3; }
 
-// One product C = op(A) op(B) + beta C + bias as the public entry points run
-// it.  `check` true: argument checks and buffer reservation alone, so that an
-// operator of several launches can make sure of all of them before the first.
+// How far a product's call goes, so that an operator of several launches can make
+// sure of all of them before the first: its arguments' checks (nothing that needs
+// the device), the reservation of its buffers, its launches.
+enum Until { UNTIL_CHECKED, UNTIL_RESERVED, UNTIL_LAUNCHED };
+
+// One product C = op(A) op(B) + beta C + bias as the public entry points run it.
 struct Gemm {
     bool a_mn, b_mn;
     int64_t M, N, K;
@@ -71,11 +74,11 @@ struct Gemm {
     const float *bias;
     const Fused *fused = nullptr;  // FUSED_GATED: N is F, B has 2F rows and the bias 2F values
 };
-emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, bool check);
+emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, Until until);
 
 // Two independent products, each `after` work queued on `stream` before the call
 // and both before work queued after it: side by side on shares of the GPU when
 // that is predicted faster than one after the other.  Either may be absent (null).
-emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, bool check);
+emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, Until until);
 
 }  // namespace emu
