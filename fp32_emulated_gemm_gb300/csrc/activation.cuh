@@ -15,7 +15,12 @@
 // times z s): a finite z of any size gives a finite value and derivative.
 // The exponential and the reciprocal are the special-function unit's own (2
 // units in the last place each), one instruction apiece; their error is below
-// the products'.  What an activation costs a product's epilogue, whose eight
+// the products'.  Largest errors over 2 million z in each of seven ranges up to
+// |z| = 30, as multiples of 2^-24 |z| for the value and of 2^-24 for the
+// derivative: gelu 5.6 and 5.6 (near z = 0; beyond 2 at most 2.7 and 3.0),
+// gelu_tanh 2.8 and 3.8, silu 2.8 and 3.6.  gelu's mean error is -0.9e-7 for 2 <
+// |z| < 4 (largest 2.1e-7 below zero, where a form with erff has 1.2e-7 and mean
+// 0.01e-7).  What an activation costs a product's epilogue, whose eight
 // warps have little else to overlap with (M = 6144, K = 256, N = 1024, plain
 // product 27.6 us): relu 27.1, gelu 29.0, gelu_tanh 28.9, silu 28.9 us; with
 // expf, erff and a division behind them gelu took 42.6 and silu 34.0.
