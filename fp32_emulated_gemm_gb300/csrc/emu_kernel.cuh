@@ -39,8 +39,9 @@
 // partial tile that the others own, and sums and stores its own part, adding
 // the S partials in a fixed order (the owner's first, then the others by
 // piece index) -- the result does not depend on timing.  The pieces count
-// their arrivals on epoch-tagged counters (one new epoch per launch), so no
-// count left by an earlier launch can be taken for this one's.
+// their arrivals on epoch-tagged counters (one new epoch per launch; a graph
+// clears them ahead of a captured one), so no count left by an earlier launch
+// can be taken for this one's.
 //
 // Chained plans (more tiles than pairs, not a whole number of waves): the
 // tiles' k-stages, taken tile by tile, are cut into one contiguous run per
@@ -268,7 +269,7 @@ struct Params {
     float* workspace;    // split tiles: S partial tiles of 256 x TN each (thread-major);
                          // chained plans: one running sum per run boundary (pairs - 1)
     unsigned long long* counters;  // split tiles: 2 per tile (pieces arrived, per CTA half), epoch-tagged
-    unsigned long long epoch;      // this launch's epoch on the counters (> 0, new for every launch)
+    unsigned long long epoch;      // this launch's epoch on the counters (> 0, new for every call)
     unsigned long long wait_budget_ns;
     unsigned* error_word;  // set by a wait that gives up
     EpiParams epi;

@@ -206,7 +206,9 @@ constexpr int64_t kMaxRegsWidth = 16384;
 // and 0.94, 1024 0.95 and 0.95, 2048 0.96 and 0.93 (backward with 256 threads
 // of 2: 0.87), 4096 0.90 and 0.88 (512 threads of 2: 0.83 and 0.60; 128 of 8:
 // 0.85 and 0.85), 8192 0.94 and 0.77 (256 of 8: 0.85 and 0.77), 16384 0.84 and
-// 0.62 (1024 of 4: 0.62 and 0.58).  Copying the rows after next to shared
+// 0.62 (1024 of 4: 0.62 and 0.58; the backward kernel holds x, dY, dw and db in
+// eight float4 each, which are all of its 128 registers, and spills 184 to 208
+// bytes a thread).  Copying the rows after next to shared
 // memory meanwhile was slower at every width up to 4096.
 template <bool BWD, class F> void for_width(int64_t N, F f) {
     auto of = [&](auto T, auto NV) { f(T, NV); };

@@ -380,7 +380,6 @@ class EmuLayerNormFunction(_Function):
     def forward(ctx, X, weight, bias, eps):
         Y, mean, rstd = layer_norm_fwd(X, weight, bias, eps=eps)
         ctx.save_for_backward(X, weight, mean, rstd)
-        ctx.has_bias = bias is not None
         return Y
 
     @staticmethod

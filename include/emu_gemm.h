@@ -18,6 +18,9 @@
  * the layer keeps its weights, bias and shapes; the input gradient also runs
  * emulated, because forces are derivatives of the energy).
  *
+ * The library needs the CUDA 13 runtime as a shared library (libcudart.so.13,
+ * looked for in the process, then in the toolkit it was built with).
+ *
  * Conventions (the blog leaves these open):
  *   - Layout: ROW-MAJOR, as in PyTorch (BLAS is column-major).  Element (i, j)
  *     of an R x C matrix X with leading dimension ldx is X[i * ldx + j].

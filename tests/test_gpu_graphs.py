@@ -324,3 +324,33 @@ def test_pdl_off_means_no_overlap(pdl):
                        env=dict(os.environ, EMU_PDL=str(pdl), PYTHONPATH=root))
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.split() == ["2", str(pdl), "2", str(pdl)], r.stdout
+
+
+@pytest.mark.parametrize("rows", [3, 1500])
+def test_a_module_in_a_graph(rows):
+    """Inference through the sub-layer's module captured as PyTorch does it,
+    after one call on the capturing stream; and larger calls meanwhile."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(rows)
+    block = emu.EmuFeedForward(96, 130, mode="tf32x3").to(_gpu.device())
+    x = torch.zeros(rows, 96, device=_gpu.device())
+    large = rand(5000, 96, seed=9)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.no_grad():
+        block(x)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s), torch.no_grad():
+        y = block(x)
+    for seed in range(20):
+        x.copy_(rand(rows, 96, seed=seed))
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s), torch.no_grad():
+            block(large)                  # grows the stream's buffers the first time
+        torch.cuda.current_stream().wait_stream(s)
+        g.replay()
+        with torch.no_grad():
+            assert torch.equal(y, block(x))
+    assert emu.emu_stream_check() == 0
