@@ -83,6 +83,7 @@ struct Workspace {
 };
 constexpr int kMaxWorkspaces = 64;   // (device, stream) pairs with a workspace at once
 Workspace g_ws[kMaxWorkspaces];
+Workspace g_side_ws[kMaxWorkspaces]; // their side streams', so that these take no caller's place
 
 // Test hook (emu_debug_fail_allocations): the next n device allocations the
 // library attempts fail as if the allocator were out of memory.
@@ -518,6 +519,8 @@ cudaError_t clear_captured_counters(unsigned long long* counters, size_t n, cuda
 Workspace* workspace_slot(int dev, cudaStream_t stream) {
     for (auto& c : g_ws)
         if (c.device == dev && c.stream == stream) return &c;
+    for (auto& c : g_side_ws)
+        if (c.device == dev && c.stream == stream) return &c;
     for (auto& c : g_ws)
         if (c.device < 0) { c.device = dev; c.stream = c.user = stream; return &c; }
     return nullptr;
@@ -600,9 +603,10 @@ emu_status_t side_stream_for(int dev, cudaStream_t stream, cudaStream_t* side, c
             return EMU_STATUS_ALLOC_FAILED;
         }
     }
-    Workspace* own = workspace_slot(dev, w->side);  // the side stream's own buffers
-    if (!own) return EMU_STATUS_ALLOC_FAILED;
-    own->user = stream;
+    Workspace& own = g_side_ws[w - g_ws];  // the side stream's own buffers
+    own.device = dev;
+    own.stream = w->side;
+    own.user = stream;
     *side = w->side; *fork = w->fork; *join = w->join;
     return EMU_STATUS_SUCCESS;
 }
@@ -1313,7 +1317,7 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
     int devid = 0;
     cudaStream_t side = nullptr;
     cudaEvent_t fork = nullptr, join = nullptr;
-    // (in turn, too, when the table of streams has no room for the side stream)
+    // (in turn, too, when the side stream cannot be had)
     if (share > 0 && (cudaGetDevice(&devid) != cudaSuccess ||
                       side_stream_for(devid, stream, &side, &fork, &join) != EMU_STATUS_SUCCESS)) {
         cudaGetLastError();
@@ -1522,7 +1526,8 @@ emu_status_t emu_shutdown(void) {
     int current = 0;
     const bool have_current = cudaGetDevice(&current) == cudaSuccess;
     emu_status_t result = EMU_STATUS_SUCCESS;
-    for (auto& w : g_ws) {
+    for (int i = 0; i < 2 * kMaxWorkspaces; ++i) {
+        Workspace& w = i < kMaxWorkspaces ? g_side_ws[i] : g_ws[i - kMaxWorkspaces];
         if (w.device < 0) continue;
         if (cudaSetDevice(w.device) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
             cudaGetLastError();

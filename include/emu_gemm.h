@@ -241,8 +241,8 @@ emu_status_t emu_linear_bwd_input_packed(emu_mode_t mode, int64_t M, int64_t N, 
  *   block's partial sums are 2F floats for every 32 rows.  A call that returns an error has
  *   enqueued nothing, as elsewhere: every launch's buffers are reserved first.
  * Streams: two independent products of a backward pass run side by side, one of
- *   them on a stream of the library's (a second entry of its table of 64; with
- *   no room there they run in turn), where the launch plans' costs predict a
+ *   them on a stream of the library's (one for each of the 64 pairs that it
+ *   tracks, with buffers of its own), where the launch plans' costs predict a
  *   gain.  The stream is ordered with `stream` by events on both sides, so for
  *   the caller the call is work on `stream` like any other.
  * Strategy: a product with an epilogue of this section always emulates; the
