@@ -39,7 +39,17 @@ _FEED_FORWARD = (
     "gated_ffn_fwd", "gated_ffn_bwd", "EmuLayerNormFunction", "EmuLinearActFunction", "EmuGatedFFNFunction",
     "EmuFeedForwardFunction", "EmuLayerNorm", "EmuLinearAct", "EmuGatedFFN", "EmuFeedForward",
 )
-__all__ += _FEED_FORWARD
+# the operators of a layer of experts (experts.py), likewise
+_EXPERTS = (
+    "EMU_OVER_CHOSEN", "EMU_OVER_ALL", "OVER", "SCALE_GROUP",
+    "emu_rms_norm_fwd", "emu_rms_norm_quant", "emu_rms_norm_bwd", "emu_expert_route", "emu_expert_sort",
+    "emu_expert_route_bwd", "emu_expert_dispatch", "emu_expert_combine_fwd", "emu_expert_combine_bwd",
+    "emu_expert_ffn_fwd", "emu_expert_ffn_bwd",
+    "rms_norm_fwd", "rms_norm_quant", "rms_norm_bwd", "ExpertPlan", "expert_route", "expert_sort", "expert_route_bwd",
+    "expert_dispatch", "expert_combine_fwd", "expert_combine_bwd", "expert_ffn_fwd", "expert_ffn_bwd",
+    "EmuRMSNormFunction", "EmuExpertFFNFunction", "EmuRMSNorm", "EmuExpertFFN", "EmuExpertFeedForward",
+)
+__all__ += _FEED_FORWARD + _EXPERTS
 
 EMU_MODE_BF16X9 = 0
 EMU_MODE_TF32X3 = 1
@@ -501,5 +511,10 @@ def __getattr__(name):
         from . import feed_forward
         for n in _FEED_FORWARD:
             globals()[n] = getattr(feed_forward, n)
+        return globals()[name]
+    if name in _EXPERTS:
+        from . import experts
+        for n in _EXPERTS:
+            globals()[n] = getattr(experts, n)
         return globals()[name]
     raise AttributeError(name)

@@ -189,7 +189,9 @@ emu_status_t device_info(DeviceInfo** out) {
             set_smem_attr<MODE_TF32X3, PIPE_SHORT_K, true>() != cudaSuccess ||
             set_smem_attr<MODE_TF32X3, PIPE_SHORT_K_PACKED, true>() != cudaSuccess ||
             kEpiAct.set_attributes() != cudaSuccess || kEpiGated.set_attributes() != cudaSuccess ||
-            kEpiGatedBwd.set_attributes() != cudaSuccess ||
+            kEpiGatedBwd.set_attributes() != cudaSuccess || kRowsStore.set_attributes() != cudaSuccess ||
+            kRowsGated.set_attributes() != cudaSuccess || kRowsGatedBwd.set_attributes() != cudaSuccess ||
+            kSumStore.set_attributes() != cudaSuccess ||
             cudaGetSymbolAddress(reinterpret_cast<void**>(&d.error_word), g_error_flag) != cudaSuccess) {
             cudaGetLastError();
             return EMU_STATUS_LAUNCH_FAILED;
@@ -234,6 +236,23 @@ bool encode_f32_2d(CUtensorMap* map, const float* base, uint64_t inner, uint64_t
         std::fprintf(stderr, "[emu] tensor map encode failed (%d): base %p dims %llu x %llu ld %llu box %u x %u\n",
                      (int)r, (const void*)base, (unsigned long long)inner, (unsigned long long)outer,
                      (unsigned long long)ld, box_inner, box_outer);
+    return r == CUDA_SUCCESS;
+}
+
+// Likewise of `groups` such matrices one behind the other (GROUP_ROWS' weights).
+bool encode_f32_3d(CUtensorMap* map, const float* base, uint64_t inner, uint64_t outer, uint64_t groups, uint64_t ld,
+                   uint32_t box_inner, uint32_t box_outer) {
+    const cuuint64_t dims[3] = {inner, outer, groups};
+    const cuuint64_t strides[2] = {ld * sizeof(float), outer * ld * sizeof(float)};
+    const cuuint32_t box[3] = {box_inner, box_outer, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides,
+                                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS && log_enabled())
+        std::fprintf(stderr, "[emu] grouped tensor map encode failed (%d): base %p %llu x %llu x %llu ld %llu\n", (int)r,
+                     (const void*)base, (unsigned long long)groups, (unsigned long long)outer, (unsigned long long)inner,
+                     (unsigned long long)ld);
     return r == CUDA_SUCCESS;
 }
 
@@ -1345,6 +1364,67 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
         return EMU_STATUS_LAUNCH_FAILED;
     }
     return st;
+}
+
+emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t stream, Until until) {
+    if (!fused_mode(mode)) return EMU_STATUS_NOT_SUPPORTED;
+    const int64_t most = INT32_MAX - 256;
+    if (g.rows > most || g.M > most || g.N > most || g.K > most) return EMU_STATUS_NOT_SUPPORTED;
+    const bool gated = g.fused && g.fused->kind == FUSED_GATED;
+    const int64_t b_n = gated ? 2 * g.N : g.N;
+    if (b_n > most) return EMU_STATUS_NOT_SUPPORTED;
+    if (!g.A || !g.B || !g.C || g.lda < (g.sum ? g.M : g.K) || g.ldb < (g.sum || g.b_mn ? g.N : g.K) || g.ldc < g.N)
+        return EMU_STATUS_INVALID_VALUE;
+    if (!aligned16(g.A) || !aligned16(g.B) || !aligned16(g.C) || (g.lda & 3) || (g.ldb & 3) || (g.ldc & 3))
+        return EMU_STATUS_NOT_SUPPORTED;
+    if (until != UNTIL_LAUNCHED) return EMU_STATUS_SUCCESS;
+
+    DeviceInfo* dev = nullptr;
+    const emu_status_t st = device_info(&dev);
+    if (st != EMU_STATUS_SUCCESS) return st;
+    Params p{};
+    const int64_t b_rows = g.b_mn ? g.K : b_n, b_cols = g.b_mn ? b_n : g.K;
+    if (!(g.sum ? encode_operand(&p.tmA, g.A, true, g.M, g.rows, g.lda, HALF) &&
+                      encode_operand(&p.tmB, g.B, true, g.N, g.rows, g.ldb, HALF)
+                : encode_operand(&p.tmA, g.A, false, g.rows, g.K, g.lda, HALF) &&
+                      encode_f32_3d(&p.tmB, g.B, (uint64_t)b_cols, (uint64_t)b_rows, (uint64_t)g.groups, (uint64_t)g.ldb, BK,
+                                    g.b_mn ? BK : HALF)))
+        return EMU_STATUS_LAUNCH_FAILED;
+    if (g.fused)
+        p.epi = {act_params(g.fused->act), (int)g.N, (g.N & 3) == 0, nullptr, 0, g.fused->d, g.fused->ldd, nullptr};
+    const int64_t tiles_n = gated ? (g.N + HALF - 1) / HALF : (g.N + TILE_M - 1) / TILE_M;
+    // rows: at most this many row tiles (every group's last may be partial)
+    const int64_t tiles_m = g.sum ? (g.M + TILE_M - 1) / TILE_M : g.rows / TILE_M + (g.rows < g.groups ? g.rows : g.groups);
+    const int64_t units = (g.sum ? g.groups : 1) * tiles_m * tiles_n;
+    if (units > most) return EMU_STATUS_NOT_SUPPORTED;
+    p.M = (int)(g.sum ? g.M : g.rows);
+    p.N = (int)g.N;
+    p.K = (int)g.K;
+    p.a_mn_major = g.sum;
+    p.b_mn_major = g.sum || g.b_mn;
+    p.tiles_m = (int)tiles_m;
+    p.tiles_n = (int)tiles_n;
+    p.num_tiles = p.num_units = (int)units;
+    p.k_stages = g.sum ? 0 : (int)((g.K + BK - 1) / BK);
+    p.tiles_a = (int)units;
+    p.split_a = p.split_b = 1;
+    p.alpha = 1.0f;
+    p.c = g.C;
+    p.c_old = g.C;
+    p.ldc = g.ldc;
+    p.wait_budget_ns = wait_budget_ns();
+    p.error_word = dev->error_word;
+    p.group = {g.list, g.count, g.M * g.ldc};
+    const int pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    const int64_t stages = g.sum ? g.rows / g.groups / BK : p.k_stages;
+    const int pipe = stages >= kLongKMinStages ? PIPE_LONG_K : PIPE_SHORT_K;
+    const EpiTable* table = g.sum ? &kSumStore : gated ? &kRowsGated : g.fused ? &kRowsGatedBwd : &kRowsStore;
+    if (log_enabled())
+        std::fprintf(stderr, "[emu] %s grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld units<=%lld pipe=%d\n", mode_name(mode),
+                     g.sum ? "sum" : "rows", (long long)g.rows, g.groups, (long long)g.M, (long long)g.N, (long long)g.K,
+                     (long long)units, pipe);
+    return launch_gemm(mode, pipe, p, (int)(units < pairs ? units : pairs), stream, table) == cudaSuccess
+               ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }
 static_assert(FUSED_ACT == EPI_ACT && FUSED_GATED == EPI_GATED && FUSED_GATED_BWD == EPI_GATED_BWD, "epilogue kinds");
 

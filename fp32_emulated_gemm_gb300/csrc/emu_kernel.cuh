@@ -238,6 +238,23 @@ struct EpiParams {
     float* sums;       // EPI_GATED_BWD: ceil(M / 32) x 2F partial column sums, or null
 };
 
+// Products whose rows lie in groups, a weight for each group (experts.cu); the
+// groups' bounds are on the device.
+// GROUP_ROWS  C[r] = op(A)[r] op(B[g]) for the rows r of group g: the tiles are
+//             listed on the device (a group's last one is clipped to its rows),
+//             tmB is a 3-D map with the group as its last coordinate
+// GROUP_SUM   C[g] = op(A)[:, rows of g] op(B)[rows of g, :]: the contraction runs
+//             over the group's rows (both operands MN-major); tile t of the list
+//             of groups is the whole C[g]
+// Whole tiles only: the bounds decide how many there are, and a plan is the host's.
+enum Group : int { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_SUM = 2 };
+
+struct GroupParams {
+    const int4* list;      // {first row, row after the last, group, -} of each row tile (GROUP_ROWS) or group
+    const int* count;      // GROUP_ROWS: row tiles listed
+    long long c_stride;    // GROUP_SUM: from one C[g] to the next
+};
+
 struct Params {
     CUtensorMap tmA;  // FP32 op(A): K-major box {32, 128} or MN-major box {32, 32}
     CUtensorMap tmB;  // FP32 op(B): K-major box {32, TN / 2} or MN-major box {32, 32};
@@ -273,6 +290,7 @@ struct Params {
     unsigned long long wait_budget_ns;
     unsigned* error_word;  // set by a wait that gives up
     EpiParams epi;
+    GroupParams group;
 };
 
 // ----------------------------------------------------------- the splits ----
@@ -368,8 +386,10 @@ __device__ __forceinline__ void store_components(uint8_t* dst, uint32_t row, uin
 // at ROWS * ROW_BYTES strides).  `t` is the thread's index among NT split
 // threads (NT a multiple of 32).  Work items are (row, 8-k group) pairs,
 // 4 * ROWS per tile.
-template <int MODE, int NT, int ROWS>
-__device__ __forceinline__ void split_operand(const uint8_t* src, uint8_t* dst, bool mn_major, uint32_t t) {
+// `k_real` (MN-major operands of GROUP_SUM): k-values from there on are taken as 0.
+template <int MODE, int NT, int ROWS, bool CLIP = false>
+__device__ __forceinline__ void split_operand(const uint8_t* src, uint8_t* dst, bool mn_major, uint32_t t,
+                                              uint32_t k_real = BK) {
     static_assert(ROWS == 128 || ROWS == 64, "tile rows");
     constexpr uint32_t ITEMS = 4 * ROWS;
     constexpr uint32_t CSTRIDE = ROWS * Cfg<MODE>::ROW_BYTES;
@@ -393,7 +413,7 @@ __device__ __forceinline__ void split_operand(const uint8_t* src, uint8_t* dst, 
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                x[i] = *reinterpret_cast<const float*>(src + off_f32_mnmajor(mn, 8 * g + i));
+                x[i] = !CLIP || 8 * g + i < k_real ? *reinterpret_cast<const float*>(src + off_f32_mnmajor(mn, 8 * g + i)) : 0.0f;
             store_components<MODE, CSTRIDE>(dst, mn, g, x);
         }
     }
@@ -432,6 +452,7 @@ enum Role : int { ROLE_TILE = 0, ROLE_HEAD = 1, ROLE_TAIL = 2 };
 struct Unit {
     int tile, piece, pieces, kb, ke, role;
     long long slot;  // first workspace partial tile of a split tile; chained plans: the running sum's slot
+    int row0, row1, group;  // grouped products: rows [row0, row1) of `group` (GROUP_ROWS: the tile's)
 };
 __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
     Unit w;
@@ -490,7 +511,19 @@ __device__ __forceinline__ Walk walk_of(const Params& p, int cid, int ncl) {
     k.hi = static_cast<int>(e - static_cast<long long>(k.last - 1) * p.k_stages);
     return k;
 }
+template <int GROUP>
 __device__ __forceinline__ Unit unit_at(const Params& p, const Walk& k, int cid, int u) {
+    if constexpr (GROUP != GROUP_NONE) {
+        const int per = GROUP == GROUP_ROWS ? p.tiles_n : p.tiles_m * p.tiles_n, at = u / per;
+        const int4 g = __ldcg(p.group.list + at);
+        Unit w;
+        w.piece = 0; w.pieces = 1; w.role = ROLE_TILE; w.slot = 0;
+        w.row0 = g.x; w.row1 = g.y; w.group = g.z;
+        w.tile = u - at * per;  // (GROUP_ROWS: the tile's column)
+        w.kb = 0;
+        w.ke = GROUP == GROUP_ROWS ? p.k_stages : (g.y - g.x + BK - 1) / BK;
+        return w;
+    }
     if (!p.chain) return unit_of(p, u);
     Unit w;
     const int lo = u == k.first ? k.lo : 0;                 // the run covers positions
@@ -537,7 +570,7 @@ __device__ __forceinline__ float4 mul4(const float4& a, const float4& b) {
 // STAGED: split tiles of many pieces read the other pieces' partials through
 // the output staging area (see the epilogue); a separate instantiation, so
 // that plans with few pieces keep the register-only reduction's code.
-template <int MODE, int PIPE, bool STAGED = false, int EPI = EPI_STORE>
+template <int MODE, int PIPE, bool STAGED = false, int EPI = EPI_STORE, int GROUP = GROUP_NONE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 emu_gemm_kernel(const __grid_constant__ Params p) {
     using C = Cfg<MODE>;
@@ -591,12 +624,20 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         return EPI == EPI_GATED ? tn * BH + p.epi.F * static_cast<int>(rank) : tn * TN + BH * static_cast<int>(rank);
     };
     // (m0, n0): this CTA's first row of op(A) and of op(B)^T in the tile
-    auto issue_load_at = [&](int s, int m0, int n0, int ks) {
+    // (grouped: k0 is the contraction's first row of the stage, `group` the weight)
+    auto issue_load_at = [&](int s, int m0, int n0, int ks, int first = 0, int group = 0) {
         uint64_t* full = &fp32_full[s];
         mbar_arrive_expect_tx(full, KC::FP32_STAGE);
         uint8_t* dA = fp32_ring + s * KC::FP32_STAGE;
         uint8_t* dB = dA + FP32_TILE_BYTES;
-        const int k0 = ks * BK;
+        const int k0 = first + ks * BK;
+        if constexpr (GROUP == GROUP_ROWS) {
+            static_assert(GROUP != GROUP_ROWS || !PACKED, "grouped rows: unpacked operands");
+            tma_load_2d(dA, &p.tmA, full, k0, m0);
+            if (!p.b_mn_major) tma_load_3d(dB, &p.tmB, full, k0, n0, group);
+            else for (int j = 0; j < BH / 32; ++j) tma_load_3d(dB + j * 4096, &p.tmB, full, n0 + 32 * j, k0, group);
+            return;
+        }
         if (!p.a_mn_major) tma_load_2d(dA, &p.tmA, full, k0, m0);
         else for (int j = 0; j < HALF / 32; ++j) tma_load_2d(dA + j * 4096, &p.tmA, full, m0 + 32 * j, k0);
         if constexpr (!PACKED) {
@@ -604,8 +645,13 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             else for (int j = 0; j < BH / 32; ++j) tma_load_2d(dB + j * 4096, &p.tmB, full, n0 + 32 * j, k0);
         }
     };
-    auto issue_load = [&](int s, int tile, int ks) {
-        issue_load_at(s, (tile / p.tiles_n) * TILE_M + HALF * rank, b_row0(tile % p.tiles_n), ks);
+    auto issue_load = [&](int s, const Unit& w, int ks) {
+        const int tile = w.tile;
+        if constexpr (GROUP == GROUP_ROWS)
+            issue_load_at(s, w.row0 + static_cast<int>(HALF * rank), b_row0(tile), ks, 0, w.group);
+        else
+            issue_load_at(s, (tile / p.tiles_n) * TILE_M + HALF * rank, b_row0(tile % p.tiles_n), ks,
+                          GROUP == GROUP_SUM ? w.row0 : 0);
     };
     // packed shapes: op(B)'s component tiles of a stage, straight into the
     // component ring (box {32 k, BH rows, 1 component} per component)
@@ -629,7 +675,11 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         for (int s = 0; s < NB; ++s) { mbar_init(&bcomp_full[s], 1); mbar_init(&bcomp_empty[s], 1); }
         *abort_flag = 0;
         // this pair's walk, worked out once for all roles
-        const Walk wk = walk_of(p, static_cast<int>(cid), static_cast<int>(ncl));
+        Walk wk = walk_of(p, static_cast<int>(cid), static_cast<int>(ncl));
+        if constexpr (GROUP == GROUP_ROWS) {
+            griddep_wait();  // the list may be the previous grid's
+            wk.last = __ldcg(p.group.count) * p.tiles_n;
+        }
         walk_sh[0] = wk.first; walk_sh[1] = wk.last; walk_sh[2] = wk.step; walk_sh[3] = wk.lo; walk_sh[4] = wk.hi;
         fence_mbar_init();
         // Where the first stages come from depends on the parameters alone:
@@ -638,12 +688,12 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         // not delay the first loads.
         constexpr int NE = PACKED && NB > NF ? NB : NF;
         int e_m0[NE], e_n0[NE], e_ks[NE], ne = 0;
-        {
+        if constexpr (GROUP == GROUP_NONE) {
             int u = wk.first, ks = 0, ke = 0, m0 = 0, n0 = 0;
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
                 while (ks >= ke && u < wk.last) {
-                    const Unit w = unit_at(p, wk, static_cast<int>(cid), u);
+                    const Unit w = unit_at<GROUP_NONE>(p, wk, static_cast<int>(cid), u);
                     const int tm = w.tile / p.tiles_n;
                     m0 = tm * TILE_M + HALF * rank;
                     n0 = b_row0(w.tile - tm * p.tiles_n);
@@ -708,11 +758,11 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             uint32_t bph = 0, bissued_mask = 0, bissued_parity = 0;
             bool ok = true;
             for (int u = walk.first; ok && u < walk.last; u += walk.step) {
-                const Unit w = unit_at(p, walk, static_cast<int>(cid), u);
+                const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u);
                 for (int ks = w.kb; ks < w.ke; ++ks, ++n) {
                     if (n >= early) {  // the first `early` loads went out before the pair sync
                         if (!mbar_wait(&fp32_empty[s], ph ^ 1u, abort_flag, budget, 1)) { ok = false; break; }
-                        issue_load(s, w.tile, ks);
+                        issue_load(s, w, ks);
                     }
                     issued_mask |= 1u << s;
                     issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
@@ -752,7 +802,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             bool ok = true, issued = false;
             const uint32_t slice_base = smem_u32(slice_ring), bcomp_base = smem_u32(bcomp_ring);
             for (int u = walk.first; ok && u < walk.last; u += walk.step) {
-                const Unit w = unit_at(p, walk, static_cast<int>(cid), u);
+                const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u);
                 for (int ks = w.kb; ks < w.ke; ++ks) {
                     if (!mbar_wait(&acc_empty[b], bph ^ 1u, abort_flag, budget, 2)) { ok = false; break; }
                     if (!mbar_wait(&slice_full[s], ph, abort_flag, budget, 2)) { ok = false; break; }
@@ -787,14 +837,27 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         uint32_t fph = 0, sph = 0, bph = 0;
         bool ok = true;
         for (int u = walk.first; ok && u < walk.last; u += walk.step) {
-            const Unit w = unit_at(p, walk, static_cast<int>(cid), u);
+            const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u);
             for (int ks = w.kb; ks < w.ke; ++ks) {
                 if (!mbar_wait_warp(&fp32_full[fs], fph, abort_flag, budget, 3)) { ok = false; break; }
                 if (!mbar_wait_warp(&slice_empty[ss], sph ^ 1u, abort_flag, budget, 3)) { ok = false; break; }
                 const uint8_t* src = fp32_ring + fs * KC::FP32_STAGE;
                 uint8_t* dst = slice_ring + ss * KC::SLICE_STAGE;
+                if constexpr (GROUP == GROUP_SUM) {
+                    // the rows behind the group's last are another group's
+                    const int left = w.row1 - w.row0 - ks * BK;
+                    if (left < BK) {
+                        split_operand<MODE, NUM_SPLIT_THREADS, HALF, true>(src, dst, true, t, left);
+                        split_operand<MODE, NUM_SPLIT_THREADS, BH, true>(src + FP32_TILE_BYTES, dst + C::NCOMP * KC::COMP_A,
+                                                                         true, t, left);
+                    } else {
+                        split_operand<MODE, NUM_SPLIT_THREADS, HALF>(src, dst, true, t);
+                        split_operand<MODE, NUM_SPLIT_THREADS, BH>(src + FP32_TILE_BYTES, dst + C::NCOMP * KC::COMP_A, true, t);
+                    }
+                } else
                 split_operand<MODE, NUM_SPLIT_THREADS, HALF>(src, dst, p.a_mn_major != 0, t);
-                if constexpr (!PACKED) {
+                if constexpr (GROUP == GROUP_SUM) {
+                } else if constexpr (!PACKED) {
                     split_operand<MODE, NUM_SPLIT_THREADS, BH>(src + FP32_TILE_BYTES, dst + C::NCOMP * KC::COMP_A,
                                                                p.b_mn_major != 0, t);
                 } else {  // op(B)'s components come by TMA into their own ring
@@ -827,7 +890,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         for (int u = walk_sh[0]; ok && u < walk_sh[1]; u += walk_sh[2]) {
             Walk wk;
             wk.first = walk_sh[0]; wk.last = walk_sh[1]; wk.step = walk_sh[2]; wk.lo = walk_sh[3]; wk.hi = walk_sh[4];
-            const Unit w = unit_at(p, wk, static_cast<int>(cid), u);
+            const Unit w = unit_at<GROUP>(p, wk, static_cast<int>(cid), u);
             // a chained tile's running sum: one 256 x TN slot per run boundary,
             // thread-major like the split-K partials below (worked out where it
             // is used, so that it holds no registers during the k-loop)
@@ -842,10 +905,11 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 const float* base = EPI == EPI_ACT ? p.epi.res : p.epi.d;
                 if (base && w.role != ROLE_HEAD) {
                     const int t = static_cast<int>(e * 32 + lane);
-                    const int row = (w.tile / p.tiles_n) * TILE_M + static_cast<int>(HALF * rank) + (t & 127);
-                    const int c0 = (w.tile % p.tiles_n) * TN, cols = p.N - c0 < TN ? (p.N - c0) & ~3 : TN;
+                    const int row = (GROUP == GROUP_ROWS ? w.row0 : (w.tile / p.tiles_n) * TILE_M) +
+                                    static_cast<int>(HALF * rank) + (t & 127);
+                    const int c0 = (GROUP == GROUP_ROWS ? w.tile : w.tile % p.tiles_n) * TN, cols = p.N - c0 < TN ? (p.N - c0) & ~3 : TN;
                     const bool up = t >= 128;
-                    if (row < p.M && cols > 0 && (!up || (EPI == EPI_GATED_BWD && p.epi.vec_up)))
+                    if (row < (GROUP == GROUP_ROWS ? w.row1 : p.M) && cols > 0 && (!up || (EPI == EPI_GATED_BWD && p.epi.vec_up)))
                         l2_prefetch(base + row * (EPI == EPI_ACT ? p.epi.ldr : p.epi.ldd) + (up ? p.epi.F : 0) + c0, 4u * cols);
                 }
             }
@@ -1039,8 +1103,10 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             // (the tile's origin is worked out here, not before the split-tile
             // reduction, so that it holds no registers there)
             constexpr int TILE_COLS = EPI == EPI_GATED ? TN / 2 : TN, WARP_COLS = EPI == EPI_GATED ? ACC / 2 : ACC;
-            const int row0 = (w.tile / p.tiles_n) * TILE_M + static_cast<int>(HALF * rank + quarter * 32u);
-            const int col0 = (w.tile % p.tiles_n) * TILE_COLS + static_cast<int>(half * WARP_COLS);
+            const int row0 = (GROUP == GROUP_ROWS ? w.row0 : (w.tile / p.tiles_n) * TILE_M) +
+                             static_cast<int>(HALF * rank + quarter * 32u);
+            const int col0 = (GROUP == GROUP_ROWS ? w.tile : w.tile % p.tiles_n) * TILE_COLS + static_cast<int>(half * WARP_COLS);
+            const int rows_end = GROUP == GROUP_ROWS ? w.row1 : p.M;  // the tile's rows beyond are not stored
             // ACC / OUT_COLS blocks of 32 rows x OUT_COLS columns: each lane stages
             // its row's sums in shared memory (rows of OUT_COLS * 4 bytes, 16-byte
             // chunks XOR-swizzled by row); the warp then reads them back as whole
@@ -1082,8 +1148,9 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                     const uint32_t rr = pass * RPP + lane / CPR;
                     const float4 v = *reinterpret_cast<const float4*>(stage + chunk_off(rr, q));
                     const int grow = row0 + static_cast<int>(rr);
-                    if (grow >= p.M) continue;
-                    float* dst = p.c + static_cast<long long>(grow) * p.ldc + gcol;
+                    if (grow >= rows_end) continue;
+                    float* dst = p.c + (GROUP == GROUP_SUM ? w.group * p.group.c_stride : 0) +
+                                 static_cast<long long>(grow) * p.ldc + gcol;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (beta != 0.0f) {
                         const float* src_old = p.c_old + static_cast<long long>(grow) * p.ldc + gcol;
@@ -1150,7 +1217,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 stage_block(ACC / 2 + OUT_COLS * c);
                 float* h = p.c + lrow * p.ldc + gcol;
                 float* d = save.value ? ep.d + lrow * ep.ldd + gcol : nullptr;
-                if (row0 + 32 <= p.M && col0 + OUT_COLS * (c + 1) <= p.N) {
+                if (row0 + 32 <= rows_end && col0 + OUT_COLS * (c + 1) <= p.N) {
 #pragma unroll
                     for (int pass = 0; pass < PASSES; pass += 2) {
                         float4 a[2], f[2], u[2];
@@ -1183,7 +1250,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 } else {
 #pragma unroll
                     for (int pass = 0; pass < PASSES; ++pass) {
-                        if (lrow + pass * RPP < p.M) {
+                        if (lrow + pass * RPP < rows_end) {
                             const float4 u = add4(staged(pass), bu);
                             float4 a, f;
                             act_value_grad4<fam.value>(ep.act, add4(g[pass], bg), a, f);
@@ -1237,7 +1304,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                     return *reinterpret_cast<const float4*>(stage + chunk_off(pass * RPP + lane / CPR, q));
                 };
                 const int gcol = col0 + OUT_COLS * c + static_cast<int>(4 * q);
-                const bool whole = row0 + 32 <= p.M && col0 + OUT_COLS * (c + 1) <= p.N;
+                const bool whole = row0 + 32 <= rows_end && col0 + OUT_COLS * (c + 1) <= p.N;
                 float* out = p.c + lrow * p.ldc + gcol;
                 constexpr int BATCH = 4;  // passes whose loads go out together
                 if constexpr (EPI == EPI_ACT) {
@@ -1275,7 +1342,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                         }
                     } else {
 #pragma unroll 1
-                        for (int pass = 0; pass < PASSES && lrow + pass * RPP < p.M; ++pass) {
+                        for (int pass = 0; pass < PASSES && lrow + pass * RPP < rows_end; ++pass) {
                             float4 v, f;
                             act_value_grad4<fam.value>(ep.act, add4(staged(pass), bb), v, f);
                             if constexpr (save.value) {
@@ -1326,7 +1393,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                         }
                     } else {
 #pragma unroll 1
-                        for (int pass = 0; pass < PASSES && lrow + pass * RPP < p.M; ++pass) {
+                        for (int pass = 0; pass < PASSES && lrow + pass * RPP < rows_end; ++pass) {
                             const float4 dh = staged(pass), dg = mul4(dh, load_cols(d, gcol, p.N, true)),
                                          du = mul4(dh, load_cols(d + ep.F, gcol, p.N, ep.vec_up));
                             store_cols(out, gcol, p.N, true, dg);
@@ -1343,7 +1410,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                             sg = add4(sg, shfl_xor4(sg, o));
                             su = add4(su, shfl_xor4(su, o));
                         }
-                        if (lane < CPR && row0 < p.M) {
+                        if (lane < CPR && row0 < rows_end) {
                             float* dst = ep.sums + static_cast<long long>(row0 / 32) * (2ll * ep.F) + gcol;
                             store_cols(dst, gcol, p.N, ep.vec_up, sg);
                             store_cols(dst + ep.F, gcol, p.N, ep.vec_up, su);

@@ -66,7 +66,7 @@ template <int V> __device__ __forceinline__ void warp_sums(float (&v)[V], int la
 
 // MR: rows of X (M of them real), NR: rows of W per warp (gated: NR / 2 of the
 // gate and the same of the up projection), WK: warps that share a row.
-template <int MR, int NR, bool GATED, bool VEC, int FAMILY>
+template <int MR, int NR, bool GATED, bool VEC, int FAMILY, bool GROUPED = false>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const FewRows p, int wk) {
     constexpr int V = MR * NR, OUT = GATED ? NR / 2 : NR;  // sums of a warp; output columns
     constexpr int U = MR <= 2 ? 4 : 2;                     // steps whose weights are in flight together
@@ -74,8 +74,17 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int groups = kWarpsPerBlock / wk, share = warp % wk;
     const int64_t n0 = ((int64_t)blockIdx.x * groups + warp / wk) * OUT;  // first output column
-    const int m0 = blockIdx.y * MR, rows = min(MR, p.M - m0);             // this block's rows of X
+    int m0 = blockIdx.y * MR, rows = min(MR, p.M - m0);                   // this block's rows of X
+    const float* W = p.W;
     if (threadIdx.x == 0) griddep_launch_dependents();
+    if constexpr (GROUPED) {
+        griddep_wait();  // the list may be the previous kernel's
+        if (static_cast<int>(blockIdx.y) >= __ldcg(p.count)) return;
+        const int4 g = __ldcg(p.list + blockIdx.y);
+        m0 = g.x;
+        rows = g.y - g.x;
+        W += g.z * ((GATED ? 2 : 1) * p.N * p.ldw);
+    }
     // this warp's part of k: whole steps of 128
     const int64_t steps = (p.K + 127) / 128, s0 = steps * share / wk, s1 = steps * (share + 1) / wk;
     const int64_t kend = min(p.K, s1 * 128);
@@ -84,7 +93,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     for (int j = 0; j < NR; ++j) {
         // (columns past the end read the last one's weights and are dropped)
         const int64_t n = min(n0 + j % OUT, p.N - 1) + (GATED && j >= OUT ? p.N : 0);
-        wrow[j] = p.W + n * p.ldw;
+        wrow[j] = W + n * p.ldw;
     }
     float acc[V];
 #pragma unroll
@@ -98,7 +107,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
             for (int j = 0; j < NR; ++j) w[u][j] = load_w<VEC>(wrow[j], at + 128 * u, kend);
     };
     load(c);
-    griddep_wait();  // X may be the previous kernel's
+    if constexpr (!GROUPED) griddep_wait();  // X may be the previous kernel's
     for (int64_t s = s0; s < s1; s += U, c += 128 * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -151,14 +160,14 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     }
 }
 
-template <int MR, int NR>
+template <int MR, int NR, bool GROUPED = false>
 cudaError_t launch(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream) {
     // 16 warps an SM keep enough of the weight in flight; a share of k is at
     // least one step
     const int out = gated ? NR / 2 : NR;
     const int64_t warps = (p.N + out - 1) / out, steps = (p.K + 127) / 128;
     int wk = 1;
-    const int64_t row_groups = (p.M + MR - 1) / MR;
+    const int64_t row_groups = GROUPED ? p.blocks : (p.M + MR - 1) / MR;
     while (wk < kWarpsPerBlock && row_groups * warps * wk < 16ll * sm_count && 2 * wk <= steps) wk *= 2;
     const int64_t groups = kWarpsPerBlock / wk, grid = (warps + groups - 1) / groups;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -177,10 +186,10 @@ cudaError_t launch(const FewRows& p, bool gated, bool after_own, int sm_count, c
     cudaError_t e = cudaSuccess;
     for_family(p.act.family, [&](auto fam) {
         constexpr int f = decltype(fam)::value;
-        e = gated ? (vec ? cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, true, true, f>, p, wk)
-                         : cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, true, false, f>, p, wk))
-                  : (vec ? cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, false, true, f>, p, wk)
-                         : cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, false, false, f>, p, wk));
+        e = gated ? (vec ? cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, true, true, f, GROUPED>, p, wk)
+                         : cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, true, false, f, GROUPED>, p, wk))
+                  : (vec ? cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, false, true, f, GROUPED>, p, wk)
+                         : cudaLaunchKernelEx(&cfg, few_rows_kernel<MR, NR, false, false, f, GROUPED>, p, wk));
     });
     if (e != cudaSuccess) cudaGetLastError();
     return e;
@@ -197,6 +206,15 @@ cudaError_t launch_few_rows(const FewRows& p, bool gated, bool after_own, int sm
     if (p.M <= 2) return launch<2, 4>(p, gated, after_own, sm_count, stream);
     if (p.M <= 4) return launch<4, 4>(p, gated, after_own, sm_count, stream);
     return launch<8, 4>(p, gated, after_own, sm_count, stream);  // eight rows a block
+}
+
+cudaError_t launch_few_rows_grouped(const FewRows& p, int block_rows, bool gated, int sm_count, cudaStream_t stream) {
+    switch (block_rows) {
+        case 1: return launch<1, 4, true>(p, gated, true, sm_count, stream);
+        case 2: return launch<2, 4, true>(p, gated, true, sm_count, stream);
+        case 4: return launch<4, 4, true>(p, gated, true, sm_count, stream);
+        default: return launch<8, 4, true>(p, gated, true, sm_count, stream);
+    }
 }
 
 }  // namespace emu

@@ -12,6 +12,13 @@
 
 namespace emu {
 
+#define EMU_TRY(expr)                                        \
+    do {                                                     \
+        const emu_status_t st_ = (expr);                     \
+        if (st_ != EMU_STATUS_SUCCESS) return st_;           \
+    } while (0)
+inline emu_status_t launched(cudaError_t e) { return e == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED; }
+
 // The current device, bound to this host thread and checked to be sm_103.
 struct DeviceCtx { int id, sm_count; };
 emu_status_t current_device(DeviceCtx* out);
@@ -80,5 +87,25 @@ emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, Until unt
 // and both before work queued after it: side by side on shares of the GPU when
 // that is predicted faster than one after the other.  Either may be absent (null).
 emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, Until until);
+
+// A product whose rows lie in groups, a weight for each (see Group in
+// emu_kernel.cuh).  The modes BF16x9 and TF32x3.
+struct GroupedGemm {
+    bool sum;         // false: C[r] = A[r] op(B[g]); true: C[g] = A[rows of g]^T B[rows of g]
+    int groups;
+    bool b_mn;        // rows: B[g] is K x N (rows are the contraction), else N x K
+    int64_t rows;     // rows of A (and, rows: of C; sum: of B): all groups' at most
+    int64_t M, N, K;  // rows: N and K; sum: M x N is C[g]
+    const float* A;
+    int64_t lda;
+    const float* B;   // rows: the groups' matrices one behind the other
+    int64_t ldb;
+    float* C;
+    int64_t ldc;      // sum: C[g] starts g M ldc after C
+    const Fused* fused = nullptr;  // rows: FUSED_GATED (N is F, B[g] has 2F rows) or FUSED_GATED_BWD
+    const int4* list = nullptr;    // the groups' tiles or bounds, on the device (Params::group)
+    const int* count = nullptr;
+};
+emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t stream, Until until);
 
 }  // namespace emu

@@ -348,6 +348,124 @@ emu_status_t emu_gated_ffn_bwd(emu_mode_t mode, int64_t M, int64_t K, int64_t F,
                                float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW_in, int64_t lddwi,
                                float *db_in, float *dW_out, int64_t lddwo, float *db_out, emu_stream_t stream);
 
+/*
+ * Operators of a layer of experts: the RMS norm in front of it, the router, the
+ * tokens' way to their experts' rows and back, and the experts' gated blocks.
+ * The conventions of the feed-forward operators hold (FP32 in and out,
+ * row-major with a leading dimension, inputs of any alignment, outputs must not
+ * overlap inputs or one another, sums in an order fixed by the sizes and the
+ * device, buffers of the library per (device, stream)), with what each call says.
+ */
+
+/*
+ * emu_rms_norm_fwd -- Y = S * rstd * weight over the rows of S = X + residual
+ *   (M x N): rstd = 1 / sqrt(mean(S^2) + eps) per row.  residual, weight (N; 1),
+ *   S and rstd (M, for the backward pass) may be NULL.  eps >= 0, else
+ *   INVALID_VALUE.  Outputs of any alignment.  The sum of a row's squares has to
+ *   be within FP32.
+ * emu_rms_norm_quant -- the same Y in 8 bits: column c of row m stands for
+ *   Q[m, c] * scales[m, c / 128], Q in e4m3 (finite, largest 448), the scale the
+ *   smallest power of two >= 2^-126 with the largest |Y| of its 128 columns
+ *   within 448 of it, Q = Y / scale rounded to nearest even.  ldscales >=
+ *   ceil(N / 128).
+ * emu_rms_norm_bwd -- with g = dY * weight and h = S * rstd: dX = rstd * (g - h *
+ *   mean(g * h)) + add (the residual's gradient too), dweight = sum over rows of
+ *   dY * h.  `add` (may be NULL) is a gradient that reaches S by another way; it
+ *   needs dX.  dX and dweight may each be NULL (not wanted).  M == 0 gives a
+ *   zero dweight.
+ */
+emu_status_t emu_rms_norm_fwd(int64_t M, int64_t N, const float *X, int64_t ldx, const float *residual, int64_t ldr,
+                              const float *weight, float eps, float *Y, int64_t ldy, float *S, int64_t lds, float *rstd,
+                              emu_stream_t stream);
+emu_status_t emu_rms_norm_quant(int64_t M, int64_t N, const float *X, int64_t ldx, const float *residual, int64_t ldr,
+                                const float *weight, float eps, uint8_t *Q, int64_t ldq, float *scales, int64_t ldscales,
+                                float *S, int64_t lds, emu_stream_t stream);
+emu_status_t emu_rms_norm_bwd(int64_t M, int64_t N, const float *dY, int64_t lddy, const float *S, int64_t lds,
+                              const float *weight, const float *rstd, const float *add, int64_t ldadd, float *dX,
+                              int64_t lddx, float *dweight, emu_stream_t stream);
+
+/* What a choice's weight is the softmax over: the token's chosen logits, or all. */
+typedef enum { EMU_OVER_CHOSEN = 0, EMU_OVER_ALL = 1 } emu_over_t;
+
+/*
+ * emu_expert_route -- each token's k largest of its E logits (M x E), the lowest
+ *   index first among equals, and the choices sorted by expert:
+ *   experts, weights  M x k, dense: the choices, largest first, and their softmax
+ *     weights.  A logit of -inf is closed to the token and never chosen; where
+ *     fewer than k are open, the rest are expert -1 with weight 0 (a row of -inf,
+ *     a padded token, goes nowhere).  NaN ranks above all and, like +inf, makes
+ *     the row's weights NaN.
+ *   offsets  E + 1: expert e's rows are offsets[e] .. offsets[e + 1], in the order
+ *     of the choices m k + j.
+ *   slots    M x k: choice (m, j)'s row, or -1.
+ *   sources  M k: row r's choice m k + j, or -1 from offsets[E] on.
+ *   1 <= k <= E, else INVALID_VALUE; E <= 1024, k <= 32 and M k < 2^31 - 256, else
+ *   NOT_SUPPORTED.  M == 0 writes zero offsets.
+ * emu_expert_sort -- the last three for given choices (experts, M x k): one that
+ *   is not within 0 .. E - 1 goes nowhere.  The same expert may come twice.
+ * emu_expert_route_bwd -- dlogits (M x E) from dweights, the route's experts and
+ *   weights and, for EMU_OVER_ALL, the logits (else they may be NULL).
+ */
+emu_status_t emu_expert_route(emu_over_t over, int64_t M, int E, int k, const float *logits, int64_t ldl,
+                              int32_t *experts, float *weights, int32_t *slots, int32_t *sources, int32_t *offsets,
+                              emu_stream_t stream);
+emu_status_t emu_expert_sort(int64_t M, int E, int k, const int32_t *experts, int32_t *slots, int32_t *sources,
+                             int32_t *offsets, emu_stream_t stream);
+emu_status_t emu_expert_route_bwd(emu_over_t over, int64_t M, int E, int k, const float *dweights, const float *logits,
+                                  int64_t ldl, const int32_t *experts, const float *weights, float *dlogits, int64_t lddl,
+                                  emu_stream_t stream);
+
+/*
+ * Tokens (M rows) to their experts' rows (M k rows) and back; slots and sources
+ * as above (a slot outside the rows counts as -1), k <= 32.  Outputs of any
+ * alignment.
+ * emu_expert_dispatch -- Xs[slots[m, j]] = X[m]; rows without a source are 0.
+ * emu_expert_combine_fwd -- Y[m] = sum over j of weights[m, j] Ys[slots[m, j]] +
+ *   residual[m], in the order of j; weights (NULL: 1) and residual may be NULL.
+ *   Without both it is also the gradient of the dispatch.
+ * emu_expert_combine_bwd -- dYs[slots[m, j]] = weights[m, j] dY[m], rows without a
+ *   source 0; dweights[m, j] = <dY[m], Ys[slots[m, j]]> (0 without a slot).  Either
+ *   may be NULL (not wanted).
+ */
+emu_status_t emu_expert_dispatch(int64_t M, int k, int64_t N, const float *X, int64_t ldx, const int32_t *slots,
+                                 const int32_t *sources, float *Xs, int64_t ldxs, emu_stream_t stream);
+emu_status_t emu_expert_combine_fwd(int64_t M, int k, int64_t N, const float *Ys, int64_t ldys, const int32_t *slots,
+                                    const float *weights, const float *residual, int64_t ldr, float *Y, int64_t ldy,
+                                    emu_stream_t stream);
+emu_status_t emu_expert_combine_bwd(int64_t M, int k, int64_t N, const float *dY, int64_t lddy, const float *Ys,
+                                    int64_t ldys, const int32_t *slots, const int32_t *sources, const float *weights,
+                                    float *dYs, int64_t lddys, float *dweights, emu_stream_t stream);
+
+/*
+ * emu_expert_ffn_fwd -- the gated blocks of E experts on rows sorted by expert:
+ *   for the rows r of expert e, offsets[e] <= r < offsets[e + 1] (device memory),
+ *   H = a(G) * U with [G | U] = X W_in[e]^T, Y = H W_out[e]^T.
+ *   X: rows x K; W_in: E matrices of 2F x K, one behind the other (the gate's F
+ *   rows, then the up projection's); W_out: E of N x F; H: rows x F; Y: rows x N;
+ *   D (rows x 2F, for the backward pass, may be NULL) as in emu_gated_fwd.  Rows
+ *   outside the offsets are neither read nor written; offsets that do not ascend
+ *   or leave the rows are taken as if clipped.
+ * emu_expert_ffn_bwd -- dZ = [dH | dH] * D with dH = dY W_out[e] (rows x 2F,
+ *   written); dX = dZ W_in[e]; over each expert's rows dW_in[e] = dZ^T X and
+ *   dW_out[e] = dY^T H (zeros for an expert without rows).  dX, dW_in and dW_out
+ *   may each be NULL (not wanted); D and dZ are used for the first two alone, H
+ *   for dW_out.
+ * The modes BF16X9 and TF32X3, with their accuracy; others, and E > 1024, are
+ * NOT_SUPPORTED.  E, K, F and N at least 1.  H, Y, D, dZ, dX, dW_in and dW_out
+ * start on a 16-byte boundary and have a leading dimension that is a multiple of
+ * 4, except in a forward pass of at most 4 E rows, which runs on the CUDA cores
+ * (few_rows) within the modes' bounds.
+ */
+emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, int E, int64_t K, int64_t F, int64_t N,
+                                const float *X, int64_t ldx, const int32_t *offsets, const float *W_in, int64_t ldwi,
+                                const float *W_out, int64_t ldwo, float *D, int64_t ldd, float *H, int64_t ldh, float *Y,
+                                int64_t ldy, emu_stream_t stream);
+emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K, int64_t F, int64_t N, const float *dY,
+                                int64_t lddy, const float *X, int64_t ldx, const int32_t *offsets, const float *W_in,
+                                int64_t ldwi, const float *W_out, int64_t ldwo, const float *D, int64_t ldd, const float *H,
+                                int64_t ldh, float *dZ, int64_t lddz, float *dX, int64_t lddx, float *dW_in,
+                                int64_t lddwi, float *dW_out, int64_t lddwo, emu_stream_t stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *emu_status_string(emu_status_t s);
 
