@@ -1366,6 +1366,20 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
     return st;
 }
 
+GroupedTiles grouped_tiles(const GroupedGemm& g) {
+    const bool gated = g.fused && g.fused->kind == FUSED_GATED;
+    const int64_t tiles_n = gated ? (g.N + HALF - 1) / HALF : (g.N + TILE_M - 1) / TILE_M;
+    if (!g.sum) return {(int)tiles_n, (int)((g.K + BK - 1) / BK)};
+    return {(int)((g.M + TILE_M - 1) / TILE_M * tiles_n), 0};
+}
+
+emu_status_t grouped_pairs(emu_mode_t mode, int* pairs) {
+    DeviceInfo* dev = nullptr;
+    const emu_status_t st = device_info(&dev);
+    if (st == EMU_STATUS_SUCCESS) *pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    return st;
+}
+
 emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t stream, Until until) {
     if (!fused_mode(mode)) return EMU_STATUS_NOT_SUPPORTED;
     const int64_t most = INT32_MAX - 256;
@@ -1377,12 +1391,23 @@ emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t st
         return EMU_STATUS_INVALID_VALUE;
     if (!aligned16(g.A) || !aligned16(g.B) || !aligned16(g.C) || (g.lda & 3) || (g.ldb & 3) || (g.ldc & 3))
         return EMU_STATUS_NOT_SUPPORTED;
-    if (until != UNTIL_LAUNCHED) return EMU_STATUS_SUCCESS;
+    // the list's entries are at most rows / 256 and one for each group, or the groups
+    const GroupedTiles tiles = grouped_tiles(g);
+    if ((g.sum ? g.groups : g.rows / TILE_M + g.groups) * (int64_t)tiles.per > most) return EMU_STATUS_NOT_SUPPORTED;
+    if (until == UNTIL_CHECKED) return EMU_STATUS_SUCCESS;
 
     DeviceInfo* dev = nullptr;
-    const emu_status_t st = device_info(&dev);
+    emu_status_t st = device_info(&dev);
     if (st != EMU_STATUS_SUCCESS) return st;
+    int devid = 0;
+    cudaGetDevice(&devid);
+    const int pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
     Params p{};
+    Workspace* w = nullptr;
+    st = workspace_for(devid, stream, (size_t)pairs * TILE_M * TILE_M, (size_t)pairs * 2, &w, &p.epoch);
+    if (st != EMU_STATUS_SUCCESS || until == UNTIL_RESERVED) return st;
+    p.workspace = static_cast<float*>(w->partials.ptr);
+    p.counters = static_cast<unsigned long long*>(w->counters.ptr);
     const int64_t b_rows = g.b_mn ? g.K : b_n, b_cols = g.b_mn ? b_n : g.K;
     if (!(g.sum ? encode_operand(&p.tmA, g.A, true, g.M, g.rows, g.lda, HALF) &&
                       encode_operand(&p.tmB, g.B, true, g.N, g.rows, g.ldb, HALF)
@@ -1392,21 +1417,14 @@ emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t st
         return EMU_STATUS_LAUNCH_FAILED;
     if (g.fused)
         p.epi = {act_params(g.fused->act), (int)g.N, (g.N & 3) == 0, nullptr, 0, g.fused->d, g.fused->ldd, nullptr};
-    const int64_t tiles_n = gated ? (g.N + HALF - 1) / HALF : (g.N + TILE_M - 1) / TILE_M;
-    // rows: at most this many row tiles (every group's last may be partial)
-    const int64_t tiles_m = g.sum ? (g.M + TILE_M - 1) / TILE_M : g.rows / TILE_M + (g.rows < g.groups ? g.rows : g.groups);
-    const int64_t units = (g.sum ? g.groups : 1) * tiles_m * tiles_n;
-    if (units > most) return EMU_STATUS_NOT_SUPPORTED;
     p.M = (int)(g.sum ? g.M : g.rows);
     p.N = (int)g.N;
     p.K = (int)g.K;
     p.a_mn_major = g.sum;
     p.b_mn_major = g.sum || g.b_mn;
-    p.tiles_m = (int)tiles_m;
-    p.tiles_n = (int)tiles_n;
-    p.num_tiles = p.num_units = (int)units;
-    p.k_stages = g.sum ? 0 : (int)((g.K + BK - 1) / BK);
-    p.tiles_a = (int)units;
+    p.tiles_n = gated ? (int)((g.N + HALF - 1) / HALF) : (int)((g.N + TILE_M - 1) / TILE_M);
+    p.tiles_m = tiles.per / p.tiles_n;
+    p.k_stages = tiles.stages;
     p.split_a = p.split_b = 1;
     p.alpha = 1.0f;
     p.c = g.C;
@@ -1414,17 +1432,19 @@ emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t st
     p.ldc = g.ldc;
     p.wait_budget_ns = wait_budget_ns();
     p.error_word = dev->error_word;
-    p.group = {g.list, g.count, g.M * g.ldc};
-    const int pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    p.group = {g.list, static_cast<const GroupWalk*>(g.walks), g.M * g.ldc};
     const int64_t stages = g.sum ? g.rows / g.groups / BK : p.k_stages;
     const int pipe = stages >= kLongKMinStages ? PIPE_LONG_K : PIPE_SHORT_K;
     const EpiTable* table = g.sum ? &kSumStore : gated ? &kRowsGated : g.fused ? &kRowsGatedBwd : &kRowsStore;
     if (log_enabled())
-        std::fprintf(stderr, "[emu] %s grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld units<=%lld pipe=%d\n", mode_name(mode),
-                     g.sum ? "sum" : "rows", (long long)g.rows, g.groups, (long long)g.M, (long long)g.N, (long long)g.K,
-                     (long long)units, pipe);
-    return launch_gemm(mode, pipe, p, (int)(units < pairs ? units : pairs), stream, table) == cudaSuccess
-               ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
+        std::fprintf(stderr, "[emu] %s grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld tiles each %d pipe=%d\n",
+                     mode_name(mode), g.sum ? "sum" : "rows", (long long)g.rows, g.groups, (long long)g.M, (long long)g.N,
+                     (long long)g.K, tiles.per, pipe);
+    if (clear_captured_counters(p.counters, (size_t)pairs * 2, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EMU_STATUS_LAUNCH_FAILED;
+    }
+    return launch_gemm(mode, pipe, p, pairs, stream, table) == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }
 static_assert(FUSED_ACT == EPI_ACT && FUSED_GATED == EPI_GATED && FUSED_GATED_BWD == EPI_GATED_BWD, "epilogue kinds");
 

@@ -246,14 +246,32 @@ struct EpiParams {
 // GROUP_SUM   C[g] = op(A)[:, rows of g] op(B)[rows of g, :]: the contraction runs
 //             over the group's rows (both operands MN-major); tile t of the list
 //             of groups is the whole C[g]
-// Whole tiles only: the bounds decide how many there are, and a plan is the host's.
+// How many tiles and stages there are is known on the device alone, so the pairs'
+// walks are worked out there too: whole tiles in turn, or runs of equal length of
+// the stages taken tile by tile.  A run may lie within a tile, so a tile may be cut
+// into several pieces: the pair whose run ends in it without having started in it
+// finishes it and adds the others' sums, which they publish, in their order (the
+// bits depend on the bounds and the device alone).  The other pieces are their
+// pairs' first or only work, so they are there when the last one is; and the runs
+// go to the pairs in reverse, so that a pair waits for pairs of lower index alone,
+// which start no later than it does.
 enum Group : int { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_SUM = 2 };
 
-struct GroupParams {
-    const int4* list;      // {first row, row after the last, group, -} of each row tile (GROUP_ROWS) or group
-    const int* count;      // GROUP_ROWS: row tiles listed
-    long long c_stride;    // GROUP_SUM: from one C[g] to the next
+struct GroupWalk {
+    int first, last, lo, hi;  // as in Walk (hi is clipped to the tile's stages)
+    int step;
+    int others;               // pieces of the last tile that the pairs before this one publish
+    int unused[2];
 };
+
+struct GroupParams {
+    const int4* list;         // {first row, row after the last, group, -} of each row tile (GROUP_ROWS) or group
+    const GroupWalk* walks;   // of each pair
+    long long c_stride;       // GROUP_SUM: from one C[g] to the next
+};
+// k-stages of a group's contraction over its rows (GROUP_SUM: at least one, whose
+// sums are zero, so that the tiles of a group without rows are stored).
+__host__ __device__ __forceinline__ int group_stages(int rows) { return rows > 0 ? (rows - 1) / 32 + 1 : 1; }
 
 struct Params {
     CUtensorMap tmA;  // FP32 op(A): K-major box {32, 128} or MN-major box {32, 32}
@@ -517,11 +535,15 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const Walk& k, int cid,
         const int per = GROUP == GROUP_ROWS ? p.tiles_n : p.tiles_m * p.tiles_n, at = u / per;
         const int4 g = __ldcg(p.group.list + at);
         Unit w;
-        w.piece = 0; w.pieces = 1; w.role = ROLE_TILE; w.slot = 0;
+        w.piece = 0; w.pieces = 1; w.slot = cid;
         w.row0 = g.x; w.row1 = g.y; w.group = g.z;
         w.tile = u - at * per;  // (GROUP_ROWS: the tile's column)
-        w.kb = 0;
-        w.ke = GROUP == GROUP_ROWS ? p.k_stages : (g.y - g.x + BK - 1) / BK;
+        const int stages = GROUP == GROUP_ROWS ? p.k_stages : group_stages(g.y - g.x);
+        const int lo = u == k.first ? k.lo : 0;
+        const int hi = u == k.last - 1 && k.hi < stages ? k.hi : stages;
+        w.kb = stages - hi;
+        w.ke = stages - lo;
+        w.role = lo > 0 ? ROLE_HEAD : hi < stages ? ROLE_TAIL : ROLE_TILE;
         return w;
     }
     if (!p.chain) return unit_of(p, u);
@@ -675,10 +697,15 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         for (int s = 0; s < NB; ++s) { mbar_init(&bcomp_full[s], 1); mbar_init(&bcomp_empty[s], 1); }
         *abort_flag = 0;
         // this pair's walk, worked out once for all roles
-        Walk wk = walk_of(p, static_cast<int>(cid), static_cast<int>(ncl));
-        if constexpr (GROUP == GROUP_ROWS) {
-            griddep_wait();  // the list may be the previous grid's
-            wk.last = __ldcg(p.group.count) * p.tiles_n;
+        Walk wk;
+        if constexpr (GROUP != GROUP_NONE) {
+            griddep_wait();  // the walks may be the previous grid's
+            const int4* at = reinterpret_cast<const int4*>(p.group.walks + cid);
+            const int4 a = __ldcg(at), b = __ldcg(at + 1);
+            wk.first = a.x; wk.last = a.y; wk.lo = a.z; wk.hi = a.w; wk.step = b.x;
+            walk_sh[5] = b.y;
+        } else {
+            wk = walk_of(p, static_cast<int>(cid), static_cast<int>(ncl));
         }
         walk_sh[0] = wk.first; walk_sh[1] = wk.last; walk_sh[2] = wk.step; walk_sh[3] = wk.lo; walk_sh[4] = wk.hi;
         fence_mbar_init();
@@ -914,7 +941,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                 }
             }
             float acc[ACC];
-            if (!STAGED && w.role == ROLE_TAIL) {
+            if (GROUP == GROUP_NONE && !STAGED && w.role == ROLE_TAIL) {
                 // Start from the running sum of the tile's low k-stages, which
                 // the next pair publishes at the start of its run.  Each warp
                 // waits for it on its own; all its loads go out at once,
@@ -969,8 +996,31 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
                            make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
                 __threadfence();
                 named_bar_sync(EPI_BARRIER, NUM_EPI_WARPS * 32);
-                if (e == 0 && lane == 0) epoch_arrive(p.counters + static_cast<size_t>(w.tile) * 2 + rank, p.epoch);
+                if (e == 0 && lane == 0) epoch_arrive(p.counters + static_cast<size_t>(GROUP == GROUP_NONE ? w.tile : static_cast<int>(cid)) * 2 + rank, p.epoch);
                 continue;
+            }
+            if constexpr (GROUP != GROUP_NONE) {
+                // the other pieces' sums, in the order of their pairs
+                const int others = w.role == ROLE_TAIL ? walk_sh[5] : 0;
+                for (int q = 1; q <= others; ++q) {
+                    const unsigned long long* ctr = p.counters + (static_cast<size_t>(cid) - q) * 2 + rank;
+                    if (!warp_wait_epoch(ctr, p.epoch, 1u, abort_flag, budget, 7)) { ok = false; break; }
+                    const float* part = chain_sum(w.slot - q);
+#pragma unroll
+                    for (int j = 0; j < ACC / 4; j += 8) {
+                        float4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(part + (j + i) * 128));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            acc[4 * (j + i)] = __fadd_rn(acc[4 * (j + i)], x[i].x);
+                            acc[4 * (j + i) + 1] = __fadd_rn(acc[4 * (j + i) + 1], x[i].y);
+                            acc[4 * (j + i) + 2] = __fadd_rn(acc[4 * (j + i) + 2], x[i].z);
+                            acc[4 * (j + i) + 3] = __fadd_rn(acc[4 * (j + i) + 3], x[i].w);
+                        }
+                    }
+                }
+                if (!ok) break;
             }
             // Split tiles: a reduce-scatter over the tile's S pieces, which all
             // run at the same time (the plan keeps a tile's pieces in one wave
@@ -981,7 +1031,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             // partial, then the other pieces' in increasing piece order, a fixed
             // order for every chunk -- and stores only those: the result does not
             // depend on timing.
-            const int S = w.pieces;
+            const int S = GROUP == GROUP_NONE ? w.pieces : 1;
             // (gated: chunks c and c + 2 are the gate and the up half of the same
             // columns, and one piece owns both)
             auto owns = [&](int c) {

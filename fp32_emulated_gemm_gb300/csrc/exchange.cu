@@ -15,7 +15,7 @@
 #include <type_traits>
 
 #include "internal.h"
-#include "row_ops.cuh"
+#include "norm_rows.cuh"
 
 namespace emu {
 namespace {
@@ -40,112 +40,190 @@ __device__ __forceinline__ float4 scale4(const float4& v, float w) {
     return make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
 }
 
-// (a slot outside the rows counts as none)
-__device__ __forceinline__ int64_t slot_of(const Exchange& p, int64_t m, int j) {
-    const int32_t s = __ldg(p.slots + m * p.k + j);
-    return (uint32_t)s < (uint32_t)p.rows ? s : -1;
+// A token's slots, T lanes a token: lane j has choice j's, asked for a token ahead
+// so that the rows' loads do not wait for it; choices beyond the lanes are read
+// where they are used.  A slot outside the rows counts as none.
+template <int T> struct Slots {
+    const Exchange& p;
+    int32_t mine, next;
+    float weight, next_weight;
+
+    __device__ __forceinline__ Slots(const Exchange& e, int64_t m) : p(e) { ask(m); }
+    __device__ __forceinline__ void ask(int64_t m) {
+        const int t = threadIdx.x % T;
+        const bool there = m < p.M && t < p.k;
+        next = there ? __ldg(p.slots + m * p.k + t) : -1;
+        next_weight = there && p.weights ? __ldg(p.weights + m * p.k + t) : 1.f;
+    }
+    // To the token asked for, and ask for the next.
+    __device__ __forceinline__ void advance(int64_t m) {
+        mine = next;
+        weight = next_weight;
+        ask(m);
+    }
+    __device__ __forceinline__ int64_t slot(int64_t m, int j) const {
+        int32_t s = __shfl_sync(0xFFFFFFFFu, mine, j % T, T);
+        if (j >= T) s = m < p.M ? __ldg(p.slots + m * p.k + j) : -1;
+        return (uint32_t)s < (uint32_t)p.rows ? s : -1;
+    }
+    __device__ __forceinline__ float of(int64_t m, int j) const {
+        float w = __shfl_sync(0xFFFFFFFFu, weight, j % T, T);
+        if (j >= T) w = m < p.M && p.weights ? __ldg(p.weights + m * p.k + j) : 1.f;
+        return w;
+    }
+};
+
+// Zeros in the rows that have no source: a warp looks at up to 32 rows at a time,
+// fewer where that leaves every warp some (they lie together, behind the others).
+template <bool VEC> __device__ __forceinline__ void clear_rows(const Exchange& p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    int chunk = 32;
+    while (chunk > 1 && 4 * chunk * warps > p.rows) chunk /= 2;
+    for (int64_t base = (blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5)) * chunk; base < p.rows; base += warps * chunk) {
+        unsigned none = __ballot_sync(0xFFFFFFFFu, lane < chunk && base + lane < p.rows && __ldg(p.sources + base + lane) < 0);
+        for (; none; none &= none - 1) {
+            float* row = p.C + (base + __ffs(none) - 1) * p.ldc;
+            for (int64_t c = VEC ? 4 * lane : lane; c < p.N; c += 128)
+                store4<VEC, 32>(row, c, p.N, make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+    }
 }
 
-// Zeros in the rows that have no source.
-template <int T, bool VEC> __device__ __forceinline__ void clear_rows(const Exchange& p) {
-    const int t = threadIdx.x % T;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / T);
-    for (int64_t r = blockIdx.x * (int64_t)(kThreads / T) + threadIdx.x / T; r < p.rows; r += step) {
-        if (__ldg(p.sources + r) >= 0) continue;
-        for (int64_t c = VEC ? 4 * t : t; c < p.N; c += 4 * T)
-            store4<VEC, T>(p.C + r * p.ldc, c, p.N, make_float4(0.f, 0.f, 0.f, 0.f));
-    }
+__device__ __forceinline__ float dot4(const float4& a, const float4& b) {
+    return fmaf(a.x, b.x, a.y * b.y) + fmaf(a.z, b.z, a.w * b.w);
 }
 
 // BWD: scaled by the weights, with their gradients.
 template <int T, int NV, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ Exchange p) {
+    constexpr int kMine = BWD ? (kMaxChoices + T - 1) / T : 1;
     const int t = threadIdx.x % T;
     const int64_t step = (int64_t)gridDim.x * (kThreads / T);
-    for (int64_t base = blockIdx.x * (int64_t)(kThreads / T); base < p.M; base += step) {
-        const int64_t m = base + threadIdx.x / T;
+    int64_t m = blockIdx.x * (int64_t)(kThreads / T) + threadIdx.x / T;
+    Slots<T> slots(p, m);
+    float4 x[NV], ahead[NV];  // the token's row, and its first columns of the next token's
+    auto load = [&](int64_t row, int64_t c0, float4 (&v)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] = load4<VEC, T>(p.A + row * p.lda, c0 + (VEC ? 4 * t : t) + 4 * T * i, row < p.M ? p.N : 0);
+    };
+    load(m, 0, ahead);
+    // (the loop is the same for all lanes of a warp: shuffles)
+    for (int64_t base = blockIdx.x * (int64_t)(kThreads / T); base < p.M; base += step, m += step) {
+        slots.advance(m + step);
         const bool real = m < p.M;
-        float mine[BWD ? kMaxChoices / T + (kMaxChoices % T != 0) : 1] = {};  // lane j % T's sum of choice j
+        float mine[kMine] = {};  // dw of the choices t, t + T, ...
         for (int64_t c0 = 0; c0 < p.N; c0 += 4 * T * NV) {
-            float4 x[NV];
+            const int64_t at = c0 + (VEC ? 4 * t : t);
+            if (c0 == 0) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                x[i] = load4<VEC, T>(p.A + m * p.lda, c0 + (VEC ? 4 * t : t) + 4 * T * i, real ? p.N : 0);
-            for (int j = 0; j < p.k; ++j) {
-                const int64_t s = real ? slot_of(p, m, j) : -1;
-                const int64_t n = s >= 0 ? p.N : 0;
-                if constexpr (!BWD) {
+                for (int i = 0; i < NV; ++i) x[i] = ahead[i];
+                load(m + step, 0, ahead);
+            } else {
+                load(m, c0, x);
+            }
+            for (int j = 0; j < p.k; j += 2) {  // two choices' rows at a time
+                int64_t s[2], n[2];
 #pragma unroll
-                    for (int i = 0; i < NV; ++i)
-                        store4<VEC, T>(p.C + s * p.ldc, c0 + (VEC ? 4 * t : t) + 4 * T * i, n, x[i]);
-                } else {
-                    const float w = s >= 0 ? __ldg(p.weights + m * p.k + j) : 0.f;
-                    float dot = 0.f;
+                for (int q = 0; q < 2; ++q) {
+                    s[q] = j + q < p.k ? slots.slot(m, j + q) : -1;
+                    n[q] = s[q] >= 0 ? p.N : 0;
+                }
+                if constexpr (BWD) {
+                    float4 y[2][NV];
                     if (p.dweights) {
-                        float4 y[NV];
 #pragma unroll
-                        for (int i = 0; i < NV; ++i)
-                            y[i] = load4<VEC, T>(p.R + s * p.ldr, c0 + (VEC ? 4 * t : t) + 4 * T * i, n);
+                        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int i = 0; i < NV; ++i)
-                            dot += fmaf(x[i].x, y[i].x, x[i].y * y[i].y) + fmaf(x[i].z, y[i].z, x[i].w * y[i].w);
+                            for (int i = 0; i < NV; ++i) y[q][i] = load4<VEC, T>(p.R + s[q] * p.ldr, at + 4 * T * i, n[q]);
                     }
                     if (p.C) {
 #pragma unroll
-                        for (int i = 0; i < NV; ++i)
-                            store4<VEC, T>(p.C + s * p.ldc, c0 + (VEC ? 4 * t : t) + 4 * T * i, n, scale4(x[i], w));
+                        for (int q = 0; q < 2; ++q) {
+                            const float w = slots.of(m, j + q < p.k ? j + q : j);
+#pragma unroll
+                            for (int i = 0; i < NV; ++i)
+                                store4<VEC, T>(p.C + s[q] * p.ldc, at + 4 * T * i, n[q], scale4(x[i], w));
+                        }
                     }
                     if (p.dweights) {
+                        float dot[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int o = T / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+                        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int q = 0; q < (int)(sizeof(mine) / sizeof(float)); ++q)
-                            if (j == t + T * q) mine[q] += dot;
+                            for (int i = 0; i < NV; ++i) dot[q] += dot4(x[i], y[q][i]);
+#pragma unroll
+                        for (int o = T / 2; o > 0; o >>= 1)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) dot[q] += __shfl_xor_sync(0xFFFFFFFFu, dot[q], o);
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                if (j + q == t + T * i) mine[i] += dot[q];
                     }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) store4<VEC, T>(p.C + s[q] * p.ldc, at + 4 * T * i, n[q], x[i]);
                 }
             }
         }
         if constexpr (BWD) {
             if (p.dweights && real) {
 #pragma unroll
-                for (int q = 0; q < (int)(sizeof(mine) / sizeof(float)); ++q)
-                    if (t + T * q < p.k) p.dweights[m * p.k + t + T * q] = mine[q];
+                for (int i = 0; i < kMine; ++i)
+                    if (t + T * i < p.k) p.dweights[m * p.k + t + T * i] = mine[i];
             }
         }
     }
-    if (p.C) clear_rows<T, VEC>(p);
+    if (p.C) clear_rows<VEC>(p);
 }
 
 template <int T, int NV, bool VEC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ Exchange p) {
     const int t = threadIdx.x % T;
     const int64_t step = (int64_t)gridDim.x * (kThreads / T);
-    for (int64_t m = blockIdx.x * (int64_t)(kThreads / T) + threadIdx.x / T; m < p.M; m += step) {
+    int64_t m = blockIdx.x * (int64_t)(kThreads / T) + threadIdx.x / T;
+    Slots<T> slots(p, m);
+    for (int64_t base = blockIdx.x * (int64_t)(kThreads / T); base < p.M; base += step, m += step) {
+        slots.advance(m + step);
+        const int64_t real = m < p.M ? p.N : 0;
         for (int64_t c0 = 0; c0 < p.N; c0 += 4 * T * NV) {
-            float4 s[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < p.k; ++j) {
-                const int64_t r = slot_of(p, m, j);
-                const int64_t n = r >= 0 ? p.N : 0;
-                const float w = p.weights ? __ldg(p.weights + m * p.k + j) : 1.f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const float4 v = load4<VEC, T>(p.A + r * p.lda, c0 + (VEC ? 4 * t : t) + 4 * T * i, n);
-                    if (r >= 0)
-                        s[i] = make_float4(fmaf(w, v.x, s[i].x), fmaf(w, v.y, s[i].y), fmaf(w, v.z, s[i].z),
-                                           fmaf(w, v.w, s[i].w));
-                }
-            }
+            const int64_t at = c0 + (VEC ? 4 * t : t);
+            float4 s[NV], r[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int64_t c = c0 + (VEC ? 4 * t : t) + 4 * T * i;
-                if (p.R) {
-                    const float4 q = load4<VEC, T>(p.R + m * p.ldr, c, p.N);
-                    s[i] = make_float4(s[i].x + q.x, s[i].y + q.y, s[i].z + q.z, s[i].w + q.w);
-                }
-                store4<VEC, T>(p.C + m * p.ldc, c, p.N, s[i]);
+                s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                r[i] = p.R ? load4<VEC, T>(p.R + m * p.ldr, at + 4 * T * i, real) : s[i];
             }
+            for (int j = 0; j < p.k; j += 2) {  // two choices' rows at a time, added in order
+                float4 v[2][NV];
+                int64_t row[2];
+                float w[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    row[q] = j + q < p.k ? slots.slot(m, j + q) : -1;
+                    w[q] = slots.of(m, j + q < p.k ? j + q : j);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        v[q][i] = load4<VEC, T>(p.A + row[q] * p.lda, at + 4 * T * i, row[q] >= 0 ? p.N : 0);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (row[q] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        s[i] = make_float4(fmaf(w[q], v[q][i].x, s[i].x), fmaf(w[q], v[q][i].y, s[i].y),
+                                           fmaf(w[q], v[q][i].z, s[i].z), fmaf(w[q], v[q][i].w, s[i].w));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                store4<VEC, T>(p.C + m * p.ldc, at + 4 * T * i, real,
+                               p.R ? make_float4(s[i].x + r[i].x, s[i].y + r[i].y, s[i].z + r[i].z, s[i].w + r[i].w) : s[i]);
         }
     }
 }
@@ -163,6 +241,13 @@ template <class F> void for_width(int64_t N, F f) {
 #undef EMU_WIDTH
 }
 
+// Blocks per SM: what is resident, in turns of equal length; three for a dispatch
+// whose rows are one load, whose writes more of them slow down.  M = 552960, k = 2,
+// N = 256, at the copy rate for the bytes of each pass: dispatch 95% (all
+// resident: 87%), combine with a residual 96%, backward 96%, dispatch's gradient
+// 95%; M = 138241, N = 1024: 88, 91, 101 and 92%; M = 65537, N = 1001 (rows off
+// the 16-byte boundaries), k = 4: 81, 85, 96 and 84%; M = 552960, N = 64, k = 8:
+// 79, 68, 90 and 67%.
 enum Kind { DISPATCH, COMBINE, COMBINE_BWD };
 
 emu_status_t launch(Kind kind, const Exchange& p, emu_stream_t stream) {
@@ -174,13 +259,20 @@ emu_status_t launch(Kind kind, const Exchange& p, emu_stream_t stream) {
     cudaGetLastError();
     for_width(p.N, [&](auto T, auto NV) {
         constexpr int t = decltype(T)::value, nv = decltype(NV)::value;
-        const int64_t groups = (p.M + kThreads / t - 1) / (kThreads / t), most = (int64_t)dev.sm_count * 8;
-        const unsigned grid = (unsigned)(groups < most ? groups : most);
+        const int64_t groups = (p.M + kThreads / t - 1) / (kThreads / t);
+        auto run = [&](auto kernel, int per_sm) {
+            const int64_t most = (int64_t)dev.sm_count * per_sm, turns = (groups + most - 1) / most;
+            kernel<<<(unsigned)((groups + turns - 1) / turns), kThreads, 0, s>>>(p);
+        };
         auto go = [&](auto VEC) {
             constexpr bool v = decltype(VEC)::value;
-            if (kind == DISPATCH) dispatch_kernel<t, nv, v, false><<<grid, kThreads, 0, s>>>(p);
-            else if (kind == COMBINE) combine_kernel<t, nv, v><<<grid, kThreads, 0, s>>>(p);
-            else dispatch_kernel<t, nv, v, true><<<grid, kThreads, 0, s>>>(p);
+            constexpr auto dispatch = dispatch_kernel<t, nv, v, false>, back = dispatch_kernel<t, nv, v, true>;
+            constexpr auto combine = combine_kernel<t, nv, v>;
+            static const int resident[3] = {resident_blocks(dispatch, kThreads), resident_blocks(combine, kThreads),
+                                            resident_blocks(back, kThreads)};
+            if (kind == DISPATCH) run(dispatch, p.N <= 512 && resident[DISPATCH] > 3 ? 3 : resident[DISPATCH]);
+            else if (kind == COMBINE) run(combine, resident[COMBINE]);
+            else run(back, resident[COMBINE_BWD]);
         };
         if (vec) go(std::true_type{}); else go(std::false_type{});
     });

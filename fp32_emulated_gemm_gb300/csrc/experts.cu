@@ -14,9 +14,9 @@
 
 #include "activation.cuh"
 #include "aligned.cuh"
+#include "emu_kernel.cuh"
 #include "few_rows.h"
 #include "internal.h"
-#include "ptx.cuh"
 
 namespace emu {
 namespace {
@@ -26,12 +26,47 @@ constexpr int kMaxExperts = 1024, kTileRows = 256;
 // The experts' row blocks (of `block` rows at most) and their bounds, from the
 // offsets, which are taken as ascending and within the rows: what breaks that
 // gets no rows, and nothing outside them is read or written.
-// list[i] = {first row, row after the last, expert, 0}; groups[e] likewise, the
-// experts of the most rows first, so that the long sums start first.
+// blocks[i] = {first row, row after the last, expert, 0}; groups[e] likewise, the
+// experts of the most rows first, so that whole tiles taken in turn leave the
+// short ones for the end.
 struct Lists { int4 *blocks, *groups; int* count; };
 
-__global__ void __launch_bounds__(kMaxExperts) list_kernel(const int32_t* offsets, int E, int rows, int block, Lists out) {
+// The walks of the CTA pairs of up to four products (GroupWalk).
+constexpr int kMaxProducts = 4;
+struct Walks {
+    int n, pairs;
+    GroupWalk* out;               // n x pairs
+    bool sum[kMaxProducts];
+    GroupedTiles tiles[kMaxProducts];
+};
+
+// A product's tiles in turn, or equal runs of its stages: what is predicted faster
+// for the longest of the pairs, in stages.  A tile's stores cost 3, publishing a
+// piece 1.5 and adding one 2 (measured: see the products' host side).
+__device__ bool cut_tiles(bool sum, GroupedTiles tiles, int entries, const int4* groups, int64_t total, int pairs) {
+    const int64_t n = (int64_t)entries * tiles.per, waves = (n + pairs - 1) / pairs;
+    if (total < 2 * pairs) return false;
+    const float run = (float)((total + pairs - 1) / pairs);
+    int longest = tiles.stages;
+    float whole = 0.f;
+    if (sum) {
+        longest = group_stages(groups[0].y - groups[0].x);
+        // (the first pair's tiles are the longest of each wave)
+        for (int64_t w = 0; w < waves && whole <= 4.f * (run + longest) + 100.f; ++w) {
+            const int4 g = groups[w * pairs / tiles.per];
+            whole += group_stages(g.y - g.x) + 3.f;
+        }
+    } else {
+        whole = (float)waves * (longest + 3.f);
+    }
+    return 1.03f * (run + 3.f * (float)waves + 1.5f + 2.f * ceilf(longest / run)) < whole;
+}
+
+__global__ void __launch_bounds__(kMaxExperts)
+list_kernel(const int32_t* offsets, int E, int rows, int block, Lists out, const __grid_constant__ Walks walks) {
     __shared__ int32_t first[kMaxExperts + 1], start[kMaxExperts + 1], sums[32];
+    __shared__ int4 sorted[kMaxExperts];
+    __shared__ int cut[kMaxProducts];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     griddep_launch_dependents();
     auto scan = [&](int v, bool largest) {  // inclusive, over the block
@@ -64,43 +99,111 @@ __global__ void __launch_bounds__(kMaxExperts) list_kernel(const int32_t* offset
     if (t == 0) first[0] = begin;
     __syncthreads();
     const int r0 = t < E ? first[t] : 0, r1 = t < E ? first[t + 1] : 0, n = r1 - r0;
+    int blocks_total = 0;
+    if (out.blocks) {
+        const int tiles = (n + block - 1) / block, at = scan(tiles, false);
+        if (t < E) start[t + 1] = at;
+        if (t == 0) start[0] = 0;
+        __syncthreads();
+        blocks_total = start[E];
+        if (t == 0) *out.count = blocks_total;
+        for (int i = t; i < blocks_total; i += kMaxExperts) {
+            int lo = 0, hi = E - 1;  // the expert whose blocks hold i: start[e] <= i < start[e + 1]
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (start[mid + 1] <= i) lo = mid + 1; else hi = mid;
+            }
+            const int b0 = first[lo] + (i - start[lo]) * block;
+            out.blocks[i] = make_int4(b0, min(b0 + block, first[lo + 1]), lo, 0);
+        }
+        __syncthreads();
+    }
     if (out.groups) {
         int rank = 0;
         for (int e = 0; e < E; ++e) {
             const int m = first[e + 1] - first[e];
             rank += m > n || (m == n && e < t);
         }
-        if (t < E) out.groups[rank] = make_int4(r0, r1, t, 0);
+        if (t < E) out.groups[rank] = sorted[rank] = make_int4(r0, r1, t, 0);
+        __syncthreads();
+        // start[i]: stages of the first i of the sorted experts
+        const int at = scan(t < E ? group_stages(sorted[t].y - sorted[t].x) : 0, false);
+        if (t < E) start[t + 1] = at;
+        if (t == 0) start[0] = 0;
+        __syncthreads();
     }
-    if (!out.blocks) return;
-    const int tiles = (n + block - 1) / block, at = scan(tiles, false);
-    if (t < E) start[t + 1] = at;
-    if (t == 0) start[0] = 0;
+    auto entries = [&](int k) { return walks.sum[k] ? E : blocks_total; };
+    auto total = [&](int k) {
+        const int64_t per = walks.tiles[k].per;
+        return walks.sum[k] ? per * start[E] : per * blocks_total * walks.tiles[k].stages;
+    };
+    if (t < walks.n)
+        cut[t] = cut_tiles(walks.sum[t], walks.tiles[t], entries(t), sorted, total(t), walks.pairs);
     __syncthreads();
-    const int total = start[E];
-    if (t == 0) *out.count = total;
-    for (int i = t; i < total; i += kMaxExperts) {
-        int lo = 0, hi = E - 1;  // the expert whose blocks hold i: start[e] <= i < start[e + 1]
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (start[mid + 1] <= i) lo = mid + 1; else hi = mid;
+    for (int i = t; i < walks.n * walks.pairs; i += kMaxExperts) {
+        const int k = i / walks.pairs, pair = i - k * walks.pairs;
+        const GroupedTiles tiles = walks.tiles[k];
+        GroupWalk w{};
+        w.hi = INT32_MAX;
+        if (!cut[k]) {
+            w.first = pair;
+            w.last = entries(k) * tiles.per;
+            w.step = walks.pairs;
+        } else {
+            const int64_t U = total(k);
+            const int run = walks.pairs - 1 - pair;
+            const int64_t s = run * U / walks.pairs, e = (run + 1) * U / walks.pairs;
+            // the tile at position x, its first position and its stages
+            auto tile_at = [&](int64_t x, int64_t& base, int& stages) {
+                if (!walks.sum[k]) {
+                    stages = tiles.stages;
+                    const int64_t tile = x / stages;
+                    base = tile * stages;
+                    return (int)tile;
+                }
+                int lo = 0, hi = E - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if ((int64_t)start[mid + 1] * tiles.per <= x) lo = mid + 1; else hi = mid;
+                }
+                stages = start[lo + 1] - start[lo];
+                base = (int64_t)start[lo] * tiles.per;
+                const int64_t j = (x - base) / stages;
+                base += j * stages;
+                return lo * tiles.per + (int)j;
+            };
+            int64_t base;
+            int stages;
+            w.first = tile_at(s, base, stages);
+            w.lo = (int)(s - base);
+            w.last = tile_at(e - 1, base, stages) + 1;
+            w.hi = (int)(e - base);
+            w.step = 1;
+            // the next runs that start within the last tile
+            for (int r = run + 1; r < walks.pairs && r * U / walks.pairs < base + stages; ++r) ++w.others;
         }
-        const int b0 = first[lo] + (i - start[lo]) * block;
-        out.blocks[i] = make_int4(b0, min(b0 + block, first[lo + 1]), lo, 0);
+        walks.out[i] = w;
     }
 }
 
 int64_t most_blocks(int64_t rows, int E, int block) { return rows / block + (rows < E ? rows : E); }
 
-// Buffer for the lists: the count, then the blocks, then the groups.
-size_t list_floats(int64_t rows, int E, int block) { return 4 * (size_t)(1 + most_blocks(rows, E, block) + E); }
-Lists lists_at(float* base, int64_t rows, int E, int block, bool blocks, bool groups) {
-    int4* p = reinterpret_cast<int4*>(base);
-    return {blocks ? p + 1 : nullptr, groups ? p + 1 + most_blocks(rows, E, block) : nullptr, reinterpret_cast<int*>(p)};
+// Buffer for the lists: the count, the blocks, the groups, the walks.
+size_t list_floats(int64_t rows, int E, int block, int walks) {
+    return 4 * (size_t)(1 + most_blocks(rows, E, block) + E) + walks * (sizeof(GroupWalk) / sizeof(float));
 }
-cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, int block, const Lists& out, cudaStream_t s) {
+struct Listed {
+    Lists lists;
+    GroupWalk* walks;
+};
+Listed lists_at(float* base, int64_t rows, int E, int block, bool blocks, bool groups) {
+    int4 *p = reinterpret_cast<int4*>(base), *g = p + 1 + most_blocks(rows, E, block);
+    return {{blocks ? p + 1 : nullptr, groups ? g : nullptr, reinterpret_cast<int*>(p)}, reinterpret_cast<GroupWalk*>(g + E)};
+}
+cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, int block, const Lists& out, const Walks& walks,
+                         cudaStream_t s) {
     cudaGetLastError();
-    list_kernel<<<1, kMaxExperts, 0, s>>>(offsets, E, (int)rows, block, out);
+    list_kernel<<<1, kMaxExperts, 0, s>>>(offsets, E, (int)rows, block, out, walks);
     return cudaGetLastError();
 }
 
@@ -110,6 +213,57 @@ bool few(int64_t rows, int E) { return rows <= 4 * (int64_t)E; }
 int few_block_rows(int64_t rows, int E) { return 4 * rows <= E ? 1 : rows <= E ? 2 : rows <= 3 * (int64_t)E ? 4 : 8; }
 
 bool size_ok(int64_t v) { return v <= INT32_MAX - 256; }
+
+// A call's grouped products, one after the other, with one launch for the lists and
+// walks of all of them.
+struct Products {
+    emu_mode_t mode;
+    int64_t rows;
+    int E, n = 0;
+    bool blocks = false, groups = false;
+    GroupedGemm g[kMaxProducts];
+
+    Products(emu_mode_t m, int64_t r, int e) : mode(m), rows(r), E(e) {}
+    void add(const GroupedGemm& p) {
+        (p.sum ? groups : blocks) = true;
+        g[n++] = p;
+    }
+    emu_status_t run(cudaStream_t s, Until until) const {
+        for (int i = 0; i < n; ++i) EMU_TRY(gemm_grouped(mode, g[i], s, until));
+        return EMU_STATUS_SUCCESS;
+    }
+    emu_status_t launch(const int32_t* offsets, const Listed& l, int pairs, cudaStream_t s) {
+        Walks w{n, pairs, l.walks, {}, {}};
+        for (int i = 0; i < n; ++i) {
+            w.sum[i] = g[i].sum;
+            w.tiles[i] = grouped_tiles(g[i]);
+            g[i].list = g[i].sum ? l.lists.groups : l.lists.blocks;
+            g[i].walks = l.walks + (int64_t)i * pairs;
+        }
+        EMU_TRY(launched(launch_lists(offsets, E, rows, kTileRows, l.lists, w, s)));
+        return run(s, UNTIL_LAUNCHED);
+    }
+};
+
+// In steps: the arguments' checks, the buffers, then the copies of odd operands,
+// the lists and the products.  make() gives the products with the operands'
+// addresses as they are at the time.
+template <class F> emu_status_t run_products(Aligned& al, F make, const int32_t* offsets, cudaStream_t s) {
+    al.stand_in();
+    Products q = make();
+    EMU_TRY(q.run(s, UNTIL_CHECKED));
+    DeviceCtx dev;
+    EMU_TRY(current_device(&dev));
+    EMU_TRY(al.reserve(s));
+    EMU_TRY(q.run(s, UNTIL_RESERVED));
+    int pairs = 0;
+    EMU_TRY(grouped_pairs(q.mode, &pairs));
+    float* scratch = nullptr;
+    EMU_TRY(reduce_scratch(dev.id, s, list_floats(q.rows, q.E, kTileRows, q.n * pairs), &scratch));
+    EMU_TRY(launched(al.launch(s)));
+    q = make();
+    return q.launch(offsets, lists_at(scratch, q.rows, q.E, kTileRows, q.blocks, q.groups), pairs, s);
+}
 
 }  // namespace
 }  // namespace emu
@@ -138,9 +292,9 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     if (few(rows, E)) {
         const int block = few_block_rows(rows, E);
         EMU_TRY(current_device(&dev));
-        EMU_TRY(reduce_scratch(dev.id, s, list_floats(rows, E, block), &scratch));
-        const Lists l = lists_at(scratch, rows, E, block, true, false);
-        EMU_TRY(launched(launch_lists(offsets, E, rows, block, l, s)));
+        EMU_TRY(reduce_scratch(dev.id, s, list_floats(rows, E, block, 0), &scratch));
+        const Lists l = lists_at(scratch, rows, E, block, true, false).lists;
+        EMU_TRY(launched(launch_lists(offsets, E, rows, block, l, Walks{}, s)));
         FewRows p{(int)rows, F, K, X, ldx, W_in, ldwi, nullptr, nullptr, 0, D, ldd, H, ldh, act_params(act)};
         p.list = l.blocks;
         p.count = l.count;
@@ -155,23 +309,14 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     al.add(X, ldx, rows, K);
     al.add(W_in, ldwi, E * 2 * F, K);
     al.add(W_out, ldwo, E * N, F);
-    Lists l{};
-    auto products = [&](Until until) {
-        const Fused f{FUSED_GATED, act, nullptr, 0, D, ldd, nullptr};
-        GroupedGemm g{false, E, false, rows, 0, F, K, X, ldx, W_in, ldwi, H, ldh, &f, l.blocks, l.count};
-        EMU_TRY(gemm_grouped(mode, g, s, until));
-        g = {false, E, false, rows, 0, N, F, H, ldh, W_out, ldwo, Y, ldy, nullptr, l.blocks, l.count};
-        return gemm_grouped(mode, g, s, until);
+    const Fused f{FUSED_GATED, act, nullptr, 0, D, ldd, nullptr};
+    auto products = [&] {
+        Products q(mode, rows, E);
+        q.add({false, E, false, rows, 0, F, K, X, ldx, W_in, ldwi, H, ldh, &f});
+        q.add({false, E, false, rows, 0, N, F, H, ldh, W_out, ldwo, Y, ldy});
+        return q;
     };
-    al.stand_in();
-    EMU_TRY(products(UNTIL_CHECKED));
-    EMU_TRY(current_device(&dev));
-    EMU_TRY(al.reserve(s));
-    EMU_TRY(reduce_scratch(dev.id, s, list_floats(rows, E, kTileRows), &scratch));
-    l = lists_at(scratch, rows, E, kTileRows, true, false);
-    EMU_TRY(launched(al.launch(s)));
-    EMU_TRY(launched(launch_lists(offsets, E, rows, kTileRows, l, s)));
-    return products(UNTIL_LAUNCHED);
+    return run_products(al, products, offsets, s);
 }
 
 emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K, int64_t F, int64_t N, const float* dY,
@@ -209,37 +354,17 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
     if (dX) al.add(W_in, ldwi, E * 2 * F, K);
     if (dW_in) al.add(X, ldx, rows, K);
     if (dW_out) al.add(H, ldh, rows, F);
-    Lists l{};
-    auto products = [&](Until until) {
-        if (inner) {
-            const Fused f{FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, nullptr};
-            const GroupedGemm g{false, E, true, rows, 0, F, N, dY, lddy, W_out, ldwo, dZ, lddz, &f, l.blocks, l.count};
-            EMU_TRY(gemm_grouped(mode, g, s, until));
-        }
-        if (dW_out) {
-            const GroupedGemm g{true, E, true, rows, N, F, 0, dY, lddy, H, ldh, dW_out, lddwo, nullptr, l.groups, nullptr};
-            EMU_TRY(gemm_grouped(mode, g, s, until));
-        }
-        if (dX) {
-            const GroupedGemm g{false, E, true, rows, 0, K, 2 * F, dZ, lddz, W_in, ldwi, dX, lddx, nullptr, l.blocks, l.count};
-            EMU_TRY(gemm_grouped(mode, g, s, until));
-        }
-        if (dW_in) {
-            const GroupedGemm g{true, E, true, rows, 2 * F, K, 0, dZ, lddz, X, ldx, dW_in, lddwi, nullptr, l.groups, nullptr};
-            EMU_TRY(gemm_grouped(mode, g, s, until));
-        }
-        return EMU_STATUS_SUCCESS;
+    Fused f{};
+    auto products = [&] {
+        f = {FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, nullptr};
+        Products q(mode, rows, E);
+        if (inner) q.add({false, E, true, rows, 0, F, N, dY, lddy, W_out, ldwo, dZ, lddz, &f});
+        if (dW_out) q.add({true, E, true, rows, N, F, 0, dY, lddy, H, ldh, dW_out, lddwo});
+        if (dX) q.add({false, E, true, rows, 0, K, 2 * F, dZ, lddz, W_in, ldwi, dX, lddx});
+        if (dW_in) q.add({true, E, true, rows, 2 * F, K, 0, dZ, lddz, X, ldx, dW_in, lddwi});
+        return q;
     };
-    al.stand_in();
-    EMU_TRY(products(UNTIL_CHECKED));
-    EMU_TRY(current_device(&dev));
-    EMU_TRY(al.reserve(s));
-    float* scratch = nullptr;
-    EMU_TRY(reduce_scratch(dev.id, s, list_floats(rows, E, kTileRows), &scratch));
-    l = lists_at(scratch, rows, E, kTileRows, inner, dW_in || dW_out);
-    EMU_TRY(launched(al.launch(s)));
-    EMU_TRY(launched(launch_lists(offsets, E, rows, kTileRows, l, s)));
-    return products(UNTIL_LAUNCHED);
+    return run_products(al, products, offsets, s);
 }
 
 }  // extern "C"

@@ -104,8 +104,14 @@ struct GroupedGemm {
     int64_t ldc;      // sum: C[g] starts g M ldc after C
     const Fused* fused = nullptr;  // rows: FUSED_GATED (N is F, B[g] has 2F rows) or FUSED_GATED_BWD
     const int4* list = nullptr;    // the groups' tiles or bounds, on the device (Params::group)
-    const int* count = nullptr;
+    const void* walks = nullptr;   // each pair's GroupWalk, on the device
 };
+// How its pairs' walks are worked out (see experts.cu): tiles for each entry of the
+// list, and a tile's k-stages (0: the group's).
+struct GroupedTiles { int per, stages; };
+GroupedTiles grouped_tiles(const GroupedGemm& g);
+// CTA pairs that a grouped product runs on.
+emu_status_t grouped_pairs(emu_mode_t mode, int* pairs);
 emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t stream, Until until);
 
 }  // namespace emu

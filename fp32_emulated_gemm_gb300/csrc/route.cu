@@ -15,10 +15,13 @@
 // histogram for each block of tokens; then every block adds up the histograms
 // (of the blocks before it and of all), and places its own choices, ranked among
 // their warp's by matching lanes.  Sums of integers alone: no order to depend on.
+// M = 552960, E = 16, k = 2 (forward 53 MB, backward 49): 25.8 and 10.5 us, 7.8 and
+// 7.2 at the copy rate; the choice is bound by its instructions, the sort by its
+// two passes over the choices and the scattered words of `sources`.
 #include <cuda_runtime.h>
 
 #include "internal.h"
-#include "ptx.cuh"
+#include "norm_rows.cuh"
 
 namespace emu {
 namespace {
@@ -35,8 +38,10 @@ struct Route {
     int32_t* experts;        // M k (sort alone: read)
     float* weights;          // M k
     int32_t *slots, *sources, *offsets;
-    int32_t* hist;           // blocks x E
-    int64_t rows_per;        // tokens of a block
+    int32_t* hist;           // choosing blocks x E
+    int hists;
+    int64_t rows_per;        // tokens of a choosing block
+    int per_place;           // choosing blocks whose choices a placing block has
 };
 
 // Logits as integers in their order; NaN above all (it shows in the weight), +0
@@ -51,9 +56,98 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key);
 }
 
-// The choices and weights of the block's tokens, T lanes a token, which hold V
-// logits each (e = lane + T i).  T >= k: lane j keeps choice j.
-template <int T, int V> __device__ __forceinline__ void choose(const Route& p, int64_t r0, int64_t r1, int32_t* hist) {
+// The choices and weights of the block's tokens [r0, r1), T lanes a token (1 or 8):
+// each goes through its share of the logits with the K (>= k) largest so far in
+// order; the lanes' lists are then merged choice by choice.
+template <int K, int T> __device__ __forceinline__ void choose_lists(const Route& p, int64_t r0, int64_t r1, int32_t* hist) {
+    const bool vec = (p.E & 3) == 0 && (p.ldl & 3) == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0;
+    const int t = threadIdx.x % T;
+    for (int64_t base = r0; base < r1; base += kThreads / T) {
+        const int64_t m = base + threadIdx.x / T;
+        const bool real = m < r1;
+        const float* row = p.logits + (real ? m : r0) * p.ldl;
+        uint32_t key[K];
+        int at[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) { key[j] = kClosed; at[j] = -1; }  // (a closed logit is not above it)
+        auto insert = [&](float v, int e) {
+            const uint32_t x = order_key(v);
+            if (x <= key[K - 1]) return;
+#pragma unroll
+            for (int j = K - 1; j > 0; --j) {
+                if (x > key[j - 1]) { key[j] = key[j - 1]; at[j] = at[j - 1]; }
+                else if (x > key[j]) { key[j] = x; at[j] = e; }
+            }
+            if (x > key[0]) { key[0] = x; at[0] = e; }
+        };
+        if (vec) {
+#pragma unroll 4
+            for (int e = 4 * t; e < p.E; e += 4 * T) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(row + e));
+                insert(v.x, e);
+                insert(v.y, e + 1);
+                insert(v.z, e + 2);
+                insert(v.w, e + 3);
+            }
+        } else {
+#pragma unroll 8
+            for (int e = t; e < p.E; e += T) insert(__ldg(row + e), e);
+        }
+        if constexpr (T > 1) {
+            // the lists' first elements: the largest, then the lowest index; its lane
+            // moves on
+            uint32_t out_key[K];
+            int out_at[K];
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                uint32_t best = key[0];
+                int e = at[0];
+#pragma unroll
+                for (int o = T / 2; o > 0; o >>= 1) {
+                    const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+                    const int f = __shfl_xor_sync(0xFFFFFFFFu, e, o);
+                    if (b > best || (b == best && f < e)) { best = b; e = f; }
+                }
+                out_key[j] = best;
+                out_at[j] = e;
+                if (at[0] == e) {
+#pragma unroll
+                    for (int i = 0; i + 1 < K; ++i) { key[i] = key[i + 1]; at[i] = at[i + 1]; }
+                    key[K - 1] = kClosed;
+                    at[K - 1] = -1;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < K; ++j) { key[j] = out_key[j]; at[j] = out_at[j]; }
+        }
+        const float top = at[0] >= 0 ? key_value(key[0]) : 0.f;
+        float w[K], total = 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            w[j] = at[j] >= 0 ? expf(key_value(key[j]) - top) : 0.f;
+            if (j < p.k) total += w[j];
+        }
+        if (p.over_all) {
+            total = 0.f;
+#pragma unroll 4
+            for (int e = t; e < p.E; e += T) total += expf(__ldg(row + e) - top);  // (exp(-inf) = 0)
+#pragma unroll
+            for (int o = T / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        }
+        if (!real) continue;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (j < p.k && j % T == t) {
+                p.experts[m * p.k + j] = at[j];
+                p.weights[m * p.k + j] = at[j] >= 0 ? w[j] / total : 0.f;
+                if (at[j] >= 0) atomicAdd(&hist[at[j]], 1);
+            }
+    }
+}
+
+// Likewise with T lanes a token, which hold V logits each (e = lane + T i) and find
+// the choices one by one.  T >= k: lane j keeps choice j.
+template <int T, int V> __device__ __forceinline__ void choose_lanes(const Route& p, int64_t r0, int64_t r1, int32_t* hist) {
     const int t = threadIdx.x % T;
     for (int64_t base = r0; base < r1; base += kThreads / T) {
         const int64_t m = base + threadIdx.x / T;
@@ -106,20 +200,36 @@ template <int T, int V> __device__ __forceinline__ void choose(const Route& p, i
     }
 }
 
-// T and V for E experts: few lanes, so that a warp has many tokens and little to
-// exchange, but at least a lane for each choice.
-#define EMU_LANES(T, V) choose<T, V>(p, r0, r1, hist)
-__device__ __forceinline__ void choose_any(const Route& p, int64_t r0, int64_t r1, int32_t* hist) {
-    const int lanes = p.k > (p.E + 3) / 4 ? p.k : (p.E + 3) / 4;
-    if (lanes <= 4) EMU_LANES(4, 4);
-    else if (lanes <= 8) EMU_LANES(8, 4);
-    else if (lanes <= 16) EMU_LANES(16, 4);
-    else if (p.E <= 128) EMU_LANES(32, 4);
-    else if (p.E <= 256) EMU_LANES(32, 8);
-    else if (p.E <= 512) EMU_LANES(32, 16);
-    else EMU_LANES(32, 32);
+// Which of the two, and its sizes (a kernel each: what holds 32 logits a thread
+// would cost the others their occupancy).
+enum Way { SORT, LIST_1, LIST_2, LIST_4, LIST_8, SHARED_1, SHARED_2, SHARED_4, SHARED_8, LANES_4, LANES_8, LANES_16, LANES_32 };
+template <int WAY> __device__ __forceinline__ void choose(const Route& p, int64_t r0, int64_t r1, int32_t* hist) {
+    if constexpr (WAY == SORT) {
+        for (int64_t c = r0 * p.k + threadIdx.x; c < r1 * p.k; c += kThreads) {
+            const int e = p.experts[c];
+            if ((unsigned)e < (unsigned)p.E) atomicAdd(&hist[e], 1);
+        }
+    } else if constexpr (WAY < SHARED_1) {
+        choose_lists<1 << (WAY - LIST_1), 1>(p, r0, r1, hist);
+    } else if constexpr (WAY < LANES_4) {
+        choose_lists<1 << (WAY - SHARED_1), 8>(p, r0, r1, hist);
+    } else {
+        choose_lanes<32, 4 << (WAY - LANES_4)>(p, r0, r1, hist);
+    }
 }
-#undef EMU_LANES
+constexpr int tokens_of(int way) { return way < SHARED_1 ? kThreads : way < LANES_4 ? kThreads / 8 : kThreads / 32; }
+// A lane a token needs the fewest instructions, which bound it, and many tokens;
+// with few, eight lanes share the wait for one.  Route and sort, a lane / eight:
+// M = 552960, E = 16, k = 2 25.8 / 57 us (one lane for all four of 16 logits and a
+// search of them for each choice: 49 us); 138240, 64, 8 56 / 80; 34560, 256, 8 55 /
+// 66; 6144, 64, 8 25 / 12; 8000, 1024, 4 91 / 43; 1000, 128, 8 35 / 12.8.  Lists of
+// more than eight would not fit a lane's registers; there a search for each choice
+// takes a warp a token.
+constexpr int64_t kSharedTokens = 20000;
+Way way_of(int64_t M, int E, int k) {
+    if (k <= 8) return Way((M < kSharedTokens ? SHARED_1 : LIST_1) + (k == 1 ? 0 : k == 2 ? 1 : k <= 4 ? 2 : 3));
+    return E <= 128 ? LANES_4 : E <= 256 ? LANES_8 : E <= 512 ? LANES_16 : LANES_32;
+}
 
 // Where the block's choices [c0, c1) go.  `count[w][e]` becomes the next row of
 // expert e for warp w; `first[e]` comes with the row of the block's first choice
@@ -131,6 +241,7 @@ __device__ __forceinline__ void place(const Route& p, int64_t c0, int64_t c1, co
     int32_t* mine = count + warp * p.E;
     for (int i = threadIdx.x; i < kWarps * p.E; i += kThreads) count[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int64_t c = w0 + lane; c < w1; c += 32) {
         const int e = p.experts[c];
         if ((unsigned)e < (unsigned)p.E) atomicAdd(&mine[e], 1);
@@ -145,9 +256,11 @@ __device__ __forceinline__ void place(const Route& p, int64_t c0, int64_t c1, co
         }
     }
     __syncthreads();
+    int next = w0 + lane < w1 ? p.experts[w0 + lane] : -1;
     for (int64_t c = w0; c < w1; c += 32) {
         const int64_t i = c + lane;
-        int e = i < w1 ? p.experts[i] : -1;
+        int e = next;
+        next = i + 32 < w1 ? p.experts[i + 32] : -1;
         if ((unsigned)e >= (unsigned)p.E) e = -1;
         const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
         const int rank = __popc(same & ((1u << lane) - 1u));
@@ -188,21 +301,13 @@ __device__ __forceinline__ void exclusive_sums(const int32_t* total, int32_t* st
 // Shared memory of a block: histogram, starts and the warps' counts.
 size_t smem_of(int E) { return (size_t)((kWarps + 2) * E + 1) * sizeof(int32_t); }
 
-// Choices (or, SORT, their histogram alone) of the block's tokens.
-template <bool SORT> __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ Route p) {
+template <int WAY> __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ Route p) {
     extern __shared__ int32_t sh[];
     if (threadIdx.x == 0) griddep_launch_dependents();
     const int64_t r0 = blockIdx.x * p.rows_per, r1 = r0 + p.rows_per < p.M ? r0 + p.rows_per : p.M;
     for (int e = threadIdx.x; e < p.E; e += kThreads) sh[e] = 0;
     __syncthreads();
-    if constexpr (SORT) {
-        for (int64_t c = r0 * p.k + threadIdx.x; c < r1 * p.k; c += kThreads) {
-            const int e = p.experts[c];
-            if ((unsigned)e < (unsigned)p.E) atomicAdd(&sh[e], 1);
-        }
-    } else {
-        choose_any(p, r0, r1, sh);
-    }
+    choose<WAY>(p, r0, r1, sh);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += kThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = sh[e];
 }
@@ -213,14 +318,23 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const __grid_constant__
     for (int e = threadIdx.x; e < p.E; e += kThreads) { total[e] = 0; before[e] = 0; }
     __syncthreads();
     griddep_wait();
-    // the threads share the histograms: expert by expert within a row of them
-    const int64_t n = (int64_t)gridDim.x * p.E, mine = (int64_t)blockIdx.x * p.E;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int32_t h = p.hist[i];
-        if (h == 0) continue;
-        const int e = (int)(i % p.E);
-        atomicAdd(&total[e], h);
-        if (i < mine) atomicAdd(&before[e], h);
+    // the threads share the histograms: some threads an expert, a sum each
+    const int parts = p.E < kThreads ? kThreads / p.E : 1, wide = kThreads / parts;
+    const int mine = blockIdx.x * p.per_place;
+    for (int e = threadIdx.x % wide, part = threadIdx.x / wide; e < p.E && part < parts; e += wide) {
+        int32_t all = 0, ahead = 0;
+        for (int b = part; b < p.hists; b += 16 * parts) {  // sixteen loads at a time
+            int32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = b + i * parts < p.hists ? __ldcg(p.hist + (int64_t)(b + i * parts) * p.E + e) : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                all += h[i];
+                if (b + i * parts < mine) ahead += h[i];
+            }
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], ahead);
     }
     __syncthreads();
     exclusive_sums(total, start, p.E);
@@ -231,25 +345,18 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const __grid_constant__
         p.sources[i] = -1;
     for (int e = threadIdx.x; e < p.E; e += kThreads) total[e] = start[e] + before[e];
     __syncthreads();
-    const int64_t r0 = blockIdx.x * p.rows_per, r1 = r0 + p.rows_per < p.M ? r0 + p.rows_per : p.M;
+    const int64_t per = p.per_place * p.rows_per, r0 = blockIdx.x * per, r1 = r0 + per < p.M ? r0 + per : p.M;
     place(p, r0 * p.k, r1 * p.k, total, count);
 }
 
 // A few tokens: one block does both.
-template <bool SORT> __global__ void __launch_bounds__(kThreads) route_small_kernel(const __grid_constant__ Route p) {
+template <int WAY> __global__ void __launch_bounds__(kThreads) route_small_kernel(const __grid_constant__ Route p) {
     extern __shared__ int32_t sh[];
     int32_t *total = sh, *start = sh + p.E, *count = start + p.E + 1;
     for (int e = threadIdx.x; e < p.E; e += kThreads) total[e] = 0;
     __syncthreads();
     const int64_t C = p.M * p.k;
-    if constexpr (SORT) {
-        for (int64_t c = threadIdx.x; c < C; c += kThreads) {
-            const int e = p.experts[c];
-            if ((unsigned)e < (unsigned)p.E) atomicAdd(&total[e], 1);
-        }
-    } else {
-        choose_any(p, 0, p.M, total);
-    }
+    choose<WAY>(p, 0, p.M, total);
     __syncthreads();
     exclusive_sums(total, start, p.E);
     for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = start[e];
@@ -257,7 +364,8 @@ template <bool SORT> __global__ void __launch_bounds__(kThreads) route_small_ker
     place(p, 0, C, start, count);
 }
 
-// dlogits, T lanes a token (T >= k: lane j holds choice j).
+// dlogits: a thread has eight columns of a token and works out the token's sum for
+// itself (the choices' words are few, and in L1 for all but the first of them).
 struct RouteBwd {
     int64_t M;
     int E, k;
@@ -269,83 +377,104 @@ struct RouteBwd {
     float* dlogits;
     int64_t lddl;
 };
-template <int T> __global__ void __launch_bounds__(256) route_bwd_kernel(const __grid_constant__ RouteBwd p) {
-    const int t = threadIdx.x % T;
-    const int64_t step = (int64_t)gridDim.x * (256 / T);
-    for (int64_t base = blockIdx.x * (int64_t)(256 / T); base < p.M; base += step) {
-        const int64_t m = base + threadIdx.x / T;
-        const bool real = m < p.M;
-        int e = -1;
-        float g = 0.f, w = 0.f;
-        if (real && t < p.k) {
-            e = p.experts[m * p.k + t];
-            w = p.weights[m * p.k + t];
-            if (e >= 0) g = w * p.dweights[m * p.k + t];
-        }
-        float inner = g;
+template <bool VEC, int K> __global__ void __launch_bounds__(256) route_bwd_kernel(const __grid_constant__ RouteBwd p) {
+    constexpr int C = 8;
+    const uint32_t quads = (p.E + C - 1) / C;
+    const int64_t n = p.M * quads, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += step) {
+        const int64_t m = n <= UINT32_MAX ? (uint32_t)i / quads : i / quads;
+        const int c = C * (int)(i - m * quads);
+        const int32_t* experts = p.experts + m * p.k;
+        const float *weights = p.weights + m * p.k, *dweights = p.dweights + m * p.k;
+        float d[C] = {}, inner = 0.f;
+        int at[K], e0 = -1;
+        float w[K], g[K], w0 = 0.f;
+        // (K choices at a time, whose loads go out together)
+        auto load = [&](int j0) {
 #pragma unroll
-        for (int o = T / 2; o > 0; o >>= 1) inner += __shfl_xor_sync(0xFFFFFFFFu, inner, o);
-        // over the chosen: w_j (dw_j - inner) for them, 0 elsewhere
-        if (!p.over_all) g = fmaf(-w, inner, g);
-        // over all: p_e = exp(l_e - l_first) w_first, and w_first is the largest
-        const int e0 = __shfl_sync(0xFFFFFFFFu, e, 0, T);
-        const float w0 = __shfl_sync(0xFFFFFFFFu, w, 0, T);
-        const bool all = p.over_all && real && e0 >= 0 && e0 < p.E;
-        const float l0 = all ? __ldg(p.logits + m * p.ldl + e0) : 0.f;
-        for (int first = 0; first < p.E; first += T) {
-            const int c = first + t;
-            float d = 0.f;
-            if (all && c < p.E) {
-                const float l = __ldg(p.logits + m * p.ldl + c);
-                d = l == -INFINITY ? 0.f : -expf(l - l0) * w0 * inner;
+            for (int j = 0; j < K; ++j) {
+                const bool there = j0 + j < p.k;
+                at[j] = there ? __ldg(experts + j0 + j) : -1;
+                w[j] = there ? __ldg(weights + j0 + j) : 0.f;
+                g[j] = there ? __ldg(dweights + j0 + j) : 0.f;
             }
-            for (int j = 0; j < p.k; ++j) {
-                const int ej = __shfl_sync(0xFFFFFFFFu, e, j, T);
-                const float gj = __shfl_sync(0xFFFFFFFFu, g, j, T);
-                if (ej == c) d += gj;
-            }
-            if (real && c < p.E) p.dlogits[m * p.lddl + c] = d;
+        };
+        for (int j0 = 0; j0 < p.k; j0 += K) {
+            load(j0);
+            if (j0 == 0) { e0 = at[0]; w0 = w[0]; }
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (at[j] >= 0) inner = fmaf(w[j], g[j], inner);
         }
+        if (p.over_all && e0 >= 0 && e0 < p.E) {
+            // p_e = exp(l_e - l_first) w_first, and w_first is the largest
+            const float l0 = __ldg(p.logits + m * p.ldl + e0);
+            const float4 l = load4<VEC, 1>(p.logits + m * p.ldl, c, p.E), h = load4<VEC, 1>(p.logits + m * p.ldl, c + 4, p.E);
+            const float v[C] = {l.x, l.y, l.z, l.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int q = 0; q < C; ++q) d[q] = v[q] == -INFINITY ? 0.f : -expf(v[q] - l0) * w0 * inner;
+        }
+        for (int j0 = 0; j0 < p.k; j0 += K) {
+            if (p.k > K) load(j0);
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                // over the chosen: w_j (dw_j - inner) for them, 0 elsewhere
+                const float s = w[j] * (p.over_all ? g[j] : g[j] - inner);
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+                    if (at[j] == c + q) d[q] += s;
+            }
+        }
+        store4<VEC, 1>(p.dlogits + m * p.lddl, c, p.E, make_float4(d[0], d[1], d[2], d[3]));
+        store4<VEC, 1>(p.dlogits + m * p.lddl, c + 4, p.E, make_float4(d[4], d[5], d[6], d[7]));
     }
 }
 
-// One block for as much as it does in the time that a second launch takes.
-constexpr int64_t kSmallLogits = 8192;
+// One block for as much as it does in the time that a second launch takes (1000
+// tokens of 8 choices: sorted by one block 13.8 us).
+constexpr int64_t kSmallLogits = 8192, kSmallChoices = 2048;
 
 bool sizes_ok(int64_t M, int E, int k) {
     return E <= kMaxExperts && k <= kMaxChoices && M <= (INT32_MAX - 256) / (k > 0 ? k : 1);
 }
 
-template <bool SORT> emu_status_t route(Route p, emu_stream_t stream) {
+template <int WAY> emu_status_t route(Route p, emu_stream_t stream) {
     DeviceCtx dev;
     emu_status_t st = current_device(&dev);
     if (st != EMU_STATUS_SUCCESS) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = smem_of(p.E);
     const StreamLock lock(s);
-    cudaGetLastError();
-    if (p.M * (SORT ? p.k : p.E) <= kSmallLogits) {
-        static const cudaError_t attr =
-            cudaFuncSetAttribute(route_small_kernel<SORT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxExperts));
+    if (p.M * p.k <= kSmallChoices && (WAY == SORT || p.M * p.E <= kSmallLogits)) {
+        static const cudaError_t attr = cudaFuncSetAttribute(
+            route_small_kernel<WAY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxExperts));
         if (attr != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
-        route_small_kernel<SORT><<<1, kThreads, smem, s>>>(p);
-        return cudaGetLastError() == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
+        cudaGetLastError();
+        route_small_kernel<WAY><<<1, kThreads, smem, s>>>(p);
+        return launched(cudaGetLastError());
     }
     static const cudaError_t attr =
         cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxExperts));
+    static const int resident = resident_blocks(choose_kernel<WAY>, kThreads);
     if (attr != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
-    int64_t blocks = (p.M + 63) / 64;
-    if (blocks > dev.sm_count) blocks = dev.sm_count;
-    p.rows_per = (p.M + blocks - 1) / blocks;
-    blocks = (p.M + p.rows_per - 1) / p.rows_per;
+    // choosing: a pass over the tokens that are resident at once, or several of equal
+    // length; placing: no more blocks than keep the histograms, which each of them
+    // reads, fewer than the choices
+    const int64_t choosers = even_grid(p.M, tokens_of(WAY), (int64_t)dev.sm_count * resident);
+    p.rows_per = (p.M + choosers - 1) / choosers;
+    p.hists = (int)((p.M + p.rows_per - 1) / p.rows_per);
+    int64_t placers = p.M * p.k / (4 * (int64_t)p.E);
+    placers = placers < 1 ? 1 : placers > p.hists ? p.hists : placers;
+    p.per_place = (int)((p.hists + placers - 1) / placers);
+    placers = (p.hists + p.per_place - 1) / p.per_place;
     float* scratch = nullptr;
-    st = reduce_scratch(dev.id, s, (size_t)blocks * p.E, &scratch);
-    if (st != EMU_STATUS_SUCCESS) return st;
+    EMU_TRY(reduce_scratch(dev.id, s, (size_t)p.hists * p.E, &scratch));
     p.hist = reinterpret_cast<int32_t*>(scratch);
-    choose_kernel<SORT><<<(unsigned)blocks, kThreads, p.E * sizeof(int32_t), s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
+    cudaGetLastError();
+    choose_kernel<WAY><<<(unsigned)p.hists, kThreads, p.E * sizeof(int32_t), s>>>(p);
+    EMU_TRY(launched(cudaGetLastError()));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.gridDim = dim3((unsigned)placers, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -385,8 +514,21 @@ emu_status_t emu_expert_route(emu_over_t over, int64_t M, int E, int k, const fl
     if (!sizes_ok(M, E, k)) return EMU_STATUS_NOT_SUPPORTED;
     if (M == 0) return no_tokens(E, offsets, stream);
     if (!logits || ldl < E || !experts || !weights || !slots || !sources || !offsets) return EMU_STATUS_INVALID_VALUE;
-    return route<false>({M, E, k, logits, ldl, over == EMU_OVER_ALL, experts, weights, slots, sources, offsets, nullptr, 0},
-                        stream);
+    const Route p{M, E, k, logits, ldl, over == EMU_OVER_ALL, experts, weights, slots, sources, offsets, nullptr, 0, 0, 0};
+    switch (way_of(M, E, k)) {
+        case LIST_1: return route<LIST_1>(p, stream);
+        case LIST_2: return route<LIST_2>(p, stream);
+        case LIST_4: return route<LIST_4>(p, stream);
+        case LIST_8: return route<LIST_8>(p, stream);
+        case SHARED_1: return route<SHARED_1>(p, stream);
+        case SHARED_2: return route<SHARED_2>(p, stream);
+        case SHARED_4: return route<SHARED_4>(p, stream);
+        case SHARED_8: return route<SHARED_8>(p, stream);
+        case LANES_4: return route<LANES_4>(p, stream);
+        case LANES_8: return route<LANES_8>(p, stream);
+        case LANES_16: return route<LANES_16>(p, stream);
+        default: return route<LANES_32>(p, stream);
+    }
 }
 
 emu_status_t emu_expert_sort(int64_t M, int E, int k, const int32_t* experts, int32_t* slots, int32_t* sources,
@@ -395,8 +537,8 @@ emu_status_t emu_expert_sort(int64_t M, int E, int k, const int32_t* experts, in
     if (!sizes_ok(M, E, k)) return EMU_STATUS_NOT_SUPPORTED;
     if (M == 0) return no_tokens(E, offsets, stream);
     if (!experts || !slots || !sources || !offsets) return EMU_STATUS_INVALID_VALUE;
-    return route<true>({M, E, k, nullptr, 0, 0, const_cast<int32_t*>(experts), nullptr, slots, sources, offsets, nullptr, 0},
-                       stream);
+    return route<SORT>({M, E, k, nullptr, 0, 0, const_cast<int32_t*>(experts), nullptr, slots, sources, offsets, nullptr, 0, 0,
+                        0}, stream);
 }
 
 emu_status_t emu_expert_route_bwd(emu_over_t over, int64_t M, int E, int k, const float* dweights, const float* logits,
@@ -412,16 +554,17 @@ emu_status_t emu_expert_route_bwd(emu_over_t over, int64_t M, int E, int k, cons
     if (st != EMU_STATUS_SUCCESS) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const RouteBwd p{M, E, k, dweights, logits, ldl, experts, weights, over == EMU_OVER_ALL, dlogits, lddl};
-    const int lanes = k > E ? k : (E < 32 ? E : 32);
+    const bool vec = (E & 3) == 0 && vec4_ok(dlogits, lddl) && (over != EMU_OVER_ALL || vec4_ok(logits, ldl));
+    const int64_t groups = (M * ((E + 7) / 8) + 255) / 256, most = (int64_t)dev.sm_count * 8;
+    const unsigned grid = (unsigned)(groups < most ? groups : most);
     cudaGetLastError();
-    auto launch = [&](auto kernel, int T) {
-        const int64_t groups = (M + 256 / T - 1) / (256 / T), most = (int64_t)dev.sm_count * 8;
-        kernel<<<(unsigned)(groups < most ? groups : most), 256, 0, s>>>(p);
-    };
-    if (lanes <= 4) launch(route_bwd_kernel<4>, 4);
-    else if (lanes <= 8) launch(route_bwd_kernel<8>, 8);
-    else if (lanes <= 16) launch(route_bwd_kernel<16>, 16);
-    else launch(route_bwd_kernel<32>, 32);
+    if (k <= 2) {
+        if (vec) route_bwd_kernel<true, 2><<<grid, 256, 0, s>>>(p);
+        else route_bwd_kernel<false, 2><<<grid, 256, 0, s>>>(p);
+    } else {
+        if (vec) route_bwd_kernel<true, 8><<<grid, 256, 0, s>>>(p);
+        else route_bwd_kernel<false, 8><<<grid, 256, 0, s>>>(p);
+    }
     return cudaGetLastError() == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }
 
