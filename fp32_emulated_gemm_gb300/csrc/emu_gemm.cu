@@ -1373,15 +1373,14 @@ GroupedTiles grouped_tiles(const GroupedGemm& g) {
     return {(int)((g.M + TILE_M - 1) / TILE_M * tiles_n), 0};
 }
 
-emu_status_t grouped_pairs(emu_mode_t mode, int* pairs) {
+emu_status_t grouped_pairs(int* pairs) {
     DeviceInfo* dev = nullptr;
     const emu_status_t st = device_info(&dev);
-    if (st == EMU_STATUS_SUCCESS) *pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    if (st == EMU_STATUS_SUCCESS) *pairs = dev->max_clusters[0];
     return st;
 }
 
-emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t stream, Until until) {
-    if (!fused_mode(mode)) return EMU_STATUS_NOT_SUPPORTED;
+emu_status_t gemm_grouped(const GroupedGemm& g, cudaStream_t stream, Until until) {
     const int64_t most = INT32_MAX - 256;
     if (g.rows > most || g.M > most || g.N > most || g.K > most) return EMU_STATUS_NOT_SUPPORTED;
     const bool gated = g.fused && g.fused->kind == FUSED_GATED;
@@ -1401,7 +1400,7 @@ emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t st
     if (st != EMU_STATUS_SUCCESS) return st;
     int devid = 0;
     cudaGetDevice(&devid);
-    const int pairs = dev->max_clusters[mode == EMU_MODE_TF32X3 ? 1 : 0];
+    const int pairs = dev->max_clusters[0];
     Params p{};
     Workspace* w = nullptr;
     st = workspace_for(devid, stream, (size_t)pairs * TILE_M * TILE_M, (size_t)pairs * 2, &w, &p.epoch);
@@ -1437,14 +1436,14 @@ emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t st
     const int pipe = stages >= kLongKMinStages ? PIPE_LONG_K : PIPE_SHORT_K;
     const EpiTable* table = g.sum ? &kSumStore : gated ? &kRowsGated : g.fused ? &kRowsGatedBwd : &kRowsStore;
     if (log_enabled())
-        std::fprintf(stderr, "[emu] %s grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld tiles each %d pipe=%d\n",
-                     mode_name(mode), g.sum ? "sum" : "rows", (long long)g.rows, g.groups, (long long)g.M, (long long)g.N,
+        std::fprintf(stderr, "[emu] grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld tiles each %d pipe=%d\n",
+                     g.sum ? "sum" : "rows", (long long)g.rows, g.groups, (long long)g.M, (long long)g.N,
                      (long long)g.K, tiles.per, pipe);
     if (clear_captured_counters(p.counters, (size_t)pairs * 2, stream) != cudaSuccess) {
         cudaGetLastError();
         return EMU_STATUS_LAUNCH_FAILED;
     }
-    return launch_gemm(mode, pipe, p, pairs, stream, table) == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
+    return launch_gemm(EMU_MODE_BF16X9, pipe, p, pairs, stream, table) == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
 }
 static_assert(FUSED_ACT == EPI_ACT && FUSED_GATED == EPI_GATED && FUSED_GATED_BWD == EPI_GATED_BWD, "epilogue kinds");
 

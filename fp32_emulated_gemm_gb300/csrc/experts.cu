@@ -10,6 +10,12 @@
 // (emu_kernel.cuh): 256-row tiles that end with the expert's rows, listed on the
 // device from the offsets, which never come to the host.  A few rows run on the
 // CUDA cores (few_rows.cu), where each expert's weight is read once.
+//
+// Both modes run as BF16x9, which is within TF32x3's bound too: TF32x3 without an
+// operand split ahead is slower (12288 rows on 8 experts, K = 256, F = 1024, the six
+// products of a training step: BF16x9 105, 48, 93, 50, 74, 80 us, TF32x3 122, 58,
+// 102, 60, 98, 98), and the sums over an expert's rows, which start anywhere, could
+// not load split rows (a copy starts on 16 bytes).
 #include <cuda_runtime.h>
 
 #include "activation.cuh"
@@ -23,13 +29,13 @@ namespace {
 
 constexpr int kMaxExperts = 1024, kTileRows = 256;
 
-// The experts' row blocks (of `block` rows at most) and their bounds, from the
+// The experts' row tiles (256 rows at most) and their bounds, from the
 // offsets, which are taken as ascending and within the rows: what breaks that
 // gets no rows, and nothing outside them is read or written.
 // blocks[i] = {first row, row after the last, expert, 0}; groups[e] likewise, the
 // experts of the most rows first, so that whole tiles taken in turn leave the
 // short ones for the end.
-struct Lists { int4 *blocks, *groups; int* count; };
+struct Lists { int4 *blocks, *groups; };
 
 // The walks of the CTA pairs of up to four products (GroupWalk).
 constexpr int kMaxProducts = 4;
@@ -40,30 +46,43 @@ struct Walks {
     GroupedTiles tiles[kMaxProducts];
 };
 
-// A product's tiles in turn, or equal runs of its stages: what is predicted faster
-// for the longest of the pairs, in stages.  A tile's stores cost 3, publishing a
-// piece 1.5 and adding one 2 (measured: see the products' host side).
-__device__ bool cut_tiles(bool sum, GroupedTiles tiles, int entries, const int4* groups, int64_t total, int pairs) {
+// A product's tiles in turn (0), or equal runs of its stages, on how many pairs: what
+// is predicted faster for the longest of them, in stages.  A tile's stores cost 3,
+// publishing a piece 1.5 and adding one 2.  Fewer runs than pairs where a tile would
+// be cut into many pieces, which one pair adds up.
+__device__ int cut_tiles(bool sum, GroupedTiles tiles, int entries, const int4* groups, int64_t total, int pairs) {
     const int64_t n = (int64_t)entries * tiles.per, waves = (n + pairs - 1) / pairs;
-    if (total < 2 * pairs) return false;
-    const float run = (float)((total + pairs - 1) / pairs);
+    if (n == 0) return 0;
+    const int shortest = (int)((total + pairs - 1) / pairs);  // a run on all pairs
     int longest = tiles.stages;
     float whole = 0.f;
     if (sum) {
         longest = group_stages(groups[0].y - groups[0].x);
         // (the first pair's tiles are the longest of each wave)
-        for (int64_t w = 0; w < waves && whole <= 4.f * (run + longest) + 100.f; ++w) {
+        for (int64_t w = 0; w < waves && whole <= 4.f * (shortest + longest) + 100.f; ++w) {
             const int4 g = groups[w * pairs / tiles.per];
             whole += group_stages(g.y - g.x) + 3.f;
         }
     } else {
         whole = (float)waves * (longest + 3.f);
     }
-    return 1.03f * (run + 3.f * (float)waves + 1.5f + 2.f * ceilf(longest / run)) < whole;
+    float best = whole / 1.03f;
+    int runs = 0;
+    for (int pieces = 0; pieces <= 8; ++pieces) {
+        const int run = pieces == 0 ? shortest : (longest + pieces - 1) / pieces;
+        if (run < shortest || run < 2) continue;
+        const int r = (int)((total + run - 1) / run);
+        const float cost = run + 3.f * (float)((n + r - 1) / r) + 1.5f + 2.f * ((longest + run - 1) / run);
+        if (cost < best) {
+            best = cost;
+            runs = r;
+        }
+    }
+    return runs;
 }
 
 __global__ void __launch_bounds__(kMaxExperts)
-list_kernel(const int32_t* offsets, int E, int rows, int block, Lists out, const __grid_constant__ Walks walks) {
+list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_constant__ Walks walks) {
     __shared__ int32_t first[kMaxExperts + 1], start[kMaxExperts + 1], sums[32];
     __shared__ int4 sorted[kMaxExperts];
     __shared__ int cut[kMaxProducts];
@@ -101,20 +120,19 @@ list_kernel(const int32_t* offsets, int E, int rows, int block, Lists out, const
     const int r0 = t < E ? first[t] : 0, r1 = t < E ? first[t + 1] : 0, n = r1 - r0;
     int blocks_total = 0;
     if (out.blocks) {
-        const int tiles = (n + block - 1) / block, at = scan(tiles, false);
+        const int tiles = (n + kTileRows - 1) / kTileRows, at = scan(tiles, false);
         if (t < E) start[t + 1] = at;
         if (t == 0) start[0] = 0;
         __syncthreads();
         blocks_total = start[E];
-        if (t == 0) *out.count = blocks_total;
         for (int i = t; i < blocks_total; i += kMaxExperts) {
             int lo = 0, hi = E - 1;  // the expert whose blocks hold i: start[e] <= i < start[e + 1]
             while (lo < hi) {
                 const int mid = (lo + hi) / 2;
                 if (start[mid + 1] <= i) lo = mid + 1; else hi = mid;
             }
-            const int b0 = first[lo] + (i - start[lo]) * block;
-            out.blocks[i] = make_int4(b0, min(b0 + block, first[lo + 1]), lo, 0);
+            const int b0 = first[lo] + (i - start[lo]) * kTileRows;
+            out.blocks[i] = make_int4(b0, min(b0 + kTileRows, first[lo + 1]), lo, 0);
         }
         __syncthreads();
     }
@@ -149,10 +167,10 @@ list_kernel(const int32_t* offsets, int E, int rows, int block, Lists out, const
             w.first = pair;
             w.last = entries(k) * tiles.per;
             w.step = walks.pairs;
-        } else {
+        } else if (pair < cut[k]) {
             const int64_t U = total(k);
-            const int run = walks.pairs - 1 - pair;
-            const int64_t s = run * U / walks.pairs, e = (run + 1) * U / walks.pairs;
+            const int runs = cut[k], run = runs - 1 - pair;
+            const int64_t s = run * U / runs, e = (run + 1) * U / runs;  // (a run has two stages or more)
             // the tile at position x, its first position and its stages
             auto tile_at = [&](int64_t x, int64_t& base, int& stages) {
                 if (!walks.sum[k]) {
@@ -180,56 +198,53 @@ list_kernel(const int32_t* offsets, int E, int rows, int block, Lists out, const
             w.hi = (int)(e - base);
             w.step = 1;
             // the next runs that start within the last tile
-            for (int r = run + 1; r < walks.pairs && r * U / walks.pairs < base + stages; ++r) ++w.others;
+            for (int r = run + 1; r < runs && r * U / runs < base + stages; ++r) ++w.others;
         }
         walks.out[i] = w;
     }
 }
 
-int64_t most_blocks(int64_t rows, int E, int block) { return rows / block + (rows < E ? rows : E); }
+int64_t most_blocks(int64_t rows, int E) { return rows / kTileRows + (rows < E ? rows : E); }
 
-// Buffer for the lists: the count, the blocks, the groups, the walks.
-size_t list_floats(int64_t rows, int E, int block, int walks) {
-    return 4 * (size_t)(1 + most_blocks(rows, E, block) + E) + walks * (sizeof(GroupWalk) / sizeof(float));
+// Buffer for the lists: the blocks, the groups, the walks.
+size_t list_floats(int64_t rows, int E, int walks) {
+    return 4 * (size_t)(most_blocks(rows, E) + E) + walks * (sizeof(GroupWalk) / sizeof(float));
 }
 struct Listed {
     Lists lists;
     GroupWalk* walks;
 };
-Listed lists_at(float* base, int64_t rows, int E, int block, bool blocks, bool groups) {
-    int4 *p = reinterpret_cast<int4*>(base), *g = p + 1 + most_blocks(rows, E, block);
-    return {{blocks ? p + 1 : nullptr, groups ? g : nullptr, reinterpret_cast<int*>(p)}, reinterpret_cast<GroupWalk*>(g + E)};
+Listed lists_at(float* base, int64_t rows, int E, bool blocks, bool groups) {
+    int4 *p = reinterpret_cast<int4*>(base), *g = p + most_blocks(rows, E);
+    return {{blocks ? p : nullptr, groups ? g : nullptr}, reinterpret_cast<GroupWalk*>(g + E)};
 }
-cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, int block, const Lists& out, const Walks& walks,
-                         cudaStream_t s) {
+cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, const Lists& out, const Walks& walks, cudaStream_t s) {
     cudaGetLastError();
-    list_kernel<<<1, kMaxExperts, 0, s>>>(offsets, E, (int)rows, block, out, walks);
+    list_kernel<<<1, kMaxExperts, 0, s>>>(offsets, E, (int)rows, out, walks);
     return cudaGetLastError();
 }
 
 // Few rows for each expert: the CUDA cores, on which the weights of the experts
 // that have rows are read once.
-bool few(int64_t rows, int E) { return rows <= 4 * (int64_t)E; }
-int few_block_rows(int64_t rows, int E) { return 4 * rows <= E ? 1 : rows <= E ? 2 : rows <= 3 * (int64_t)E ? 4 : 8; }
+bool few(int64_t rows, int E) { return rows <= 8 * (int64_t)E; }
 
 bool size_ok(int64_t v) { return v <= INT32_MAX - 256; }
 
 // A call's grouped products, one after the other, with one launch for the lists and
 // walks of all of them.
 struct Products {
-    emu_mode_t mode;
     int64_t rows;
     int E, n = 0;
     bool blocks = false, groups = false;
     GroupedGemm g[kMaxProducts];
 
-    Products(emu_mode_t m, int64_t r, int e) : mode(m), rows(r), E(e) {}
+    Products(int64_t r, int e) : rows(r), E(e) {}
     void add(const GroupedGemm& p) {
         (p.sum ? groups : blocks) = true;
         g[n++] = p;
     }
     emu_status_t run(cudaStream_t s, Until until) const {
-        for (int i = 0; i < n; ++i) EMU_TRY(gemm_grouped(mode, g[i], s, until));
+        for (int i = 0; i < n; ++i) EMU_TRY(gemm_grouped(g[i], s, until));
         return EMU_STATUS_SUCCESS;
     }
     emu_status_t launch(const int32_t* offsets, const Listed& l, int pairs, cudaStream_t s) {
@@ -240,7 +255,7 @@ struct Products {
             g[i].list = g[i].sum ? l.lists.groups : l.lists.blocks;
             g[i].walks = l.walks + (int64_t)i * pairs;
         }
-        EMU_TRY(launched(launch_lists(offsets, E, rows, kTileRows, l.lists, w, s)));
+        EMU_TRY(launched(launch_lists(offsets, E, rows, l.lists, w, s)));
         return run(s, UNTIL_LAUNCHED);
     }
 };
@@ -257,12 +272,12 @@ template <class F> emu_status_t run_products(Aligned& al, F make, const int32_t*
     EMU_TRY(al.reserve(s));
     EMU_TRY(q.run(s, UNTIL_RESERVED));
     int pairs = 0;
-    EMU_TRY(grouped_pairs(q.mode, &pairs));
+    EMU_TRY(grouped_pairs(&pairs));
     float* scratch = nullptr;
-    EMU_TRY(reduce_scratch(dev.id, s, list_floats(q.rows, q.E, kTileRows, q.n * pairs), &scratch));
+    EMU_TRY(reduce_scratch(dev.id, s, list_floats(q.rows, q.E, q.n * pairs), &scratch));
     EMU_TRY(launched(al.launch(s)));
     q = make();
-    return q.launch(offsets, lists_at(scratch, q.rows, q.E, kTileRows, q.blocks, q.groups), pairs, s);
+    return q.launch(offsets, lists_at(scratch, q.rows, q.E, q.blocks, q.groups), pairs, s);
 }
 
 }  // namespace
@@ -288,21 +303,15 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const StreamLock lock(s);
     DeviceCtx dev;
-    float* scratch = nullptr;
     if (few(rows, E)) {
-        const int block = few_block_rows(rows, E);
         EMU_TRY(current_device(&dev));
-        EMU_TRY(reduce_scratch(dev.id, s, list_floats(rows, E, block, 0), &scratch));
-        const Lists l = lists_at(scratch, rows, E, block, true, false).lists;
-        EMU_TRY(launched(launch_lists(offsets, E, rows, block, l, Walks{}, s)));
         FewRows p{(int)rows, F, K, X, ldx, W_in, ldwi, nullptr, nullptr, 0, D, ldd, H, ldh, act_params(act)};
-        p.list = l.blocks;
-        p.count = l.count;
-        p.blocks = (int)most_blocks(rows, E, block);
-        EMU_TRY(launched(launch_few_rows_grouped(p, block, true, dev.sm_count, s)));
+        p.offsets = offsets;
+        p.groups = E;
+        EMU_TRY(launched(launch_few_rows_grouped(p, true, false, dev.sm_count, s)));
         p.N = N; p.K = F; p.X = H; p.ldx = ldh; p.W = W_out; p.ldw = ldwo; p.D = nullptr; p.Y = Y; p.ldy = ldy;
         p.act = act_params(ACT_NONE);
-        return launched(launch_few_rows_grouped(p, block, false, dev.sm_count, s));
+        return launched(launch_few_rows_grouped(p, false, true, dev.sm_count, s));
     }
     if (D && !vec4_ok(D, ldd)) return EMU_STATUS_NOT_SUPPORTED;
     Aligned al;
@@ -311,7 +320,7 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     al.add(W_out, ldwo, E * N, F);
     const Fused f{FUSED_GATED, act, nullptr, 0, D, ldd, nullptr};
     auto products = [&] {
-        Products q(mode, rows, E);
+        Products q(rows, E);
         q.add({false, E, false, rows, 0, F, K, X, ldx, W_in, ldwi, H, ldh, &f});
         q.add({false, E, false, rows, 0, N, F, H, ldh, W_out, ldwo, Y, ldy});
         return q;
@@ -357,7 +366,7 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
     Fused f{};
     auto products = [&] {
         f = {FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, nullptr};
-        Products q(mode, rows, E);
+        Products q(rows, E);
         if (inner) q.add({false, E, true, rows, 0, F, N, dY, lddy, W_out, ldwo, dZ, lddz, &f});
         if (dW_out) q.add({true, E, true, rows, N, F, 0, dY, lddy, H, ldh, dW_out, lddwo});
         if (dX) q.add({false, E, true, rows, 0, K, 2 * F, dZ, lddz, W_in, ldwi, dX, lddx});

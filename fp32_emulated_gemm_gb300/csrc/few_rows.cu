@@ -64,6 +64,43 @@ template <int V> __device__ __forceinline__ void warp_sums(float (&v)[V], int la
     }
 }
 
+// The `at`-th of the blocks of MR rows at most that the groups' rows make, group by
+// group: {first row, rows (0: there are fewer blocks), group}.  Each warp finds it
+// for itself, 32 groups at a time: about 0.3 us, where a kernel of its own for a
+// list of the blocks took 3.
+__device__ __forceinline__ int3 rows_of_block(const int32_t* offsets, int groups, int M, int MR, int at) {
+    const int lane = threadIdx.x & 31;
+    int last = min(max(__ldcg(offsets), 0), M);  // where the groups so far end
+    for (int base = 0; base < groups; base += 32) {
+        // ends, made ascending
+        int end = base + lane < groups ? min(max(__ldcg(offsets + base + lane + 1), 0), M) : 0;
+        end = max(end, last);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, end, o);
+            if (lane >= o) end = max(end, up);
+        }
+        const int prev = __shfl_up_sync(0xFFFFFFFFu, end, 1), first = lane == 0 ? last : prev;
+        const int n = (end - first + MR - 1) / MR;
+        int through = n;  // blocks of this group and those before it
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, through, o);
+            if (lane >= o) through += up;
+        }
+        const unsigned mine = __ballot_sync(0xFFFFFFFFu, at < through);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            const int f = __shfl_sync(0xFFFFFFFFu, first, src), e = __shfl_sync(0xFFFFFFFFu, end, src);
+            const int b = at - __shfl_sync(0xFFFFFFFFu, through - n, src);
+            return make_int3(f + b * MR, min(MR, e - f - b * MR), base + src);
+        }
+        at -= __shfl_sync(0xFFFFFFFFu, through, 31);
+        last = __shfl_sync(0xFFFFFFFFu, end, 31);
+    }
+    return make_int3(0, 0, 0);
+}
+
 // MR: rows of X (M of them real), NR: rows of W per warp (gated: NR / 2 of the
 // gate and the same of the up projection), WK: warps that share a row.
 template <int MR, int NR, bool GATED, bool VEC, int FAMILY, bool GROUPED = false>
@@ -78,11 +115,11 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     const float* W = p.W;
     if (threadIdx.x == 0) griddep_launch_dependents();
     if constexpr (GROUPED) {
-        griddep_wait();  // the list may be the previous kernel's
-        if (static_cast<int>(blockIdx.y) >= __ldcg(p.count)) return;
-        const int4 g = __ldcg(p.list + blockIdx.y);
+        griddep_wait();  // the offsets and X may be the previous kernel's
+        const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
+        if (g.y <= 0) return;
         m0 = g.x;
-        rows = g.y - g.x;
+        rows = g.y;
         W += g.z * ((GATED ? 2 : 1) * p.N * p.ldw);
     }
     // this warp's part of k: whole steps of 128
@@ -167,7 +204,8 @@ cudaError_t launch(const FewRows& p, bool gated, bool after_own, int sm_count, c
     const int out = gated ? NR / 2 : NR;
     const int64_t warps = (p.N + out - 1) / out, steps = (p.K + 127) / 128;
     int wk = 1;
-    const int64_t row_groups = GROUPED ? p.blocks : (p.M + MR - 1) / MR;
+    // (every group's last block may be partial)
+    const int64_t row_groups = GROUPED ? p.M / MR + (p.M < p.groups ? p.M : p.groups) : (p.M + MR - 1) / MR;
     while (wk < kWarpsPerBlock && row_groups * warps * wk < 16ll * sm_count && 2 * wk <= steps) wk *= 2;
     const int64_t groups = kWarpsPerBlock / wk, grid = (warps + groups - 1) / groups;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -208,13 +246,13 @@ cudaError_t launch_few_rows(const FewRows& p, bool gated, bool after_own, int sm
     return launch<8, 4>(p, gated, after_own, sm_count, stream);  // eight rows a block
 }
 
-cudaError_t launch_few_rows_grouped(const FewRows& p, int block_rows, bool gated, int sm_count, cudaStream_t stream) {
-    switch (block_rows) {
-        case 1: return launch<1, 4, true>(p, gated, true, sm_count, stream);
-        case 2: return launch<2, 4, true>(p, gated, true, sm_count, stream);
-        case 4: return launch<4, 4, true>(p, gated, true, sm_count, stream);
-        default: return launch<8, 4, true>(p, gated, true, sm_count, stream);
-    }
+cudaError_t launch_few_rows_grouped(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream) {
+    // (the blocks' rows: about what a group has)
+    const int64_t m = p.M, g = p.groups;
+    if (4 * m <= g) return launch<1, 4, true>(p, gated, after_own, sm_count, stream);
+    if (m <= g) return launch<2, 4, true>(p, gated, after_own, sm_count, stream);
+    if (m <= 3 * g) return launch<4, 4, true>(p, gated, after_own, sm_count, stream);
+    return launch<8, 4, true>(p, gated, after_own, sm_count, stream);
 }
 
 }  // namespace emu

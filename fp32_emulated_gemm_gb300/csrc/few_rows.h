@@ -42,13 +42,13 @@ struct FewRows {
     int64_t ldy;
     ActParams act;
     // Rows in groups, a weight for each (W: one behind the other; no bias, no R):
-    // {first row, row after the last, group} of each block of rows, on the device.
-    const int4* list = nullptr;
-    const int* count = nullptr;
-    int blocks = 0;  // at most this many are listed
+    // group e has the rows offsets[e] .. offsets[e + 1] (on the device; taken as
+    // ascending and within the M rows).
+    const int32_t* offsets = nullptr;
+    int groups = 0;
 };
 cudaError_t launch_few_rows(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream);
-// With rows in groups: blocks of `block_rows` (1, 2, 4 or 8) rows at most.
-cudaError_t launch_few_rows_grouped(const FewRows& p, int block_rows, bool gated, int sm_count, cudaStream_t stream);
+// With rows in groups.
+cudaError_t launch_few_rows_grouped(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream);
 
 }  // namespace emu

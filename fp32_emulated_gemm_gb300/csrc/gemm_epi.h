@@ -17,7 +17,7 @@ struct EpiTable {
 };
 extern const EpiTable kEpiAct, kEpiGated, kEpiGatedBwd;
 // Grouped products (GROUP_ROWS with each epilogue of the experts, GROUP_SUM):
-// unpacked shapes alone.
+// BF16x9 and unpacked shapes alone.
 extern const EpiTable kRowsStore, kRowsGated, kRowsGatedBwd, kSumStore;
 
 // The TF32 modes have one unpacked and one packed shape (PIPE_LONG_K* read as
@@ -55,7 +55,6 @@ cudaError_t group_set_attribute() {
 template <int EPI, int GROUP> cudaError_t group_set_attributes() {
     cudaError_t e = group_set_attribute<MODE_BF16X9, PIPE_SHORT_K, EPI, GROUP>();
     if (e == cudaSuccess) e = group_set_attribute<MODE_BF16X9, PIPE_LONG_K, EPI, GROUP>();
-    if (e == cudaSuccess) e = group_set_attribute<MODE_TF32X3, PIPE_SHORT_K, EPI, GROUP>();
     return e;
 }
 template <int MODE, int PIPE, int EPI, int GROUP>
@@ -63,8 +62,7 @@ cudaError_t group_launch_one(cudaLaunchConfig_t cfg, const Params& p) {
     cfg.dynamicSmemBytes = smem_bytes<MODE, PIPE>();
     return cudaLaunchKernelEx(&cfg, emu_gemm_kernel<MODE, PIPE, false, EPI, GROUP>, p);
 }
-template <int EPI, int GROUP> cudaError_t group_launch(int mode, int pipe, cudaLaunchConfig_t cfg, const Params& p) {
-    if (mode == MODE_TF32X3) return group_launch_one<MODE_TF32X3, PIPE_SHORT_K, EPI, GROUP>(cfg, p);
+template <int EPI, int GROUP> cudaError_t group_launch(int, int pipe, cudaLaunchConfig_t cfg, const Params& p) {
     return pipe == PIPE_LONG_K ? group_launch_one<MODE_BF16X9, PIPE_LONG_K, EPI, GROUP>(cfg, p)
                                : group_launch_one<MODE_BF16X9, PIPE_SHORT_K, EPI, GROUP>(cfg, p);
 }

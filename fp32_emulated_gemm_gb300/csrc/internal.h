@@ -89,7 +89,7 @@ emu_status_t gemm(emu_mode_t mode, const Gemm& g, cudaStream_t stream, Until unt
 emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_t stream, Until until);
 
 // A product whose rows lie in groups, a weight for each (see Group in
-// emu_kernel.cuh).  The modes BF16x9 and TF32x3.
+// emu_kernel.cuh), in BF16x9.
 struct GroupedGemm {
     bool sum;         // false: C[r] = A[r] op(B[g]); true: C[g] = A[rows of g]^T B[rows of g]
     int groups;
@@ -111,7 +111,7 @@ struct GroupedGemm {
 struct GroupedTiles { int per, stages; };
 GroupedTiles grouped_tiles(const GroupedGemm& g);
 // CTA pairs that a grouped product runs on.
-emu_status_t grouped_pairs(emu_mode_t mode, int* pairs);
-emu_status_t gemm_grouped(emu_mode_t mode, const GroupedGemm& g, cudaStream_t stream, Until until);
+emu_status_t grouped_pairs(int* pairs);
+emu_status_t gemm_grouped(const GroupedGemm& g, cudaStream_t stream, Until until);
 
 }  // namespace emu
