@@ -14,6 +14,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -190,8 +191,8 @@ emu_status_t device_info(DeviceInfo** out) {
             set_smem_attr<MODE_TF32X3, PIPE_SHORT_K_PACKED, true>() != cudaSuccess ||
             kEpiAct.set_attributes() != cudaSuccess || kEpiGated.set_attributes() != cudaSuccess ||
             kEpiGatedBwd.set_attributes() != cudaSuccess || kRowsStore.set_attributes() != cudaSuccess ||
-            kRowsGated.set_attributes() != cudaSuccess || kRowsGatedBwd.set_attributes() != cudaSuccess ||
-            kSumStore.set_attributes() != cudaSuccess ||
+            kRowsGated.set_attributes() != cudaSuccess || kTwoStore.set_attributes() != cudaSuccess ||
+            kTwoGatedBwd.set_attributes() != cudaSuccess ||
             cudaGetSymbolAddress(reinterpret_cast<void**>(&d.error_word), g_error_flag) != cudaSuccess) {
             cudaGetLastError();
             return EMU_STATUS_LAUNCH_FAILED;
@@ -1013,6 +1014,24 @@ cudaError_t launch_gemm(emu_mode_t mode, int pipe, const Params& p, int clusters
     return e;
 }
 
+cudaError_t launch_two(int pipe, const ParamsTwo& p, int clusters, cudaStream_t stream, const TwoTable& table) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_on() ? 1 : 0;
+    const cudaError_t e = table.launch(pipe, cfg, p);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        if (log_enabled()) std::fprintf(stderr, "[emu] launch failed: %s\n", cudaGetErrorName(e));
+    }
+    return e;
+}
+
 // One launch of the pack kernel on `stream` (the caller checked the arguments).
 cudaError_t launch_pack(emu_mode_t mode, int64_t N, int64_t K, const float* B, int64_t ldb, bool k_major,
                         void* packed, int sm_count, cudaStream_t stream) {
@@ -1367,10 +1386,10 @@ emu_status_t gemm_two(emu_mode_t mode, const Gemm* a, const Gemm* b, cudaStream_
 }
 
 GroupedTiles grouped_tiles(const GroupedGemm& g) {
-    const bool gated = g.fused && g.fused->kind == FUSED_GATED;
+    const bool gated = g.fused && g.fused->kind == FUSED_GATED, bwd = g.fused && g.fused->kind == FUSED_GATED_BWD;
     const int64_t tiles_n = gated ? (g.N + HALF - 1) / HALF : (g.N + TILE_M - 1) / TILE_M;
-    if (!g.sum) return {(int)tiles_n, (int)((g.K + BK - 1) / BK)};
-    return {(int)((g.M + TILE_M - 1) / TILE_M * tiles_n), 0};
+    if (!g.sum) return {false, (int)tiles_n, (int)((g.K + BK - 1) / BK), bwd ? 14 : gated && g.fused->d ? 5 : 3};
+    return {true, (int)((g.M + TILE_M - 1) / TILE_M * tiles_n), 0, 3};
 }
 
 emu_status_t grouped_pairs(int* pairs) {
@@ -1380,70 +1399,93 @@ emu_status_t grouped_pairs(int* pairs) {
     return st;
 }
 
-emu_status_t gemm_grouped(const GroupedGemm& g, cudaStream_t stream, Until until) {
+namespace {
+emu_status_t check_grouped(const GroupedGemm& g) {
     const int64_t most = INT32_MAX - 256;
     if (g.rows > most || g.M > most || g.N > most || g.K > most) return EMU_STATUS_NOT_SUPPORTED;
-    const bool gated = g.fused && g.fused->kind == FUSED_GATED;
-    const int64_t b_n = gated ? 2 * g.N : g.N;
-    if (b_n > most) return EMU_STATUS_NOT_SUPPORTED;
+    if ((g.fused && g.fused->kind == FUSED_GATED ? 2 : 1) * g.N > most) return EMU_STATUS_NOT_SUPPORTED;
     if (!g.A || !g.B || !g.C || g.lda < (g.sum ? g.M : g.K) || g.ldb < (g.sum || g.b_mn ? g.N : g.K) || g.ldc < g.N)
         return EMU_STATUS_INVALID_VALUE;
     if (!aligned16(g.A) || !aligned16(g.B) || !aligned16(g.C) || (g.lda & 3) || (g.ldb & 3) || (g.ldc & 3))
         return EMU_STATUS_NOT_SUPPORTED;
     // the list's entries are at most rows / 256 and one for each group, or the groups
-    const GroupedTiles tiles = grouped_tiles(g);
-    if ((g.sum ? g.groups : g.rows / TILE_M + g.groups) * (int64_t)tiles.per > most) return EMU_STATUS_NOT_SUPPORTED;
-    if (until == UNTIL_CHECKED) return EMU_STATUS_SUCCESS;
+    if ((g.sum ? g.groups : g.rows / TILE_M + g.groups) * (int64_t)grouped_tiles(g).per > most) return EMU_STATUS_NOT_SUPPORTED;
+    return EMU_STATUS_SUCCESS;
+}
 
+// The parameters of one product (all but the workspace's).
+bool grouped_params(const GroupedGemm& g, unsigned* error_word, Params* p) {
+    const bool gated = g.fused && g.fused->kind == FUSED_GATED;
+    const int64_t b_n = gated ? 2 * g.N : g.N;
+    const int64_t b_rows = g.b_mn ? g.K : b_n, b_cols = g.b_mn ? b_n : g.K;
+    if (!(g.sum ? encode_operand(&p->tmA, g.A, true, g.M, g.rows, g.lda, HALF) &&
+                      encode_operand(&p->tmB, g.B, true, g.N, g.rows, g.ldb, HALF)
+                : encode_operand(&p->tmA, g.A, false, g.rows, g.K, g.lda, HALF) &&
+                      encode_f32_3d(&p->tmB, g.B, (uint64_t)b_cols, (uint64_t)b_rows, (uint64_t)g.groups, (uint64_t)g.ldb, BK,
+                                    g.b_mn ? BK : HALF)))
+        return false;
+    const GroupedTiles tiles = grouped_tiles(g);
+    if (g.fused)
+        p->epi = {act_params(g.fused->act), (int)g.N, (g.N & 3) == 0, nullptr, 0, g.fused->d, g.fused->ldd, nullptr};
+    p->M = (int)(g.sum ? g.M : g.rows);
+    p->N = (int)g.N;
+    p->K = (int)g.K;
+    p->a_mn_major = g.sum;
+    p->b_mn_major = g.sum || g.b_mn;
+    p->tiles_n = (int)(gated ? (g.N + HALF - 1) / HALF : (g.N + TILE_M - 1) / TILE_M);
+    p->tiles_m = tiles.per / p->tiles_n;
+    p->k_stages = tiles.stages;
+    p->split_a = p->split_b = 1;
+    p->alpha = 1.0f;
+    p->c = g.C;
+    p->c_old = g.C;
+    p->ldc = g.ldc;
+    p->wait_budget_ns = wait_budget_ns();
+    p->error_word = error_word;
+    p->group = {g.list, static_cast<const GroupWalk*>(g.walks), g.M * g.ldc};
+    return true;
+}
+}  // namespace
+
+emu_status_t gemm_grouped(const GroupedGemm* rows, const GroupedGemm* sum, cudaStream_t stream, Until until) {
+    if (rows) EMU_TRY(check_grouped(*rows));
+    if (sum) EMU_TRY(check_grouped(*sum));
+    if (until == UNTIL_CHECKED) return EMU_STATUS_SUCCESS;
     DeviceInfo* dev = nullptr;
-    emu_status_t st = device_info(&dev);
-    if (st != EMU_STATUS_SUCCESS) return st;
+    EMU_TRY(device_info(&dev));
     int devid = 0;
     cudaGetDevice(&devid);
     const int pairs = dev->max_clusters[0];
-    Params p{};
     Workspace* w = nullptr;
-    st = workspace_for(devid, stream, (size_t)pairs * TILE_M * TILE_M, (size_t)pairs * 2, &w, &p.epoch);
-    if (st != EMU_STATUS_SUCCESS || until == UNTIL_RESERVED) return st;
-    p.workspace = static_cast<float*>(w->partials.ptr);
-    p.counters = static_cast<unsigned long long*>(w->counters.ptr);
-    const int64_t b_rows = g.b_mn ? g.K : b_n, b_cols = g.b_mn ? b_n : g.K;
-    if (!(g.sum ? encode_operand(&p.tmA, g.A, true, g.M, g.rows, g.lda, HALF) &&
-                      encode_operand(&p.tmB, g.B, true, g.N, g.rows, g.ldb, HALF)
-                : encode_operand(&p.tmA, g.A, false, g.rows, g.K, g.lda, HALF) &&
-                      encode_f32_3d(&p.tmB, g.B, (uint64_t)b_cols, (uint64_t)b_rows, (uint64_t)g.groups, (uint64_t)g.ldb, BK,
-                                    g.b_mn ? BK : HALF)))
+    unsigned long long epoch = 0;
+    EMU_TRY(workspace_for(devid, stream, (size_t)pairs * TILE_M * TILE_M, (size_t)pairs * 2, &w, &epoch));
+    if (until == UNTIL_RESERVED) return EMU_STATUS_SUCCESS;
+    ParamsTwo p{};
+    if ((rows && !grouped_params(*rows, dev->error_word, &p.rows)) || (sum && !grouped_params(*sum, dev->error_word, &p.sum)))
         return EMU_STATUS_LAUNCH_FAILED;
-    if (g.fused)
-        p.epi = {act_params(g.fused->act), (int)g.N, (g.N & 3) == 0, nullptr, 0, g.fused->d, g.fused->ldd, nullptr};
-    p.M = (int)(g.sum ? g.M : g.rows);
-    p.N = (int)g.N;
-    p.K = (int)g.K;
-    p.a_mn_major = g.sum;
-    p.b_mn_major = g.sum || g.b_mn;
-    p.tiles_n = gated ? (int)((g.N + HALF - 1) / HALF) : (int)((g.N + TILE_M - 1) / TILE_M);
-    p.tiles_m = tiles.per / p.tiles_n;
-    p.k_stages = tiles.stages;
-    p.split_a = p.split_b = 1;
-    p.alpha = 1.0f;
-    p.c = g.C;
-    p.c_old = g.C;
-    p.ldc = g.ldc;
-    p.wait_budget_ns = wait_budget_ns();
-    p.error_word = dev->error_word;
-    p.group = {g.list, static_cast<const GroupWalk*>(g.walks), g.M * g.ldc};
-    const int64_t stages = g.sum ? g.rows / g.groups / BK : p.k_stages;
+    for (Params* q : {&p.rows, &p.sum}) {
+        q->workspace = static_cast<float*>(w->partials.ptr);
+        q->counters = static_cast<unsigned long long*>(w->counters.ptr);
+        q->epoch = epoch;
+        q->group.walks = static_cast<const GroupWalk*>((rows ? rows : sum)->walks);
+    }
+    const int64_t stages = rows && sum ? std::max<int64_t>(p.rows.k_stages, sum->rows / sum->groups / BK)
+                           : rows ? p.rows.k_stages : sum->rows / sum->groups / BK;
     const int pipe = stages >= kLongKMinStages ? PIPE_LONG_K : PIPE_SHORT_K;
-    const EpiTable* table = g.sum ? &kSumStore : gated ? &kRowsGated : g.fused ? &kRowsGatedBwd : &kRowsStore;
+    const FusedKind kind = rows && rows->fused ? (FusedKind)rows->fused->kind : FusedKind{};
     if (log_enabled())
-        std::fprintf(stderr, "[emu] grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld tiles each %d pipe=%d\n",
-                     g.sum ? "sum" : "rows", (long long)g.rows, g.groups, (long long)g.M, (long long)g.N,
-                     (long long)g.K, tiles.per, pipe);
-    if (clear_captured_counters(p.counters, (size_t)pairs * 2, stream) != cudaSuccess) {
+        for (const GroupedGemm* g : {rows, sum})
+            if (g)
+                std::fprintf(stderr, "[emu] grouped %s rows=%lld groups=%d M=%lld N=%lld K=%lld tiles each %d pipe=%d\n",
+                             g->sum ? "sum" : "rows", (long long)g->rows, g->groups, (long long)g->M, (long long)g->N,
+                             (long long)g->K, grouped_tiles(*g).per, pipe);
+    if (clear_captured_counters(p.rows.counters, (size_t)pairs * 2, stream) != cudaSuccess) {
         cudaGetLastError();
         return EMU_STATUS_LAUNCH_FAILED;
     }
-    return launch_gemm(EMU_MODE_BF16X9, pipe, p, pairs, stream, table) == cudaSuccess ? EMU_STATUS_SUCCESS : EMU_STATUS_LAUNCH_FAILED;
+    if (!sum && kind != FUSED_GATED_BWD)
+        return launched(launch_gemm(EMU_MODE_BF16X9, pipe, p.rows, pairs, stream, kind == FUSED_GATED ? &kRowsGated : &kRowsStore));
+    return launched(launch_two(pipe, p, pairs, stream, kind == FUSED_GATED_BWD ? kTwoGatedBwd : kTwoStore));
 }
 static_assert(FUSED_ACT == EPI_ACT && FUSED_GATED == EPI_GATED && FUSED_GATED_BWD == EPI_GATED_BWD, "epilogue kinds");
 

@@ -261,7 +261,8 @@ struct GroupWalk {
     int first, last, lo, hi;  // as in Walk (hi is clipped to the tile's stages)
     int step;
     int others;               // pieces of the last tile that the pairs before this one publish
-    int unused[2];
+    int second;               // two products in a launch: of the second
+    int unused;
 };
 
 struct GroupParams {
@@ -529,11 +530,17 @@ __device__ __forceinline__ Walk walk_of(const Params& p, int cid, int ncl) {
     k.hi = static_cast<int>(e - static_cast<long long>(k.last - 1) * p.k_stages);
     return k;
 }
+// A grouped product's entry of the list for unit u, which the roles ask for a unit
+// ahead: the load takes most of a stage.
+template <int GROUP> __device__ __forceinline__ int4 entry_at(const Params& p, int u, int last) {
+    if constexpr (GROUP == GROUP_NONE) return make_int4(0, 0, 0, 0);
+    const int per = GROUP == GROUP_ROWS ? p.tiles_n : p.tiles_m * p.tiles_n;
+    return u < last ? __ldcg(p.group.list + u / per) : make_int4(0, 0, 0, 0);
+}
 template <int GROUP>
-__device__ __forceinline__ Unit unit_at(const Params& p, const Walk& k, int cid, int u) {
+__device__ __forceinline__ Unit unit_at(const Params& p, const Walk& k, int cid, int u, const int4& g = int4()) {
     if constexpr (GROUP != GROUP_NONE) {
         const int per = GROUP == GROUP_ROWS ? p.tiles_n : p.tiles_m * p.tiles_n, at = u / per;
-        const int4 g = __ldcg(p.group.list + at);
         Unit w;
         w.piece = 0; w.pieces = 1; w.slot = cid;
         w.row0 = g.x; w.row1 = g.y; w.group = g.z;
@@ -592,9 +599,8 @@ __device__ __forceinline__ float4 mul4(const float4& a, const float4& b) {
 // STAGED: split tiles of many pieces read the other pieces' partials through
 // the output staging area (see the epilogue); a separate instantiation, so
 // that plans with few pieces keep the register-only reduction's code.
-template <int MODE, int PIPE, bool STAGED = false, int EPI = EPI_STORE, int GROUP = GROUP_NONE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
-emu_gemm_kernel(const __grid_constant__ Params p) {
+template <int MODE, int PIPE, bool STAGED, int EPI, int GROUP>
+__device__ __forceinline__ void emu_gemm_body(const Params& p) {
     using C = Cfg<MODE>;
     using KC = KCfg<MODE, PIPE>;
     constexpr int NF = KC::NF, NS = KC::NS, NB = KC::NB, OUT_COLS = KC::OUT_COLS;
@@ -784,8 +790,10 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             uint32_t ph = 0, issued_mask = 0, issued_parity = 0;
             uint32_t bph = 0, bissued_mask = 0, bissued_parity = 0;
             bool ok = true;
+            int4 entry = entry_at<GROUP>(p, walk.first, walk.last);
             for (int u = walk.first; ok && u < walk.last; u += walk.step) {
-                const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u);
+                const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u, entry);
+                entry = entry_at<GROUP>(p, u + walk.step, walk.last);
                 for (int ks = w.kb; ks < w.ke; ++ks, ++n) {
                     if (n >= early) {  // the first `early` loads went out before the pair sync
                         if (!mbar_wait(&fp32_empty[s], ph ^ 1u, abort_flag, budget, 1)) { ok = false; break; }
@@ -828,8 +836,10 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
             uint32_t ph = 0, bph = 0;
             bool ok = true, issued = false;
             const uint32_t slice_base = smem_u32(slice_ring), bcomp_base = smem_u32(bcomp_ring);
+            int4 entry = entry_at<GROUP>(p, walk.first, walk.last);
             for (int u = walk.first; ok && u < walk.last; u += walk.step) {
-                const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u);
+                const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u, entry);
+                entry = entry_at<GROUP>(p, u + walk.step, walk.last);
                 for (int ks = w.kb; ks < w.ke; ++ks) {
                     if (!mbar_wait(&acc_empty[b], bph ^ 1u, abort_flag, budget, 2)) { ok = false; break; }
                     if (!mbar_wait(&slice_full[s], ph, abort_flag, budget, 2)) { ok = false; break; }
@@ -863,8 +873,10 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         int fs = 0, ss = 0, bs = 0;
         uint32_t fph = 0, sph = 0, bph = 0;
         bool ok = true;
+        int4 entry = entry_at<GROUP>(p, walk.first, walk.last);
         for (int u = walk.first; ok && u < walk.last; u += walk.step) {
-            const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u);
+            const Unit w = unit_at<GROUP>(p, walk, static_cast<int>(cid), u, entry);
+            entry = entry_at<GROUP>(p, u + walk.step, walk.last);
             for (int ks = w.kb; ks < w.ke; ++ks) {
                 if (!mbar_wait_warp(&fp32_full[fs], fph, abort_flag, budget, 3)) { ok = false; break; }
                 if (!mbar_wait_warp(&slice_empty[ss], sph ^ 1u, abort_flag, budget, 3)) { ok = false; break; }
@@ -917,7 +929,7 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
         for (int u = walk_sh[0]; ok && u < walk_sh[1]; u += walk_sh[2]) {
             Walk wk;
             wk.first = walk_sh[0]; wk.last = walk_sh[1]; wk.step = walk_sh[2]; wk.lo = walk_sh[3]; wk.hi = walk_sh[4];
-            const Unit w = unit_at<GROUP>(p, wk, static_cast<int>(cid), u);
+            const Unit w = unit_at<GROUP>(p, wk, static_cast<int>(cid), u, entry_at<GROUP>(p, u, wk.last));
             // a chained tile's running sum: one 256 x TN slot per run boundary,
             // thread-major like the split-K partials below (worked out where it
             // is used, so that it holds no registers during the k-loop)
@@ -1487,6 +1499,29 @@ emu_gemm_kernel(const __grid_constant__ Params p) {
     cluster_sync();  // no CTA leaves while its peer may still use its TMEM or barriers
     tc_fence_after();
     if (warp == WARP_MMA) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+template <int MODE, int PIPE, bool STAGED = false, int EPI = EPI_STORE, int GROUP = GROUP_NONE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+emu_gemm_kernel(const __grid_constant__ Params p) {
+    emu_gemm_body<MODE, PIPE, STAGED, EPI, GROUP>(p);
+}
+
+// Two grouped products that do not depend on one another, side by side: each pair's
+// walk says whose it is.  (Products of a few tiles leave most pairs idle, and each
+// launch takes the 15 to 20 us of its longest pair.)
+struct ParamsTwo { Params rows, sum; };
+template <int MODE, int PIPE, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+emu_gemm_two_kernel(const __grid_constant__ ParamsTwo p) {
+    __shared__ int second;
+    if (threadIdx.x == 0) {
+        griddep_wait();  // the walks may be the previous grid's
+        second = __ldcg(&p.rows.group.walks[cluster_id_x()].second);
+    }
+    __syncthreads();
+    if (second) emu_gemm_body<MODE, PIPE, false, EPI_STORE, GROUP_SUM>(p.sum);
+    else emu_gemm_body<MODE, PIPE, false, EPI, GROUP_ROWS>(p.rows);
 }
 
 }  // namespace emu

@@ -8,7 +8,9 @@
 //   dW_in[e] = dZ^T X, dW_out[e] = dY^T H over the expert's rows.
 // The products run on the emulated kernel with rows or contraction in groups
 // (emu_kernel.cuh): 256-row tiles that end with the expert's rows, listed on the
-// device from the offsets, which never come to the host.  A few rows run on the
+// device from the offsets, which never come to the host.  Backward, the products
+// that do not depend on one another share a launch (dZ and dW_out, dX and dW_in).
+// A few rows run on the
 // CUDA cores (few_rows.cu), where each expert's weight is read once.
 //
 // Both modes run as BF16x9, which is within TF32x3's bound too: TF32x3 without an
@@ -37,57 +39,63 @@ constexpr int kMaxExperts = 1024, kTileRows = 256;
 // short ones for the end.
 struct Lists { int4 *blocks, *groups; };
 
-// The walks of the CTA pairs of up to four products (GroupWalk).
-constexpr int kMaxProducts = 4;
+// The walks of the CTA pairs of up to two launches (GroupWalk), each of a product
+// over rows, a sum over the experts' rows, or both side by side.
+constexpr int kMaxLaunches = 2, kMaxPairs = 1024;
 struct Walks {
     int n, pairs;
-    GroupWalk* out;               // n x pairs
-    bool sum[kMaxProducts];
-    GroupedTiles tiles[kMaxProducts];
+    GroupWalk* out;                  // n x pairs
+    int sum_store;                   // a sum's GroupedTiles::store
+    GroupedTiles tiles[kMaxLaunches][2];  // rows, sum; per 0: there is none
 };
 
-// A product's tiles in turn (0), or equal runs of its stages, on how many pairs: what
-// is predicted faster for the longest of them, in stages.  A tile's stores cost 3,
-// publishing a piece 1.5 and adding one 2.  Fewer runs than pairs where a tile would
-// be cut into many pieces, which one pair adds up.
-__device__ int cut_tiles(bool sum, GroupedTiles tiles, int entries, const int4* groups, int64_t total, int pairs) {
-    const int64_t n = (int64_t)entries * tiles.per, waves = (n + pairs - 1) / pairs;
-    if (n == 0) return 0;
-    const int shortest = (int)((total + pairs - 1) / pairs);  // a run on all pairs
-    int longest = tiles.stages;
-    float whole = 0.f;
-    if (sum) {
-        longest = group_stages(groups[0].y - groups[0].x);
-        // (the first pair's tiles are the longest of each wave)
-        for (int64_t w = 0; w < waves && whole <= 4.f * (shortest + longest) + 100.f; ++w) {
-            const int4 g = groups[w * pairs / tiles.per];
-            whole += group_stages(g.y - g.x) + 3.f;
+// A tile costs its k-stages and, for its stores, `tiles.store` more: its length.
+__device__ __forceinline__ int tile_length(const GroupedTiles& tiles, const int4& group) {
+    return tiles.store + (tiles.sum ? group_stages(group.y - group.x) : tiles.stages);
+}
+
+// How a product's tiles go to `pairs` pairs: in turn (runs 0), or cut into runs of
+// equal length; and the longest pair's time, in stages.  Publishing a piece costs 1.5
+// and adding one 2.  Fewer runs than pairs where a tile would be cut into many
+// pieces, which one pair adds up.  (All in FP32: integer divisions in a chain would
+// cost this kernel more than they are worth.)
+struct Cut {
+    float cost;
+    int runs;
+};
+__device__ Cut cut_tiles(const GroupedTiles& tiles, int entries, const int4* groups, int64_t total, int pairs) {
+    const int64_t n = (int64_t)entries * tiles.per;
+    if (n == 0 || pairs == 0) return {n == 0 ? 0.f : 1e30f, 0};
+    const float waves = ceilf((float)n / (float)pairs), shortest = ceilf((float)total / (float)pairs);  // a run on all pairs
+    const float longest = (float)tile_length(tiles, groups[0]);  // (sorted)
+    float whole = waves * longest;
+    if (tiles.sum) {
+        whole = shortest + 0.5f * longest;
+        if (waves <= 8.f) {  // the first pair's tiles are the longest of each wave
+            whole = 0.f;
+            for (int w = 0; w < (int)waves; ++w)
+                whole += (float)tile_length(tiles, groups[min(w * pairs / tiles.per, entries - 1)]);
         }
-    } else {
-        whole = (float)waves * (longest + 3.f);
     }
-    float best = whole / 1.03f;
-    int runs = 0;
+    Cut best{whole, 0};
+#pragma unroll
     for (int pieces = 0; pieces <= 8; ++pieces) {
-        const int run = pieces == 0 ? shortest : (longest + pieces - 1) / pieces;
-        if (run < shortest || run < 2) continue;
-        const int r = (int)((total + run - 1) / run);
-        const float cost = run + 3.f * (float)((n + r - 1) / r) + 1.5f + 2.f * ((longest + run - 1) / run);
-        if (cost < best) {
-            best = cost;
-            runs = r;
-        }
+        const float run = pieces == 0 ? shortest : ceilf(longest * (1.f / pieces));
+        if (run < shortest || run < 2.f) continue;
+        const float cost = run + 1.5f + 2.f * ceilf(longest / run);
+        if (1.03f * cost < best.cost) best = {cost, (int)fminf(ceilf((float)total / run), (float)pairs)};
     }
-    return runs;
+    return best;
 }
 
 __global__ void __launch_bounds__(kMaxExperts)
 list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_constant__ Walks walks) {
     __shared__ int32_t first[kMaxExperts + 1], start[kMaxExperts + 1], sums[32];
     __shared__ int4 sorted[kMaxExperts];
-    __shared__ int cut[kMaxProducts];
+    __shared__ int split[kMaxLaunches], runs[kMaxLaunches][2];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     griddep_launch_dependents();
+    griddep_wait();  // the offsets are another kernel's, and the last call's products may still read the lists
     auto scan = [&](int v, bool largest) {  // inclusive, over the block
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -144,61 +152,91 @@ list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_con
         }
         if (t < E) out.groups[rank] = sorted[rank] = make_int4(r0, r1, t, 0);
         __syncthreads();
-        // start[i]: stages of the first i of the sorted experts
-        const int at = scan(t < E ? group_stages(sorted[t].y - sorted[t].x) : 0, false);
+        // start[i]: lengths of a tile of each of the first i of the sorted experts (all
+        // sums' stores cost the same)
+        const int at = scan(t < E ? group_stages(sorted[t].y - sorted[t].x) + walks.sum_store : 0, false);
         if (t < E) start[t + 1] = at;
         if (t == 0) start[0] = 0;
         __syncthreads();
     }
-    auto entries = [&](int k) { return walks.sum[k] ? E : blocks_total; };
-    auto total = [&](int k) {
-        const int64_t per = walks.tiles[k].per;
-        return walks.sum[k] ? per * start[E] : per * blocks_total * walks.tiles[k].stages;
+    auto entries = [&](const GroupedTiles& k) { return k.sum ? E : blocks_total; };
+    auto total = [&](const GroupedTiles& k) {
+        return k.sum ? (int64_t)k.per * start[E] : (int64_t)k.per * blocks_total * (k.stages + k.store);
     };
-    if (t < walks.n)
-        cut[t] = cut_tiles(walks.sum[t], walks.tiles[t], entries(t), sorted, total(t), walks.pairs);
+    // a launch's pairs: the rows' product has the first `split`; of 32 splits, a lane
+    // each, the one whose longer side is the shortest
+    if (warp < walks.n) {
+        const GroupedTiles &r = walks.tiles[warp][0], &s = walks.tiles[warp][1];
+        const int pairs = walks.pairs, first_pairs = s.per == 0 ? pairs : r.per == 0 ? 0 : 1 + (pairs - 2) * lane / 31;
+        Cut a{0.f, 0}, b{0.f, 0};
+        if (r.per) a = cut_tiles(r, entries(r), sorted, total(r), first_pairs);
+        if (s.per) b = cut_tiles(s, entries(s), sorted, total(s), pairs - first_pairs);
+        const float cost = fmaxf(a.cost, b.cost);
+        float least = cost;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+        if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, cost == least)) - 1) {
+            split[warp] = first_pairs;
+            runs[warp][0] = a.runs;
+            runs[warp][1] = b.runs;
+        }
+    }
     __syncthreads();
     for (int i = t; i < walks.n * walks.pairs; i += kMaxExperts) {
-        const int k = i / walks.pairs, pair = i - k * walks.pairs;
-        const GroupedTiles tiles = walks.tiles[k];
+        const int k = i / walks.pairs, cid = i - k * walks.pairs, second = cid >= split[k];
+        const GroupedTiles tiles = walks.tiles[k][second];
+        const int pair = cid - (second ? split[k] : 0), pairs = second ? walks.pairs - split[k] : split[k];
+        const int cut = runs[k][second], run = cut - 1 - pair;
         GroupWalk w{};
         w.hi = INT32_MAX;
-        if (!cut[k]) {
+        w.second = second;
+        w.step = 1;
+        if (cut == 0) {
             w.first = pair;
-            w.last = entries(k) * tiles.per;
-            w.step = walks.pairs;
-        } else if (pair < cut[k]) {
-            const int64_t U = total(k);
-            const int runs = cut[k], run = runs - 1 - pair;
-            const int64_t s = run * U / runs, e = (run + 1) * U / runs;  // (a run has two stages or more)
-            // the tile at position x, its first position and its stages
-            auto tile_at = [&](int64_t x, int64_t& base, int& stages) {
-                if (!walks.sum[k]) {
-                    stages = tiles.stages;
-                    const int64_t tile = x / stages;
-                    base = tile * stages;
-                    return (int)tile;
-                }
-                int lo = 0, hi = E - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi) / 2;
-                    if ((int64_t)start[mid + 1] * tiles.per <= x) lo = mid + 1; else hi = mid;
-                }
-                stages = start[lo + 1] - start[lo];
-                base = (int64_t)start[lo] * tiles.per;
-                const int64_t j = (x - base) / stages;
-                base += j * stages;
-                return lo * tiles.per + (int)j;
+            w.last = entries(tiles) * tiles.per;
+            w.step = pairs;
+        } else if (run >= 0) {
+            const int64_t U = total(tiles);
+            // where run r starts, r U / cut (a run has a length of two or more)
+            auto start_of = [&](int r) {
+                return U <= INT32_MAX / kMaxPairs ? (int64_t)((uint32_t)r * (uint32_t)U / (uint32_t)cut) : r * U / cut;
             };
-            int64_t base;
-            int stages;
-            w.first = tile_at(s, base, stages);
-            w.lo = (int)(s - base);
-            w.last = tile_at(e - 1, base, stages) + 1;
-            w.hi = (int)(e - base);
-            w.step = 1;
-            // the next runs that start within the last tile
-            for (int r = run + 1; r < runs && r * U / runs < base + stages; ++r) ++w.others;
+            // the tile that length x falls into, its end, and the stage: the first
+            // `store` of a tile's length are its stores, and a run that starts within
+            // them has the whole tile
+            struct At { int tile, stage; int64_t end; };
+            auto at = [&](int64_t x) {
+                int length = tiles.stages + tiles.store, first_tile = 0;
+                int64_t base = 0;
+                if (tiles.sum) {
+                    int lo = 0, hi = E - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi) / 2;
+                        if ((int64_t)start[mid + 1] * tiles.per <= x) lo = mid + 1; else hi = mid;
+                    }
+                    length = start[lo + 1] - start[lo];
+                    base = (int64_t)start[lo] * tiles.per;
+                    first_tile = lo * tiles.per;
+                }
+                const int64_t j = x - base <= UINT32_MAX ? (uint32_t)(x - base) / (uint32_t)length : (x - base) / length;
+                base += j * length;
+                return At{first_tile + (int)j, max((int)(x - base) - tiles.store, 0), base + length};
+            };
+            const At s = at(start_of(run));
+            w.first = s.tile;
+            w.lo = s.stage;
+            if (run + 1 == cut) {
+                w.last = entries(tiles) * tiles.per;
+            } else {
+                const At e = at(start_of(run + 1));
+                w.last = e.tile;
+                if (e.stage > 0 && !(e.tile == s.tile && e.stage <= s.stage)) {
+                    w.last = e.tile + 1;
+                    w.hi = e.stage;
+                    // the next runs that start within the last tile
+                    for (int r = run + 1; r < cut && start_of(r) < e.end; ++r) ++w.others;
+                }
+            }
         }
         walks.out[i] = w;
     }
@@ -219,9 +257,18 @@ Listed lists_at(float* base, int64_t rows, int E, bool blocks, bool groups) {
     return {{blocks ? p : nullptr, groups ? g : nullptr}, reinterpret_cast<GroupWalk*>(g + E)};
 }
 cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, const Lists& out, const Walks& walks, cudaStream_t s) {
-    cudaGetLastError();
-    list_kernel<<<1, kMaxExperts, 0, s>>>(offsets, E, (int)rows, out, walks);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(kMaxExperts, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, list_kernel, offsets, E, (int)rows, out, walks);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 // Few rows for each expert: the CUDA cores, on which the weights of the experts
@@ -230,31 +277,40 @@ bool few(int64_t rows, int E) { return rows <= 8 * (int64_t)E; }
 
 bool size_ok(int64_t v) { return v <= INT32_MAX - 256; }
 
-// A call's grouped products, one after the other, with one launch for the lists and
+// A call's grouped products, a launch or two, with one kernel for the lists and
 // walks of all of them.
 struct Products {
     int64_t rows;
     int E, n = 0;
-    bool blocks = false, groups = false;
-    GroupedGemm g[kMaxProducts];
+    struct Launch {
+        bool has[2] = {false, false};
+        GroupedGemm g[2];  // over rows, a sum
+        const GroupedGemm* product(int i) const { return has[i] ? &g[i] : nullptr; }
+    } launches[kMaxLaunches];
 
     Products(int64_t r, int e) : rows(r), E(e) {}
+    void begin() { ++n; }  // a launch; what follows is its products
     void add(const GroupedGemm& p) {
-        (p.sum ? groups : blocks) = true;
-        g[n++] = p;
+        launches[n - 1].has[p.sum] = true;
+        launches[n - 1].g[p.sum] = p;
     }
     emu_status_t run(cudaStream_t s, Until until) const {
-        for (int i = 0; i < n; ++i) EMU_TRY(gemm_grouped(g[i], s, until));
+        for (int i = 0; i < n; ++i)
+            EMU_TRY(gemm_grouped(launches[i].product(0), launches[i].product(1), s, until));
         return EMU_STATUS_SUCCESS;
     }
-    emu_status_t launch(const int32_t* offsets, const Listed& l, int pairs, cudaStream_t s) {
-        Walks w{n, pairs, l.walks, {}, {}};
-        for (int i = 0; i < n; ++i) {
-            w.sum[i] = g[i].sum;
-            w.tiles[i] = grouped_tiles(g[i]);
-            g[i].list = g[i].sum ? l.lists.groups : l.lists.blocks;
-            g[i].walks = l.walks + (int64_t)i * pairs;
-        }
+    emu_status_t launch(const int32_t* offsets, float* scratch, int pairs, cudaStream_t s) {
+        const Listed l = lists_at(scratch, rows, E, launches[0].has[0] || launches[n - 1].has[0],
+                                  launches[0].has[1] || launches[n - 1].has[1]);
+        Walks w{n, pairs, l.walks, 0, {}};
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < 2; ++j)
+                if (launches[i].has[j]) {
+                    w.tiles[i][j] = grouped_tiles(launches[i].g[j]);
+                    if (j) w.sum_store = w.tiles[i][j].store;
+                    launches[i].g[j].list = j ? l.lists.groups : l.lists.blocks;
+                    launches[i].g[j].walks = l.walks + (int64_t)i * pairs;
+                }
         EMU_TRY(launched(launch_lists(offsets, E, rows, l.lists, w, s)));
         return run(s, UNTIL_LAUNCHED);
     }
@@ -273,11 +329,12 @@ template <class F> emu_status_t run_products(Aligned& al, F make, const int32_t*
     EMU_TRY(q.run(s, UNTIL_RESERVED));
     int pairs = 0;
     EMU_TRY(grouped_pairs(&pairs));
+    if (pairs > kMaxPairs) return EMU_STATUS_NOT_SUPPORTED;
     float* scratch = nullptr;
     EMU_TRY(reduce_scratch(dev.id, s, list_floats(q.rows, q.E, q.n * pairs), &scratch));
     EMU_TRY(launched(al.launch(s)));
     q = make();
-    return q.launch(offsets, lists_at(scratch, q.rows, q.E, q.blocks, q.groups), pairs, s);
+    return q.launch(offsets, scratch, pairs, s);
 }
 
 }  // namespace
@@ -321,7 +378,9 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     const Fused f{FUSED_GATED, act, nullptr, 0, D, ldd, nullptr};
     auto products = [&] {
         Products q(rows, E);
+        q.begin();
         q.add({false, E, false, rows, 0, F, K, X, ldx, W_in, ldwi, H, ldh, &f});
+        q.begin();
         q.add({false, E, false, rows, 0, N, F, H, ldh, W_out, ldwo, Y, ldy});
         return q;
     };
@@ -367,8 +426,10 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
     auto products = [&] {
         f = {FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, nullptr};
         Products q(rows, E);
+        q.begin();
         if (inner) q.add({false, E, true, rows, 0, F, N, dY, lddy, W_out, ldwo, dZ, lddz, &f});
         if (dW_out) q.add({true, E, true, rows, N, F, 0, dY, lddy, H, ldh, dW_out, lddwo});
+        if (inner) q.begin();
         if (dX) q.add({false, E, true, rows, 0, K, 2 * F, dZ, lddz, W_in, ldwi, dX, lddx});
         if (dW_in) q.add({true, E, true, rows, 2 * F, K, 0, dZ, lddz, X, ldx, dW_in, lddwi});
         return q;

@@ -2,5 +2,5 @@
 #include "gemm_epi.h"
 
 namespace emu {
-const EpiTable kRowsStore = {group_set_attributes<EPI_STORE, GROUP_ROWS>, group_launch<EPI_STORE, GROUP_ROWS>};
+const EpiTable kRowsStore = {rows_set_attributes<EPI_STORE>, rows_launch<EPI_STORE>};
 }

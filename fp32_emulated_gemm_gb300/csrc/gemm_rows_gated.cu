@@ -2,5 +2,5 @@
 #include "gemm_epi.h"
 
 namespace emu {
-const EpiTable kRowsGated = {group_set_attributes<EPI_GATED, GROUP_ROWS>, group_launch<EPI_GATED, GROUP_ROWS>};
+const EpiTable kRowsGated = {rows_set_attributes<EPI_GATED>, rows_launch<EPI_GATED>};
 }

@@ -107,11 +107,17 @@ struct GroupedGemm {
     const void* walks = nullptr;   // each pair's GroupWalk, on the device
 };
 // How its pairs' walks are worked out (see experts.cu): tiles for each entry of the
-// list, and a tile's k-stages (0: the group's).
-struct GroupedTiles { int per, stages; };
+// list, a tile's k-stages (0: the group's), and what its stores cost in stages.
+struct GroupedTiles {
+    bool sum;
+    int per, stages, store;
+};
 GroupedTiles grouped_tiles(const GroupedGemm& g);
 // CTA pairs that a grouped product runs on.
 emu_status_t grouped_pairs(int* pairs);
-emu_status_t gemm_grouped(const GroupedGemm& g, cudaStream_t stream, Until until);
+// One launch of a product over rows, a sum over the groups' rows, or (not with
+// FUSED_GATED) both side by side, which must not depend on one another; either may be
+// null.  The walks are the launch's.
+emu_status_t gemm_grouped(const GroupedGemm* rows, const GroupedGemm* sum, cudaStream_t stream, Until until);
 
 }  // namespace emu

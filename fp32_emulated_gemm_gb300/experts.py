@@ -15,7 +15,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _check, _mode
 from . import feed_forward as ff
-from .feed_forward import _NONE, _SIGNATURES, _act, _c_name, _empty, _flat, _float32, _fn, _Function, _new, _new_vector
+from .feed_forward import _NONE, _SIGNATURES, _act, _c_name, _empty, _flat, _float32, _fn, _Function, _new_vector
 from .feed_forward import _result, _rows, _stream_of, _vector
 
 EMU_OVER_CHOSEN, EMU_OVER_ALL = range(2)
@@ -48,6 +48,16 @@ emu_expert_ffn_fwd = _c_name("emu_expert_ffn_fwd")
 emu_expert_ffn_bwd = _c_name("emu_expert_ffn_bwd")
 
 _int32 = torch.int32
+
+
+def _new(M, N, device):
+    """A new matrix with rows on 16-byte boundaries."""
+    if not N & 3:
+        t, ld = _empty((M, N), device=device, dtype=_float32), N
+    else:   # (a view of a padded matrix costs the host 2.5 us more)
+        ld = (N + 3) // 4 * 4
+        t = torch.empty_strided((M, N), (ld, 1), device=device, dtype=_float32)
+    return t, t.data_ptr(), ld
 
 
 def _ints(t, name, shape):
@@ -250,7 +260,7 @@ def expert_combine_fwd(Ys, plan, weights=None, *, residual=None, out=None):
         raise ValueError(f"Ys must have the plan's {M * k} rows, not {Ys.shape[0]}")
     weights, pw = (None, None) if weights is None else _dense(weights, "weights", (M, k))
     residual, pr, ldr = _NONE if residual is None else _rows(residual, "residual", (M, N))
-    Y, pyo, ldy = _result(out, (M, N), Ys.device, "out")
+    Y, pyo, ldy = _new(M, N, Ys.device) if out is None else _result(out, (M, N), Ys.device, "out")
     _check(_fn("emu_expert_combine_fwd")(M, k, N, py, ldys, psl, pw, pr, ldr, pyo, ldy,
                                          _stream_of("expert_combine_fwd", Ys, slots, weights, residual, Y)),
            "emu_expert_combine_fwd")
