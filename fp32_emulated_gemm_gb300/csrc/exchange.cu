@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 #pragma unroll
                         for (int i = 0; i < kMine; ++i)
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                if (j + q == t + T * i) mine[i] += dot[q];
+                            for (int q = 0; q < 2; ++q)  // (none: 0, whatever is in dY)
+                                if (j + q == t + T * i && s[q] >= 0) mine[i] += dot[q];
                     }
                 } else {
 #pragma unroll

@@ -443,6 +443,12 @@ class EmuRMSNorm(torch.nn.Module):
         return y.reshape(shape) if residual is None else (y.reshape(shape), s.reshape(shape))
 
 
+def _token_mask(mask, x):
+    if tuple(mask.shape) != tuple(x.shape[:-1]) or mask.dtype != torch.bool:
+        raise ValueError(f"the mask must be bool of shape {tuple(x.shape[:-1])}")
+    return mask.reshape(-1)
+
+
 class EmuExpertFFN(torch.nn.Module):
     """A layer of experts: each token goes through the gated blocks of the `k`
     experts that the router's logits favour, weighted by their softmax (`over` the
@@ -479,9 +485,7 @@ class EmuExpertFFN(torch.nn.Module):
         rows, residual, shape = _flat(x, residual, self.in_features, self.out_features)
         logits = self.router(rows)
         if mask is not None:
-            if tuple(mask.shape) != tuple(x.shape[:-1]) or mask.dtype != torch.bool:
-                raise ValueError(f"the mask must be bool of shape {tuple(x.shape[:-1])}")
-            logits = logits.masked_fill(~mask.reshape(-1, 1), float("-inf"))
+            logits = logits.masked_fill(~_token_mask(mask, x)[:, None], float("-inf"))
         y = EmuExpertFFNFunction.apply(rows, logits, self.weight_in, self.weight_out, residual, self.k, self.over, self.act,
                                        self.mode)
         return y.reshape(shape)
@@ -501,4 +505,4 @@ class EmuExpertFeedForward(torch.nn.Module):
     def forward(self, x, mask=None):
         rows, _, shape = _flat(x, None, self.norm.features, self.norm.features)
         y, s = EmuRMSNormFunction.apply(rows, self.norm.weight, None, self.norm.eps)
-        return self.ffn(y, residual=s, mask=None if mask is None else mask.reshape(-1)).reshape(shape)
+        return self.ffn(y, residual=s, mask=None if mask is None else _token_mask(mask, x)).reshape(shape)

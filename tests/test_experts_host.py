@@ -201,6 +201,11 @@ def test_module_shapes_and_refusals(plain):
                 lambda: emu.EmuExpertFFN(6, 8, 4, 2, mode="fp32"), lambda: emu.EmuRMSNorm(6)(torch.randn(5, 7))):
         with pytest.raises(ValueError):
             bad()
+    f = emu.EmuExpertFeedForward(6, 8, 4, 2)
+    assert f(torch.randn(2, 3, 6)).shape == (2, 3, 6)
+    for mask in (torch.ones(3, 2, dtype=torch.bool), torch.ones(6, dtype=torch.bool), torch.ones(2, 3)):
+        with pytest.raises(ValueError):
+            f(torch.randn(2, 3, 6), mask)
     n = emu.EmuRMSNorm(6)
     y, s = n(torch.randn(2, 3, 6), torch.randn(2, 3, 6))
     assert y.shape == s.shape == (2, 3, 6) and n(torch.randn(2, 6)).shape == (2, 6)

@@ -326,6 +326,27 @@ def test_exchange(M, N, k, kind):
     want.check(host(dw1), "dweights alone")
 
 
+@pytest.mark.parametrize("N", [16, 333, 1024])
+def test_exchange_of_padded_tokens_that_hold_nan(N):
+    """Tokens that go nowhere may hold anything: it reaches no row, no other token,
+    and no weight's gradient."""
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("nan", N)
+    M, k, E = 50, 3, 4
+    e = rng.integers(0, E, (M, k))
+    e[40:] = -1
+    e[7, 1] = -1
+    plan = emu.expert_sort(ints(e), E)
+    x, dy, ys, w = f32(rng, M, N), f32(rng, M, N), f32(rng, M * k, N), f32(rng, M, k)
+    want = [host(t) for t in (emu.expert_dispatch(dev(x), plan), *emu.expert_combine_bwd(dev(dy), dev(ys), plan, dev(w)))]
+    x[40:], dy[40:], w[40:] = np.nan, INF, np.nan
+    got = [host(t) for t in (emu.expert_dispatch(dev(x), plan), *emu.expert_combine_bwd(dev(dy), dev(ys), plan, dev(w)))]
+    y = host(emu.expert_combine_fwd(dev(ys), plan, dev(w)))
+    done()
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    assert not got[2][40:].any() and got[2][7, 1] == 0 and not y[40:].any() and np.isfinite(y).all()
+
+
 def test_exchange_leaves_out_wrong_slots():
     """Slots outside the rows count as none: nothing is read or written there."""
     import torch
@@ -405,6 +426,34 @@ def test_expert_ffn(counts, K, F, N, act, mode):
                                 (dwi[e], dwi_, "dW_in"), (dwo[e], dwo_, "dW_out"), (again[0][r], dx_, "dX again")):
             want.check(host(got), f"expert {e} {name}")
     assert torch.equal(dwi, again[1]) and torch.equal(dwo, again[2])
+
+
+@pytest.mark.parametrize("E,K,F,N,most", [(70, 64, 160, 96, 700), (3, 2300, 40, 70, 260), (2, 40, 70, 2300, 3000), (300, 33, 17, 20, 60),
+                                          (1024, 8, 8, 8, 30)])
+def test_expert_ffn_uneven_experts(E, K, F, N, most):
+    """Many experts of very different sizes; tiles of very many and of few stages,
+    whose stages several pairs share."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("uneven", E, K, F)
+    counts = (most * rng.random(E) ** 6).astype(np.int64)
+    counts[E // 2] = most
+    if E > 8 * 3:
+        counts[:3] = 0
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    rows = int(offsets[-1])
+    x, dy = f32(rng, rows, K), f32(rng, rows, N)
+    wi, wo = f32(rng, E, 2 * F, K, std=K ** -0.5), f32(rng, E, N, F, std=F ** -0.5)
+    plan = emu.ExpertPlan(None, None, None, ints(offsets))
+    y, d, h = emu.expert_ffn_fwd(dev(x), dev(wi), dev(wo), plan, save=True)
+    dx, dwi, dwo = emu.expert_ffn_bwd(dev(dy), dev(x), dev(wi), dev(wo), d, h, plan)
+    done()
+    got = [host(t) for t in (y, h, dx, dwi, dwo)]
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        want = expert_reference(x[r], wi[e], wo[e], "silu", "bf16x9", dy[r])
+        for g, w, name in zip((got[0][r], got[1][r], got[2][r], got[3][e], got[4][e]), want, ("Y", "H", "dX", "dW_in", "dW_out")):
+            w.check(g, f"expert {e} {name}")
 
 
 def test_expert_ffn_only_wanted_gradients():
@@ -537,7 +586,7 @@ def test_sub_layer_and_its_gradients(M, over, mode, masked):
     y64.backward(g.double().cpu())
     for name, a, b in [("y", y, y64), ("dx", x.grad, x64.grad)] + [(n, t.grad, p[n].grad) for n, t in m.named_parameters()]:
         assert a.shape == b.shape
-        assert float((a.detach().double().cpu() - b).abs().max()) <= 1e-5 * float(b.abs().max()), name
+        assert float((a.detach().double().cpu() - b).abs().max()) <= 1e-5 * float(b.detach().abs().max()), name
     if mask is not None:
         assert torch.equal(y.detach()[~mask], x.detach()[~mask])
 
@@ -561,6 +610,25 @@ def test_sub_layer_against_differences():
     got = float((x.grad.double().cpu() * d).sum())
     # differences: h^2 of the third derivative and 2^-52 |f| / h; the gradient's own 1e-5 of its size
     assert abs(got - want) <= 1e-5 * float((x.grad.double().cpu() * d).abs().sum()) + 1e-7 * max(1.0, abs(f(x64)))
+
+
+def test_no_tokens_and_no_open_experts():
+    """An empty batch, and one whose tokens are all padding: the residual alone, and
+    zero gradients of the experts."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(2)
+    m = emu.EmuExpertFeedForward(32, 24, 4, 2).cuda()
+    for M, mask in ((0, None), (5, torch.zeros(5, dtype=torch.bool, device="cuda")),
+                    (400, torch.zeros(400, dtype=torch.bool, device="cuda"))):
+        x = torch.randn(M, 32, device="cuda", requires_grad=True)
+        m.zero_grad()
+        y = m(x, mask)
+        y.backward(torch.ones_like(y))
+        done()
+        assert torch.equal(y, x) and bool((x.grad == 1).all())
+        for n, p in m.named_parameters():
+            assert p.grad.shape == p.shape and not p.grad.any(), (M, n)
 
 
 def test_modules_want_only_some_gradients():
