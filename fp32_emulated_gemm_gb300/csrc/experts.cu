@@ -271,9 +271,21 @@ cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, const List
     return e;
 }
 
-// Few rows for each expert: the CUDA cores, on which the weights of the experts
-// that have rows are read once.
-bool few(int64_t rows, int E) { return rows <= 8 * (int64_t)E; }
+// Few rows for the experts' sizes run on the CUDA cores, on which the weights of the
+// experts that have rows are read once for eight rows.  With W weights an expert
+// that form takes about rows W / 8e6 us, wherever the rows lie, and the tiles 50 us
+// and 2.2 us for a million weights of all experts (measured, tiles / CUDA cores: 8
+// experts, K = 1024, F = 4096, 128 rows 250 / 215 us, 256 rows 255 / 349; K = 256, F =
+// 1024, 256 rows 61 / 34, 512 rows 60 / 59; 64 experts, K = 512, F = 1024, 1024 rows
+// 262 / 216; 16 experts, K = F = 1024, 256 rows 149 / 96, 512 rows 150 / 181).
+constexpr int64_t kFewRowsMost = 32768;
+bool few(int64_t rows, int E, int64_t K, int64_t F, int64_t N) {
+    const double W = (double)F * (2.0 * K + N);
+    return rows <= kFewRowsMost && rows * W <= 400e6 + 17.6 * E * W;
+}
+// Lots of weight rows (two of each half, or four) that make the streaming form the
+// faster one (few_rows.cu).
+bool many_lots(int64_t rows, int64_t F, int64_t N) { return rows * (F / 2 + N / 4) >= 8192; }
 
 bool size_ok(int64_t v) { return v <= INT32_MAX - 256; }
 
@@ -357,20 +369,21 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     if (!X || !offsets || !W_in || !W_out || !H || !Y || ldx < K || ldwi < K || ldwo < F || ldh < F || ldy < N ||
         (D && ldd < 2 * F))
         return EMU_STATUS_INVALID_VALUE;
+    if (!vec4_ok(H, ldh) || !vec4_ok(Y, ldy) || (D && !vec4_ok(D, ldd))) return EMU_STATUS_NOT_SUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const StreamLock lock(s);
     DeviceCtx dev;
-    if (few(rows, E)) {
+    if (few(rows, E, K, F, N)) {
+        const bool streaming = many_lots(rows, F, N);
         EMU_TRY(current_device(&dev));
         FewRows p{(int)rows, F, K, X, ldx, W_in, ldwi, nullptr, nullptr, 0, D, ldd, H, ldh, act_params(act)};
         p.offsets = offsets;
         p.groups = E;
-        EMU_TRY(launched(launch_few_rows_grouped(p, true, false, dev.sm_count, s)));
+        EMU_TRY(launched(launch_few_rows_grouped(p, true, streaming, false, dev.sm_count, s)));
         p.N = N; p.K = F; p.X = H; p.ldx = ldh; p.W = W_out; p.ldw = ldwo; p.D = nullptr; p.Y = Y; p.ldy = ldy;
         p.act = act_params(ACT_NONE);
-        return launched(launch_few_rows_grouped(p, false, true, dev.sm_count, s));
+        return launched(launch_few_rows_grouped(p, false, streaming, true, dev.sm_count, s));
     }
-    if (D && !vec4_ok(D, ldd)) return EMU_STATUS_NOT_SUPPORTED;
     Aligned al;
     al.add(X, ldx, rows, K);
     al.add(W_in, ldwi, E * 2 * F, K);

@@ -21,6 +21,8 @@
 // (K = 1024, N = 4096, eight tokens: 12.0 us), for they halve the warps.
 #include "few_rows.h"
 
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "row_ops.cuh"
@@ -197,6 +199,149 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     }
 }
 
+// Rows in groups with work for every warp of the GPU: a warp takes whole rows of
+// its group's weight, four at a time, one lot after the other, and asks for the next
+// steps' weights across the lots, so that loads are always in flight; a block's rows
+// of X come from L1.  The same sums in the same order as above with wk = 1.
+// Gated blocks of 8 experts, K = 1024, F = 4096 (both products; 59 us at the copy rate
+// for their weights): 16 rows 68 us, 64 rows 128, 128 rows 215, where a lot a warp
+// above takes 94, 205 and 366 us; 64 experts, K = 512, F = 1024 (59 us), 512 rows 129
+// and 241.  With few lots the form above keeps more warps busy: 2 rows 34 and 22 us, 4
+// rows 44 and 39.
+template <int MR, bool GATED, bool VEC, int FAMILY>
+__global__ void __launch_bounds__(32 * kWarpsPerBlock, 2) few_rows_stream_kernel(const FewRows p, int lots) {
+    constexpr int NR = 4, V = MR * NR, OUT = GATED ? NR / 2 : NR;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();  // the offsets and X may be the previous kernel's
+    const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
+    const int rows = g.y;
+    if (rows <= 0) return;
+    const float* X = p.X + g.x * p.ldx + (VEC ? 4 * lane : lane);
+    const float* W = p.W + g.z * ((GATED ? 2 : 1) * p.N * p.ldw) + (VEC ? 4 * lane : lane);
+    const int64_t last = (p.N + OUT - 1) / OUT;                                        // lots of the weight
+    const int64_t l0 = (int64_t)blockIdx.x * lots + warp, l1 = min((int64_t)(blockIdx.x + 1) * lots, last);
+    const int steps = (int)((p.K + 127) / 128);
+    float4 w[2][NR];
+    // the weights of step s of lot l, and the step after it
+    int64_t ahead_lot = l0;
+    int ahead_step = 0;
+    const float* row[NR];
+    auto rows_of_lot = [&] {
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            // (columns past the end read the last one's weights and are dropped)
+            const int64_t n = min(ahead_lot * OUT + j % OUT, p.N - 1) + (GATED && j >= OUT ? p.N : 0);
+            row[j] = W + n * p.ldw;
+        }
+    };
+    rows_of_lot();
+    const int64_t kl = p.K - (VEC ? 4 * lane : lane);  // this lane's columns end there
+    auto load = [&](float4 (&v)[NR]) {
+        if (ahead_lot >= l1) return;
+        const int64_t at = 128 * (int64_t)ahead_step;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) v[j] = load_w<VEC>(row[j], at, kl);
+        if (++ahead_step == steps) {
+            ahead_step = 0;
+            ahead_lot += kWarpsPerBlock;
+            rows_of_lot();
+        }
+    };
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    int64_t lot = l0;
+    int step = 0;
+    auto work = [&](float4 (&v)[NR]) {
+        const int64_t at = 128 * (int64_t)step;
+        constexpr int B = MR < 4 ? MR : 4;  // rows of X loaded together
+#pragma unroll
+        for (int m0 = 0; m0 < MR; m0 += B) {
+            if (m0 >= rows) break;
+            float4 x[B];
+#pragma unroll
+            for (int m = 0; m < B; ++m) x[m] = load4<VEC, 32>(X + (m0 + m) * p.ldx, at, m0 + m < rows ? kl : 0);
+#pragma unroll
+            for (int m = 0; m < B; ++m)
+#pragma unroll
+                for (int j = 0; j < NR; ++j) {
+                    float& a = acc[(m0 + m) * NR + j];
+                    a = fmaf(x[m].x, v[j].x, a);
+                    a = fmaf(x[m].y, v[j].y, a);
+                    a = fmaf(x[m].z, v[j].z, a);
+                    a = fmaf(x[m].w, v[j].w, a);
+                }
+        }
+        load(v);
+        if (++step < steps) return;
+        // the lot's outputs: value i in the lanes from 32 / V i on
+        warp_sums<V>(acc, lane);
+        const int i = lane / (32 / V), r = i / NR, j = i % NR;
+        const int64_t n = lot * OUT + j;
+        float z = acc[0], a, d;
+        act_value_grad<FAMILY>(p.act, z, a, d);
+        const float u = GATED ? __shfl_down_sync(0xFFFFFFFFu, z, OUT * (32 / V)) : 0.f;
+        if (lane % (32 / V) == 0 && r < rows && j < OUT && n < p.N) {
+            const int64_t m = g.x + r;
+            if constexpr (GATED) {
+                if (p.D) {
+                    p.D[m * p.ldd + n] = u * d;
+                    p.D[m * p.ldd + p.N + n] = a;
+                }
+                p.Y[m * p.ldy + n] = a * u;
+            } else {
+                p.Y[m * p.ldy + n] = a;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        step = 0;
+        lot += kWarpsPerBlock;
+    };
+    load(w[0]);
+    load(w[1]);
+    while (lot < l1) {
+        work(w[0]);
+        if (lot < l1) work(w[1]);
+    }
+}
+
+template <int MR>
+cudaError_t launch_stream(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream) {
+    const int out = gated ? 2 : 4;
+    const int64_t row_blocks = p.M / MR + (p.M < p.groups ? p.M : p.groups), all = (p.N + out - 1) / out;
+    // about three turns of the two blocks that an SM holds
+    int64_t lots = all * row_blocks / ((int64_t)sm_count * 6);
+    lots = lots < kWarpsPerBlock ? kWarpsPerBlock : (lots + kWarpsPerBlock - 1) / kWarpsPerBlock * kWarpsPerBlock;
+    const int64_t grid = (all + lots - 1) / lots;
+    if (grid > INT32_MAX || row_blocks > 65535) return cudaErrorInvalidConfiguration;
+    const bool vec = (p.K & 3) == 0 && vec4_ok(p.X, p.M > 1 ? p.ldx : 0) && vec4_ok(p.W, p.ldw);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)row_blocks, 1);
+    cfg.blockDim = dim3(32 * kWarpsPerBlock, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (after_own && pdl_enabled()) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaSuccess;
+    for_family(p.act.family, [&](auto fam) {
+        constexpr int f = decltype(fam)::value;
+        if (gated) e = vec ? cudaLaunchKernelEx(&cfg, few_rows_stream_kernel<MR, true, true, f>, p, (int)lots)
+                           : cudaLaunchKernelEx(&cfg, few_rows_stream_kernel<MR, true, false, f>, p, (int)lots);
+        else if constexpr (f == FAMILY_LINEAR)  // (the output projection: no activation)
+            e = vec ? cudaLaunchKernelEx(&cfg, few_rows_stream_kernel<MR, false, true, f>, p, (int)lots)
+                    : cudaLaunchKernelEx(&cfg, few_rows_stream_kernel<MR, false, false, f>, p, (int)lots);
+        else e = cudaErrorInvalidValue;
+    });
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 template <int MR, int NR, bool GROUPED = false>
 cudaError_t launch(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream) {
     // 16 warps an SM keep enough of the weight in flight; a share of k is at
@@ -246,13 +391,19 @@ cudaError_t launch_few_rows(const FewRows& p, bool gated, bool after_own, int sm
     return launch<8, 4>(p, gated, after_own, sm_count, stream);  // eight rows a block
 }
 
-cudaError_t launch_few_rows_grouped(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream) {
-    // (the blocks' rows: about what a group has)
+cudaError_t launch_few_rows_grouped(const FewRows& p, bool gated, bool streaming, bool after_own, int sm_count,
+                                    cudaStream_t stream) {
+    auto form = [&](auto MR) {
+        constexpr int mr = decltype(MR)::value;
+        return streaming ? launch_stream<mr>(p, gated, after_own, sm_count, stream)
+                         : launch<mr, 4, true>(p, gated, after_own, sm_count, stream);
+    };
+    // (a block's rows: about what a group has)
     const int64_t m = p.M, g = p.groups;
-    if (4 * m <= g) return launch<1, 4, true>(p, gated, after_own, sm_count, stream);
-    if (m <= g) return launch<2, 4, true>(p, gated, after_own, sm_count, stream);
-    if (m <= 3 * g) return launch<4, 4, true>(p, gated, after_own, sm_count, stream);
-    return launch<8, 4, true>(p, gated, after_own, sm_count, stream);
+    if (4 * m <= g) return form(std::integral_constant<int, 1>{});
+    if (m <= g) return form(std::integral_constant<int, 2>{});
+    if (m <= 3 * g) return form(std::integral_constant<int, 4>{});
+    return form(std::integral_constant<int, 8>{});
 }
 
 }  // namespace emu

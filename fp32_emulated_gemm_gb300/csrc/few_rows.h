@@ -48,7 +48,9 @@ struct FewRows {
     int groups = 0;
 };
 cudaError_t launch_few_rows(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream);
-// With rows in groups.
-cudaError_t launch_few_rows_grouped(const FewRows& p, bool gated, bool after_own, int sm_count, cudaStream_t stream);
+// With rows in groups (at most 65535 blocks of 8 rows and one more for each group);
+// `streaming`: the form for many lots of weight rows (not gated: act none alone).
+cudaError_t launch_few_rows_grouped(const FewRows& p, bool gated, bool streaming, bool after_own, int sm_count,
+                                    cudaStream_t stream);
 
 }  // namespace emu

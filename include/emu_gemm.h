@@ -453,8 +453,9 @@ emu_status_t emu_expert_combine_bwd(int64_t M, int k, int64_t N, const float *dY
  * The modes BF16X9 and TF32X3, with their accuracy; others, and E > 1024, are
  * NOT_SUPPORTED.  E, K, F and N at least 1.  H, Y, D, dZ, dX, dW_in and dW_out
  * start on a 16-byte boundary and have a leading dimension that is a multiple of
- * 4, except in a forward pass of at most 4 E rows, which runs on the CUDA cores
- * (few_rows) within the modes' bounds.
+ * 4.  The products run as BF16X9 in both modes, and a forward pass of few rows for
+ * the weights' size (at most 32768, rows W <= 400e6 + 17.6 E W with W = F (2 K + N))
+ * on the CUDA cores in FP32, within the modes' bounds.
  */
 emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, int E, int64_t K, int64_t F, int64_t N,
                                 const float *X, int64_t ldx, const int32_t *offsets, const float *W_in, int64_t ldwi,
