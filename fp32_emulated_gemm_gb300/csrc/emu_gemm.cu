@@ -1469,10 +1469,11 @@ emu_status_t gemm_grouped(const GroupedGemm* rows, const GroupedGemm* sum, cudaS
         q->epoch = epoch;
         q->group.walks = static_cast<const GroupWalk*>((rows ? rows : sum)->walks);
     }
-    const int64_t stages = rows && sum ? std::max<int64_t>(p.rows.k_stages, sum->rows / sum->groups / BK)
-                           : rows ? p.rows.k_stages : sum->rows / sum->groups / BK;
-    const int pipe = stages >= kLongKMinStages ? PIPE_LONG_K : PIPE_SHORT_K;
     const FusedKind kind = rows && rows->fused ? (FusedKind)rows->fused->kind : FusedKind{};
+    // (FUSED_GATED_BWD's stores take as long as a long k-loop: 12288 rows, 8 experts, K
+    // = 256, F = 1024 backward 306 us with the long-k shape, 299 with the other)
+    const int64_t stages = std::max<int64_t>(rows ? p.rows.k_stages : 0, sum ? sum->rows / sum->groups / BK : 0);
+    const int pipe = stages >= kLongKMinStages && kind != FUSED_GATED_BWD ? PIPE_LONG_K : PIPE_SHORT_K;
     if (log_enabled())
         for (const GroupedGemm* g : {rows, sum})
             if (g)

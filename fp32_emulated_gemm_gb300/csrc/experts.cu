@@ -341,7 +341,7 @@ template <class F> emu_status_t run_products(Aligned& al, F make, const int32_t*
     EMU_TRY(q.run(s, UNTIL_RESERVED));
     int pairs = 0;
     EMU_TRY(grouped_pairs(&pairs));
-    if (pairs > kMaxPairs) return EMU_STATUS_NOT_SUPPORTED;
+    if (pairs < 2 || pairs > kMaxPairs) return EMU_STATUS_NOT_SUPPORTED;  // (two products share them)
     float* scratch = nullptr;
     EMU_TRY(reduce_scratch(dev.id, s, list_floats(q.rows, q.E, q.n * pairs), &scratch));
     EMU_TRY(launched(al.launch(s)));

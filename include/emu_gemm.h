@@ -443,8 +443,8 @@ emu_status_t emu_expert_combine_bwd(int64_t M, int k, int64_t N, const float *dY
  *   X: rows x K; W_in: E matrices of 2F x K, one behind the other (the gate's F
  *   rows, then the up projection's); W_out: E of N x F; H: rows x F; Y: rows x N;
  *   D (rows x 2F, for the backward pass, may be NULL) as in emu_gated_fwd.  Rows
- *   outside the offsets are neither read nor written; offsets that do not ascend
- *   or leave the rows are taken as if clipped.
+ *   outside the offsets are not used (they may hold anything) and not written;
+ *   offsets that do not ascend or leave the rows are taken as if clipped.
  * emu_expert_ffn_bwd -- dZ = [dH | dH] * D with dH = dY W_out[e] (rows x 2F,
  *   written); dX = dZ W_in[e]; over each expert's rows dW_in[e] = dZ^T X and
  *   dW_out[e] = dY^T H (zeros for an expert without rows).  dX, dW_in and dW_out
@@ -455,7 +455,9 @@ emu_status_t emu_expert_combine_bwd(int64_t M, int k, int64_t N, const float *dY
  * start on a 16-byte boundary and have a leading dimension that is a multiple of
  * 4.  The products run as BF16X9 in both modes, and a forward pass of few rows for
  * the weights' size (at most 32768, rows W <= 400e6 + 17.6 E W with W = F (2 K + N))
- * on the CUDA cores in FP32, within the modes' bounds.
+ * on the CUDA cores in FP32, within the modes' bounds.  Buffers: the products take
+ * lists of their tiles (16 bytes for 256 rows and for an expert) and the split-K
+ * workspace with 256 KiB for each CTA pair (19 MiB on 152 SMs).
  */
 emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, int E, int64_t K, int64_t F, int64_t N,
                                 const float *X, int64_t ldx, const int32_t *offsets, const float *W_in, int64_t ldwi,

@@ -726,6 +726,91 @@ def test_training_step_in_a_graph():
     done()
 
 
+def test_training_of_the_module_in_a_graph():
+    """The module's forward and backward pass captured as torch does it: the
+    parameters' gradients of each replay are those of the tokens of the time."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(6)
+    m = emu.EmuExpertFeedForward(48, 40, 5, 2).cuda()
+    x, g = torch.randn(600, 48, device="cuda"), torch.randn(600, 48, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            m.zero_grad(set_to_none=True)
+            m(x).backward(g)
+    torch.cuda.current_stream().wait_stream(s)
+    m.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        y = m(x)
+        y.backward(g)
+    static = {n: p.grad for n, p in m.named_parameters()}
+    for seed in range(3):
+        x.copy_(torch.randn(600, 48, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in static.items()}
+        twin = emu.EmuExpertFeedForward(48, 40, 5, 2).cuda()
+        twin.load_state_dict(m.state_dict())
+        want = twin(x)
+        want.backward(g)
+        assert torch.equal(y, want)
+        for n, p in twin.named_parameters():
+            assert torch.equal(got[n], p.grad), n
+    done()
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_threads_on_one_stream(own_stream):
+    """Several host threads call on one stream: a call's launches, which share the
+    stream's buffers, follow one another."""
+    import contextlib
+    import threading
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+
+    def calls(seed):
+        rng = rng_of("threads", seed)
+        E, K, F, N, M = 4 + seed, 300 + 64 * seed, 260, 301, 900 + 100 * seed
+        logits, x = dev(f32(rng, 9000 + seed, 12)), dev(f32(rng, 2 * M, K))
+        wi, wo, dy = dev(f32(rng, E, 2 * F, K)), dev(f32(rng, E, N, F)), dev(f32(rng, 2 * M, N))
+        plan = emu.expert_route(dev(f32(rng, M, E)), 2)[0]
+        y, d, h = emu.expert_ffn_fwd(x, wi, wo, plan, save=True)
+        rstd = dev(f32(rng, 2 * M))
+        return [lambda: emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan), lambda: [*emu.expert_route(logits, 3)[0][1:]],
+                lambda: emu.rms_norm_bwd(x, x, None, rstd), lambda: [emu.expert_ffn_fwd(x, wi, wo, plan)]]
+
+    sets = [calls(seed) for seed in range(3)]
+    want = [[[t.clone() for t in call()] for call in s] for s in sets]
+    torch.cuda.synchronize()
+    emu.emu_shutdown()                       # the buffers grow again while the threads run
+    stream = torch.cuda.Stream()
+    wrong, start = [], threading.Barrier(len(sets))
+
+    def worker(i):
+        try:
+            with torch.cuda.stream(stream) if own_stream else contextlib.nullcontext():
+                start.wait(60)
+                for rep in range(40):
+                    k = (rep + i) % len(sets[i])
+                    for j, (got, w) in enumerate(zip(sets[i][k](), want[i][k])):
+                        if not torch.equal(got, w):
+                            wrong.append((i, rep, k, j))
+        except Exception as e:
+            wrong.append((i, repr(e)))
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(300)
+    assert not any(t.is_alive() for t in threads)
+    assert not wrong, wrong[:8]
+    assert emu.emu_stream_check(stream if own_stream else None) == 0
+
+
 def test_two_streams_at_once():
     """Two layers on two streams: each has its own buffers."""
     import torch
