@@ -653,12 +653,12 @@ __device__ __forceinline__ void emu_gemm_body(const Params& p) {
     };
     // (m0, n0): this CTA's first row of op(A) and of op(B)^T in the tile
     // (grouped: k0 is the contraction's first row of the stage, `group` the weight)
-    auto issue_load_at = [&](int s, int m0, int n0, int ks, int first = 0, int group = 0) {
+    auto issue_load_at = [&](int s, int m0, int n0, int ks, [[maybe_unused]] int first = 0, [[maybe_unused]] int group = 0) {
         uint64_t* full = &fp32_full[s];
         mbar_arrive_expect_tx(full, KC::FP32_STAGE);
         uint8_t* dA = fp32_ring + s * KC::FP32_STAGE;
         uint8_t* dB = dA + FP32_TILE_BYTES;
-        const int k0 = first + ks * BK;
+        const int k0 = (GROUP == GROUP_SUM ? first : 0) + ks * BK;
         if constexpr (GROUP == GROUP_ROWS) {
             static_assert(GROUP != GROUP_ROWS || !PACKED, "grouped rows: unpacked operands");
             tma_load_2d(dA, &p.tmA, full, k0, m0);
@@ -673,13 +673,14 @@ __device__ __forceinline__ void emu_gemm_body(const Params& p) {
             else for (int j = 0; j < BH / 32; ++j) tma_load_2d(dB + j * 4096, &p.tmB, full, n0 + 32 * j, k0);
         }
     };
-    auto issue_load = [&](int s, const Unit& w, int ks) {
-        const int tile = w.tile;
+    auto issue_load = [&](int s, int tile, int ks) {
+        issue_load_at(s, (tile / p.tiles_n) * TILE_M + HALF * rank, b_row0(tile % p.tiles_n), ks);
+    };
+    auto issue_group_load = [&](int s, const Unit& w, int ks) {
         if constexpr (GROUP == GROUP_ROWS)
-            issue_load_at(s, w.row0 + static_cast<int>(HALF * rank), b_row0(tile), ks, 0, w.group);
+            issue_load_at(s, w.row0 + static_cast<int>(HALF * rank), b_row0(w.tile), ks, 0, w.group);
         else
-            issue_load_at(s, (tile / p.tiles_n) * TILE_M + HALF * rank, b_row0(tile % p.tiles_n), ks,
-                          GROUP == GROUP_SUM ? w.row0 : 0);
+            issue_load_at(s, (w.tile / p.tiles_n) * TILE_M + HALF * rank, b_row0(w.tile % p.tiles_n), ks, w.row0);
     };
     // packed shapes: op(B)'s component tiles of a stage, straight into the
     // component ring (box {32 k, BH rows, 1 component} per component)
@@ -703,16 +704,15 @@ __device__ __forceinline__ void emu_gemm_body(const Params& p) {
         for (int s = 0; s < NB; ++s) { mbar_init(&bcomp_full[s], 1); mbar_init(&bcomp_empty[s], 1); }
         *abort_flag = 0;
         // this pair's walk, worked out once for all roles
-        Walk wk;
-        if constexpr (GROUP != GROUP_NONE) {
+        auto walk_of_pair = [&] {
+            if constexpr (GROUP == GROUP_NONE) return walk_of(p, static_cast<int>(cid), static_cast<int>(ncl));
             griddep_wait();  // the walks may be the previous grid's
             const int4* at = reinterpret_cast<const int4*>(p.group.walks + cid);
             const int4 a = __ldcg(at), b = __ldcg(at + 1);
-            wk.first = a.x; wk.last = a.y; wk.lo = a.z; wk.hi = a.w; wk.step = b.x;
             walk_sh[5] = b.y;
-        } else {
-            wk = walk_of(p, static_cast<int>(cid), static_cast<int>(ncl));
-        }
+            return Walk{a.x, a.y, b.x, a.z, a.w};
+        };
+        const Walk wk = walk_of_pair();
         walk_sh[0] = wk.first; walk_sh[1] = wk.last; walk_sh[2] = wk.step; walk_sh[3] = wk.lo; walk_sh[4] = wk.hi;
         fence_mbar_init();
         // Where the first stages come from depends on the parameters alone:
@@ -797,7 +797,8 @@ __device__ __forceinline__ void emu_gemm_body(const Params& p) {
                 for (int ks = w.kb; ks < w.ke; ++ks, ++n) {
                     if (n >= early) {  // the first `early` loads went out before the pair sync
                         if (!mbar_wait(&fp32_empty[s], ph ^ 1u, abort_flag, budget, 1)) { ok = false; break; }
-                        issue_load(s, w, ks);
+                        if constexpr (GROUP == GROUP_NONE) issue_load(s, w.tile, ks);
+                        else issue_group_load(s, w, ks);
                     }
                     issued_mask |= 1u << s;
                     issued_parity = (issued_parity & ~(1u << s)) | (ph << s);

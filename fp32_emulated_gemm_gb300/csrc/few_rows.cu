@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     const float* W = p.W;
     if (threadIdx.x == 0) griddep_launch_dependents();
     if constexpr (GROUPED) {
-        griddep_wait();  // the offsets and X may be the previous kernel's
+        // (the offsets are there before the kernel that this one may overlap)
         const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
         if (g.y <= 0) return;
         m0 = g.x;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
             for (int j = 0; j < NR; ++j) w[u][j] = load_w<VEC>(wrow[j], at + 128 * u, kend);
     };
     load(c);
-    if constexpr (!GROUPED) griddep_wait();  // X may be the previous kernel's
+    griddep_wait();  // X may be the previous kernel's
     for (int64_t s = s0; s < s1; s += U, c += 128 * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, 2) few_rows_stream_kernel
     constexpr int NR = 4, V = MR * NR, OUT = GATED ? NR / 2 : NR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();  // the offsets and X may be the previous kernel's
+    // (the offsets are there before the kernel that this one may overlap)
     const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
     const int rows = g.y;
     if (rows <= 0) return;
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, 2) few_rows_stream_kernel
     };
     load(w[0]);
     load(w[1]);
+    griddep_wait();  // X may be the previous kernel's
     while (lot < l1) {
         work(w[0]);
         if (lot < l1) work(w[1]);

@@ -43,7 +43,7 @@ struct FewRows {
     ActParams act;
     // Rows in groups, a weight for each (W: one behind the other; no bias, no R):
     // group e has the rows offsets[e] .. offsets[e + 1] (on the device; taken as
-    // ascending and within the M rows).
+    // ascending and within the M rows; with `after_own` they are older than that kernel).
     const int32_t* offsets = nullptr;
     int groups = 0;
 };
