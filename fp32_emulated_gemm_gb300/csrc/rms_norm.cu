@@ -11,7 +11,10 @@
 // FP32's is e4m3's own, and costs no precision: e4m3 is a floating format, the
 // scale only has to keep it in range.
 //
-// Bound by memory: the sum needs one pass, the rows stay in registers.
+// Bound by memory: the sum needs one pass, the rows stay in registers.  The threads'
+// sums of squares are added in two FP32 words, so that a row's mean is off by little
+// more than its rounding: what lies next to one of e4m3's borders is rounded by the
+// last bit of r.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -50,6 +53,42 @@ struct RmsFwd {
 template <int T> constexpr int kStride = T < 32 ? T : 32;
 template <int T, bool VEC> __device__ __forceinline__ int64_t first_col(int t, int i) {
     return (VEC ? 4 * t : T <= 32 ? t : kGroup * (t / 32) + t % 32) + (int64_t)4 * T * i;
+}
+
+// a + b and what its rounding leaves (Knuth's two-sum).
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+// The sum over the T threads of a row, in two words until the last rounding.
+// `flip`: as for row_sum2.
+template <int T> __device__ __forceinline__ float row_sum_exact(float v, int& flip) {
+    float low = 0.f;
+    auto add = [&](float hi, float lo) {
+        const float2 s = two_sum(v, hi);
+        v = s.x;
+        low += lo + s.y;
+    };
+#pragma unroll
+    for (int o = T < 32 ? T / 2 : 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xFFFFFFFFu, v, o), lo = __shfl_xor_sync(0xFFFFFFFFu, low, o);
+        add(hi, lo);
+    }
+    if constexpr (T > 32) {
+        __shared__ float2 part[2][T / 32];
+        float2* p = part[flip];
+        flip ^= 1;
+        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(v, low);
+        __syncthreads();
+        v = p[0].x;
+        low = p[0].y;
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) add(p[i].x, p[i].y);
+    }
+    return v + low;
+}
+__device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps) {
+    return 1.0f / sqrtf(__fadd_rn(__fmul_rn(sum, inv_n), eps));
 }
 
 __device__ __forceinline__ float max4(const float4& v) {
@@ -106,7 +145,7 @@ __global__ void __launch_bounds__(kBlockThreads<T>) rms_fwd_regs_kernel(const __
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) s += fmaf(x[i].x, x[i].x, x[i].y * x[i].y) + fmaf(x[i].z, x[i].z, x[i].w * x[i].w);
-        const float rs = 1.0f / sqrtf(fmaf(row_sum2<T>(s, 0.f, flip).x, inv_n, p.eps));
+        const float rs = rstd_of(row_sum_exact<T>(s, flip), inv_n, p.eps);
         if (p.S) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) store4<VEC, S>(p.S + r * p.lds, first_col<T, VEC>(t, i), n, x[i]);
