@@ -66,7 +66,7 @@ struct Cut {
 __device__ Cut cut_tiles(const GroupedTiles& tiles, int entries, const int4* groups, int64_t total, int pairs) {
     const int64_t n = (int64_t)entries * tiles.per;
     if (n == 0 || pairs == 0) return {n == 0 ? 0.f : 1e30f, 0};
-    const float waves = ceilf((float)n / (float)pairs), shortest = ceilf((float)total / (float)pairs);  // a run on all pairs
+    const float waves = ceilf(__fdividef((float)n, (float)pairs)), shortest = ceilf(__fdividef((float)total, (float)pairs));  // a run on all pairs
     const float longest = (float)tile_length(tiles, groups[0]);  // (sorted)
     float whole = waves * longest;
     if (tiles.sum) {
@@ -78,16 +78,22 @@ __device__ Cut cut_tiles(const GroupedTiles& tiles, int entries, const int4* gro
         }
     }
     Cut best{whole, 0};
-#pragma unroll
+    float best_run = 0.f;
+#pragma unroll 1
     for (int pieces = 0; pieces <= 8; ++pieces) {
-        const float run = pieces == 0 ? shortest : ceilf(longest * (1.f / pieces));
+        const float run = pieces == 0 ? shortest : ceilf(__fdividef(longest, (float)pieces));
         if (run < shortest || run < 2.f) continue;
-        const float cost = run + 1.5f + 2.f * ceilf(longest / run);
-        if (1.03f * cost < best.cost) best = {cost, (int)fminf(ceilf((float)total / run), (float)pairs)};
+        const float cost = run + 1.5f + 2.f * ceilf(__fdividef(longest, run));
+        if (1.03f * cost < best.cost) {
+            best.cost = cost;
+            best_run = run;
+        }
     }
+    if (best_run > 0.f) best.runs = (int)fminf(ceilf((float)total / best_run), (float)pairs);
     return best;
 }
 
+// Threads: at least one an expert (all sums over the experts are one scan) and 256.
 __global__ void __launch_bounds__(kMaxExperts)
 list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_constant__ Walks walks) {
     __shared__ int32_t first[kMaxExperts + 1], start[kMaxExperts + 1], sums[32];
@@ -105,7 +111,7 @@ list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_con
         if (lane == 31) sums[warp] = v;
         __syncthreads();
         if (warp == 0) {
-            int s = sums[lane];
+            int s = lane < (int)blockDim.x / 32 ? sums[lane] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xFFFFFFFFu, s, o);
@@ -133,7 +139,7 @@ list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_con
         if (t == 0) start[0] = 0;
         __syncthreads();
         blocks_total = start[E];
-        for (int i = t; i < blocks_total; i += kMaxExperts) {
+        for (int i = t; i < blocks_total; i += (int)blockDim.x) {
             int lo = 0, hi = E - 1;  // the expert whose blocks hold i: start[e] <= i < start[e + 1]
             while (lo < hi) {
                 const int mid = (lo + hi) / 2;
@@ -182,7 +188,7 @@ list_kernel(const int32_t* offsets, int E, int rows, Lists out, const __grid_con
         }
     }
     __syncthreads();
-    for (int i = t; i < walks.n * walks.pairs; i += kMaxExperts) {
+    for (int i = t; i < walks.n * walks.pairs; i += (int)blockDim.x) {
         const int k = i / walks.pairs, cid = i - k * walks.pairs, second = cid >= split[k];
         const GroupedTiles tiles = walks.tiles[k][second];
         const int pair = cid - (second ? split[k] : 0), pairs = second ? walks.pairs - split[k] : split[k];
@@ -259,7 +265,7 @@ Listed lists_at(float* base, int64_t rows, int E, bool blocks, bool groups) {
 cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, const Lists& out, const Walks& walks, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
-    cfg.blockDim = dim3(kMaxExperts, 1, 1);
+    cfg.blockDim = dim3(E <= 256 ? 256 : kMaxExperts, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
