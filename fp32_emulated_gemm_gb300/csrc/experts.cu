@@ -10,8 +10,8 @@
 // (emu_kernel.cuh): 256-row tiles that end with the expert's rows, listed on the
 // device from the offsets, which never come to the host.  Backward, the products
 // that do not depend on one another share a launch (dZ and dW_out, dX and dW_in).
-// A few rows run on the
-// CUDA cores (few_rows.cu), where each expert's weight is read once.
+// A few rows run on the CUDA cores (few_rows.cu), where each expert's weight is
+// read once.
 //
 // Both modes run as BF16x9, which is within TF32x3's bound too: TF32x3 without an
 // operand split ahead is slower (12288 rows on 8 experts, K = 256, F = 1024, the six
@@ -277,17 +277,33 @@ cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, const List
     return e;
 }
 
-// Few rows for the experts' sizes run on the CUDA cores, on which the weights of the
-// experts that have rows are read once for eight rows.  With W weights an expert
-// that form takes about rows W / 8e6 us, wherever the rows lie, and the tiles 50 us
-// and 2.2 us for a million weights of all experts (measured, tiles / CUDA cores: 8
-// experts, K = 1024, F = 4096, 128 rows 250 / 215 us, 256 rows 255 / 349; K = 256, F =
-// 1024, 256 rows 61 / 34, 512 rows 60 / 59; 64 experts, K = 512, F = 1024, 1024 rows
-// 262 / 216; 16 experts, K = F = 1024, 256 rows 149 / 96, 512 rows 150 / 181).
+// Whether a forward pass runs on the CUDA cores, where the weights of the experts
+// that have rows are read once for eight rows, or in 256-row tiles: the predicted
+// times in us.  The CUDA cores' is the rows' share of each step of 128 of each lot
+// of weight rows and of the lots' sums, and the weights' traffic where L2 does not
+// hold them; the tiles' their lengths (k-stages and stores) over the CTA pairs, or
+// the longest's own, cut in pieces.  Measured, CUDA cores / tiles: 8 experts, K = 1024,
+// F = 4096, 64 rows 125 / 250 us, 256 rows 349 / 255; 8 experts, K = 256, F = 1024, 256
+// rows 32 / 61, 512 rows 58 / 60; 64 experts, K = 512, F = 1024, 512 rows 127 / 242; 16
+// experts, K = F = 1024, 256 rows 95 / 149, 512 rows 180 / 150; 2 experts, K = F = 64,
+// 4096 rows 25 / 34, 16384 rows 74 / 35; 4 experts, K = F = 512, 256 rows 31 / 60, 1024
+// rows 95 / 64.
 constexpr int64_t kFewRowsMost = 32768;
-bool few(int64_t rows, int E, int64_t K, int64_t F, int64_t N) {
-    const double W = (double)F * (2.0 * K + N);
-    return rows <= kFewRowsMost && rows * W <= 400e6 + 17.6 * E * W;
+constexpr int kPairs = 76;
+constexpr double kL2Weights = 25e6;  // weights that stay in L2 beside the rest
+bool few(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs) {
+    if (rows > kFewRowsMost) return false;
+    auto over = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
+    const double T = (double)rows, used = rows < E ? T : (double)E, W = (double)F * (2.0 * K + N);
+    const double lots = 0.5 * F + 0.25 * N, steps = 0.5 * F * over(K, 128) + 0.25 * N * over(F, 128);
+    double cores = 4.0 + T * (3.74e-5 * steps + 3.4e-5 * lots);
+    if (E * W > kL2Weights) cores += (T / 8 + 0.5 * used) * W * 4 / 8e6;
+    const double half = T / 256 + 0.5 * E, tiles = used > half ? used : half;
+    auto product = [&](double columns, double stages) {
+        const double length = stages + 3, share = tiles * columns * length / pairs, least = length < 12 ? length : 12;
+        return 1.44 * (share > least ? share : least);
+    };
+    return cores <= 22.0 + product(over(F, 128), over(K, 32)) + product(over(N, 256), over(F, 32));
 }
 // Lots of weight rows (two of each half, or four) that make the streaming form the
 // faster one (few_rows.cu).
@@ -379,7 +395,7 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const StreamLock lock(s);
     DeviceCtx dev;
-    if (few(rows, E, K, F, N)) {
+    if (few(rows, E, K, F, N, kPairs)) {
         const bool streaming = many_lots(rows, F, N);
         EMU_TRY(current_device(&dev));
         FewRows p{(int)rows, F, K, X, ldx, W_in, ldwi, nullptr, nullptr, 0, D, ldd, H, ldh, act_params(act)};

@@ -116,6 +116,23 @@ def test_rms_norm(M, N, kind):
 
 
 @pytest.mark.parametrize("N", [7, 256, 1001, 5000, 17000])
+def test_rms_norm_quant_keeps_nan_in_its_row(N):
+    """A NaN or an infinity makes its row NaN (as the FP32 output's); the other rows
+    and all scales are as without it."""
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("nanquant", N)
+    x = f32(rng, 5, N)
+    want = [host(t.float()) for t in emu.rms_norm_quant(dev(x), eps=EPS)]
+    x[1, N // 2], x[3, N - 1] = np.nan, INF
+    y = host(emu.rms_norm_fwd(dev(x), eps=EPS, save=False))
+    Q, s = (host(t.float()) for t in emu.rms_norm_quant(dev(x), eps=EPS))
+    done()
+    assert np.isnan(Q[1]).all() and np.isnan(y[1]).all() and np.array_equal(np.isnan(Q[3]), np.isnan(y[3])) and np.isnan(Q[3, N - 1])
+    keep = [0, 2, 4]
+    assert np.array_equal(Q[keep], want[0][keep]) and np.array_equal(s[keep], want[1][keep]) and np.isfinite(s).all()
+
+
+@pytest.mark.parametrize("N", [7, 256, 1001, 5000, 17000])
 def test_rms_norm_hard_rows(N):
     """Rows that are zero, constant, huge, tiny, or hold one outlier; a residual
     that cancels; NaN stays in its row."""
@@ -392,7 +409,7 @@ def expert_reference(x, wi, wo, act, mode, dy=None):
 
 COUNTS = {"one": [1], "few": [1, 0, 2, 0, 0, 1], "few_uneven": [0, 0, 9, 0, 1, 0], "many_for_one": [0, 300, 0, 0],
           "edges": [256, 0, 257, 1, 255, 31, 33], "ragged": [70, 513, 0, 5, 130], "last_empty": [40, 200, 0, 0],
-          "nothing": [0, 0, 0]}
+          "nothing": [0, 0, 0], "tall": [5000, 0, 257, 3300]}
 
 
 @pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
@@ -401,8 +418,8 @@ COUNTS = {"one": [1], "few": [1, 0, 2, 0, 0, 1], "few_uneven": [0, 0, 9, 0, 1, 0
 @pytest.mark.parametrize("counts", COUNTS)
 def test_expert_ffn(counts, K, F, N, act, mode):
     """Rows beyond the last expert's are there too: they hold NaN and stay out.  (The
-    widest with the counts "edges" and "ragged" run in tiles, the others' forward
-    passes on the CUDA cores.)"""
+    forward passes with the counts "tall" run in tiles, most others on the CUDA
+    cores.)"""
     import torch
     import fp32_emulated_gemm_gb300 as emu
     counts = COUNTS[counts]
