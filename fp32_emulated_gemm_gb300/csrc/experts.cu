@@ -10,8 +10,8 @@
 // (emu_kernel.cuh): 256-row tiles that end with the expert's rows, listed on the
 // device from the offsets, which never come to the host.  Backward, the products
 // that do not depend on one another share a launch (dZ and dW_out, dX and dW_in).
-// A few rows run on the CUDA cores (few_rows.cu), where each expert's weight is
-// read once.
+// A few rows run on the CUDA cores (few_rows.cu, few_rows_bwd.cu), where each
+// expert's weight is read once.
 //
 // Both modes run as BF16x9, which is within TF32x3's bound too: TF32x3 without an
 // operand split ahead is slower (12288 rows on 8 experts, K = 256, F = 1024, the six
@@ -24,6 +24,7 @@
 #include "aligned.cuh"
 #include "emu_kernel.cuh"
 #include "few_rows.h"
+#include "few_rows_bwd.h"
 #include "internal.h"
 
 namespace emu {
@@ -305,6 +306,29 @@ bool few(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs) {
     };
     return cores <= 22.0 + product(over(F, 128), over(K, 32)) + product(over(N, 256), over(F, 32));
 }
+// Likewise for a backward pass (few_rows_bwd.cu): the weights read and their gradients
+// written, and the rows' products or, for small weights, the sums' way through an
+// expert's rows; the tiles' two launches, whose length dZ's stores and a sum's few
+// stages make.  Measured, CUDA cores / tiles: 8 experts, K = 256, F = 1024, 8 rows 24 / 81
+// us, 128 rows 56 / 87, 512 rows 134 / 94; 64 experts, K = 512, F = 1024, 64 rows 206 /
+// 309, 512 rows 415 / 456, 1024 rows 634 / 498; 8 experts, K = 1024, F = 4096, 2 rows 132 /
+// 212, 32 rows 318 / 383, 128 rows 604 / 445; 2 experts, K = F = 64, 64 rows 32 / 46, 128
+// rows 54 / 48.
+bool few_bwd(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs) {
+    if (rows > kFewRowsMost) return false;
+    auto over = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
+    const double T = (double)rows, used = rows < E ? T : (double)E, W = (double)F * (2.0 * K + N);
+    const double product = 2.4e-7 * W, latency = 1.1 / E;
+    const double cores = 1.15 * (12.0 + (E + used) * W * 4 / 5.5e6 + T * (product > latency ? product : latency));
+    const double half = T / 256 + 0.5 * E, tiles = used > half ? used : half;
+    const double stages = T / E / 32 < 1 ? 1.0 : T / E / 32;  // a sum's
+    auto launch = [&](double columns, double length, double sums) {
+        const double share = (tiles * columns * length + E * sums * (stages + 3)) / pairs, least = length < 16 ? length : 16;
+        return 1.44 * (share > least ? share : least);
+    };
+    return cores <= 28.0 + launch(over(F, 256), over(N, 32) + 14, over(N, 256) * over(F, 256)) +
+                        launch(over(K, 256), over(2 * F, 32) + 3, over(2 * F, 256) * over(K, 256));
+}
 // Lots of weight rows (two of each half, or four) that make the streaming form the
 // faster one (few_rows.cu).
 bool many_lots(int64_t rows, int64_t F, int64_t N) { return rows * (F / 2 + N / 4) >= 8192; }
@@ -457,6 +481,41 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
     if (dX) al.add(W_in, ldwi, E * 2 * F, K);
     if (dW_in) al.add(X, ldx, rows, K);
     if (dW_out) al.add(H, ldh, rows, F);
+    if (few_bwd(rows, E, K, F, N, kPairs)) {
+        // (the tiles' checks of alignment, for the same contract)
+        if ((inner && !vec4_ok(dZ, lddz)) || !vec4_ok(dX, dX ? lddx : 0) || !vec4_ok(dW_in, dW_in ? lddwi : 0) ||
+            !vec4_ok(dW_out, dW_out ? lddwo : 0))
+            return EMU_STATUS_NOT_SUPPORTED;
+        al.stand_in();  // (the copies' leading dimensions; reserve gives their addresses)
+        EMU_TRY(current_device(&dev));
+        EMU_TRY(al.reserve(s));
+        const int M = (int)rows;
+        // blocks that share a contraction, and the buffer for what they leave
+        const int64_t ldf = (F + 3) & ~int64_t(3), ldk = (K + 3) & ~int64_t(3);
+        const int fs = inner ? few_columns_shares(rows, E, F, N, dev.sm_count) : 1;
+        const int ks = dX ? few_columns_shares(rows, E, K, 2 * F, dev.sm_count) : 1;
+        const size_t floats_f = fs > 1 ? (size_t)fs * rows * ldf : 0, floats_k = ks > 1 ? (size_t)ks * rows * ldk : 0;
+        float* shares = nullptr;
+        if (floats_f || floats_k) EMU_TRY(reduce_scratch(dev.id, s, floats_f > floats_k ? floats_f : floats_k, &shares));
+        EMU_TRY(launched(al.launch(s)));
+        bool after = false;
+        if (inner) {
+            EMU_TRY(launched(launch_few_columns({M, E, offsets, F, N, dY, lddy, W_out, ldwo, D, ldd, dZ, lddz, shares, ldf}, fs,
+                                                after, s)));
+            after = true;
+        }
+        if (dW_out) {
+            EMU_TRY(launched(launch_few_sums({M, E, offsets, N, F, dY, lddy, H, ldh, dW_out, lddwo}, after, s)));
+            after = true;
+        }
+        if (dX) {
+            EMU_TRY(launched(launch_few_columns({M, E, offsets, K, 2 * F, dZ, lddz, W_in, ldwi, nullptr, 0, dX, lddx, shares,
+                                                 ldk}, ks, after, s)));
+            after = true;
+        }
+        if (dW_in) EMU_TRY(launched(launch_few_sums({M, E, offsets, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi}, after, s)));
+        return EMU_STATUS_SUCCESS;
+    }
     Fused f{};
     auto products = [&] {
         f = {FUSED_GATED_BWD, ACT_NONE, nullptr, 0, const_cast<float*>(D), ldd, nullptr};

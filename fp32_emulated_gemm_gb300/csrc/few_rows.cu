@@ -23,6 +23,7 @@
 
 #include <type_traits>
 
+#include "group_rows.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "row_ops.cuh"
@@ -64,43 +65,6 @@ template <int V> __device__ __forceinline__ void warp_sums(float (&v)[V], int la
             v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
         }
     }
-}
-
-// The `at`-th of the blocks of MR rows at most that the groups' rows make, group by
-// group: {first row, rows (0: there are fewer blocks), group}.  Each warp finds it
-// for itself, 32 groups at a time: about 0.3 us, where a kernel of its own for a
-// list of the blocks took 3.
-__device__ __forceinline__ int3 rows_of_block(const int32_t* offsets, int groups, int M, int MR, int at) {
-    const int lane = threadIdx.x & 31;
-    int last = min(max(__ldcg(offsets), 0), M);  // where the groups so far end
-    for (int base = 0; base < groups; base += 32) {
-        // ends, made ascending
-        int end = base + lane < groups ? min(max(__ldcg(offsets + base + lane + 1), 0), M) : 0;
-        end = max(end, last);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xFFFFFFFFu, end, o);
-            if (lane >= o) end = max(end, up);
-        }
-        const int prev = __shfl_up_sync(0xFFFFFFFFu, end, 1), first = lane == 0 ? last : prev;
-        const int n = (end - first + MR - 1) / MR;
-        int through = n;  // blocks of this group and those before it
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xFFFFFFFFu, through, o);
-            if (lane >= o) through += up;
-        }
-        const unsigned mine = __ballot_sync(0xFFFFFFFFu, at < through);
-        if (mine) {
-            const int src = __ffs(mine) - 1;
-            const int f = __shfl_sync(0xFFFFFFFFu, first, src), e = __shfl_sync(0xFFFFFFFFu, end, src);
-            const int b = at - __shfl_sync(0xFFFFFFFFu, through - n, src);
-            return make_int3(f + b * MR, min(MR, e - f - b * MR), base + src);
-        }
-        at -= __shfl_sync(0xFFFFFFFFu, through, 31);
-        last = __shfl_sync(0xFFFFFFFFu, end, 31);
-    }
-    return make_int3(0, 0, 0);
 }
 
 // MR: rows of X (M of them real), NR: rows of W per warp (gated: NR / 2 of the

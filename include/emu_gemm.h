@@ -453,8 +453,8 @@ emu_status_t emu_expert_combine_bwd(int64_t M, int k, int64_t N, const float *dY
  * The modes BF16X9 and TF32X3, with their accuracy; others, and E > 1024, are
  * NOT_SUPPORTED.  E, K, F and N at least 1.  H, Y, D, dZ, dX, dW_in and dW_out
  * start on a 16-byte boundary and have a leading dimension that is a multiple of
- * 4.  The products run as BF16X9 in both modes, and a forward pass of few rows for
- * the weights' size (at most 32768; where that is predicted faster, from the sizes
+ * 4.  The products run as BF16X9 in both modes, and those of few rows for the
+ * weights' size (at most 32768; where that is predicted faster, from the sizes
  * alone) on the CUDA cores in FP32, within the modes' bounds.  Buffers: the products take
  * lists of their tiles (16 bytes for 256 rows and for an expert) and the split-K
  * workspace with 256 KiB for each CTA pair (19 MiB on 152 SMs).
