@@ -475,6 +475,47 @@ def test_expert_ffn_uneven_experts(E, K, F, N, most):
             w.check(g, f"expert {e} {name}")
 
 
+@pytest.mark.parametrize("counts,K,F,N", [([1, 0, 0, 0, 0, 0, 0, 1], 700, 1500, 1026), ([0, 3, 1, 0], 1030, 2050, 515),
+                                          ([0, 3, 2, 4], 1030, 2050, 515), ([0, 13, 3], 515, 1030, 771), ([9, 0, 2, 1, 0], 300, 1111, 2300),
+                                          ([0] * 20 + [1] + [0] * 11 + [2], 260, 700, 1300)])
+def test_expert_ffn_few_rows_of_long_contractions(counts, K, F, N):
+    """The CUDA cores' backward products, several blocks to a contraction, with rows
+    before and behind the experts'; the same results from a graph and in each wanted
+    gradient alone."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("long", sum(counts), K, F)
+    E, offsets = len(counts), 1 + np.concatenate([[0], np.cumsum(counts)])
+    rows = int(offsets[-1]) + 1
+    x, dy = f32(rng, rows, K), f32(rng, rows, N)
+    x[0], dy[0], x[-1], dy[-1] = (np.nan,) * 4
+    wi, wo = f32(rng, E, 2 * F, K, std=K ** -0.5), f32(rng, E, N, F, std=F ** -0.5)
+    plan = emu.ExpertPlan(None, None, None, ints(offsets))
+    X, DY, WI, WO = dev(x), dev(dy), dev(wi), dev(wo)
+    y, d, h = emu.expert_ffn_fwd(X, WI, WO, plan, save=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = emu.expert_ffn_bwd(DY, X, WI, WO, d, h, plan)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        replayed = emu.expert_ffn_bwd(DY, X, WI, WO, d, h, plan)
+    graph.replay()
+    done()
+    alone = [emu.expert_ffn_bwd(DY, X, WI, WO, d if i < 2 else None, h if i == 2 else None, plan, need=[j == i for j in range(3)])[i]
+             for i in range(3)]
+    done()
+    own = slice(int(offsets[0]), int(offsets[-1]))
+    for a, b, c in zip(got, replayed, alone):
+        cut = own if a.shape[0] == rows else slice(None)
+        assert torch.equal(a[cut], b[cut]) and torch.equal(a[cut], c[cut])
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        want = expert_reference(x[r], wi[e], wo[e], "silu", "bf16x9", dy[r])
+        for g, w, name in zip((y[r], h[r], got[0][r], got[1][e], got[2][e]), want, ("Y", "H", "dX", "dW_in", "dW_out")):
+            w.check(host(g), f"expert {e} {name}")
+
+
 def test_expert_ffn_only_wanted_gradients():
     import torch
     import fp32_emulated_gemm_gb300 as emu
@@ -878,6 +919,32 @@ def test_allocation_failure_enqueues_nothing():
     for _, call in calls:
         call()
     done()
+
+
+def test_allocation_failure_of_the_backward_buffers_enqueues_nothing():
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("allocb")
+    E, K, F, N, rows = 4, 515, 1030, 771, 8   # (few rows: copies of odd operands, shares of contractions)
+    o = ints([0, 3, 3, 4, 8])
+    x, dy, wi, wo, d, h = (dev(f32(rng, *s)) for s in ((rows, K), (rows, N), (E, 2 * F, K), (E, N, F), (rows, 2 * F), (rows, F)))
+    new = lambda r, c: torch.full((r, c), 7.0, device="cuda")
+    dz, dx, dwi, dwo = new(rows, 2 * F), new(rows, 516), new(E * 2 * F, 516), new(E * N, 1032)
+    call = lambda: emu.emu_expert_ffn_bwd(0, rows, E, K, F, N, dy, N, x, K, o, wi, K, wo, F, d, 2 * F, h, F, dz, 2 * F, dx, 516, dwi,
+                                          516, dwo, 1032)
+    emu.emu_shutdown()
+    emu.emu_debug_fail_allocations(1)
+    try:
+        with pytest.raises(emu.EmuError) as e:
+            call()
+        assert e.value.status == 4
+    finally:
+        emu.emu_debug_fail_allocations(0)
+    done()
+    assert all(bool((t == 7).all()) for t in (dz, dx, dwi, dwo))
+    call()
+    done()
+    assert not any(bool((t[:, :c] == 7).any()) for t, c in ((dz, 2 * F), (dx, K), (dwi, K), (dwo, F)))
 
 
 def test_refusals():
