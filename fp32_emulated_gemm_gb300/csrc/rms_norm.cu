@@ -60,8 +60,9 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
     return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
-// The sum over the T threads of a row, in two words until the last rounding.
-// `flip`: as for row_sum2.
+// The sum over the T threads of a row, in two words until the last rounding (none
+// of a sum that is infinite or NaN, whose second word is NaN).  `flip`: as for
+// row_sum2.
 template <int T> __device__ __forceinline__ float row_sum_exact(float v, int& flip) {
     float low = 0.f;
     auto add = [&](float hi, float lo) {
@@ -85,7 +86,7 @@ template <int T> __device__ __forceinline__ float row_sum_exact(float v, int& fl
 #pragma unroll
         for (int i = 1; i < T / 32; ++i) add(p[i].x, p[i].y);
     }
-    return v + low;
+    return fabsf(v) < INFINITY ? v + low : v;
 }
 __device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps) {
     return 1.0f / sqrtf(__fadd_rn(__fmul_rn(sum, inv_n), eps));

@@ -117,8 +117,8 @@ def test_rms_norm(M, N, kind):
 
 @pytest.mark.parametrize("N", [7, 256, 1001, 5000, 17000])
 def test_rms_norm_quant_keeps_nan_in_its_row(N):
-    """A NaN or an infinity makes its row NaN (as the FP32 output's); the other rows
-    and all scales are as without it."""
+    """A NaN makes its row NaN, an infinity itself (as the FP32 output's); the other
+    rows and all scales are as without them."""
     import fp32_emulated_gemm_gb300 as emu
     rng = rng_of("nanquant", N)
     x = f32(rng, 5, N)
@@ -156,6 +156,26 @@ def test_rms_norm_hard_rows(N):
         ref.check(host(got), name)
     assert not np.any(host(cancel[0])) and not np.any(host(cancel[1]))
     assert np.isnan(yb[3]).all() and np.array_equal(np.delete(yb, 3, 0), np.delete(host(y), 3, 0))
+
+
+@pytest.mark.parametrize("N", [7, 256, 1001, 5000, 17000])
+def test_rms_norm_of_rows_whose_squares_overflow(N):
+    """The sum of squares is infinite: 1 / sqrt of it is 0, and so are the row, its
+    gradient and its part of the weight's; an infinity itself becomes NaN."""
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("overflow", N)
+    x, dy = f32(rng, 4, N), f32(rng, 4, N)
+    x[1, N // 2], x[2], x[3, 0] = 1e30, 1.7e19, INF   # (one square beyond FP32's range; the sum of all; infinity)
+    y, s, rstd = emu.rms_norm_fwd(dev(x), eps=EPS)
+    Q, scales = emu.rms_norm_quant(dev(x), eps=EPS)
+    dx, dw = emu.rms_norm_bwd(dev(dy[:3]), s[:3], None, rstd[:3])
+    dx0, dw0 = emu.rms_norm_bwd(dev(dy[:1]), s[:1], None, rstd[:1])
+    done()
+    y, Q, r = host(y), host(Q.float()), host(rstd)
+    assert np.isfinite(r).all() and not r[1:].any() and r[0] > 0
+    assert not y[1:3].any() and not Q[1:3].any() and not y[3, 1:].any() and np.isnan(y[3, 0]) and np.isnan(Q[3, 0])
+    assert np.isfinite(host(scales)).all()
+    assert not host(dx)[1:].any() and np.array_equal(host(dx)[0], host(dx0)[0]) and np.array_equal(host(dw), host(dw0))
 
 
 def test_rms_norm_many_rows_and_repeatable():
