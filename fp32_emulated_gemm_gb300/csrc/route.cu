@@ -438,6 +438,13 @@ bool sizes_ok(int64_t M, int E, int k) {
     return E <= kMaxExperts && k <= kMaxChoices && M <= (INT32_MAX - 256) / (k > 0 ? k : 1);
 }
 
+// What a launch may have without being asked for is 48 KB (682 experts); beyond it
+// the current device is asked, call by call.
+template <class K> emu_status_t allow_smem(K kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return EMU_STATUS_SUCCESS;
+    return launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+}
+
 template <int WAY> emu_status_t route(Route p, emu_stream_t stream) {
     DeviceCtx dev;
     emu_status_t st = current_device(&dev);
@@ -446,17 +453,13 @@ template <int WAY> emu_status_t route(Route p, emu_stream_t stream) {
     const size_t smem = smem_of(p.E);
     const StreamLock lock(s);
     if (p.M * p.k <= kSmallChoices && (WAY == SORT || p.M * p.E <= kSmallLogits)) {
-        static const cudaError_t attr = cudaFuncSetAttribute(
-            route_small_kernel<WAY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxExperts));
-        if (attr != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
+        EMU_TRY(allow_smem(route_small_kernel<WAY>, smem));
         cudaGetLastError();
         route_small_kernel<WAY><<<1, kThreads, smem, s>>>(p);
         return launched(cudaGetLastError());
     }
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxExperts));
     static const int resident = resident_blocks(choose_kernel<WAY>, kThreads);
-    if (attr != cudaSuccess) return EMU_STATUS_LAUNCH_FAILED;
+    EMU_TRY(allow_smem(place_kernel, smem));
     // choosing: a pass over the tokens that are resident at once, or several of equal
     // length; placing: no more blocks than keep the histograms, which each of them
     // reads, fewer than the choices
