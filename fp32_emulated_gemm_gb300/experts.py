@@ -481,11 +481,15 @@ class EmuExpertFFN(torch.nn.Module):
 
     def forward(self, x, residual=None, mask=None):
         """`mask` (x's shape without the features, False for padded tokens): tokens
-        that go to no expert and get the residual alone."""
+        that go to no expert and get the residual alone.  What they hold, NaN too,
+        reaches no other token and no weight's gradient."""
         rows, residual, shape = _flat(x, residual, self.in_features, self.out_features)
+        if mask is not None:
+            closed = ~_token_mask(mask, x)[:, None]
+            rows = rows.masked_fill(closed, 0.0)   # (the router's weight gradient has them times 0)
         logits = self.router(rows)
         if mask is not None:
-            logits = logits.masked_fill(~_token_mask(mask, x)[:, None], float("-inf"))
+            logits = logits.masked_fill(closed, float("-inf"))
         y = EmuExpertFFNFunction.apply(rows, logits, self.weight_in, self.weight_out, residual, self.k, self.over, self.act,
                                        self.mode)
         return y.reshape(shape)
@@ -504,5 +508,9 @@ class EmuExpertFeedForward(torch.nn.Module):
 
     def forward(self, x, mask=None):
         rows, _, shape = _flat(x, None, self.norm.features, self.norm.features)
-        y, s = EmuRMSNormFunction.apply(rows, self.norm.weight, None, self.norm.eps)
-        return self.ffn(y, residual=s, mask=None if mask is None else _token_mask(mask, x)).reshape(shape)
+        if mask is None:
+            y, s = EmuRMSNormFunction.apply(rows, self.norm.weight, None, self.norm.eps)
+        else:   # (what padded tokens hold stays out of the norm's weight gradient too)
+            mask, s = _token_mask(mask, x), rows
+            y = self.norm(rows.masked_fill(~mask[:, None], 0.0))
+        return self.ffn(y, residual=s, mask=mask).reshape(shape)

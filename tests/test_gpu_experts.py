@@ -408,6 +408,125 @@ def test_exchange_leaves_out_wrong_slots():
     assert torch.equal(buf, want) and torch.equal(y, rows)
 
 
+@pytest.mark.parametrize("M,E,k", [(7, 1024, 2), (8, 1000, 9), (5, 700, 1)])
+def test_many_experts_and_few_tokens(M, E, k):
+    """One block, whose counts of all experts take more shared memory than a launch
+    has by itself."""
+    import fp32_emulated_gemm_gb300 as emu
+    l = f32(rng_of("fewmany", M, E), M, E)
+    plan, w = emu.expert_route(dev(l), k)
+    done()
+    experts, want = route_oracle(l, k, "chosen")
+    check_plan(plan, experts, E)
+    want.check(host(w), "weights")
+
+
+# ---------------------------------------- offsets that 32 bits do not hold --
+def last(n, count=64):
+    """Places among n: the first, some between, the last ones."""
+    return np.unique(np.concatenate([[0, 1, n // 2], np.arange(n - count, n)]))
+
+
+def test_rms_norm_beyond_32_bits():
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    M, N = 1100000, 2048
+    x = torch.randn(M, N, device="cuda")
+    w = torch.randn(N, device="cuda")
+    y, s, rstd = emu.rms_norm_fwd(x, w, residual=x, eps=EPS)
+    Q, scales = emu.rms_norm_quant(x, w, residual=x, eps=EPS)[:2]
+    at = torch.from_numpy(last(M)).cuda()
+    xs = host(x[at])
+    want, s64, r = rms_norm(xs, xs, host(w))
+    assert np.array_equal(host(s[at]), s64.val.astype(np.float32))
+    want.check(host(y[at]), "Y")
+    check_quant(want, host(Q[at].float()).astype(np.float64), host(scales[at]))
+    del y, Q
+    dx, dw = emu.rms_norm_bwd(x, s, w, rstd, add=x)
+    rms_grads(xs, s64.val, host(w), host(rstd[at]).astype(np.float64), xs)[0].check(host(dx[at]), "dX")
+    # dweight, here the sum of 2 x^2 rstd: chains of at most 4096 positive terms (a block's rows, then the blocks)
+    size = sum((2 * x[i:i + 50000].double().square() * rstd[i:i + 50000, None].double()).sum(0) for i in range(0, M, 50000))
+    done()
+    assert float(((dw.double() - size) / size).abs().max()) < 4100 * U
+
+
+def test_route_and_exchange_beyond_32_bits():
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    M, E, k = 2200000, 1000, 2
+    logits = torch.randn(M, E, device="cuda")
+    plan, w = emu.expert_route(logits, k)
+    at = torch.from_numpy(last(M)).cuda()
+    experts, want = route_oracle(host(logits[at]), k, "chosen")
+    assert np.array_equal(host(plan.experts[at]), experts)
+    want.check(host(w[at]), "weights")
+    check_plan(plan, host(plan.experts), E)
+    dl = emu.expert_route_bwd(torch.ones_like(w), logits, plan, w)
+    done()
+    assert float(dl[at].abs().max()) <= 8 * U
+    del dl, logits
+    N = 512                                  # M k N > 2^31
+    x = torch.randn(M, N, device="cuda")
+    xs = emu.expert_dispatch(x, plan)
+    rows = torch.from_numpy(last(M * k)).cuda()
+    assert torch.equal(xs[rows], x[plan.sources[rows].long() // k]) and torch.equal(xs[plan.slots[at].long()], x[at, None].expand(-1, k, -1))
+    y = emu.expert_combine_fwd(xs, plan, w, residual=x)
+    dys, dw = emu.expert_combine_bwd(x, xs, plan, w)
+    done()
+    xa, wa = x[at].double(), w[at].double()
+    assert bool(((y[at].double() - xa * (1 + wa.sum(1, keepdim=True))).abs() <= 6 * U * xa.abs() * 2).all())
+    assert torch.equal(dys[plan.slots[at].long()], w[at][..., None] * x[at, None])
+    n2 = xa.square().sum(1, keepdim=True)
+    assert bool(((dw[at].double() - n2).abs() <= 40 * U * n2).all())     # chains of N / 32 + 8 positive terms
+
+
+def test_expert_ffn_of_rows_beyond_32_bits():
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(3)
+    rows, K, F, N, E = 1100000, 8, 1024, 12, 3             # rows 2F > 2^31
+    offsets = [0, 1099000, 1099700, rows]
+    x, dy = torch.randn(rows, K, device="cuda"), torch.randn(rows, N, device="cuda")
+    wi, wo = torch.randn(E, 2 * F, K, device="cuda") / K ** 0.5, torch.randn(E, N, F, device="cuda") / F ** 0.5
+    plan = emu.ExpertPlan(None, None, None, ints(offsets))
+    y, d, h = emu.expert_ffn_fwd(x, wi, wo, plan, save=True)
+    dx, dwi, dwo = emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan)
+    done()
+    for e in range(E):
+        r = slice(max(offsets[e], offsets[e + 1] - 400), offsets[e + 1])
+        want = expert_reference(host(x[r]), host(wi[e]), host(wo[e]), "silu", "bf16x9", host(dy[r]))
+        for got, ref, name in zip((y[r], h[r], dx[r]), want, ("Y", "H", "dX")):
+            ref.check(host(got), f"expert {e} {name}")
+    r = slice(offsets[2], rows)
+    want = expert_reference(host(x[r]), host(wi[2]), host(wo[2]), "silu", "bf16x9", host(dy[r]))
+    want[3].check(host(dwi[2]), "dW_in")
+    want[4].check(host(dwo[2]), "dW_out")
+
+
+@pytest.mark.parametrize("counts", [[2, 0, 3], [39800, 0, 200]])
+def test_expert_ffn_of_weights_beyond_32_bits(counts):
+    """On the CUDA cores, and in tiles."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(4)
+    E, K, F, N = 600, 1800, 1024, 8                        # E 2F K > 2^31
+    first, _, tail = counts
+    rows = first + tail
+    offsets = np.full(E + 1, first)
+    offsets[0], offsets[-1] = 0, rows
+    x, dy = torch.randn(rows, K, device="cuda"), torch.randn(rows, N, device="cuda")
+    wi, wo = torch.randn(E, 2 * F, K, device="cuda") / K ** 0.5, torch.randn(E, N, F, device="cuda") / F ** 0.5
+    plan = emu.ExpertPlan(None, None, None, ints(offsets))
+    y, d, h = emu.expert_ffn_fwd(x, wi, wo, plan, save=True)
+    dx, dwi, dwo = emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan)
+    done()
+    r = slice(first, rows)
+    want = expert_reference(host(x[r]), host(wi[-1]), host(wo[-1]), "silu", "bf16x9", host(dy[r]))
+    for got, ref, name in zip((y[r], h[r], dx[r], dwi[-1], dwo[-1]), want, ("Y", "H", "dX", "dW_in", "dW_out")):
+        ref.check(host(got), name)
+    assert not bool(dwi[1:-1].any()) and not bool(dwo[1:-1].any())
+
+
 # ---------------------------------------------------------------- experts --
 def expert_reference(x, wi, wo, act, mode, dy=None):
     """One expert's rows: (Y, D halves, H) and with dy (dX, dW_in, dW_out)."""
@@ -670,6 +789,31 @@ def test_sub_layer_and_its_gradients(M, over, mode, masked):
         assert float((a - b).abs().max()) <= 1e-5 * float(b.abs().max()), name
     if mask is not None:
         assert torch.equal(y.detach()[~mask], x.detach()[~mask])
+
+
+@pytest.mark.parametrize("M,over", [(300, "chosen"), (5, "all")])
+@pytest.mark.parametrize("fill", [float("nan"), INF, -3e38])
+def test_padded_tokens_reach_nothing(M, over, fill):
+    """Whatever padded tokens and their gradients hold: the others' outputs and
+    gradients and the weights' gradients are those of zeros in their place."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    torch.manual_seed(M)
+    for layer in (emu.EmuExpertFeedForward(48, 40, 6, 2, over=over).cuda(), emu.EmuExpertFFN(48, 40, 6, 2, over=over).cuda()):
+        mask = torch.arange(M, device="cuda") % 3 != 1
+        x, g = torch.randn(M, 48, device="cuda"), torch.randn(M, 48, device="cuda")
+        results = []
+        for value in (0.0, fill):
+            a = x.masked_fill(~mask[:, None], value).requires_grad_()
+            y = layer(a, mask=mask)
+            layer.zero_grad()
+            y.backward(g.masked_fill(~mask[:, None], value))
+            results.append([y.detach()[mask], a.grad[mask]] + [p.grad.clone() for p in layer.parameters()])
+            with torch.no_grad():
+                assert torch.equal(layer(a, mask=mask)[mask], y.detach()[mask])
+        done()
+        for want, got in zip(*results):
+            assert bool(torch.isfinite(want).all()) and torch.equal(want, got)
 
 
 def test_sub_layer_against_differences():
