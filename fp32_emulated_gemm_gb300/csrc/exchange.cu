@@ -7,9 +7,10 @@
 //                that is dispatch's gradient too
 //   combine_bwd  dYs[slots[m, j]] = w[m, j] dY[m], rows without a source 0;
 //                dw[m, j] = <dY[m], Ys[slots[m, j]]>
-// Bound by memory.  All go through the tokens, T lanes each: a token's row is
-// read once for its k copies, which are whole rows wherever they lie, and the
-// sum over the choices is one thread's, in order: no atomics.
+// Bound by memory.  All go through the tokens, T lanes each (a block for each of a
+// few wide ones): a token's row is read once for its k copies, which are whole rows
+// wherever they lie, and the sum over the choices is one thread's, in order: no
+// atomics.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -94,13 +95,15 @@ __device__ __forceinline__ float dot4(const float4& a, const float4& b) {
     return fmaf(a.x, b.x, a.y * b.y) + fmaf(a.z, b.z, a.w * b.w);
 }
 
-// BWD: scaled by the weights, with their gradients.
-template <int T, int NV, bool VEC, bool BWD>
+// S groups of T lanes share a token's columns.  BWD: scaled by the weights, with
+// their gradients.
+template <int T, int NV, int S, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ Exchange p) {
-    constexpr int kMine = BWD ? (kMaxChoices + T - 1) / T : 1;
-    const int t = threadIdx.x % T;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / T);
-    int64_t m = blockIdx.x * (int64_t)(kThreads / T) + threadIdx.x / T;
+    constexpr int kMine = BWD ? (kMaxChoices + T - 1) / T : 1, kTokens = kThreads / T / S;
+    static_assert(S == 1 || T == 32, "the shared sums: a warp's lanes have a choice each");
+    const int t = threadIdx.x % T, share = threadIdx.x / T % S;
+    const int64_t step = (int64_t)gridDim.x * kTokens, first = share * (4 * T * NV);
+    int64_t m = blockIdx.x * (int64_t)kTokens + threadIdx.x / (T * S);
     Slots<T> slots(p, m);
     float4 x[NV], ahead[NV];  // the token's row, and its first columns of the next token's
     auto load = [&](int64_t row, int64_t c0, float4 (&v)[NV]) {
@@ -108,18 +111,18 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
         for (int i = 0; i < NV; ++i)
             v[i] = load4<VEC, T>(p.A + row * p.lda, c0 + (VEC ? 4 * t : t) + 4 * T * i, row < p.M ? p.N : 0);
     };
-    load(m, 0, ahead);
-    // (the loop is the same for all lanes of a warp: shuffles)
-    for (int64_t base = blockIdx.x * (int64_t)(kThreads / T); base < p.M; base += step, m += step) {
+    load(m, first, ahead);
+    // (the loop is the same for all threads of a block: shuffles and barriers)
+    for (int64_t base = blockIdx.x * (int64_t)kTokens; base < p.M; base += step, m += step) {
         slots.advance(m + step);
         const bool real = m < p.M;
         float mine[kMine] = {};  // dw of the choices t, t + T, ...
-        for (int64_t c0 = 0; c0 < p.N; c0 += 4 * T * NV) {
+        for (int64_t c0 = first; c0 < p.N; c0 += 4 * T * NV * S) {
             const int64_t at = c0 + (VEC ? 4 * t : t);
-            if (c0 == 0) {
+            if (c0 == first) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) x[i] = ahead[i];
-                load(m + step, 0, ahead);
+                load(m + step, first, ahead);
             } else {
                 load(m, c0, x);
             }
@@ -172,7 +175,18 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
             }
         }
         if constexpr (BWD) {
-            if (p.dweights && real) {
+            if constexpr (S > 1) {
+                if (p.dweights) {  // the shares' sums, added in order
+                    __shared__ float sums[kTokens][S][T];
+                    float* mine_of = sums[threadIdx.x / (T * S)][0];
+                    mine_of[share * T + t] = mine[0];
+                    __syncthreads();
+#pragma unroll
+                    for (int q = 1; q < S; ++q) mine[0] = q == 1 ? mine_of[t] + mine_of[T + t] : mine[0] + mine_of[q * T + t];
+                    __syncthreads();
+                }
+            }
+            if (p.dweights && real && share == 0) {
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
                     if (t + T * i < p.k) p.dweights[m * p.k + t + T * i] = mine[i];
@@ -182,16 +196,17 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
     if (p.C) clear_rows<VEC>(p);
 }
 
-template <int T, int NV, bool VEC>
+template <int T, int NV, int S, bool VEC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ Exchange p) {
-    const int t = threadIdx.x % T;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / T);
-    int64_t m = blockIdx.x * (int64_t)(kThreads / T) + threadIdx.x / T;
+    constexpr int kTokens = kThreads / T / S;
+    const int t = threadIdx.x % T, share = threadIdx.x / T % S;
+    const int64_t step = (int64_t)gridDim.x * kTokens;
+    int64_t m = blockIdx.x * (int64_t)kTokens + threadIdx.x / (T * S);
     Slots<T> slots(p, m);
-    for (int64_t base = blockIdx.x * (int64_t)(kThreads / T); base < p.M; base += step, m += step) {
+    for (int64_t base = blockIdx.x * (int64_t)kTokens; base < p.M; base += step, m += step) {
         slots.advance(m + step);
         const int64_t real = m < p.M ? p.N : 0;
-        for (int64_t c0 = 0; c0 < p.N; c0 += 4 * T * NV) {
+        for (int64_t c0 = share * (4 * T * NV); c0 < p.N; c0 += 4 * T * NV * S) {
             const int64_t at = c0 + (VEC ? 4 * t : t);
             float4 s[NV], r[NV];
 #pragma unroll
@@ -228,16 +243,26 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
     }
 }
 
-template <class F> void for_width(int64_t N, F f) {
-    auto of = [&](auto T, auto NV) { f(T, NV); };
+// f(T, NV, S) for the sizes.  Few tokens have a block each, whose warps share the
+// columns: dispatch, combine, backward of 64 tokens of 4096, k = 8, 19, 22.5 and 29.6
+// us with a warp a token, 4.2, 4.7 and 6.1 with a block; 596 of 3104, k = 7, 15.6, 18.2,
+// 39.3 and 9.1, 8.1, 20.0; 1000 of 4096, k = 2, 7.6, 10.0, 12.7 and 7.5, 7.5, 11.0, but 1000
+// of 256, k = 2, 2.6, 2.3, 3.2 and 3.4, 3.4, 4.6, and 2400 of 2048 8.1, 7.2, 11.5 and
+// 8.0, 9.5, 16.7.
+template <class F> void for_width(int64_t M, int64_t N, int sm_count, F f) {
     using std::integral_constant;
-#define EMU_WIDTH(T, NV) of(integral_constant<int, T>{}, integral_constant<int, NV>{})
-    if (N <= 16) EMU_WIDTH(4, 1);
-    else if (N <= 32) EMU_WIDTH(8, 1);
-    else if (N <= 64) EMU_WIDTH(16, 1);
-    else if (N <= 128) EMU_WIDTH(32, 1);
-    else if (N <= 256) EMU_WIDTH(32, 2);
-    else EMU_WIDTH(32, 4);
+#define EMU_WIDTH(T, NV, S) f(integral_constant<int, T>{}, integral_constant<int, NV>{}, integral_constant<int, S>{})
+    if (N <= 16) EMU_WIDTH(4, 1, 1);
+    else if (N <= 32) EMU_WIDTH(8, 1, 1);
+    else if (N <= 64) EMU_WIDTH(16, 1, 1);
+    else if (N <= 128) EMU_WIDTH(32, 1, 1);
+    else if (M <= (N <= 1024 ? 4 : 8) * (int64_t)sm_count) {
+        if (N <= 1024) EMU_WIDTH(32, 1, 8);
+        else if (N <= 2048) EMU_WIDTH(32, 2, 8);
+        else EMU_WIDTH(32, 4, 8);
+    }
+    else if (N <= 256) EMU_WIDTH(32, 2, 1);
+    else EMU_WIDTH(32, 4, 1);
 #undef EMU_WIDTH
 }
 
@@ -257,17 +282,17 @@ emu_status_t launch(Kind kind, const Exchange& p, emu_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool vec = (p.N & 3) == 0 && vec4_ok(p.A, p.lda) && vec4_ok(p.R, p.R ? p.ldr : 0) && vec4_ok(p.C, p.C ? p.ldc : 0);
     cudaGetLastError();
-    for_width(p.N, [&](auto T, auto NV) {
-        constexpr int t = decltype(T)::value, nv = decltype(NV)::value;
-        const int64_t groups = (p.M + kThreads / t - 1) / (kThreads / t);
+    for_width(p.M, p.N, dev.sm_count, [&](auto T, auto NV, auto S) {
+        constexpr int t = decltype(T)::value, nv = decltype(NV)::value, s_ = decltype(S)::value, tokens = kThreads / t / s_;
+        const int64_t groups = (p.M + tokens - 1) / tokens;
         auto run = [&](auto kernel, int per_sm) {
             const int64_t most = (int64_t)dev.sm_count * per_sm, turns = (groups + most - 1) / most;
             kernel<<<(unsigned)((groups + turns - 1) / turns), kThreads, 0, s>>>(p);
         };
         auto go = [&](auto VEC) {
             constexpr bool v = decltype(VEC)::value;
-            constexpr auto dispatch = dispatch_kernel<t, nv, v, false>, back = dispatch_kernel<t, nv, v, true>;
-            constexpr auto combine = combine_kernel<t, nv, v>;
+            constexpr auto dispatch = dispatch_kernel<t, nv, s_, v, false>, back = dispatch_kernel<t, nv, s_, v, true>;
+            constexpr auto combine = combine_kernel<t, nv, s_, v>;
             static const int resident[3] = {resident_blocks(dispatch, kThreads), resident_blocks(combine, kThreads),
                                             resident_blocks(back, kThreads)};
             if (kind == DISPATCH) run(dispatch, p.N <= 512 && resident[DISPATCH] > 3 ? 3 : resident[DISPATCH]);

@@ -315,7 +315,7 @@ def test_expert_sort_takes_any_choices(M, E, k):
 # --------------------------------------------------------------- exchange --
 EXCHANGE_SHAPES = [(1, 1, 1), (1, 1024, 2), (5, 3, 3), (77, 16, 2), (60, 20, 4), (300, 31, 1), (129, 64, 3), (100, 65, 8),
                    (64, 128, 2), (1000, 256, 2), (333, 333, 3), (50, 512, 32), (40, 1001, 5), (9, 4099, 2), (20000, 24, 2),
-                   (12, 8, 32)]
+                   (12, 8, 32), (700, 300, 3), (1300, 1030, 2), (1217, 4100, 1), (30, 2000, 4), (610, 2049, 3)]
 
 
 @pytest.mark.parametrize("M,N,k", EXCHANGE_SHAPES)
