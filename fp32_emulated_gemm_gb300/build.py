@@ -9,10 +9,10 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("emu_gemm.cu", "exchange.cu", "experts.cu", "feed_forward.cu", "few_rows.cu", "few_rows_bwd.cu", "gemm_act.cu", "gemm_gated.cu",
+SOURCES = [os.path.join(CSRC, f) for f in ("emu_gemm.cu", "exchange.cu", "experts.cu", "feed_forward.cu", "few_rows.cu", "few_rows_bwd.cu", "few_tiles.cu", "gemm_act.cu", "gemm_gated.cu",
                                               "gemm_gated_bwd.cu", "gemm_rows.cu", "gemm_rows_gated.cu",
                                               "gemm_two.cu", "gemm_two_gated_bwd.cu", "layer_norm.cu", "rms_norm.cu", "route.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("activation.cuh", "aligned.cuh", "emu_kernel.cuh", "few_rows.h", "few_rows_bwd.h", "gemm_epi.h", "group_rows.cuh", "internal.h",
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("activation.cuh", "aligned.cuh", "emu_kernel.cuh", "few_rows.h", "few_rows_bwd.h", "few_tiles.h", "gemm_epi.h", "group_rows.cuh", "internal.h",
                                                   "norm_rows.cuh",
                                                   "ptx.cuh", "row_ops.cuh")] + [
     os.path.join(os.path.dirname(HERE), "include", "emu_gemm.h")]

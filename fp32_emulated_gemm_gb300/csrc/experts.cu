@@ -10,8 +10,8 @@
 // (emu_kernel.cuh): 256-row tiles that end with the expert's rows, listed on the
 // device from the offsets, which never come to the host.  Backward, the products
 // that do not depend on one another share a launch (dZ and dW_out, dX and dW_in).
-// A few rows run on the CUDA cores (few_rows.cu, few_rows_bwd.cu), where each
-// expert's weight is read once.
+// A few rows run on the CUDA cores (few_rows.cu, few_tiles.cu, few_rows_bwd.cu), where
+// each expert's weight is read once.
 //
 // Both modes run as BF16x9, which is within TF32x3's bound too: TF32x3 without an
 // operand split ahead is slower (12288 rows on 8 experts, K = 256, F = 1024, the six
@@ -25,6 +25,7 @@
 #include "emu_kernel.cuh"
 #include "few_rows.h"
 #include "few_rows_bwd.h"
+#include "few_tiles.h"
 #include "internal.h"
 
 namespace emu {
@@ -278,33 +279,38 @@ cudaError_t launch_lists(const int32_t* offsets, int E, int64_t rows, const List
     return e;
 }
 
-// Whether a forward pass runs on the CUDA cores, where the weights of the experts
-// that have rows are read once for eight rows, or in 256-row tiles: the predicted
-// times in us.  The CUDA cores' is the rows' share of each step of 128 of each lot
-// of weight rows and of the lots' sums, and the weights' traffic where L2 does not
-// hold them; the tiles' their lengths (k-stages and stores) over the CTA pairs, or
-// the longest's own, cut in pieces.  Measured, CUDA cores / tiles: 8 experts, K = 1024,
-// F = 4096, 64 rows 125 / 250 us, 256 rows 349 / 255; 8 experts, K = 256, F = 1024, 256
-// rows 32 / 61, 512 rows 58 / 60; 64 experts, K = 512, F = 1024, 512 rows 127 / 242; 16
-// experts, K = F = 1024, 256 rows 95 / 149, 512 rows 180 / 150; 2 experts, K = F = 64,
-// 4096 rows 25 / 34, 16384 rows 74 / 35; 4 experts, K = F = 512, 256 rows 31 / 60, 1024
-// rows 95 / 64.
+// A forward pass in one of three forms: on the CUDA cores, where the weights of the
+// experts that have rows are read once for eight rows (few_rows.cu) or for 16 or 32
+// through shared memory (few_tiles.cu), or in 256-row tiles: the one of the least
+// predicted time, in us.  The first one's is the rows' share of each step of 128 of
+// each lot of weight rows and of the lots' sums, and the weights' traffic where L2 does
+// not hold them; the second's its FMAs, an expert's last rows rounded up; the tiles'
+// their lengths (k-stages and stores) over the CTA pairs, or the longest's own, cut in
+// pieces.  Measured, first / second / tiles: 8 experts, K = 1024, F = 4096, 32 rows 89 /
+// 120 / 251 us, 128 rows 196 / 141 / 253, 512 rows 688 / 403 / 261; 8 experts, K = 256, F
+// = 1024, 256 rows 33 / 32 / 59, 512 rows 58 / 35 / 60, 2048 rows - / 93 / 69; 64 experts,
+// K = 512, F = 1024, 256 rows 87 / 101 / 218, 512 rows 125 / 117 / 232, 1024 rows 215 / 149
+// / 257; 16 experts, K = F = 1024, 64 rows 51 / 64 / 147, 256 rows 110 / 85 / 150, 1024 rows
+// 321 / 208 / 152; 2 experts, K = F = 64, 256 rows 6 / 12 / 33, 16384 rows 74 / - / 35.
 constexpr int64_t kFewRowsMost = 32768;
 constexpr int kPairs = 76;
 constexpr double kL2Weights = 25e6;  // weights that stay in L2 beside the rest
-bool few(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs) {
-    if (rows > kFewRowsMost) return false;
+enum Form { FORM_ROWS, FORM_SHARED, FORM_TILES };
+Form form_of(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs, bool shared_fits) {
+    if (rows > kFewRowsMost) return FORM_TILES;
     auto over = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
     const double T = (double)rows, used = rows < E ? T : (double)E, W = (double)F * (2.0 * K + N);
     const double lots = 0.5 * F + 0.25 * N, steps = 0.5 * F * over(K, 128) + 0.25 * N * over(F, 128);
     double cores = 4.0 + T * (3.74e-5 * steps + 3.4e-5 * lots);
     if (E * W > kL2Weights) cores += (T / 8 + 0.5 * used) * W * 4 / 8e6;
+    const double shared = shared_fits ? 9.0 + (T + 10 * used) * W / 17.5e6 : 1e30;
     const double half = T / 256 + 0.5 * E, tiles = used > half ? used : half;
     auto product = [&](double columns, double stages) {
         const double length = stages + 3, share = tiles * columns * length / pairs, least = length < 12 ? length : 12;
         return 1.44 * (share > least ? share : least);
     };
-    return cores <= 22.0 + product(over(F, 128), over(K, 32)) + product(over(N, 256), over(F, 32));
+    const double tiled = 22.0 + product(over(F, 128), over(K, 32)) + product(over(N, 256), over(F, 32));
+    return cores <= tiled && cores <= shared ? FORM_ROWS : shared <= tiled ? FORM_SHARED : FORM_TILES;
 }
 // Likewise for a backward pass (few_rows_bwd.cu): the weights read and their gradients
 // written, and the rows' products or, for small weights, the sums' way through an
@@ -419,16 +425,22 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const StreamLock lock(s);
     DeviceCtx dev;
-    if (few(rows, E, K, F, N, kPairs)) {
+    FewRows in{(int)rows, F, K, X, ldx, W_in, ldwi, nullptr, nullptr, 0, D, ldd, H, ldh, act_params(act)};
+    in.offsets = offsets;
+    in.groups = E;
+    FewRows out{(int)rows, N, F, H, ldh, W_out, ldwo, nullptr, nullptr, 0, nullptr, 0, Y, ldy, act_params(ACT_NONE)};
+    out.offsets = offsets;
+    out.groups = E;
+    const Form form = form_of(rows, E, K, F, N, kPairs, few_tiles_fit(in) && few_tiles_fit(out));
+    if (form != FORM_TILES) EMU_TRY(current_device(&dev));
+    if (form == FORM_ROWS) {
         const bool streaming = many_lots(rows, F, N);
-        EMU_TRY(current_device(&dev));
-        FewRows p{(int)rows, F, K, X, ldx, W_in, ldwi, nullptr, nullptr, 0, D, ldd, H, ldh, act_params(act)};
-        p.offsets = offsets;
-        p.groups = E;
-        EMU_TRY(launched(launch_few_rows_grouped(p, true, streaming, false, dev.sm_count, s)));
-        p.N = N; p.K = F; p.X = H; p.ldx = ldh; p.W = W_out; p.ldw = ldwo; p.D = nullptr; p.Y = Y; p.ldy = ldy;
-        p.act = act_params(ACT_NONE);
-        return launched(launch_few_rows_grouped(p, false, streaming, true, dev.sm_count, s));
+        EMU_TRY(launched(launch_few_rows_grouped(in, true, streaming, false, dev.sm_count, s)));
+        return launched(launch_few_rows_grouped(out, false, streaming, true, dev.sm_count, s));
+    }
+    if (form == FORM_SHARED) {
+        EMU_TRY(launched(launch_few_tiles(in, true, false, dev.sm_count, s)));
+        return launched(launch_few_tiles(out, false, true, dev.sm_count, s));
     }
     Aligned al;
     al.add(X, ldx, rows, K);

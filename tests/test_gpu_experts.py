@@ -655,6 +655,46 @@ def test_expert_ffn_few_rows_of_long_contractions(counts, K, F, N):
             w.check(host(g), f"expert {e} {name}")
 
 
+@pytest.mark.parametrize("counts,K,F,N,act", [
+    ([0, 13, 64, 33, 1, 90, 16, 31], 1028, 1540, 129, "silu"), ([0, 13, 64, 33, 1, 90, 16, 31], 36, 2052, 1030, "gelu"),
+    ([40, 17, 5, 33], 36, 2052, 1030, "gelu_tanh"), ([200, 0, 7, 120, 65, 31], 256, 512, 260, "silu"),
+    ([200, 0, 7, 120, 65, 31], 1028, 260, 516, "none"), ([9] * 30 + [0, 33], 1028, 1540, 129, "gelu"),
+    ([9] * 30 + [0, 33], 2052, 640, 65, "silu")])
+def test_expert_ffn_of_some_rows(counts, K, F, N, act):
+    """Between few and many rows an expert: the CUDA cores' products through shared
+    memory, blocks of 1 to 32 rows, shared contractions; the rows before and behind the
+    experts' hold NaN and their outputs, as all around, stay what they were."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("some", sum(counts), K, F)
+    E, offsets = len(counts), 1 + np.concatenate([[0], np.cumsum(counts)])
+    rows = int(offsets[-1]) + 2
+    x = f32(rng, rows, K)
+    x[0], x[-2:] = np.nan, np.nan
+    wi, wo = f32(rng, E, 2 * F, K, std=K ** -0.5), f32(rng, E, N, F, std=F ** -0.5)
+    X, WI, WO, o = dev(x), dev(wi), dev(wo), ints(offsets)
+    G, up = 7.25, lambda n: (n + 3) // 4 * 4
+    widths = (2 * F, F, N)
+    bufs = [torch.full((rows + 2, up(c) + 8), G, device="cuda") for c in widths]
+    d, h, y = (b[1:-1, 4:4 + c] for b, c in zip(bufs, widths))
+    emu.emu_expert_ffn_fwd(0, emu.ACTS[act], rows, E, K, F, N, X, K, o, WI, K, WO, F,
+                           d, d.stride(0), h, h.stride(0), y, y.stride(0))
+    plan = emu.ExpertPlan(None, None, None, o)
+    y0 = emu.expert_ffn_fwd(X, WI, WO, plan, act=act)
+    y1, d1, h1 = emu.expert_ffn_fwd(X, WI, WO, plan, act=act, save=True)
+    done()
+    own = slice(1, rows - 2)
+    assert all(torch.equal(a[own], b[own]) for a, b in ((y, y0), (y, y1), (h, h1), (d, d1)))
+    for b, c in zip(bufs, widths):
+        rim = b.clone()
+        rim[2:rows - 1, 4:4 + c] = G
+        assert bool((rim == G).all())
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        for g, w, name in zip((y[r], h[r]), expert_reference(x[r], wi[e], wo[e], act, "bf16x9"), ("Y", "H")):
+            w.check(host(g), f"expert {e} {name}")
+
+
 def test_expert_ffn_only_wanted_gradients():
     import torch
     import fp32_emulated_gemm_gb300 as emu
