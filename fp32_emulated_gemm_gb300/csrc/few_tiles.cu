@@ -14,10 +14,10 @@
 // tiles 252), 128 rows 141 (196, 253), 256 rows 248 (358, 256); 64 experts, K = 512, F =
 // 1024: 512 rows 117 (125, 232), 1024 rows 149 (215, 257); 16 experts, K = F = 1024, 256
 // rows 85 (110, 150).  Bound by latency at 12 warps an SM: the FMA pipe is busy half of
-// the time, shared memory's likewise (32 rows a group; 8 experts).  More and shorter
-// shares of a contraction than fill the GPU once gained nothing; 32 rows a block for
-// groups of 16 neither, eight rows a thread cost what leaving out a partial block's
-// empty rows gains (129 -> 120 us at 32 rows, 261 -> 248 at 256).
+// the time, shared memory's likewise (32 rows a group, 8 experts).  Neither more and
+// shorter shares of a contraction nor 32 rows a block for groups of 8 to 16 gained
+// anything; leaving out a partial block's empty rows did (32 rows 129 -> 120 us, 256
+// rows 261 -> 248).
 #include "few_tiles.h"
 
 #include <type_traits>
