@@ -439,10 +439,12 @@ bool sizes_ok(int64_t M, int E, int k) {
 }
 
 // What a launch may have without being asked for is 48 KB (682 experts); beyond it
-// the current device is asked, call by call.
+// the current device is asked, call by call, for the most that any call needs: the
+// limit is the kernel's, and another thread's call with fewer experts must not lower
+// it between this one's request and its launch.
 template <class K> emu_status_t allow_smem(K kernel, size_t bytes) {
     if (bytes <= 48 * 1024) return EMU_STATUS_SUCCESS;
-    return launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+    return launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxExperts)));
 }
 
 template <int WAY> emu_status_t route(Route p, emu_stream_t stream) {

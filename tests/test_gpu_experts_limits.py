@@ -1,0 +1,51 @@
+"""The operators of a layer of experts where calls meet limits or one another."""
+import threading
+
+import pytest
+
+from tests.test_gpu_experts import check_plan, route_oracle
+from tests.test_gpu_feed_forward import dev, done, f32, rng_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M", [8, 200])
+def test_routes_of_many_experts_from_several_threads(M):
+    """Calls on streams of their own, with more shared memory than a launch may have
+    without asking and different amounts of it (one block; two launches): none takes
+    another's away."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    sizes = [1024, 700, 1000, 690]
+    sets = []
+    for E in sizes:
+        l = f32(rng_of("limits", M, E), M, E)
+        plan, weights = emu.expert_route(dev(l), 2)
+        done()
+        check_plan(plan, route_oracle(l, 2, "chosen")[0], E)
+        sets.append((dev(l), [t.clone() for t in (*plan, weights)]))
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(len(sizes))
+
+    def worker(i):
+        try:
+            logits, want = sets[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                emu.expert_route(logits, 2)
+                start.wait(60)
+                for rep in range(1500):
+                    plan, weights = emu.expert_route(logits, 2)
+                    if rep % 100 == 0 and not all(torch.equal(a, b) for a, b in zip((*plan, weights), want)):
+                        wrong.append((i, rep))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            wrong.append((i, repr(e)))
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(300)
+    assert not any(t.is_alive() for t in threads)
+    assert not wrong, wrong[:8]
+    done()
