@@ -83,7 +83,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock) few_rows_kernel(const Few
     if constexpr (GROUPED) {
         // (the offsets are there before the kernel that this one may overlap)
         const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
-        if (g.y <= 0) return;
+        if (g.y <= 0) {
+            griddep_wait();  // the launch ends after the one before it, if no block has rows too
+            return;
+        }
         m0 = g.x;
         rows = g.y;
         W += g.z * ((GATED ? 2 : 1) * p.N * p.ldw);
@@ -180,7 +183,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, 2) few_rows_stream_kernel
     // (the offsets are there before the kernel that this one may overlap)
     const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
     const int rows = g.y;
-    if (rows <= 0) return;
+    if (rows <= 0) {
+        griddep_wait();  // (as above)
+        return;
+    }
     const float* X = p.X + g.x * p.ldx + (VEC ? 4 * lane : lane);
     const float* W = p.W + g.z * ((GATED ? 2 : 1) * p.N * p.ldw) + (VEC ? 4 * lane : lane);
     const int64_t last = (p.N + OUT - 1) / OUT;                                        // lots of the weight

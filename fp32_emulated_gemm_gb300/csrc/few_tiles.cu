@@ -60,7 +60,10 @@ __global__ void __launch_bounds__(kThreads, 3) few_tiles_kernel(const __grid_con
     // (the offsets are there before the kernel that this one may overlap)
     const int3 g = rows_of_block(p.offsets, p.groups, p.M, MR, blockIdx.y);
     const int rows = g.y;
-    if (rows <= 0) return;  // (all of a cluster)
+    if (rows <= 0) {  // (all of a cluster)
+        griddep_wait();  // the launch ends after the one before it, if no block has rows too
+        return;
+    }
     const float *X = p.X + g.x * p.ldx, *W = p.W + g.z * ((GATED ? 2 : 1) * p.N * p.ldw);
     const int64_t n0 = blockIdx.x * (int64_t)OUT;
     const int steps = (int)((p.K + kStep - 1) / kStep), shares = gridDim.z, share = blockIdx.z;

@@ -3,7 +3,7 @@ import threading
 
 import pytest
 
-from tests.test_gpu_experts import check_plan, route_oracle
+from tests.test_gpu_experts import check_plan, ints, route_oracle
 from tests.test_gpu_feed_forward import dev, done, f32, rng_of
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +49,24 @@ def test_routes_of_many_experts_from_several_threads(M):
     assert not any(t.is_alive() for t in threads)
     assert not wrong, wrong[:8]
     done()
+
+
+@pytest.mark.parametrize("E,rows,K,F", [(8, 16, 256, 512), (64, 4, 64, 64), (8, 300, 128, 256)])
+def test_passes_without_rows_end_before_what_follows(E, rows, K, F):
+    """No expert has rows, and the next call on the stream gives the offsets other
+    values: the pass before it reads the old ones alone and writes nothing.  (Forward
+    on the CUDA cores: lots a warp, streaming, through shared memory.)"""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("norows", E, rows)
+    x, wi, wo = dev(f32(rng, rows, K)), dev(f32(rng, E, 2 * F, K)), dev(f32(rng, E, K, F))
+    some, none = ints([rows] * (E + 1)), ints([0] * (E + 1))
+    full = ints([0] + [rows] * E)
+    offsets = none.clone()
+    h, y, d = (torch.full((rows, n), 7.0, device="cuda") for n in (F, K, 2 * F))
+    for i in range(200):
+        offsets.copy_(some if i % 2 else none)
+        emu.emu_expert_ffn_fwd(0, 4, rows, E, K, F, K, x, K, offsets, wi, K, wo, F, d, 2 * F, h, F, y, K)
+        offsets.copy_(full)
+    done()
+    assert all(bool((t == 7).all()) for t in (h, y, d))
