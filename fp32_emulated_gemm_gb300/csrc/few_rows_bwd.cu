@@ -22,12 +22,19 @@ namespace {
 constexpr int kWarps = 8, kColumns = 128, kSumRows = 8;
 
 // Columns c .. c + 3 of a row of n (aligned): the words that exist, else zeros.
-__device__ __forceinline__ float4 columns(const float* row, int64_t c, int64_t n) {
-    if (c + 3 < n) return __ldg(reinterpret_cast<const float4*>(row + c));
+// PLAIN: of a matrix that a launch of the same call writes, which this one may
+// overlap: the read-only path is for data that nobody writes while the kernel runs,
+// also where it is read behind the wait.
+template <bool PLAIN = false> __device__ __forceinline__ float4 columns(const float* row, int64_t c, int64_t n) {
+    auto load = [](const auto* p) {
+        if constexpr (PLAIN) return *p;
+        else return __ldg(p);
+    };
+    if (c + 3 < n) return load(reinterpret_cast<const float4*>(row + c));
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < n) v.x = __ldg(row + c);
-    if (c + 1 < n) v.y = __ldg(row + c + 1);
-    if (c + 2 < n) v.z = __ldg(row + c + 2);
+    if (c < n) v.x = load(row + c);
+    if (c + 1 < n) v.y = load(row + c + 1);
+    if (c + 2 < n) v.z = load(row + c + 2);
     return v;
 }
 // (the last columns word by word: what lies behind them is not the output's)
@@ -102,7 +109,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) few_columns_kernel(const __gri
             float4 a[H];
 #pragma unroll
             for (int m = 0; m < H; ++m)
-                a[m] = m0 + m < rows ? columns(A + (m0 + m) * p.lda, 4 * q, p.K) : make_float4(0.f, 0.f, 0.f, 0.f);
+                a[m] = m0 + m < rows ? columns<true>(A + (m0 + m) * p.lda, 4 * q, p.K) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int m = 0; m < H; ++m) {
                 fma4(a[m].x, v[0], acc[m0 + m]);
@@ -175,8 +182,8 @@ __global__ void __launch_bounds__(32 * kWarps) few_sums_kernel(const __grid_cons
             const bool there = m0 + i < g.y;
             const int64_t m = there ? m0 + i : m0;
             b[i] = columns(p.B + m * p.ldb, c, there ? p.N : 0);
-            a[i] = columns(p.A + m * p.lda, r0, there ? p.R : 0);
-            e[i] = columns(p.A + m * p.lda, r0 + 4, there ? p.R : 0);
+            a[i] = columns<true>(p.A + m * p.lda, r0, there ? p.R : 0);
+            e[i] = columns<true>(p.A + m * p.lda, r0 + 4, there ? p.R : 0);
         }
 #pragma unroll
         for (int i = 0; i < B; ++i) {

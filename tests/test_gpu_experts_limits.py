@@ -1,6 +1,7 @@
 """The operators of a layer of experts where calls meet limits or one another."""
 import threading
 
+import numpy as np
 import pytest
 
 from tests.test_gpu_experts import check_plan, ints, route_oracle
@@ -70,3 +71,31 @@ def test_passes_without_rows_end_before_what_follows(E, rows, K, F):
         offsets.copy_(full)
     done()
     assert all(bool((t == 7).all()) for t in (h, y, d))
+
+
+@pytest.mark.parametrize("counts,K,F,N", [([3, 0, 9, 1], 256, 512, 260), ([2] * 40 + [70], 64, 64, 64), ([5, 200, 0, 40], 132, 65, 36)])
+def test_backward_passes_that_write_the_same_dz(counts, K, F, N):
+    """Passes of different inputs one behind the other, on the CUDA cores, into one dZ
+    and one set of gradients: each reads its own dZ, not the last one's."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("samedz", sum(counts), K)
+    E, offsets = len(counts), ints(np.concatenate([[0], np.cumsum(counts)]))
+    rows, pad = sum(counts), lambda n: (n + 3) // 4 * 4
+    wi, wo = dev(f32(rng, E, 2 * F, K)), dev(f32(rng, E, N, F))
+    plan = emu.ExpertPlan(None, None, None, offsets)
+    sets = []
+    for _ in range(3):
+        x, dy = dev(f32(rng, rows, K)), dev(f32(rng, rows, N))
+        y, d, h = emu.expert_ffn_fwd(x, wi, wo, plan, save=True)
+        sets.append((x, dy, d, h, emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan)))
+    done()
+    new = lambda r, c: torch.empty_strided((r, c), (pad(c), 1), device="cuda")
+    dz, dx, dwi, dwo = new(rows, 2 * F), new(rows, K), new(E * 2 * F, K), new(E * N, F)
+    for i in range(60):
+        x, dy, d, h, want = sets[i % 3]
+        emu.emu_expert_ffn_bwd(0, rows, E, K, F, N, dy, N, x, K, offsets, wi, K, wo, F, d, d.stride(0), h, h.stride(0), dz, pad(2 * F),
+                               dx, pad(K), dwi, pad(K), dwo, pad(F))
+        got = dx, dwi.unflatten(0, (E, 2 * F)), dwo.unflatten(0, (E, N))
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+    done()
