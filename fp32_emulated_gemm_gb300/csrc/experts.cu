@@ -319,7 +319,8 @@ Form form_of(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs, bo
 // us, 128 rows 56 / 87, 512 rows 134 / 94; 64 experts, K = 512, F = 1024, 64 rows 206 /
 // 309, 512 rows 415 / 456, 1024 rows 634 / 498; 8 experts, K = 1024, F = 4096, 2 rows 132 /
 // 212, 32 rows 318 / 383, 128 rows 604 / 445; 2 experts, K = F = 64, 64 rows 32 / 46, 128
-// rows 54 / 48.
+// rows 54 / 48.  (Chunks of an expert's rows, for the sums of more than 64, cost 1 to 5%
+// of these and hold the form's time where one expert has most rows: few_rows_bwd.cu.)
 bool few_bwd(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs) {
     if (rows > kFewRowsMost) return false;
     auto over = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
@@ -502,22 +503,31 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
         EMU_TRY(current_device(&dev));
         EMU_TRY(al.reserve(s));
         const int M = (int)rows;
-        // blocks that share a contraction, and the buffer for what they leave
+        // blocks that share a contraction or a sum, and the buffer for what they leave: the
+        // contractions' in turn, the sums' until the end
         const int64_t ldf = (F + 3) & ~int64_t(3), ldk = (K + 3) & ~int64_t(3);
         const int fs = inner ? few_columns_shares(rows, E, F, N, dev.sm_count) : 1;
         const int ks = dX ? few_columns_shares(rows, E, K, 2 * F, dev.sm_count) : 1;
+        const int fc = few_sums_chunk(rows, N, F, dev.sm_count), kc = few_sums_chunk(rows, 2 * F, K, dev.sm_count);
         const size_t floats_f = fs > 1 ? (size_t)fs * rows * ldf : 0, floats_k = ks > 1 ? (size_t)ks * rows * ldk : 0;
+        const size_t floats_o = dW_out ? (size_t)few_sums_pieces(rows, fc) * N * ldf : 0;
+        const size_t floats_i = dW_in ? (size_t)few_sums_pieces(rows, kc) * 2 * F * ldk : 0;
+        const size_t floats_s = floats_f > floats_k ? floats_f : floats_k;
         float* shares = nullptr;
-        if (floats_f || floats_k) EMU_TRY(reduce_scratch(dev.id, s, floats_f > floats_k ? floats_f : floats_k, &shares));
+        if (floats_s + floats_o + floats_i) EMU_TRY(reduce_scratch(dev.id, s, floats_s + floats_o + floats_i, &shares));
+        float *pieces_o = shares + floats_s, *pieces_i = pieces_o + floats_o;  // (all multiples of four floats)
         EMU_TRY(launched(al.launch(s)));
         bool after = false;
+        FewSums sums[2];
+        int n = 0;
         if (inner) {
             EMU_TRY(launched(launch_few_columns({M, E, offsets, F, N, dY, lddy, W_out, ldwo, D, ldd, dZ, lddz, shares, ldf}, fs,
                                                 after, s)));
             after = true;
         }
         if (dW_out) {
-            EMU_TRY(launched(launch_few_sums({M, E, offsets, N, F, dY, lddy, H, ldh, dW_out, lddwo}, after, s)));
+            sums[n] = {M, E, offsets, N, F, dY, lddy, H, ldh, dW_out, lddwo, fc, pieces_o, ldf};
+            EMU_TRY(launched(launch_few_sums(sums[n++], after, s)));
             after = true;
         }
         if (dX) {
@@ -525,8 +535,11 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
                                                  ldk}, ks, after, s)));
             after = true;
         }
-        if (dW_in) EMU_TRY(launched(launch_few_sums({M, E, offsets, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi}, after, s)));
-        return EMU_STATUS_SUCCESS;
+        if (dW_in) {
+            sums[n] = {M, E, offsets, 2 * F, K, dZ, lddz, X, ldx, dW_in, lddwi, kc, pieces_i, ldk};
+            EMU_TRY(launched(launch_few_sums(sums[n++], after, s)));
+        }
+        return launched(launch_add_pieces(sums, n, s));
     }
     Fused f{};
     auto products = [&] {

@@ -9,8 +9,15 @@
 // several share a contraction through a buffer, and a second kernel adds what they
 // leave.  The shares are added in order.
 // few_sums: a warp has eight rows of C and 128 columns and goes through the group's
-// rows in order; every element is written once.
+// rows in order.  Nobody but the device knows how many those are: an expert that has
+// most of them is shared out in chunks, whose sums a second kernel adds in order.  All
+// rows on one of 64 experts, K = F = N = 64, 2500 rows: backward pass 1507 us with the
+// rows in one chain, 82 in chunks (spread evenly 56 and 58); 256 experts, 12000 rows
+// 7190 and 246 (149 and 159); 128 experts, K = F = N = 128, 4096 rows 1776 and 139 (77
+// and 82); 64 experts, K = N = 512, F = 1024, 512 rows 454 and 377 (333 and 350).
 #include "few_rows_bwd.h"
+
+#include <algorithm>
 
 #include "group_rows.cuh"
 #include "internal.h"
@@ -163,17 +170,30 @@ __global__ void __launch_bounds__(256) add_shares_kernel(const __grid_constant__
     put_row(p, r, c, s);
 }
 
+// PIECES: some group may have more than a chunk of rows.
+template <bool PIECES>
 __global__ void __launch_bounds__(32 * kWarps) few_sums_kernel(const __grid_constant__ FewSums p, unsigned column_blocks) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const int2 g = rows_of_group(p.offsets, p.M, blockIdx.y);
+    int2 g;
+    if (!PIECES || blockIdx.y < p.groups) {
+        g = rows_of_group(p.offsets, p.M, blockIdx.y);
+        if constexpr (PIECES) g.y = min(g.y, g.x + p.chunk);
+    } else {  // a chunk of the groups' rows behind their first ones
+        if (!any_group_above(p.offsets, p.groups, p.M, p.chunk)) {
+            griddep_wait();
+            return;
+        }
+        const int3 b = rows_of_block<1>(p.offsets, p.groups, p.M, p.chunk, (int)blockIdx.y - p.groups);
+        g = make_int2(b.x, b.x + b.y);
+    }
     const int64_t r0 = (int64_t)(blockIdx.x / column_blocks) * (kWarps * kSumRows) + warp * kSumRows;
     const int64_t c = (int64_t)(blockIdx.x % column_blocks) * kColumns + 4 * lane;
     float4 acc[kSumRows];
 #pragma unroll
     for (int i = 0; i < kSumRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     griddep_wait();  // A and B
-    if (r0 >= p.R) return;
+    if (r0 >= p.R || (PIECES && blockIdx.y >= p.groups && g.y == g.x)) return;
     constexpr int B = 4;  // rows whose loads go out together
     for (int m0 = g.x; m0 < g.y; m0 += B) {
         float4 b[B], a[B], e[B];
@@ -198,10 +218,42 @@ __global__ void __launch_bounds__(32 * kWarps) few_sums_kernel(const __grid_cons
             fma4(e[i].w, b[i], acc[7]);
         }
     }
-    float* out = p.C + (blockIdx.y * p.R + r0) * p.ldc;
+    const bool first = !PIECES || blockIdx.y < p.groups;
+    float* out = first ? p.C + (blockIdx.y * p.R + r0) * p.ldc : p.pieces + ((blockIdx.y - p.groups) * p.R + r0) * p.ldpieces;
+    const int64_t ld = first ? p.ldc : p.ldpieces;
 #pragma unroll
     for (int i = 0; i < kSumRows; ++i)
-        if (r0 + i < p.R) put_columns(out + i * p.ldc, c, p.N, acc[i]);
+        if (r0 + i < p.R) put_columns(out + i * ld, c, p.N, acc[i]);
+}
+
+// The pieces of a group's sums, added to its first chunk's: the blocks of the group's
+// first piece do it.  (Both sums of a call in one launch at its end: 2 us less.)
+struct TwoSums { FewSums sums[2]; };
+__global__ void __launch_bounds__(32 * kWarps) add_pieces_kernel(const __grid_constant__ TwoSums two) {
+    const FewSums& p = two.sums[blockIdx.z];
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    if (!any_group_above(p.offsets, p.groups, p.M, p.chunk)) {
+        griddep_wait();
+        return;
+    }
+    const int3 b = rows_of_block<1>(p.offsets, p.groups, p.M, p.chunk, blockIdx.y);
+    const int2 g = rows_of_group(p.offsets, p.M, b.z);
+    griddep_wait();  // the sums
+    if (b.y == 0 || b.x != g.x + p.chunk) return;
+    const uint32_t quads = (uint32_t)((p.N + 3) / 4);
+    const int n = (g.y - g.x - 1) / p.chunk;
+    for (int64_t i = blockIdx.x * (32ll * kWarps) + threadIdx.x; i < p.R * quads; i += gridDim.x * (32ll * kWarps)) {
+        const int64_t r = i / quads, c = 4 * (i - r * quads);
+        float* out = p.C + (b.z * p.R + r) * p.ldc;
+        const float* piece = p.pieces + (blockIdx.y * p.R + r) * p.ldpieces;
+        float4 s = columns<true>(out, c, p.N);
+#pragma unroll 8
+        for (int z = 0; z < n; ++z) {
+            const float4 v = columns<true>(piece + z * p.R * p.ldpieces, c, p.N);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        put_columns(out, c, p.N, s);
+    }
 }
 
 template <class K, class... Args>
@@ -227,6 +279,7 @@ namespace {
 int block_rows(int64_t m, int64_t g) { return 4 * m <= g ? 1 : m <= g ? 2 : m <= 3 * g ? 4 : 8; }
 int64_t row_blocks(int64_t m, int64_t g) { return m / block_rows(m, g) + (m < g ? m : g); }  // (every group's last may be partial)
 int64_t column_blocks(int64_t n) { return (n + kColumns - 1) / kColumns; }
+int64_t sum_row_blocks(int64_t r) { return (r + kWarps * kSumRows - 1) / (kWarps * kSumRows); }
 }  // namespace
 
 int few_columns_shares(int64_t M, int64_t groups, int64_t N, int64_t K, int sm_count) {
@@ -257,11 +310,38 @@ cudaError_t launch_few_columns(const FewColumns& p, int shares, bool after_own, 
     return launch(add_shares_kernel, dim3((unsigned)adders, 1, 1), true, stream, p, shares);
 }
 
+int few_sums_chunk(int64_t M, int64_t R, int64_t N, int sm_count) {
+    // pieces for the two blocks that an SM holds if one group has all rows, of 64 rows at least
+    const int64_t blocks = column_blocks(N) * sum_row_blocks(R), most = 2 * (int64_t)sm_count, pieces = (most + blocks - 1) / blocks;
+    const int64_t chunk = (M + pieces - 1) / pieces;
+    return (int)(chunk < 64 ? 64 : chunk);
+}
+
 cudaError_t launch_few_sums(const FewSums& p, bool after_own, cudaStream_t stream) {
-    if (!vec4_ok(p.A, p.lda) || !vec4_ok(p.B, p.ldb) || !vec4_ok(p.C, p.ldc)) return cudaErrorMisalignedAddress;
-    const int64_t columns = (p.N + kColumns - 1) / kColumns, rows = (p.R + kWarps * kSumRows - 1) / (kWarps * kSumRows);
-    if (columns * rows > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch(few_sums_kernel, dim3((unsigned)(columns * rows), (unsigned)p.groups, 1), after_own, stream, p, (unsigned)columns);
+    const int64_t pieces = few_sums_pieces(p.M, p.chunk);
+    if (!vec4_ok(p.A, p.lda) || !vec4_ok(p.B, p.ldb) || !vec4_ok(p.C, p.ldc) || (pieces > 0 && !vec4_ok(p.pieces, p.ldpieces)))
+        return cudaErrorMisalignedAddress;
+    const int64_t columns = column_blocks(p.N), rows = sum_row_blocks(p.R);
+    if (columns * rows > INT32_MAX || p.groups + pieces > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(columns * rows), (unsigned)(p.groups + pieces), 1);
+    return pieces == 0 ? launch(few_sums_kernel<false>, grid, after_own, stream, p, (unsigned)columns)
+                       : launch(few_sums_kernel<true>, grid, after_own, stream, p, (unsigned)columns);
+}
+
+cudaError_t launch_add_pieces(const FewSums* sums, int n, cudaStream_t stream) {
+    TwoSums two;
+    int64_t adders = 0, pieces = 0;
+    int with = 0;
+    for (int i = 0; i < n; ++i) {
+        const int64_t mine = few_sums_pieces(sums[i].M, sums[i].chunk);
+        if (mine == 0) continue;
+        two.sums[with++] = sums[i];
+        const int64_t blocks = ((sums[i].N + 3) / 4 * sums[i].R + 32 * kWarps - 1) / (32 * kWarps), most = 1024 / mine + 1;
+        adders = std::max(adders, std::min(blocks, most));
+        pieces = std::max(pieces, mine);
+    }
+    if (with == 0) return cudaSuccess;
+    return launch(add_pieces_kernel, dim3((unsigned)adders, (unsigned)pieces, (unsigned)with), true, stream, two);
 }
 
 }  // namespace emu

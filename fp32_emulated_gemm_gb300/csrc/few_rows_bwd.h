@@ -26,7 +26,9 @@ struct FewColumns {
     int64_t ldshares = 0;
 };
 // C[g] = sum over the rows r of group g of A[r]^T B[r] (groups x R x N; zero for a group
-// without rows); alignment likewise.
+// without rows); alignment likewise.  A group's rows behind its first `chunk` are summed
+// by further blocks, a chunk each, in `pieces` (R x ldpieces floats for each of
+// few_sums_pieces()), which launch_add_pieces adds, for up to two sums.
 struct FewSums {
     int M, groups;
     const int32_t* offsets;
@@ -37,11 +39,18 @@ struct FewSums {
     int64_t ldb;
     float* C;
     int64_t ldc;
+    int chunk;
+    float* pieces = nullptr;
+    int64_t ldpieces = 0;
 };
-// `after_own`: the launch follows one of these two, with nothing in between.
+int few_sums_chunk(int64_t M, int64_t R, int64_t N, int sm_count);
+inline int64_t few_sums_pieces(int64_t M, int chunk) { return (M - 1) / chunk; }
+// `after_own`: the launch follows one of these, with nothing in between.
 // `shares`: blocks that share a contraction, few_columns_shares() or less.
 int few_columns_shares(int64_t M, int64_t groups, int64_t N, int64_t K, int sm_count);
 cudaError_t launch_few_columns(const FewColumns& p, int shares, bool after_own, cudaStream_t stream);
 cudaError_t launch_few_sums(const FewSums& p, bool after_own, cudaStream_t stream);
+// (Behind the sums' launches or others of these; nothing if there can be no pieces.)
+cudaError_t launch_add_pieces(const FewSums* sums, int n, cudaStream_t stream);
 
 }  // namespace emu

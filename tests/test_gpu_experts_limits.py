@@ -4,8 +4,8 @@ import threading
 import numpy as np
 import pytest
 
-from tests.test_gpu_experts import check_plan, ints, route_oracle
-from tests.test_gpu_feed_forward import dev, done, f32, rng_of
+from tests.test_gpu_experts import check_plan, expert_reference, ints, route_oracle
+from tests.test_gpu_feed_forward import dev, done, f32, host, rng_of
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,82 @@ def test_backward_passes_that_write_the_same_dz(counts, K, F, N):
         got = dx, dwi.unflatten(0, (E, 2 * F)), dwo.unflatten(0, (E, N))
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
     done()
+
+
+def skewed(E, rows, hot, rng):
+    """Counts of `rows` rows, all but a few of them expert `hot`'s."""
+    counts = np.zeros(E, np.int64)
+    others = rng.integers(0, E, size=min(E // 2, rows // 8))
+    np.add.at(counts, others, 1)
+    counts[hot] += rows - counts.sum()
+    return counts
+
+
+@pytest.mark.parametrize("E,rows,K,F,N", [(64, 2500, 64, 64, 64), (256, 9000, 36, 33, 20), (1024, 9000, 16, 8, 12), (8, 70, 700, 300, 260),
+                                          (64, 600, 256, 260, 132), (128, 4096, 128, 128, 128), (3, 65, 64, 64, 64)])
+@pytest.mark.parametrize("kind", ["one", "first", "last", "even"])
+def test_backward_of_rows_on_one_expert(E, rows, K, F, N, kind):
+    """All rows on one expert, or nearly all on the first or the last: the gradients,
+    their bits in each wanted one alone and on every run; experts without rows get
+    zeros."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("hot", E, rows, kind)
+    counts = np.zeros(E, np.int64)
+    if kind == "even":
+        counts[:] = rows // E
+        counts[:rows % E] += 1
+    elif kind == "one":
+        counts[E // 3] = rows
+    else:
+        counts = skewed(E, rows, 0 if kind == "first" else E - 1, rng)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    x, dy = f32(rng, rows, K), f32(rng, rows, N)
+    wi, wo = f32(rng, E, 2 * F, K, std=K ** -0.5), f32(rng, E, N, F, std=F ** -0.5)
+    plan = emu.ExpertPlan(None, None, None, ints(offsets))
+    X, DY, WI, WO = dev(x), dev(dy), dev(wi), dev(wo)
+    y, d, h = emu.expert_ffn_fwd(X, WI, WO, plan, save=True)
+    got = emu.expert_ffn_bwd(DY, X, WI, WO, d, h, plan)
+    again = emu.expert_ffn_bwd(DY, X, WI, WO, d, h, plan)
+    alone = [emu.expert_ffn_bwd(DY, X, WI, WO, d, h, plan, need=[j == i for j in range(3)])[i] for i in range(3)]
+    done()
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(got, again, alone))
+    assert not bool(got[1][dev(counts == 0)].any()) and not bool(got[2][dev(counts == 0)].any())
+    for e in np.flatnonzero(counts)[np.argsort(-counts[counts > 0])][:12]:
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        want = expert_reference(x[r], wi[e], wo[e], "silu", "bf16x9", dy[r])
+        for g, w, name in zip((y[r], h[r], got[0][r], got[1][e], got[2][e]), want, ("Y", "H", "dX", "dW_in", "dW_out")):
+            w.check(host(g), f"expert {e} {name}")
+
+
+@pytest.mark.parametrize("E,rows,width", [(64, 2500, 64), (256, 12000, 64)])
+def test_backward_time_of_rows_on_one_expert(E, rows, width):
+    """The same rows, spread evenly and all on one expert: the pass's time does not
+    grow with an expert's rows.  (It was 25 to 100 times the even one's where one
+    block went through all of an expert's rows in order, which is far from the six
+    that are allowed here.)"""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("hottime", E, rows)
+    K = F = N = width
+    x, dy, wi, wo = (dev(f32(rng, *s)) for s in ((rows, K), (rows, N), (E, 2 * F, K), (E, N, F)))
+    even = ints(rows * np.arange(E + 1) // E)
+    one = ints(np.where(np.arange(E + 1) > E // 3, rows, 0))
+    best = []
+    for offsets in (even, one):
+        plan = emu.ExpertPlan(None, None, None, offsets)
+        y, d, h = emu.expert_ffn_fwd(x, wi, wo, plan, save=True)
+        run = lambda: emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan)
+        times = []
+        for _ in range(8):
+            run()
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            for _ in range(10):
+                run()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        best.append(min(times))
+    done()
+    assert best[1] <= 6 * best[0], best
