@@ -4,7 +4,8 @@ import threading
 import numpy as np
 import pytest
 
-from tests.test_gpu_experts import check_plan, expert_reference, ints, route_oracle
+from tests._running import U, V
+from tests.test_gpu_experts import EPS, check_plan, expert_reference, ints, route_oracle
 from tests.test_gpu_feed_forward import dev, done, f32, host, rng_of
 
 pytestmark = pytest.mark.gpu
@@ -178,3 +179,31 @@ def test_backward_time_of_rows_on_one_expert(E, rows, width):
         best.append(min(times))
     done()
     assert best[1] <= 6 * best[0], best
+
+
+@pytest.mark.parametrize("N", [20000, 40003, 100000])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm_of_wide_rows_adds_its_squares_in_two_words(N, residual):
+    """A large value and many whose squares are each below half of its last bit: sums
+    in one word drop them wherever they meet it.  Each quad of squares is off by three
+    roundings at most, their sum in two words by its last one; the mean and the
+    addition of eps add three, the root halves those seven, and rounds, and so does
+    the reciprocal: 5.5 in all."""
+    import fp32_emulated_gemm_gb300 as emu
+    small = np.float32(2.0 ** -12.25)
+    x = np.full((3, N), small, np.float32)
+    x[0, 0], x[1, N - 1], x[2, N // 2] = 1, 1, 1
+    q = None
+    if residual:                              # (the sums are exact: a half and a half)
+        q = (x / 2).astype(np.float32)
+        x = q.copy()
+    y, s, rstd = emu.rms_norm_fwd(dev(x), residual=dev(q), eps=EPS)
+    Q, scales, *_ = emu.rms_norm_quant(dev(x), residual=dev(q), eps=EPS)
+    done()
+    s64 = (x if q is None else x + q).astype(np.float64)
+    want = 1 / np.sqrt((s64 ** 2).mean(1) + float(np.float32(EPS)))
+    V(want, 5.6 * U * want).check(host(rstd), "rstd")
+    y64 = s64 * want[:, None]
+    V(y64, 6.7 * U * np.abs(y64)).check(host(y), "Y")
+    wide = np.repeat(host(scales).astype(np.float64), 128, 1)[:, :N]
+    assert np.all(np.abs(host(Q.float()) * wide - y64) <= 2.0 ** -4 * y64 * (1 + 8 * U) + 8 * U * y64 + 2.0 ** -10 * wide)
