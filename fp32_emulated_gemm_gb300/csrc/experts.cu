@@ -341,6 +341,10 @@ bool few_bwd(int64_t rows, int E, int64_t K, int64_t F, int64_t N, int pairs) {
 bool many_lots(int64_t rows, int64_t F, int64_t N) { return rows * (F / 2 + N / 4) >= 8192; }
 
 bool size_ok(int64_t v) { return v <= INT32_MAX - 256; }
+// (each size before its products, which would overflow)
+bool sizes_ok(int64_t rows, int E, int64_t K, int64_t F, int64_t N) {
+    return E <= kMaxExperts && size_ok(rows) && size_ok(K) && size_ok(F) && size_ok(N) && size_ok(E * 2 * F) && size_ok(E * N);
+}
 
 // A call's grouped products, a launch or two, with one kernel for the lists and
 // walks of all of them.
@@ -415,9 +419,7 @@ emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, in
                                 int64_t ldy, emu_stream_t stream) {
     if (act < EMU_ACT_NONE || act > EMU_ACT_SILU || rows < 0 || E < 1 || K < 1 || F < 1 || N < 1)
         return EMU_STATUS_INVALID_VALUE;
-    if (!fused_mode(mode) || E > kMaxExperts || !size_ok(rows) || !size_ok(K) || !size_ok(2 * F) || !size_ok(N) ||
-        !size_ok(E * 2 * F) || !size_ok(E * N))
-        return EMU_STATUS_NOT_SUPPORTED;
+    if (!fused_mode(mode) || !sizes_ok(rows, E, K, F, N)) return EMU_STATUS_NOT_SUPPORTED;
     if (rows == 0) return EMU_STATUS_SUCCESS;
     if (!X || !offsets || !W_in || !W_out || !H || !Y || ldx < K || ldwi < K || ldwo < F || ldh < F || ldy < N ||
         (D && ldd < 2 * F))
@@ -465,9 +467,7 @@ emu_status_t emu_expert_ffn_bwd(emu_mode_t mode, int64_t rows, int E, int64_t K,
                                 int64_t ldh, float* dZ, int64_t lddz, float* dX, int64_t lddx, float* dW_in, int64_t lddwi,
                                 float* dW_out, int64_t lddwo, emu_stream_t stream) {
     if (rows < 0 || E < 1 || K < 1 || F < 1 || N < 1) return EMU_STATUS_INVALID_VALUE;
-    if (!fused_mode(mode) || E > kMaxExperts || !size_ok(rows) || !size_ok(K) || !size_ok(2 * F) || !size_ok(N) ||
-        !size_ok(E * 2 * F) || !size_ok(E * N))
-        return EMU_STATUS_NOT_SUPPORTED;
+    if (!fused_mode(mode) || !sizes_ok(rows, E, K, F, N)) return EMU_STATUS_NOT_SUPPORTED;
     if ((dW_in && lddwi < K) || (dW_out && lddwo < F)) return EMU_STATUS_INVALID_VALUE;
     const bool inner = dX || dW_in;
     if (!inner && !dW_out) return EMU_STATUS_SUCCESS;

@@ -122,6 +122,17 @@ def test_expert_products_checks(ex, p):
     assert b(dX=None, dWi=None, dWo=None) == 0
 
 
+def test_expert_products_sizes_that_overflow(ex, p):
+    """Sizes whose products leave 64 bits are refused like other large ones, also
+    where there are no rows."""
+    fn = lambda name, *a: ex._fn(name)(*a, None)
+    for rows in (0, 40):
+        for E, K, F, N in ((1, 4, 2 ** 62, 4), (2, 4, 2 ** 62, 4), (1, 4, 2 ** 63 - 4, 4), (4, 4, 4, 2 ** 62), (1, 2 ** 62, 4, 4)):
+            assert fn("emu_expert_ffn_fwd", 0, 4, rows, E, K, F, N, p, K, p, p, K, p, F, None, 0, p, F, p, N) == NOT_SUPPORTED
+            assert fn("emu_expert_ffn_bwd", 0, rows, E, K, F, N, p, N, p, K, p, p, K, p, F, p, 2 ** 62, p, F, p, 2 ** 62, p, K, None, 0,
+                      None, 0) == NOT_SUPPORTED
+
+
 @pytest.fixture
 def plain(monkeypatch):
     """The functional calls replaced by plain ones on the CPU that record how they
