@@ -4,6 +4,7 @@ import threading
 import numpy as np
 import pytest
 
+from tests import _running as R
 from tests._running import U, V
 from tests.test_gpu_experts import EPS, check_plan, expert_reference, ints, route_oracle
 from tests.test_gpu_feed_forward import dev, done, f32, host, rng_of
@@ -207,3 +208,53 @@ def test_rms_norm_of_wide_rows_adds_its_squares_in_two_words(N, residual):
     V(y64, 6.7 * U * np.abs(y64)).check(host(y), "Y")
     wide = np.repeat(host(scales).astype(np.float64), 128, 1)[:, :N]
     assert np.all(np.abs(host(Q.float()) * wide - y64) <= 2.0 ** -4 * y64 * (1 + 8 * U) + 8 * U * y64 + 2.0 ** -10 * wide)
+
+
+@pytest.mark.parametrize("counts,K,F,N,act", [
+    ([3, 0, 5], 36, 100, 60, "silu"), ([1, 0, 0, 2], 700, 1540, 129, "gelu"), ([40, 17, 5, 33], 36, 2052, 1030, "gelu_tanh"),
+    ([200, 0, 7, 120], 256, 512, 260, "silu"), ([1500, 0, 257, 900], 260, 387, 72, "silu"), ([5000, 0, 257, 3300], 64, 100, 60, "none")])
+def test_saved_derivatives_and_outputs(counts, K, F, N, act):
+    """D = [u a'(g) | a(g)], H and Y of each form of the forward pass against the
+    definition."""
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("saved", sum(counts), K)
+    E, offsets = len(counts), np.concatenate([[0], np.cumsum(counts)])
+    x = f32(rng, sum(counts), K)
+    wi, wo = f32(rng, E, 2 * F, K, std=K ** -0.5), f32(rng, E, N, F, std=F ** -0.5)
+    y, d, h = emu.expert_ffn_fwd(dev(x), dev(wi), dev(wo), emu.ExpertPlan(None, None, None, ints(offsets)), act=act, save=True)
+    done()
+    assert d.shape == (sum(counts), 2 * F)
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        z = R.product(x[r], wi[e].T, "bf16x9")
+        g, u = z.cols(0, F), z.cols(F, 2 * F)
+        a = R.act_value(act, g) if act != "none" else g
+        slope = R.act_grad(act, g) if act != "none" else V(np.ones_like(g.val))
+        (u * slope).check(host(d[r, :F]), f"expert {e} u a'(g)")
+        a.check(host(d[r, F:]), f"expert {e} a(g)")
+        (a * u).check(host(h[r]), f"expert {e} H")
+        R.product(a * u, wo[e].T, "bf16x9").check(host(y[r]), f"expert {e} Y")
+
+
+@pytest.mark.parametrize("mode", ["bf16x9", "tf32x3"])
+@pytest.mark.parametrize("M", [7, 100, 2048])
+def test_one_expert_and_the_dense_block(M, mode):
+    """One expert with every row and the gated block agree in D, H and Y within both
+    calls' bounds (their sums are cut differently, so not bit for bit)."""
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("dense", M)
+    K, F, N = 256, 512, 132
+    x, wi, wo = f32(rng, M, K), f32(rng, 1, 2 * F, K, std=0.06), f32(rng, 1, N, F, std=0.04)
+    y, d, h = emu.expert_ffn_fwd(dev(x), dev(wi), dev(wo), emu.ExpertPlan(None, None, None, ints([0, M])), mode=mode, save=True)
+    h2, d2 = emu.gated_fwd(dev(x), dev(wi[0]), mode=mode, save=True)
+    y2 = emu.linear_fwd(h2, dev(wo[0]), mode=mode)
+    done()
+    z = R.product(x, wi[0].T, mode)
+    g, u = z.cols(0, F), z.cols(F, 2 * F)
+    a, slope = R.act_value("silu", g), R.act_grad("silu", g)
+    ud = u * slope
+    for one, dense, want, name in ((d[:, :F], d2[:, :F], ud, "u a'(g)"), (d[:, F:], d2[:, F:], a, "a(g)"), (h, h2, a * u, "H"),
+                                   (y, y2, R.product(a * u, wo[0].T, mode), "Y")):
+        want.check(host(one), name)
+        want.check(host(dense), name + " of the dense block")
+        assert np.all(np.abs(host(one).astype(np.float64) - host(dense)) <= 2 * want.err + 2 * U * np.abs(want.val) + 1e-37), name
