@@ -457,7 +457,9 @@ emu_status_t emu_expert_combine_bwd(int64_t M, int k, int64_t N, const float *dY
  * weights' size (at most 32768; where that is predicted faster, from the sizes
  * alone) on the CUDA cores in FP32, within the modes' bounds.  Buffers: the products take
  * lists of their tiles (16 bytes for 256 rows and for an expert) and the split-K
- * workspace with 256 KiB for each CTA pair (19 MiB on 152 SMs).
+ * workspace with 256 KiB for each CTA pair (19 MiB on 152 SMs); a backward pass of few
+ * rows takes room for shares of its contractions and for sums over parts of an
+ * expert's rows.
  */
 emu_status_t emu_expert_ffn_fwd(emu_mode_t mode, emu_act_t act, int64_t rows, int E, int64_t K, int64_t F, int64_t N,
                                 const float *X, int64_t ldx, const int32_t *offsets, const float *W_in, int64_t ldwi,

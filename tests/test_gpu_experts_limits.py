@@ -152,7 +152,7 @@ def test_backward_of_rows_on_one_expert(E, rows, K, F, N, kind):
 @pytest.mark.parametrize("E,rows,width", [(64, 2500, 64), (256, 12000, 64)])
 def test_backward_time_of_rows_on_one_expert(E, rows, width):
     """The same rows, spread evenly and all on one expert: the pass's time does not
-    grow with an expert's rows.  (It was 25 to 100 times the even one's where one
+    grow with an expert's rows.  (It was 27 and 48 times the even one's where one
     block went through all of an expert's rows in order, which is far from the six
     that are allowed here.)"""
     import torch
