@@ -258,3 +258,34 @@ def test_one_expert_and_the_dense_block(M, mode):
         want.check(host(one), name)
         want.check(host(dense), name + " of the dense block")
         assert np.all(np.abs(host(one).astype(np.float64) - host(dense)) <= 2 * want.err + 2 * U * np.abs(want.val) + 1e-37), name
+
+
+def test_chunks_of_rows_in_a_graph():
+    """A captured backward pass whose replays meet other offsets than the capture did:
+    even ones, all rows on one expert, none at all."""
+    import torch
+    import fp32_emulated_gemm_gb300 as emu
+    rng = rng_of("chunkgraph")
+    E, rows, K, F, N = 64, 2500, 64, 65, 60
+    x, dy, wi, wo = (dev(f32(rng, *s)) for s in ((rows, K), (rows, N), (E, 2 * F, K), (E, N, F)))
+    kinds = [ints(rows * np.arange(E + 1) // E), ints(np.where(np.arange(E + 1) > 7, rows, 0)), ints([0] * (E + 1)),
+             ints(np.concatenate([[5], np.full(E, 9)]))]
+    offsets = kinds[0].clone()
+    plan = emu.ExpertPlan(None, None, None, offsets)
+    d, h = dev(f32(rng, rows, 2 * F)), dev(f32(rng, rows, F))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = emu.expert_ffn_bwd(dy, x, wi, wo, d, h, plan)
+    for i in (0, 1, 2, 3, 1, 0):
+        offsets.copy_(kinds[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = emu.expert_ffn_bwd(dy, x, wi, wo, d, h, emu.ExpertPlan(None, None, None, kinds[i]))
+        torch.cuda.synchronize()
+        r = slice(int(kinds[i][0]), int(kinds[i][-1]))
+        assert torch.equal(got[0][r], want[0][r]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2]), i
+    done()
